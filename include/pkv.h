@@ -15,17 +15,17 @@
  *   - `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *     stream).  Every call only enqueues work on `stream` and returns; none
  *     synchronises except pkv_get_error.  Work is stream ordered as usual:
- *     the write and attention calls (not pkv_prepare_step) launch their
- *     kernels with programmatic dependent launch,
- *     so a kernel may begin its set-up while the work before it on the
+ *     the write and attention calls (pkv_write_rope among them, not
+ *     pkv_prepare_step) launch their kernels with programmatic dependent
+ *     launch, so a kernel may begin its set-up while the work before it on the
  *     stream is finishing, but it writes no global memory, and reads none
  *     that that work produces, until that work has finished.  One
  *     refinement: the step plan of pkv_attention, pkv_attention_int8,
  *     pkv_attention_noalloc and pkv_plan reads query_start_loc and seq_lens
  *     as soon as its kernel starts, which is after the kernel before it on
- *     the stream has finished, or, when that kernel is pkv_write's (or
- *     pkv_write_int8's) or another plan's, after everything before that
- *     kernel has finished: so enqueue the metadata before the write (as a
+ *     the stream has finished, or, when that kernel is a cache write's
+ *     (pkv_write*) or another plan's, after everything before that kernel
+ *     has finished: so enqueue the metadata before the write (as a
  *     step does), or from a kernel launched without programmatic
  *     serialisation.  Within a bf16 attention call that has prefill work,
  *     the decode kernel leaves some SMs to the prefill kernel, whose items
@@ -82,6 +82,7 @@ extern "C" {
                                     written).  The library sizes the workspace
                                     so that this does not happen; the bit
                                     reports a broken bound, never truncation */
+#define PKV_DEV_ERR_POSITION 256 /* pkv_write_rope: a position outside the table */
 
 /*
  * pkv_write — the cache-write scatter.
@@ -114,6 +115,63 @@ int pkv_write(const void* k, int64_t k_row_stride, const void* v, int64_t v_row_
               void* key_cache, void* value_cache, int64_t num_blocks, int32_t block_size,
               int32_t num_kv_heads, int32_t head_size, const int64_t* slot_mapping,
               int64_t n_tokens, void* stream);
+
+/*
+ * pkv_write_rope — the cache write with the position rotation (and optional
+ * per-head norms) of queries and keys on the way.
+ *
+ * For t in [0, n_tokens) with s = slot_mapping[t] >= 0 and p = positions[t],
+ * every head row x (128 values) of q[t] and k[t] becomes, in fp32,
+ *   y = x                                               without a weight,
+ *   y = x / sqrt(mean(x^2) + eps) * (w + weight_offset)  with q_weight / k_weight,
+ * and its first rotary_dim values are rotated: with half = rotary_dim / 2,
+ * c = cos_sin[p][i], d = cos_sin[p][half + i], for every i < half
+ *   (y_a, y_b) -> (y_a c - y_b d, y_b c + y_a d),
+ * (a, b) = (i, i + half), or (2 i, 2 i + 1) when interleaved is not 0.  The
+ * result is rounded once, to bf16: query rows go to q_out[t], key rows to
+ * key_cache[s / block_size][s % block_size], and the value rows of v[t] are
+ * copied bit for bit to value_cache there.  A token with a negative slot is
+ * padding: nothing of it is read or written (its q_out row included).
+ *
+ *   q, q_out      bf16 [n_tokens, num_heads, head_size], rows strided as in
+ *                 pkv_attention.  q_out may be q with the same row stride
+ *                 (in place); any other overlap is not allowed.
+ *   k, v, caches, slot_mapping, n_tokens  as in pkv_write; num_heads is any
+ *                 positive count (no relation to num_kv_heads is needed).
+ *   q_weight,     bf16 [head_size], or NULL: that side is not normalised.
+ *   k_weight      weight_offset is added to both (0; 1 for models that store
+ *                 w - 1).  eps >= 0.
+ *   cos_sin       fp32 [max_positions, rotary_dim], contiguous: cos | sin of
+ *                 each position's angles.
+ *   rotary_dim    a multiple of 16 from 16 to 128 (else PKV_ERR_UNSUPPORTED).
+ *   positions     int64 [n_tokens].
+ * A slot past the pool, or a position outside [0, max_positions), skips the
+ * whole token and sets PKV_DEV_ERR_SLOT_RANGE / PKV_DEV_ERR_POSITION.
+ * Alignment: q, k, v, q_out, caches, cos_sin, weights 16-byte aligned; row
+ * strides * 2 bytes multiples of 16.
+ *
+ * pkv_write_rope_int8 — the same into int8 caches: key and value codes are
+ * clamp(rne(y / scale), -127, 127) of the fp32 values (not of a bf16
+ * rounding of them), as in pkv_write_int8; q_out stays bf16.
+ */
+int pkv_write_rope(const void* q, int64_t q_row_stride, int32_t num_heads, const void* k,
+                   int64_t k_row_stride, const void* v, int64_t v_row_stride,
+                   const void* q_weight, const void* k_weight, float weight_offset, float eps,
+                   const float* cos_sin, int64_t max_positions, int32_t rotary_dim,
+                   int32_t interleaved, const int64_t* positions, void* q_out,
+                   int64_t q_out_row_stride, void* key_cache, void* value_cache,
+                   int64_t num_blocks, int32_t block_size, int32_t num_kv_heads,
+                   int32_t head_size, const int64_t* slot_mapping, int64_t n_tokens,
+                   void* stream);
+int pkv_write_rope_int8(const void* q, int64_t q_row_stride, int32_t num_heads, const void* k,
+                        int64_t k_row_stride, const void* v, int64_t v_row_stride,
+                        const void* q_weight, const void* k_weight, float weight_offset,
+                        float eps, const float* cos_sin, int64_t max_positions,
+                        int32_t rotary_dim, int32_t interleaved, const int64_t* positions,
+                        void* q_out, int64_t q_out_row_stride, void* key_cache,
+                        void* value_cache, float k_scale, float v_scale, int64_t num_blocks,
+                        int32_t block_size, int32_t num_kv_heads, int32_t head_size,
+                        const int64_t* slot_mapping, int64_t n_tokens, void* stream);
 
 /*
  * pkv_attention — varlen causal attention over the paged cache for a packed

@@ -15,12 +15,14 @@ DEV_ERR_BITS = {
     "TIMEOUT": 32,
     "INT8_PREFILL": 64,
     "CAPACITY": 128,
+    "POSITION": 256,
 }
 
 EXPORTS = ["pkv_write", "pkv_attention", "pkv_reserve_workspace", "pkv_get_error",
            "pkv_last_error_string", "pkv_num_sms", "pkv_trace_enable", "pkv_trace_read",
            "pkv_launch_count", "pkv_prepare_step", "pkv_write_int8", "pkv_attention_int8",
-           "pkv_plan", "pkv_attention_planned", "pkv_workspace_size"]
+           "pkv_plan", "pkv_attention_planned", "pkv_workspace_size", "pkv_write_rope",
+           "pkv_write_rope_int8"]
 TRACE_KINDS = ["write", "plan", "decode", "prefill", "combine", "prepare"]
 
 
@@ -55,6 +57,12 @@ def load():
     L.pkv_attention_int8.restype = ctypes.c_int
     L.pkv_attention_int8.argtypes = [vp, i64, i64, i32, vp, vp, f32, f32, i64, i32, i32, i32, vp,
                                      vp, vp, i64, i32, f32, vp, i64, vp]
+    rope = [vp, i64, i32, vp, i64, vp, i64, vp, vp, f32, f32, vp, i64, i32, i32, vp, vp, i64, vp,
+            vp]
+    L.pkv_write_rope.restype = ctypes.c_int
+    L.pkv_write_rope.argtypes = rope + [i64, i32, i32, i32, vp, i64, vp]
+    L.pkv_write_rope_int8.restype = ctypes.c_int
+    L.pkv_write_rope_int8.argtypes = rope + [f32, f32, i64, i32, i32, i32, vp, i64, vp]
     L.pkv_plan.restype = ctypes.c_int
     L.pkv_plan.argtypes = [i64, i32, i32, vp, vp, i64, i32, vp]
     L.pkv_attention_planned.restype = ctypes.c_int
@@ -233,6 +241,91 @@ def _caches(key_cache, value_cache, dtype):
     if key_cache.shape != value_cache.shape:
         raise ValueError("key_cache and value_cache shapes differ")
     return key_cache.shape
+
+
+def _on_current_device(*named):
+    """Checks (tensor, name, dtype) triples: the dtype, and that each tensor
+    lives on the current CUDA device, whose stream the call enqueues on.
+    Tensors that are None are skipped."""
+    torch = _T()
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -2
+    for t, name, dtype in named:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_cuda:
+            _require(t, dtype, name)
+        if t.get_device() != dev:
+            raise ValueError("%s is on cuda:%d, the current device is cuda:%d" %
+                             (name, t.get_device(), dev))
+
+
+def _heads3(t, name):
+    """(rows, heads, row stride) of a [rows, heads, 128] tensor."""
+    if t.dim() != 3:
+        raise ValueError("%s must be [rows, heads, head_size]" % name)
+    rows, heads, _ = t.shape
+    return rows, heads, _rows3(t, name)
+
+
+def _write_rope(q, k, v, positions, cos_sin, key_cache, value_cache, slot_mapping, q_out,
+                interleaved, q_weight, k_weight, weight_offset, eps, n_tokens, stream, scales):
+    torch = _T()
+    bf16 = torch.bfloat16
+    cache = torch.int8 if scales else bf16
+    _on_current_device((q, "q", bf16), (k, "k", bf16), (v, "v", bf16), (q_out, "q_out", bf16),
+                       (key_cache, "key_cache", cache), (value_cache, "value_cache", cache),
+                       (cos_sin, "cos_sin", torch.float32), (positions, "positions", torch.int64),
+                       (slot_mapping, "slot_mapping", torch.int64), (q_weight, "q_weight", bf16),
+                       (k_weight, "k_weight", bf16))
+    nb, bs, hkv, d = _caches(key_cache, value_cache, cache)
+    qr, hq, qs = _heads3(q, "q")
+    qor, hqo, qos = _heads3(q_out, "q_out")
+    kr, hk, ks = _heads3(k, "k")
+    vr, hv, vs = _heads3(v, "v")
+    if hqo != hq or hk != hkv or hv != hkv or not (q.shape[2] == q_out.shape[2] == k.shape[2] ==
+                                                   v.shape[2] == d):
+        raise ValueError("q and q_out must have the same heads, k and v those of the caches, all "
+                         "head_size %d" % d)
+    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None and (t.shape != (d,) or not t.is_contiguous()):
+            raise ValueError("%s must be a contiguous [head_size]" % name)
+    if cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        raise ValueError("cos_sin must be a contiguous [max_positions, rotary_dim]")
+    if not (slot_mapping.is_contiguous() and positions.is_contiguous()):
+        raise ValueError("slot_mapping and positions must be contiguous")
+    n = slot_mapping.shape[0] if n_tokens is None else int(n_tokens)
+    if n > min(slot_mapping.shape[0], positions.shape[0], qr, qor, kr, vr):
+        raise ValueError("n_tokens exceeds the rows of q/k/v/q_out/positions/slot_mapping")
+    L = load()
+    fn = L.pkv_write_rope_int8 if scales else L.pkv_write_rope
+    _check(fn(q.data_ptr(), qs, hq, k.data_ptr(), ks, v.data_ptr(), vs,
+              None if q_weight is None else q_weight.data_ptr(),
+              None if k_weight is None else k_weight.data_ptr(), weight_offset, eps,
+              cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], 1 if interleaved else 0,
+              positions.data_ptr(), q_out.data_ptr(), qos, key_cache.data_ptr(),
+              value_cache.data_ptr(), *scales, nb, bs, hkv, d, slot_mapping.data_ptr(), n,
+              _stream(stream)))
+
+
+def pkv_write_rope(q, k, v, positions, cos_sin, key_cache, value_cache, slot_mapping, q_out,
+                   interleaved=False, q_weight=None, k_weight=None, weight_offset=0.0, eps=1e-6,
+                   n_tokens=None, stream=None):
+    """pkv_write with the rotation of q and k ([n, heads, 128] bf16) at
+    positions (int64) by cos_sin ([max_positions, rotary_dim] fp32, cos | sin),
+    after a per-head RMS norm where a weight ([128] bf16) is given: rotated
+    queries into q_out (q itself for in place), keys and values into the caches."""
+    _write_rope(q, k, v, positions, cos_sin, key_cache, value_cache, slot_mapping, q_out,
+                interleaved, q_weight, k_weight, weight_offset, eps, n_tokens, stream, ())
+
+
+def pkv_write_rope_int8(q, k, v, positions, cos_sin, key_cache, value_cache, slot_mapping,
+                        k_scale, v_scale, q_out, interleaved=False, q_weight=None, k_weight=None,
+                        weight_offset=0.0, eps=1e-6, n_tokens=None, stream=None):
+    """pkv_write_rope into int8 caches: codes clamp(rne(x / scale), -127, 127)
+    of the rotated fp32 keys and of the values."""
+    _write_rope(q, k, v, positions, cos_sin, key_cache, value_cache, slot_mapping, q_out,
+                interleaved, q_weight, k_weight, weight_offset, eps, n_tokens, stream,
+                (k_scale, v_scale))
 
 
 def pkv_write_int8(k, v, key_cache, value_cache, slot_mapping, k_scale, v_scale, n_tokens=None,

@@ -125,6 +125,36 @@ cudaError_t launch_write_int8(const uint16_t* k, int64_t k_stride, const uint16_
                               int hkv, const int64_t* slots, int64_t n_tokens, float k_scale,
                               float v_scale, int* err, int sms, cudaStream_t st);
 
+// The cache write with the rotation (and the optional norms) of queries and
+// keys (pkv_rope.cu).
+struct RopeArgs {
+  const uint16_t* q;
+  int64_t q_stride;
+  int hq;
+  const uint16_t* k;
+  int64_t k_stride;
+  const uint16_t* v;
+  int64_t v_stride;
+  const uint16_t* q_weight;  // [128] bf16, or null: queries are not normalised
+  const uint16_t* k_weight;
+  float weight_offset, eps;
+  const float* table;        // [max_positions][rotary_dim]: cos | sin
+  int64_t max_positions;
+  int rotary_dim, interleaved;
+  const int64_t* positions;
+  uint16_t* q_out;
+  int64_t q_out_stride;
+  void* kc;
+  void* vc;
+  float k_scale, v_scale;    // int8 caches
+  int64_t num_slots;
+  int hkv;
+  const int64_t* slots;
+  int64_t n_tokens;
+  int* err;
+};
+cudaError_t launch_write_rope(const RopeArgs& a, bool int8, int sms, cudaStream_t st);
+
 struct AttnArgs {
   const uint16_t* q;
   int64_t q_stride;
