@@ -20,9 +20,8 @@
  *     launch, so a kernel may begin its set-up while the work before it on the
  *     stream is finishing, but it writes no global memory, and reads none
  *     that that work produces, until that work has finished.  One
- *     refinement: the step plan of pkv_attention, pkv_attention_int8,
- *     pkv_attention_noalloc and pkv_plan reads query_start_loc and seq_lens
- *     as soon as its kernel starts, which is after the kernel before it on
+ *     refinement: the step plan of the attention calls and of pkv_plan reads
+ *     query_start_loc and seq_lens (and prefix_lens) as soon as its kernel starts, which is after the kernel before it on
  *     the stream has finished, or, when that kernel is a cache write's
  *     (pkv_write*) or another plan's, after everything before that kernel
  *     has finished: so enqueue the metadata before the write (as a
@@ -222,6 +221,53 @@ int pkv_attention(const void* q, int64_t q_row_stride, int64_t q_rows, int32_t n
                   const int32_t* query_start_loc, const int32_t* seq_lens,
                   const int32_t* block_table, int64_t block_table_width, int32_t num_reqs,
                   float scale, void* out, int64_t out_row_stride, void* stream);
+
+/*
+ * pkv_attention_scored — pkv_attention with modified scores: a tanh cap, a
+ * bias by distance, a sliding window, a prefix that every row sees.
+ *
+ * For query row i of request r (position p = ctx + i, L = seq_lens[r]) and
+ * head h, with s_j = scale * q . K_j:
+ *   softcap > 0       s_j -> softcap * tanh(s_j / softcap)
+ *   alibi_slopes      s_j -> s_j - alibi_slopes[h] * |p - j|
+ *   visible keys      lo <= j < hi:
+ *                     lo = window > 0 ? max(0, p - window + 1) : 0
+ *                     hi = max(p + 1, min(prefix_lens[r], L))
+ *   out = sum_j softmax_j(s) V_j over the visible keys.
+ * A row always sees its own key.  Without any of the four (0, 0, NULL, NULL)
+ * the formula is pkv_attention's.  Keys past hi inside the prefix must be in
+ * the cache already: a prompt prefilled in chunks sees of its prefix what
+ * its earlier chunks and this one have written (seq_len keys).
+ *
+ *   scale         finite, > 0.
+ *   softcap       finite, >= 0; 0: no cap.  scale / softcap must stay in
+ *                 fp32's range (else PKV_ERR_ARG).
+ *   window        >= 0; 0: no window; 1: each row sees only its own key (and
+ *                 the prefix keys after it, when there is a prefix).
+ *   alibi_slopes  fp32 [num_heads] device, or NULL.
+ *   prefix_lens   int32 [num_reqs] device, or NULL; negative counts as 0.
+ * Pages that lie wholly before a request's window (keys before
+ * max(0, ctx - window + 1)) are not read, nor are their block_table entries,
+ * so a cache that frees them may leave anything there.  A masked key's K may
+ * hold anything.  V of a key that some row of the same request sees must be
+ * finite: the rows that do not see it weigh it with an exact zero.
+ *
+ * Other arguments, layouts, checks, alignment and errors are those of
+ * pkv_attention (bf16 caches; any query_len; the plan reads prefix_lens when
+ * it reads query_start_loc).  The call makes its own plan in the shared
+ * workspace (pkv_reserve_workspace covers it); the plan does not serve
+ * pkv_attention_planned.  As with every call that uses the workspace, calls
+ * on one device must not overlap on the GPU (two streams, two captured
+ * graphs replayed at once): they share one plan and one set of partials.
+ */
+int pkv_attention_scored(const void* q, int64_t q_row_stride, int64_t q_rows, int32_t num_heads,
+                         const void* key_cache, const void* value_cache, int64_t num_blocks,
+                         int32_t block_size, int32_t num_kv_heads, int32_t head_size,
+                         const int32_t* query_start_loc, const int32_t* seq_lens,
+                         const int32_t* block_table, int64_t block_table_width, int32_t num_reqs,
+                         float scale, float softcap, int32_t window, const float* alibi_slopes,
+                         const int32_t* prefix_lens, void* out, int64_t out_row_stride,
+                         void* stream);
 
 /*
  * pkv_plan / pkv_attention_planned — one step plan serving every layer.

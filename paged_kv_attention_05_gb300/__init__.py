@@ -10,6 +10,8 @@ the library is missing or no sm_103 device is present, the calls raise.
                   block_table, num_reqs, scale, out)
     pkv_write_int8 / pkv_attention_int8: the same over int8 caches with one
                   scale per cache (decode-path requests)
+    pkv_attention_scored: attention with a tanh cap, a distance bias, a sliding
+                  window, a prefix mask
     pkv_write_rope / pkv_write_rope_int8: the write with the position rotation
                   (and per-head norms) of queries and keys on the way
     pkv_plan / pkv_attention_planned: one step plan, then one call per layer
@@ -21,7 +23,7 @@ current stream) and return immediately.
 """
 from ._binding import (DEV_ERR_BITS, TRACE_KINDS, PkvError, library_path, load,
                        pkv_attention, pkv_attention_int8, pkv_attention_noalloc,
-                       pkv_attention_planned, pkv_get_error, pkv_plan,
+                       pkv_attention_planned, pkv_attention_scored, pkv_get_error, pkv_plan,
                        pkv_launch_count, pkv_num_sms, pkv_prepare_step,
                        pkv_reserve_workspace, pkv_trace_enable, pkv_trace_read,
                        pkv_workspace_size, pkv_write, pkv_write_int8, pkv_write_rope,
@@ -29,7 +31,7 @@ from ._binding import (DEV_ERR_BITS, TRACE_KINDS, PkvError, library_path, load,
 
 __all__ = ["pkv_write", "pkv_attention", "pkv_attention_noalloc", "pkv_prepare_step",
            "pkv_write_int8", "pkv_attention_int8", "pkv_write_rope", "pkv_write_rope_int8",
-           "pkv_plan", "pkv_attention_planned", "pkv_get_error",
+           "pkv_plan", "pkv_attention_planned", "pkv_attention_scored", "pkv_get_error",
            "pkv_reserve_workspace", "pkv_workspace_size",
            "pkv_num_sms", "pkv_trace_enable", "pkv_trace_read", "pkv_launch_count",
            "PkvError", "DEV_ERR_BITS", "TRACE_KINDS", "load", "library_path"]

@@ -22,7 +22,7 @@ EXPORTS = ["pkv_write", "pkv_attention", "pkv_reserve_workspace", "pkv_get_error
            "pkv_last_error_string", "pkv_num_sms", "pkv_trace_enable", "pkv_trace_read",
            "pkv_launch_count", "pkv_prepare_step", "pkv_write_int8", "pkv_attention_int8",
            "pkv_plan", "pkv_attention_planned", "pkv_workspace_size", "pkv_write_rope",
-           "pkv_write_rope_int8"]
+           "pkv_write_rope_int8", "pkv_attention_scored"]
 TRACE_KINDS = ["write", "plan", "decode", "prefill", "combine", "prepare"]
 
 
@@ -51,6 +51,9 @@ def load():
     L.pkv_attention.argtypes = [vp, i64, i64, i32, vp, vp, i64, i32, i32, i32, vp, vp, vp, i64,
                                 i32, f32, vp, i64, vp]
     f32 = ctypes.c_float
+    L.pkv_attention_scored.restype = ctypes.c_int
+    L.pkv_attention_scored.argtypes = [vp, i64, i64, i32, vp, vp, i64, i32, i32, i32, vp, vp, vp,
+                                       i64, i32, f32, f32, i32, vp, vp, vp, i64, vp]
     L.pkv_write_int8.restype = ctypes.c_int
     L.pkv_write_int8.argtypes = [vp, i64, vp, i64, vp, vp, f32, f32, i64, i32, i32, i32, vp, i64,
                                  vp]
@@ -377,6 +380,51 @@ def pkv_attention_int8(q, key_cache, value_cache, k_scale, v_scale, query_start_
                                      block_table.data_ptr(), bt_width, int(num_reqs),
                                      float(scale), out.data_ptr(), _rows3(out, "out"),
                                      _stream(stream)))
+
+
+def pkv_attention_scored(q, key_cache, value_cache, query_start_loc, seq_lens, block_table,
+                         num_reqs, scale, out, softcap=0.0, window=0, alibi_slopes=None,
+                         prefix_lens=None, stream=None):
+    """pkv_attention with modified scores: softcap * tanh(s / softcap), the
+    bias -alibi_slopes[head] * distance (fp32 [Hq]), a sliding window of keys
+    and a prefix (int32 [num_reqs]) that every row sees; see include/pkv.h."""
+    torch = _T()
+    bf16, i32 = torch.bfloat16, torch.int32
+    _on_current_device((q, "q", bf16), (key_cache, "key_cache", bf16),
+                       (value_cache, "value_cache", bf16), (out, "out", bf16),
+                       (query_start_loc, "query_start_loc", i32), (seq_lens, "seq_lens", i32),
+                       (block_table, "block_table", i32),
+                       (alibi_slopes, "alibi_slopes", torch.float32),
+                       (prefix_lens, "prefix_lens", i32))
+    nb, bs, hkv, d = _caches(key_cache, value_cache, bf16)
+    rows, hq, qs = _heads3(q, "q")
+    orows, ohq, os_ = _heads3(out, "out")
+    if orows < rows or ohq != hq or out.shape[2] != d or q.shape[2] != d:
+        raise ValueError("q and out must be [rows, num_heads, %d] with as many rows of out" % d)
+    num_reqs, window = int(num_reqs), int(window)
+    for t, name in ((query_start_loc, "query_start_loc"), (seq_lens, "seq_lens"),
+                    (block_table, "block_table"), (alibi_slopes, "alibi_slopes"),
+                    (prefix_lens, "prefix_lens")):
+        if t is not None and not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+    two = block_table.dim() == 2
+    if not two and (block_table.dim() != 1 or num_reqs > 1):
+        raise ValueError("block_table must be [num_reqs, width]")
+    if num_reqs > 0 and (query_start_loc.numel() < num_reqs + 1 or seq_lens.numel() < num_reqs or
+                         (two and block_table.shape[0] < num_reqs) or
+                         (prefix_lens is not None and prefix_lens.numel() < num_reqs)):
+        raise ValueError("metadata shorter than num_reqs")
+    if alibi_slopes is not None and alibi_slopes.shape != (hq,):
+        raise ValueError("alibi_slopes must be [num_heads]")
+    if not -1 <= window < 1 << 31 or num_reqs >= 1 << 31:
+        raise ValueError("window or num_reqs out of range")
+    _check(load().pkv_attention_scored(
+        q.data_ptr(), qs, rows, hq, key_cache.data_ptr(), value_cache.data_ptr(), nb, bs, hkv, d,
+        query_start_loc.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(),
+        block_table.shape[-1], num_reqs, scale, softcap, window,
+        None if alibi_slopes is None else alibi_slopes.data_ptr(),
+        None if prefix_lens is None else prefix_lens.data_ptr(), out.data_ptr(), os_,
+        _stream(stream)))
 
 
 def pkv_plan(q_rows, num_heads, num_kv_heads, query_start_loc, seq_lens, block_table_width,

@@ -445,7 +445,8 @@ int check_meta(int64_t q_rows, int32_t num_heads, int32_t num_kv_heads,
 // Builds the step plan into the device workspace (state lock held).
 int plan_locked(DeviceState* s, int64_t q_rows, int32_t num_heads, int32_t num_kv_heads,
                 const int32_t* query_start_loc, const int32_t* seq_lens,
-                int64_t block_table_width, int32_t num_reqs, int kv_int8, cudaStream_t st) {
+                int64_t block_table_width, int32_t num_reqs, int kv_int8, const ScoreArgs& score,
+                cudaStream_t st) {
   const int workers = decode_workers(num_heads / num_kv_heads, kv_int8, s->sms);
   const Sizes z = with_wave_room(
       sizes_for(num_reqs, q_rows, block_table_width, num_heads, num_kv_heads), q_rows,
@@ -462,10 +463,12 @@ int plan_locked(DeviceState* s, int64_t q_rows, int32_t num_heads, int32_t num_k
   a.bt_width = block_table_width;
   a.num_reqs = num_reqs;
   a.kv_int8 = kv_int8;
+  a.score = score;
   cudaError_t e = traced(1, st, [&] { return launch_plan(a, ws, workers, st); });
   if (e != cudaSuccess) return cuda_fail(e, "plan launch");
-  // an int8 plan leaves prefill-class requests out: it cannot serve a bf16 call
-  s->plan_valid = !kv_int8;
+  // an int8 plan leaves prefill-class requests out, a scored one the keys
+  // before its window: neither can serve a planned call
+  s->plan_valid = !kv_int8 && !score.on;
   s->plan_q_rows = q_rows;
   s->plan_bt_width = block_table_width;
   s->plan_hq = num_heads;
@@ -480,7 +483,7 @@ int plan_locked(DeviceState* s, int64_t q_rows, int32_t num_heads, int32_t num_k
 int run_locked(DeviceState* s, const void* q, int64_t q_row_stride, const void* key_cache,
                const void* value_cache, int64_t num_blocks, const int32_t* block_table,
                float scale, void* out, int64_t out_row_stride, int kv_int8, float k_scale,
-               float v_scale, cudaStream_t st) {
+               float v_scale, const ScoreArgs& score, cudaStream_t st) {
   Workspace ws = carve_workspace(s->ws, s->plan_sizes, s->err);
   AttnArgs a{};
   a.q = static_cast<const uint16_t*>(q);
@@ -502,6 +505,7 @@ int run_locked(DeviceState* s, const void* q, int64_t q_row_stride, const void* 
   a.kv_int8 = kv_int8;
   a.k_scale = kv_int8 ? k_scale : 1.f;
   a.v_scale = kv_int8 ? v_scale : 1.f;
+  a.score = score;
   // Decode first.  When the step also has prefill work, the decode grid
   // leaves some SMs to it at once and the prefill grid (its programmatic
   // dependent) runs its items there beside the decode units; the prefill
@@ -548,7 +552,7 @@ int attention_common(const void* q, int64_t q_row_stride, int64_t q_rows, int32_
                      const int32_t* query_start_loc, const int32_t* seq_lens,
                      const int32_t* block_table, int64_t block_table_width, int32_t num_reqs,
                      float scale, void* out, int64_t out_row_stride, void* stream, int kv_int8,
-                     float k_scale, float v_scale) {
+                     float k_scale, float v_scale, const ScoreArgs& score = ScoreArgs()) {
   g_msg[0] = 0;
   int rc = check_geometry(block_size, num_kv_heads, head_size);
   if (rc) return rc;
@@ -569,10 +573,10 @@ int attention_common(const void* q, int64_t q_row_stride, int64_t q_rows, int32_
   if (rc) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   rc = plan_locked(s, q_rows, num_heads, num_kv_heads, query_start_loc, seq_lens,
-                   block_table_width, num_reqs, kv_int8, st);
+                   block_table_width, num_reqs, kv_int8, score, st);
   if (rc) return rc;
   return run_locked(s, q, q_row_stride, key_cache, value_cache, num_blocks, block_table, scale,
-                    out, out_row_stride, kv_int8, k_scale, v_scale, st);
+                    out, out_row_stride, kv_int8, k_scale, v_scale, score, st);
 }
 
 }  // namespace
@@ -598,7 +602,8 @@ extern "C" int pkv_plan(int64_t q_rows, int32_t num_heads, int32_t num_kv_heads,
     return PKV_OK;
   }
   return plan_locked(s, q_rows, num_heads, num_kv_heads, query_start_loc, seq_lens,
-                     block_table_width, num_reqs, 0, static_cast<cudaStream_t>(stream));
+                     block_table_width, num_reqs, 0, ScoreArgs(),
+                     static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int pkv_attention_planned(const void* q, int64_t q_row_stride, int32_t num_heads,
@@ -633,7 +638,7 @@ extern "C" int pkv_attention_planned(const void* q, int64_t q_row_stride, int32_
   cudaError_t e = cudaMemsetAsync(&hdr->dec_counter, 0, 2 * sizeof(int), st);
   if (e != cudaSuccess) return cuda_fail(e, "cursor reset");
   return run_locked(s, q, q_row_stride, key_cache, value_cache, num_blocks, block_table, scale,
-                    out, out_row_stride, 0, 1.f, 1.f, st);
+                    out, out_row_stride, 0, 1.f, 1.f, ScoreArgs(), st);
 }
 
 extern "C" int pkv_attention(const void* q, int64_t q_row_stride, int64_t q_rows,
@@ -661,6 +666,36 @@ extern "C" int pkv_attention_int8(const void* q, int64_t q_row_stride, int64_t q
                           block_size, num_kv_heads, head_size, query_start_loc, seq_lens,
                           block_table, block_table_width, num_reqs, scale, out, out_row_stride,
                           stream, 1, k_scale, v_scale);
+}
+
+extern "C" int pkv_attention_scored(const void* q, int64_t q_row_stride, int64_t q_rows,
+                                    int32_t num_heads, const void* key_cache,
+                                    const void* value_cache, int64_t num_blocks,
+                                    int32_t block_size, int32_t num_kv_heads, int32_t head_size,
+                                    const int32_t* query_start_loc, const int32_t* seq_lens,
+                                    const int32_t* block_table, int64_t block_table_width,
+                                    int32_t num_reqs, float scale, float softcap, int32_t window,
+                                    const float* alibi_slopes, const int32_t* prefix_lens,
+                                    void* out, int64_t out_row_stride, void* stream) {
+  g_msg[0] = 0;
+  if (!(scale > 0.f && scale < INFINITY))
+    return fail(PKV_ERR_ARG, "scale must be finite and positive");
+  if (!(softcap >= 0.f && softcap < INFINITY))
+    return fail(PKV_ERR_ARG, "softcap must be finite and >= 0 (0: none)");
+  // the kernels form 2 log2(e) scale / softcap and softcap log2(e) in fp32
+  if (softcap > 0.f && !(fabsf(3.f * (scale / softcap)) < INFINITY && 1.5f * softcap < INFINITY))
+    return fail(PKV_ERR_ARG, "scale / softcap is out of range");
+  if (window < 0) return fail(PKV_ERR_ARG, "window %d < 0 (0: none)", window);
+  ScoreArgs score;
+  score.on = 1;
+  score.softcap = softcap;
+  score.window = window;
+  score.slopes = alibi_slopes;
+  score.prefix = prefix_lens;
+  return attention_common(q, q_row_stride, q_rows, num_heads, key_cache, value_cache, num_blocks,
+                          block_size, num_kv_heads, head_size, query_start_loc, seq_lens,
+                          block_table, block_table_width, num_reqs, scale, out, out_row_stride,
+                          stream, 0, 1.f, 1.f, score);
 }
 
 extern "C" int pkv_reserve_workspace(int32_t max_reqs, int64_t max_q_rows,

@@ -135,7 +135,59 @@ __device__ __forceinline__ uint32_t mask_pair(uint32_t v, int tok_lo, int valid)
   const uint32_t hi = tok_lo + 1 < valid ? 0xFFFF0000u : 0u;
   return v & (lo | hi);
 }
+// keep the halves whose key index is at least `first`
+__device__ __forceinline__ uint32_t mask_pair_low(uint32_t v, int tok_lo, int first) {
+  const uint32_t lo = tok_lo >= first ? 0x0000FFFFu : 0u;
+  const uint32_t hi = tok_lo + 1 >= first ? 0xFFFF0000u : 0u;
+  return v & (lo | hi);
+}
 
+// What a scored call does to one query row of a decode unit.
+struct RowScore {
+  int pos, low;  // the row's position; first key it sees
+  float slope2;  // bias slope, log2 units
+};
+// The row at position pos of request r, head h; *vis (keys it sees end here)
+// grows to the request's prefix, clipped to the unit.
+__device__ __forceinline__ RowScore row_score(const AttnArgs& a, int r, int pos, int h, int k1,
+                                              int* vis) {
+  RowScore s;
+  s.pos = pos;
+  s.low = first_key(pos, a.score.window);
+  s.slope2 = a.score.slopes ? __ldg(a.score.slopes + h) * kLog2e : 0.f;
+  if (a.score.prefix) *vis = max(*vis, min(k1, __ldg(a.score.prefix + r)));
+  return s;
+}
+// A step's raw products q.K (n registers) to logits in log2 units, the cap
+// applied: one form for the whole warp, chosen by the keys its rows see
+// (seen(i, e): register e of tile i), since the others may hold anything.
+template <int n, class Seen>
+__device__ __forceinline__ void cap_scores(const ScoreParams& sp, float (&s)[n][4], Seen&& seen) {
+  if (!sp.cap) {
+#pragma unroll
+    for (int i = 0; i < 4 * n; ++i) s[i >> 2][i & 3] *= sp.lin;
+    return;
+  }
+  float big = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4 * n; ++i)
+    big = fmaxf(big, seen(i >> 2, i & 3) ? fabsf(s[i >> 2][i & 3]) : 0.f);
+  if (__all_sync(0xffffffffu, big * sp.k <= 1.f)) {
+#pragma unroll
+    for (int i = 0; i < 4 * n; ++i) s[i >> 2][i & 3] = capped_poly(s[i >> 2][i & 3], sp);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4 * n; ++i) s[i >> 2][i & 3] = capped_exp(s[i >> 2][i & 3], sp);
+  }
+}
+// The logit x of key j with the row's bias; -inf where the row does not see
+// the key.
+__device__ __forceinline__ float scored_logit(const RowScore& rs, float x, int j, int vis) {
+  x = fmaf(-rs.slope2, fabsf((float)(rs.pos - j)), x);
+  return j >= rs.low && j < vis ? x : -INFINITY;
+}
+
+template <bool kScored>
 __global__ void __launch_bounds__(Cfg::kThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, AttnArgs a, Workspace ws) {
@@ -175,6 +227,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
   const int n_units = ws.hdr->n_dec_units;
   const uint64_t pol = l2_evict_first();  // K/V pages are read once
   const float sl2 = a.scale * kLog2e;
+  const ScoreParams sp = score_params(a);
   const int gid = lane >> 2, tig = lane & 3;
   const int mi = lane >> 3, rr = lane & 7;
   uint32_t page_cnt = 0;
@@ -224,11 +277,16 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     // last visible key + 1 of the two rows this thread holds: row (token i,
     // head) sees keys < ctx + i + 1, clipped to the unit
     int vis[2];
+    RowScore rs[2];
+    const int vlow = kScored ? first_key(un.ctx, a.score.window) : 0;  // no row sees keys below
 #pragma unroll
     for (int hrow = 0; hrow < 2; ++hrow) {
       const int row = (lane >> 2) + hrow * 8;
       const int ti = row < nrows ? row / G : qn - 1;
       vis[hrow] = min(k1, un.ctx + ti + 1);
+      if (kScored)
+        rs[hrow] = row_score(a, un.r, un.ctx + ti, row < nrows ? ug * G + row % G : ug * G, k1,
+                             &vis[hrow]);
     }
 
     // page p of the unit into stage (page_cnt + p) % kStages; the stage's
@@ -301,13 +359,21 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       uint32_t pa[4];
       {
         float xs[2][4];
+        if (kScored)
+          cap_scores(sp, sacc, [&](int nt, int e) {
+            const int j = pos0 + nt * 8 + tig * 2 + (e & 1);
+            return j >= rs[e >> 1].low && j < vis[e >> 1];
+          });
         float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int tok = nt * 8 + tig * 2 + (e & 1);
-            xs[nt][e] = pos0 + tok < vis[e >> 1] ? sacc[nt][e] * sl2 : -INFINITY;
+            if (kScored)
+              xs[nt][e] = scored_logit(rs[e >> 1], sacc[nt][e], pos0 + tok, vis[e >> 1]);
+            else
+              xs[nt][e] = pos0 + tok < vis[e >> 1] ? sacc[nt][e] * sl2 : -INFINITY;
           }
           mx0 = fmaxf(mx0, fmaxf(xs[nt][0], xs[nt][1]));
           mx1 = fmaxf(mx1, fmaxf(xs[nt][2], xs[nt][3]));
@@ -363,6 +429,12 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           b2 = mask_pair(b2, 2 * tig, valid);
           b1 = mask_pair(b1, 8 + 2 * tig, valid);
           b3 = mask_pair(b3, 8 + 2 * tig, valid);
+        }
+        if (kScored && pos0 < vlow) {  // the first page of a window
+          b0 = mask_pair_low(b0, 2 * tig, vlow - pos0);
+          b2 = mask_pair_low(b2, 2 * tig, vlow - pos0);
+          b1 = mask_pair_low(b1, 8 + 2 * tig, vlow - pos0);
+          b3 = mask_pair_low(b3, 8 + 2 * tig, vlow - pos0);
         }
         mma_bf16(o[dn], pa, b0, b1);
         mma_bf16(o[dn + 1], pa, b2, b3);
@@ -445,6 +517,7 @@ struct CfgP {
 };
 static_assert(CfgP::kSmem <= 232448, "shared memory per CTA");
 
+template <bool kScored>
 __global__ void __launch_bounds__(CfgP::kThreads, 1)
     decode_pair_kernel(const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, AttnArgs a, Workspace ws) {
@@ -485,6 +558,7 @@ __global__ void __launch_bounds__(CfgP::kThreads, 1)
   const int n_units = ws.hdr->n_dec_units;
   const uint64_t pol = l2_evict_first();  // K/V pages are read once
   const float sl2 = a.scale * kLog2e;
+  const ScoreParams sp = score_params(a);
   const int gid = lane >> 2, tig = lane & 3;
   const int mi = lane >> 3, rr = lane & 7;
   const int roff = 16 * tile;  // this warp's rows (heads of the group)
@@ -574,7 +648,14 @@ __global__ void __launch_bounds__(CfgP::kThreads, 1)
       if (!ok) break;
     }
     // every row sees keys < ctx + 1, clipped to the unit
-    const int vis = min(k1, un.ctx + 1);
+    int vis = min(k1, un.ctx + 1);
+    RowScore rs[2];
+    const int vlow = kScored ? first_key(un.ctx, a.score.window) : 0;
+    if (kScored) {
+#pragma unroll
+      for (int hrow = 0; hrow < 2; ++hrow)
+        rs[hrow] = row_score(a, un.r, un.ctx, ug * G + min(roff + gid + 8 * hrow, G - 1), k1, &vis);
+    }
     // the A fragments of the warp's 16 query rows (heads roff + gid and
     // roff + gid + 8 of the group; k-step k: dimensions 16k + 2tig, + 1 in
     // registers 0 / 1 and 16k + 8 + 2tig, + 1 in 2 / 3); rows past the
@@ -639,13 +720,21 @@ __global__ void __launch_bounds__(CfgP::kThreads, 1)
       uint32_t pa[2][4];
       {
         float xs[4][4];
+        if (kScored)
+          cap_scores(sp, sacc, [&](int nt, int e) {
+            const int j = pos0 + nt * 8 + tig * 2 + (e & 1);
+            return j >= rs[e >> 1].low && j < vis;
+          });
         float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int tok = nt * 8 + tig * 2 + (e & 1);
-            xs[nt][e] = pos0 + tok < vis ? sacc[nt][e] * sl2 : -INFINITY;
+            if (kScored)
+              xs[nt][e] = scored_logit(rs[e >> 1], sacc[nt][e], pos0 + tok, vis);
+            else
+              xs[nt][e] = pos0 + tok < vis ? sacc[nt][e] * sl2 : -INFINITY;
           }
           mx0 = fmaxf(mx0, fmaxf(xs[nt][0], xs[nt][1]));
           mx1 = fmaxf(mx1, fmaxf(xs[nt][2], xs[nt][3]));
@@ -706,6 +795,13 @@ __global__ void __launch_bounds__(CfgP::kThreads, 1)
             b2 = mask_pair(b2, 2 * tig, valid[pg]);
             b1 = mask_pair(b1, 8 + 2 * tig, valid[pg]);
             b3 = mask_pair(b3, 8 + 2 * tig, valid[pg]);
+          }
+          if (kScored && pos0 < vlow) {  // the first page of a window
+            const int first = vlow - pos0 - pg * kBlockSize;
+            b0 = mask_pair_low(b0, 2 * tig, first);
+            b2 = mask_pair_low(b2, 2 * tig, first);
+            b1 = mask_pair_low(b1, 8 + 2 * tig, first);
+            b3 = mask_pair_low(b3, 8 + 2 * tig, first);
           }
           mma_bf16(o[dn], pa[pg], b0, b1);
           mma_bf16(o[dn + 1], pa[pg], b2, b3);
@@ -768,28 +864,30 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(AttnArgs a, Wo
   combine_splits(a, ws, blockIdx.x * kWarpsPerBlock + (threadIdx.x >> 5), gridDim.x * kWarpsPerBlock);
 }
 
+template <bool kScored>
 cudaError_t launch_one_tile(const AttnArgs& a, const Workspace& ws, int sms, cudaStream_t st) {
   using C = Cfg;
   static std::atomic<bool> attr[kMaxAttrDevices];
-  if (cudaError_t e = smem_attr_once(decode_kernel, C::kSmem, attr)) return e;
+  if (cudaError_t e = smem_attr_once(decode_kernel<kScored>, C::kSmem, attr)) return e;
   const int G = a.hq / a.hkv;
   CUtensorMap tq, tk, tv;
   if (!make_rows_map(&tq, a.q, a.q_rows, a.hq, a.q_stride, G, 1) ||
       !make_cache_map(&tk, a.kc, a.num_blocks, a.hkv) ||
       !make_cache_map(&tv, a.vc, a.num_blocks, a.hkv))
     return cudaErrorInvalidValue;
-  return launch_dependent(decode_kernel, dim3(sms), dim3(C::kThreads), C::kSmem, st, tq, tk,
+  return launch_dependent(decode_kernel<kScored>, dim3(sms), dim3(C::kThreads), C::kSmem, st, tq, tk,
                           tv, a, ws);
 }
 
+template <bool kScored>
 cudaError_t launch_pair(const AttnArgs& a, const Workspace& ws, int sms, cudaStream_t st) {
   static std::atomic<bool> attr[kMaxAttrDevices];
-  if (cudaError_t e = smem_attr_once(decode_pair_kernel, CfgP::kSmem, attr)) return e;
+  if (cudaError_t e = smem_attr_once(decode_pair_kernel<kScored>, CfgP::kSmem, attr)) return e;
   CUtensorMap tk, tv;  // (query rows: plain loads, 16-byte aligned by the API's checks)
   if (!make_cache_map(&tk, a.kc, a.num_blocks, a.hkv) ||
       !make_cache_map(&tv, a.vc, a.num_blocks, a.hkv))
     return cudaErrorInvalidValue;
-  return launch_dependent(decode_pair_kernel, dim3(sms), dim3(CfgP::kThreads), CfgP::kSmem, st,
+  return launch_dependent(decode_pair_kernel<kScored>, dim3(sms), dim3(CfgP::kThreads), CfgP::kSmem, st,
                           tk, tv, a, ws);
 }
 
@@ -802,7 +900,9 @@ int decode_workers(int group, int kv_int8, int sms) {
 cudaError_t launch_decode(const AttnArgs& a, const Workspace& ws, int sms, cudaStream_t st) {
   const int G = a.hq / a.hkv;
   if (a.kv_int8) return launch_decode_i8(a, ws, sms, st);
-  return G <= 16 ? launch_one_tile(a, ws, sms, st) : launch_pair(a, ws, sms, st);
+  if (a.score.on)
+    return G <= 16 ? launch_one_tile<true>(a, ws, sms, st) : launch_pair<true>(a, ws, sms, st);
+  return G <= 16 ? launch_one_tile<false>(a, ws, sms, st) : launch_pair<false>(a, ws, sms, st);
 }
 
 cudaError_t launch_combine(const AttnArgs& a, const Workspace& ws, int sms, cudaStream_t st) {

@@ -40,10 +40,11 @@ struct __align__(16) DecUnit {
 
 // One prefill work entry: request r (n query rows from q0, seq_len L),
 // 128-row query tile qt; nkv = number of 128-key tiles it reads (the work
-// estimate used for longest-first ordering).
+// estimate used for longest-first ordering), the first of them starting at
+// key `base`; every row sees the keys below `prefix` (scored calls; 0 else).
 struct __align__(16) PreEntry {
   int r, qt, nkv, q0;
-  int n, L, pad0, pad1;
+  int n, L, base, prefix;
 };
 
 // A (request, KV head) whose keys were split over several decode units: split
@@ -155,6 +156,30 @@ struct RopeArgs {
 };
 cudaError_t launch_write_rope(const RopeArgs& a, bool int8, int sms, cudaStream_t st);
 
+// What pkv_attention_scored does to the scores: a tanh cap, a distance bias,
+// and the visible keys of a row at position p, lo <= j < hi with
+// lo = window ? max(0, p - window + 1) : 0 and hi = max(p + 1, min(prefix, L)).
+struct ScoreArgs {
+  int on = 0;                       // 0: the plain causal call, nothing below is read
+  float softcap = 0.f;              // 0: none
+  int window = 0;                   // 0: none
+  const float* slopes = nullptr;    // [hq], or null
+  const int32_t* prefix = nullptr;  // [num_reqs], or null
+};
+
+// First key any row of a request sees, rounded down to its page: the keys a
+// decode request's units cover start here (ctx = keys before its first row).
+__host__ __device__ inline int first_key(int ctx, int window) {
+  return window > 0 && ctx >= window ? (ctx - window + 1) : 0;
+}
+__host__ __device__ inline int first_page_key(int ctx, int window) {
+  return first_key(ctx, window) & ~(kBlockSize - 1);
+}
+// min(max(prefix, 0), L): the keys every row of the request sees
+__host__ __device__ inline int clip_prefix(int prefix, int L) {
+  return prefix < 0 ? 0 : (prefix < L ? prefix : L);
+}
+
 struct AttnArgs {
   const uint16_t* q;
   int64_t q_stride;
@@ -177,6 +202,7 @@ struct AttnArgs {
   int kv_int8;
   float k_scale;
   float v_scale;
+  ScoreArgs score;
 };
 
 // TMA descriptors (pkv_tma.cu).  rows map: [rows, heads, 128] bf16 with a row

@@ -102,11 +102,13 @@ __device__ __forceinline__ int find_owner(const int* off, int n, int x) {
 struct ReqInfo {
   int kind;  // 0 nothing, 1 decode, 2 prefill
   int n, L, q0;
+  int kb;    // first key its decode units cover (0 without a window)
   int bad;   // PKV_DEV_ERR_* bits of a request that fails a check
 };
 
+template <bool kScored>
 __device__ ReqInfo classify(const AttnArgs& a, int r) {
-  ReqInfo ri{0, 0, 0, 0, 0};
+  ReqInfo ri{0, 0, 0, 0, 0, 0};
   const int q0 = __ldcg(a.qsl + r), q1 = __ldcg(a.qsl + r + 1), L = __ldcg(a.seq_lens + r);
   int bad = 0;
   if (q0 < 0 || q1 < q0 || (int64_t)q1 > a.q_rows)
@@ -122,6 +124,7 @@ __device__ ReqInfo classify(const AttnArgs& a, int r) {
   ri.n = q1 - q0;
   ri.L = L;
   ri.q0 = q0;
+  if (kScored) ri.kb = first_page_key(ri.L - ri.n, a.score.window);
   // decode: the query tokens x heads of a KV head fit one decode unit's rows
   // (speculative / multi-token decode included); prefill: anything longer
   const int G = a.hq / a.hkv;
@@ -133,6 +136,22 @@ __device__ ReqInfo classify(const AttnArgs& a, int r) {
   return ri;
 }
 
+// The keys a prefill entry reads: rows 128 t .. of a request of n rows, L keys
+// and (scored calls) a prefix clipped to L; *base = first key, page aligned.
+template <bool kScored>
+__device__ __forceinline__ int entry_tiles(const AttnArgs& a, int n, int L, int t, int prefix,
+                                           int* base) {
+  const int ctx = L - n;
+  int hi = ctx + min(kPreTileQ * (t + 1), n);
+  *base = 0;
+  if (kScored) {
+    hi = max(hi, prefix);
+    *base = first_page_key(ctx + kPreTileQ * t, a.score.window);
+  }
+  return (hi - *base + kPreTileQ - 1) / kPreTileQ;
+}
+
+template <bool kScored>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(AttnArgs a, Workspace ws,
                                                             int dec_grid) {
   __shared__ int4 smem33[33], smem33b[33];
@@ -155,22 +174,25 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(AttnArgs a, Workspac
   long long dec_keys = 0;
   int dec_reqs = 0, dec_lmax = 0, dec_rmax = 0;  // rmax: most query rows of a decode
   int pre_tiles = 0, pre_max = 0;  // key tiles of the prefill entries: sum, longest
-  ReqInfo first{0, 0, 0, 0, 0};
+  ReqInfo first{0, 0, 0, 0, 0, 0};
   for (int r = tid; r < a.num_reqs; r += nt) {
-    ReqInfo ri = classify(a, r);
+    ReqInfo ri = classify<kScored>(a, r);
     if (r == tid) first = ri;
     if (ri.kind == 1) {
-      dec_keys += ri.L;
+      dec_keys += ri.L - ri.kb;
       dec_reqs += 1;
-      dec_lmax = max(dec_lmax, ri.L);
+      dec_lmax = max(dec_lmax, ri.L - ri.kb);
       dec_rmax = max(dec_rmax, ri.n * (a.hq / a.hkv));
     } else if (ri.kind == 2) {
       // query tile t (rows up to min(128 (t + 1), n)) reads ctx + its last row
       // keys; the last tile reads them all
-      const int ctx = ri.L - ri.n;
-      for (int t = 0; t * kPreTileQ < ri.n; ++t)
-        pre_tiles += (ctx + min(kPreTileQ * (t + 1), ri.n) + kPreTileQ - 1) / kPreTileQ;
-      pre_max = max(pre_max, (ri.L + kPreTileQ - 1) / kPreTileQ);
+      const int pfx = kScored && a.score.prefix ? clip_prefix(__ldcg(a.score.prefix + r), ri.L) : 0;
+      for (int t = 0; t * kPreTileQ < ri.n; ++t) {
+        int base;
+        const int tiles = entry_tiles<kScored>(a, ri.n, ri.L, t, pfx, &base);
+        pre_tiles += tiles;
+        pre_max = max(pre_max, tiles);
+      }
     }
   }
 #pragma unroll
@@ -297,10 +319,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(AttnArgs a, Workspac
   int4 cnt = make_int4(0, 0, 0, 0);  // units of classes 0..3 of this thread's requests
                                      // (class 4 comes last: its count is not needed)
   for (int r = tid; r < a.num_reqs; r += nt) {
-    const ReqInfo ri = r == tid ? first : classify(a, r);
+    const ReqInfo ri = r == tid ? first : classify<kScored>(a, r);
     if (ri.kind != 1) continue;
-    cnt.x += (ri.L / chunk) * a.hkv;
-    const int c = last_class(ri.L);
+    cnt.x += ((ri.L - ri.kb) / chunk) * a.hkv;
+    const int c = last_class(ri.L - ri.kb);
     if (c == 1) cnt.y += a.hkv;
     if (c == 2) cnt.z += a.hkv;
     if (c == 3) cnt.w += a.hkv;
@@ -341,15 +363,16 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(AttnArgs a, Workspac
   int cls_carry[5] = {0, 0, 0, 0, 0};
   for (int base = 0; base < a.num_reqs; base += nt) {
     const int r = base + tid;
-    ReqInfo ri{0, 0, 0, 0, 0};
-    if (r < a.num_reqs) ri = base == 0 ? first : classify(a, r);
+    ReqInfo ri{0, 0, 0, 0, 0, 0};
+    if (r < a.num_reqs) ri = base == 0 ? first : classify<kScored>(a, r);
     if (ri.bad && blockIdx.x == 0) atomicOr(ws.err, ri.bad);
     int units = 0, parts = 0, tiles = 0, pairs = 0, fulls = 0, lcls = 0;
     if (ri.kind == 1) {
-      const int nsplit = (ri.L + chunk - 1) / chunk;
+      const int span = ri.L - ri.kb;
+      const int nsplit = (span + chunk - 1) / chunk;
       units = nsplit * a.hkv;
-      fulls = (ri.L / chunk) * a.hkv;
-      lcls = last_class(ri.L);
+      fulls = (span / chunk) * a.hkv;
+      lcls = last_class(span);
       parts = nsplit > 1 ? units * ri.n * G : 0;  // partial rows
       pairs = nsplit > 1 ? a.hkv : 0;
       if (nsplit > 1) atomicMax(&s_max_rows, ri.n * G);
@@ -396,7 +419,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(AttnArgs a, Workspac
       const int cnt_u = s_off_u[lo + 1] - s_off_u[lo];
       if (cnt_u == 0) continue;
       const int L = s_len[lo], qn = s_n[lo];
-      const int nsplit = (L + chunk - 1) / chunk, nfull = L / chunk;
+      const int kb = kScored ? first_page_key(L - qn, a.score.window) : 0;
+      const int nsplit = (L - kb + chunk - 1) / chunk, nfull = (L - kb) / chunk;
       for (int rem = ln; rem < cnt_u; rem += 32) {
         const int sp = rem / a.hkv, g = rem - sp * a.hkv;
         const int64_t idx = sp < nfull ? (int64_t)s_off_f[lo] + rem : (int64_t)s_off_l[lo] + g;
@@ -404,7 +428,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(AttnArgs a, Workspac
         // two 16-byte stores per unit
         int4* dst = reinterpret_cast<int4*>(ws.units + idx);
         dst[0] = make_int4(base + lo, g | (qn << 16), L - qn, nsplit);
-        dst[1] = make_int4(sp * chunk, min(L, (sp + 1) * chunk),
+        dst[1] = make_int4(kb + sp * chunk, min(L, kb + (sp + 1) * chunk),
                            nsplit > 1 ? s_off_p[lo] + (g * nsplit + sp) * qn * G : -1, s_q0[lo]);
       }
       const int cnt_q = s_off_q[lo + 1] - s_off_q[lo];
@@ -420,14 +444,17 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(AttnArgs a, Workspac
       const int lo = find_owner(s_off_t, nt, i);
       // a request's query tiles from the last (most keys) to the first, so
       // that the persistent prefill grid starts with the longest items
-      const int n = s_n[lo], ctx = s_len[lo] - n;
+      const int n = s_n[lo], L = s_len[lo];
       const int t = (n + kPreTileQ - 1) / kPreTileQ - 1 - (i - s_off_t[lo]);
       const int64_t idx = (int64_t)pre_carry + i;
       if (idx >= ws.max_pre) break;
-      const int last_row = min(kPreTileQ * (t + 1), n);
+      const int pfx =
+          kScored && a.score.prefix ? clip_prefix(__ldcg(a.score.prefix + base + lo), L) : 0;
+      int kb;
+      const int tiles = entry_tiles<kScored>(a, n, L, t, pfx, &kb);
       int4* dst = reinterpret_cast<int4*>(ws.pre + idx);
-      dst[0] = make_int4(base + lo, t, (ctx + last_row + kPreTileQ - 1) / kPreTileQ, s_q0[lo]);
-      dst[1] = make_int4(n, s_len[lo], 0, 0);
+      dst[0] = make_int4(base + lo, t, tiles, s_q0[lo]);
+      dst[1] = make_int4(n, L, kb, pfx);
     }
     unit_carry += tot_u;
     cls_carry[0] += tot2.x;
@@ -471,7 +498,8 @@ cudaError_t launch_plan(const AttnArgs& a, const Workspace& ws, int dec_grid, cu
   const int warps = threads / 32;
   const int want = (std::min(a.num_reqs, threads) + warps - 1) / warps;
   const int grid = std::max(1, std::min(16, want));
-  return launch_dependent(plan_kernel, dim3(grid), dim3(threads), 0, st, a, ws, dec_grid);
+  return launch_dependent(a.score.on ? plan_kernel<true> : plan_kernel<false>, dim3(grid),
+                          dim3(threads), 0, st, a, ws, dec_grid);
 }
 
 }  // namespace pkv

@@ -96,8 +96,17 @@ constexpr int kSmemBytes = kOffBarLF1 + 16 + 1024;  // + alignment slack
 struct Item {
   int r, qt, ha, hb;  // hb < 0: single-tile item
   int g, q0, n, L;
-  int ctx, nkv, pad0, pad1;
+  int ctx, nkv, base, prefix;  // first key of the tiles; keys every row sees (scored)
 };
+
+// First key of the j-th tile an item processes.  With a distance bias the
+// tiles run from the diagonal back: the bias falls with distance, so a row's
+// maximum is found in its first tile and stays (forward, steep slopes would
+// raise it, and rescale the output, at every tile).
+template <bool kBias>
+__device__ __forceinline__ int tile_key0(const Item& it, int j) {
+  return it.base + (kBias ? it.nkv - 1 - j : j) * kTileK;
+}
 
 // a prefill entry written by the plan kernel, read through L2
 __device__ __forceinline__ PreEntry load_entry(const PreEntry* p) {
@@ -214,6 +223,8 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
 }
 
+// kScored: a window, a prefix (runtime), and per instance a cap, a bias.
+template <bool kScored, bool kCap, bool kBias>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, AttnArgs a, Workspace ws) {
@@ -315,7 +326,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         it.n = q1 - q0;
         it.L = Lr;
         it.ctx = Lr - it.n;
-        it.pad0 = it.pad1 = 0;
+        it.base = kScored ? e.base : 0;
+        it.prefix = kScored ? e.prefix : 0;
       }
       if (lane == 0) {
         items[slot] = it;
@@ -346,17 +358,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       // lane p < pages(j) holds the block id of page p of tile j
-      auto tile_pages = [&](int j) { return min(8, (it.L - j * kTileK + 15) / 16); };
-      int blk_nxt = lane < tile_pages(0) ? __ldcg(btrow + lane) : 0;
+      auto tile_key = [&](int j) { return tile_key0<kBias>(it, j); };
+      auto tile_pages = [&](int key) { return min(8, (it.L - key + 15) / 16); };
+      // first key any row of the item sees (its tiles start at this key's page)
+      const int vlow = kScored ? first_key(it.ctx + it.qt * kPreTileQ, a.score.window) : 0;
+      int blk_nxt = lane < tile_pages(tile_key(0)) ? __ldcg(btrow + (tile_key(0) >> 4) + lane) : 0;
       for (int j = 0; ok && j < it.nkv; ++j) {
         const uint32_t c = tile_cnt++;
         const int s = c % kStages;
-        const int key0 = j * kTileK;
-        const int pages = tile_pages(j);
-        const bool tail = key0 + kTileK > it.L;
+        const int key0 = tile_key(j);
+        const int pages = tile_pages(key0);
+        const bool tail = key0 + kTileK > it.L || (kScored && key0 < vlow);
         int blk = blk_nxt;
-        if (j + 1 < it.nkv && lane < tile_pages(j + 1))
-          blk_nxt = __ldcg(btrow + ((key0 + kTileK) >> 4) + lane);
+        if (j + 1 < it.nkv && lane < tile_pages(tile_key(j + 1)))
+          blk_nxt = __ldcg(btrow + (tile_key(j + 1) >> 4) + lane);
         if (c >= (uint32_t)kStages &&
             !mbar_wait_warp(bar(B_KE + s), ((c / kStages) - 1) & 1, abort, ws.err)) {
           ok = false;
@@ -388,17 +403,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_4d(vdst + kHalfBytes + lane * kPageBoxBytes, &tm_v, vbar, 64, it.g, 0, blk);
         }
         if (tail) {
-          // wait for the V boxes, zero the rows of keys >= seq_len, publish
+          // wait for the V boxes, zero the rows of keys >= seq_len (and, at a
+          // window's start, of the keys no row sees), publish
           ok = mbar_wait_warp(bar(B_VT + s), vt_uses[s] & 1, abort, ws.err);
           vt_uses[s]++;
           if (!ok) break;
-          const int z0 = it.L - key0;
           uint8_t* v = smem + kOffV + s * kTileBytes;
-          for (int i = lane; i < (kTileK - z0) * 16; i += 32) {
-            const int row = z0 + (i >> 4), within = i & 15;
-            *reinterpret_cast<uint4*>(v + (within >> 3) * kHalfBytes + row * 128 +
-                                      (within & 7) * 16) = make_uint4(0, 0, 0, 0);
-          }
+          auto zero_rows = [&](int z0, int z1) {
+            for (int i = lane; i < (z1 - z0) * 16; i += 32) {
+              const int row = z0 + (i >> 4), within = i & 15;
+              *reinterpret_cast<uint4*>(v + (within >> 3) * kHalfBytes + row * 128 +
+                                        (within & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+          };
+          zero_rows(min(it.L - key0, kTileK), kTileK);
+          if (kScored) zero_rows(0, vlow - key0);
           fence_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(B_VF + s));
@@ -517,7 +536,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = qd * 32 + lane;  // == TMEM lane
     const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
     float* xch = reinterpret_cast<float*>(smem + kOffXch);
-    const float sl2 = a.scale * kLog2e;
+    const ScoreParams sp = score_params(a);
+    // the factor from what load_scores leaves to log2 units
+    const float smul = kCap || kBias ? 1.f : a.scale * kLog2e;
     uint32_t s_cnt[2] = {0, 0}, x_cnt = 0;
     bool ok = true;
     // this lane's value out, the other warp's value for the same row back
@@ -541,11 +562,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nx = it.hb >= 0 ? 2 : 1;
       const int qrow = it.qt * kPreTileQ + row;  // row inside the request
       const bool valid_row = qrow < it.n;
-      const int qpos = valid_row ? it.ctx + qrow : 0;  // last visible key
+      // last visible key; in a scored call rows past the request's repeat its
+      // last row, so that they take part in no decision of their own
+      const int rpos = it.ctx + (valid_row ? qrow : it.n - 1);
+      const int qpos = kScored ? max(rpos, it.prefix - 1) : (valid_row ? it.ctx + qrow : 0);
+      const int rlow = kScored ? first_key(rpos, a.score.window) : 0;  // first visible key
+      float slope2[2] = {0.f, 0.f};
+      if (kBias) {
+        slope2[0] = __ldg(a.score.slopes + it.ha) * kLog2e;
+        if (it.hb >= 0) slope2[1] = __ldg(a.score.slopes + it.hb) * kLog2e;
+      }
       float m_used[2] = {-INFINITY, -INFINITY}, l_part[2] = {0.f, 0.f};
       for (int j = 0; j < it.nkv && ok; ++j) {
-        const int lim = qpos - j * kTileK - 64 * hf;  // my columns <= lim are visible
-        const bool masked = !__all_sync(0xffffffffu, lim >= 63);
+        const int key0 = tile_key0<kBias>(it, j) + 64 * hf;  // key of my first column
+        const int lim = qpos - key0;   // my columns <= lim are visible
+        const int low = rlow - key0;   // (scored) and >= low
+        const bool masked = !__all_sync(0xffffffffu, lim >= 63 && (!kScored || low <= 0));
         for (int x = 0; x < nx && ok; ++x) {
           if (!mbar_wait_warp(bar(B_SF + x), s_cnt[x]++ & 1, abort, ws.err)) {
             ok = false;
@@ -559,9 +591,38 @@ __global__ void __launch_bounds__(kThreads, 1)
             PKV_LD32(t_s + 0, (sv + 0));
             PKV_LD32(t_s + 32, (sv + 32));
             tmem_wait_ld();
+            if (kCap) {
+              // one form for the warp, by the keys its rows see (the others,
+              // and the rows past the request's, may hold anything)
+              float big = 0.f;
+              if (masked) {
+#pragma unroll
+                for (int i = 0; i < 64; ++i)
+                  big = fmaxf(big, i <= lim && i >= low ? fabsf(sv[i]) : 0.f);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 64; ++i) big = fmaxf(big, fabsf(sv[i]));
+              }
+              if (!valid_row) big = 0.f;
+              if (__all_sync(0xffffffffu, big * sp.k <= 1.f)) {
+#pragma unroll
+                for (int i = 0; i < 64; ++i) sv[i] = capped_poly(sv[i], sp);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 64; ++i) sv[i] = capped_exp(sv[i], sp);
+              }
+            }
+            if (kBias) {
+#pragma unroll
+              for (int i = 0; i < 64; ++i) {
+                const float v = kCap ? sv[i] : sv[i] * sp.lin;
+                sv[i] = fmaf(-(x ? slope2[1] : slope2[0]), fabsf((float)(rpos - key0 - i)), v);
+              }
+            }
             if (masked) {
 #pragma unroll
-              for (int i = 0; i < 64; ++i) sv[i] = (i <= lim) ? sv[i] : -INFINITY;
+              for (int i = 0; i < 64; ++i)
+                sv[i] = (i <= lim && (!kScored || i >= low)) ? sv[i] : -INFINITY;
             }
           };
           // p = exp2(s * scale * log2(e) - m) two columns at a time (packed
@@ -570,11 +631,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           float rs[4];
           auto exp_pack = [&](float m) {
             rs[0] = rs[1] = rs[2] = rs[3] = 0.f;
-            const float nm = -m;
+            // (a row that has seen no key yet has no maximum: 0 is its reference)
+            const float nm = kScored && m == -INFINITY ? 0.f : -m;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               float x0, x1;
-              fma2(x0, x1, sv[2 * i], sv[2 * i + 1], sl2, sl2, nm, nm);
+              fma2(x0, x1, sv[2 * i], sv[2 * i + 1], smul, smul, nm, nm);
               const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
               add2(rs[2 * (i & 1)], rs[2 * (i & 1) + 1], p0, p1);
               sv[i] = __uint_as_float(pack_bf16(p0, p1));
@@ -591,7 +653,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!need_max) {
             exp_pack(m_used[x]);
             const float tot = (rs[0] + rs[1]) + (rs[2] + rs[3]);
-            const float mine = (tot <= 256.f) ? 0.f : 1.f;
+            float mine = (tot <= 256.f) ? 0.f : 1.f;
+            // a window's or a reversed order's row may see its first key in
+            // any tile: it takes the max pass until it has a maximum
+            if (kScored && m_used[x] == -INFINITY) mine = 1.f;
+            if (kScored && !valid_row) mine = 0.f;
             const float other = exchange(mine);
             if (!ok) break;
             need_max = __any_sync(0xffffffffu, mine + other > 0.f);
@@ -613,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float po = exchange(pm);
             if (!ok) break;
             // (both warps form the same value: the halves in a fixed order)
-            const float mt = (hf == 0 ? fmaxf(pm, po) : fmaxf(po, pm)) * sl2;
+            const float mt = (hf == 0 ? fmaxf(pm, po) : fmaxf(po, pm)) * smul;
             resc = mt > m_used[x] + kRescaleThreshold;
             if (resc) {
               alpha = fast_exp2(m_used[x] - mt);  // 0 on the first tile
@@ -759,18 +825,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   combine_splits(a, ws, blockIdx.x * (kThreads / 32) + warp, gridDim.x * (kThreads / 32));
 }
 
-}  // namespace
-
-cudaError_t launch_prefill(const AttnArgs& a, const Workspace& ws, int sms, cudaStream_t st) {
+template <bool kScored, bool kCap, bool kBias>
+cudaError_t launch_prefill_as(const AttnArgs& a, const Workspace& ws, int sms, cudaStream_t st) {
   static std::atomic<bool> attr[kMaxAttrDevices];
-  if (cudaError_t e = smem_attr_once(prefill_kernel, kSmemBytes, attr)) return e;
+  auto* kernel = prefill_kernel<kScored, kCap, kBias>;
+  if (cudaError_t e = smem_attr_once(kernel, kSmemBytes, attr)) return e;
   CUtensorMap tq, tk, tv;
   if (!make_rows_map(&tq, a.q, a.q_rows, a.hq, a.q_stride, 1, kPreTileQ) ||
       !make_cache_map(&tk, a.kc, a.num_blocks, a.hkv) ||
       !make_cache_map(&tv, a.vc, a.num_blocks, a.hkv))
     return cudaErrorInvalidValue;
-  return launch_dependent(prefill_kernel, dim3(sms), dim3(kThreads), kSmemBytes, st, tq, tk, tv,
-                          a, ws);
+  return launch_dependent(kernel, dim3(sms), dim3(kThreads), kSmemBytes, st, tq, tk, tv, a, ws);
+}
+
+}  // namespace
+
+cudaError_t launch_prefill(const AttnArgs& a, const Workspace& ws, int sms, cudaStream_t st) {
+  if (!a.score.on) return launch_prefill_as<false, false, false>(a, ws, sms, st);
+  if (a.score.softcap > 0.f)
+    return a.score.slopes ? launch_prefill_as<true, true, true>(a, ws, sms, st)
+                          : launch_prefill_as<true, true, false>(a, ws, sms, st);
+  return a.score.slopes ? launch_prefill_as<true, false, true>(a, ws, sms, st)
+                        : launch_prefill_as<true, false, false>(a, ws, sms, st);
 }
 
 }  // namespace pkv
