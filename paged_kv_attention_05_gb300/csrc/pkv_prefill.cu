@@ -99,13 +99,110 @@ struct Item {
   int ctx, nkv, base, prefix;  // first key of the tiles; keys every row sees (scored)
 };
 
+// What an instance does to the scores.  kFixed: a cap of at most
+// kFixedCap2 log2 units (see fixed-reference softmax below).
+enum Cap { kNoCap, kAnyCap, kFixedCap };
+constexpr float kFixedCap2 = 80.f;
+
 // First key of the j-th tile an item processes.  With a distance bias the
 // tiles run from the diagonal back: the bias falls with distance, so a row's
 // maximum is found in its first tile and stays (forward, steep slopes would
-// raise it, and rescale the output, at every tile).
-template <bool kBias>
+// raise it, and rescale the output, at every tile).  Where a window cuts the
+// first tile, it comes last: in the one after it every row sees all or most
+// keys, so that the running maximum settles there.
+template <bool kScored, bool kBias>
 __device__ __forceinline__ int tile_key0(const Item& it, int j) {
-  return it.base + (kBias ? it.nkv - 1 - j : j) * kTileK;
+  int t = j;
+  if (kBias)
+    t = it.nkv - 1 - j;
+  else if (kScored && it.base > 0)
+    t = j + 1 < it.nkv ? j + 1 : 0;
+  return it.base + t * kTileK;
+}
+
+// 32 raw products s = q.K (columns i of one row) to logits in log2 units, with
+// nm added: the cap and the bias applied, -inf outside low <= i <= lim when
+// `masked` (columns there may hold anything).  d0: distance of column 0's key.
+// The cap takes the cheapest form that serves the warp's visible scores (x =
+// s * scale / cap): |x| <= 1/4, s times a degree-2 polynomial in s^2 whose
+// coefficients hold the powers of scale / cap (5.5e-7 relative error, four
+// packed operations a pair); |x| <= 1, the polynomial of capped_poly; else
+// the exponential form.  (A switch of the whole warp per 32 columns: the code
+// of all three stays small enough for the instruction cache, which an
+// unrolled row of 64 outgrew: 2.2 ms against X for the large capped prefill.)
+struct CapForm {
+  float a0, a1, a2, wlim;  // the degree-2 form; s^2 <= wlim selects it
+};
+__device__ __forceinline__ CapForm cap_form(const ScoreParams& sp) {
+  CapForm c;
+  const float k2 = sp.k * sp.k;
+  c.a0 = sp.lin;
+  c.a1 = sp.lin * -0.33324572f * k2;
+  c.a2 = sp.lin * 0.12876421f * k2 * k2;
+  // (outside this range of k a power of it or of s could leave fp32's)
+  c.wlim = sp.k >= 0x1p-24f && sp.k <= 0x1p24f ? 0.0625f / k2 : -1.f;
+  return c;
+}
+template <bool kCap, bool kBias>
+__device__ __forceinline__ void logits32(float (&s)[32], const ScoreParams& sp, const CapForm& cf,
+                                         float nm, bool masked, int lim, int low, bool valid_row,
+                                         float slope2, float d0, bool sym) {
+  if (kCap) {
+    if (masked) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) s[i] = i <= lim && i >= low ? s[i] : 0.f;
+    }
+    float wm = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) wm = max3f(wm, fabsf(s[i]), fabsf(s[i + 1]));
+    if (!valid_row) wm = 0.f;
+    const float w1 = wm * sp.k;
+    if (__all_sync(0xffffffffu, wm * wm <= cf.wlim)) {
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        float w0, wq, q0, q1;
+        mul2(w0, wq, s[i], s[i + 1], s[i], s[i + 1]);
+        fma2(q0, q1, w0, wq, cf.a2, cf.a2, cf.a1, cf.a1);
+        fma2(q0, q1, q0, q1, w0, wq, cf.a0, cf.a0);
+        fma2(s[i], s[i + 1], s[i], s[i + 1], q0, q1, nm, nm);
+      }
+    } else if (__all_sync(0xffffffffu, w1 <= 1.f)) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) s[i] = capped_poly(s[i], sp) + nm;
+    } else {
+      const float c2 = sp.cap2 + nm;
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        s[i] = fmaf(-2.f * sp.cap2, fast_rcp(1.f + fast_exp2(s[i] * sp.mul)), c2);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; i += 2)
+      fma2(s[i], s[i + 1], s[i], s[i + 1], sp.lin, sp.lin, nm, nm);
+  }
+  if (kBias) {
+    if (sym) {  // a prefix: keys after the row's position too
+#pragma unroll
+      for (int i = 0; i < 32; ++i) s[i] = fmaf(-slope2, fabsf(d0 - (float)i), s[i]);
+    } else {
+      const float b0 = -slope2 * d0;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) s[i] += fmaf(slope2, (float)i, b0);
+    }
+  }
+  if (masked) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s[i] = i <= lim && i >= low ? s[i] : -INFINITY;
+  }
+}
+// p = exp2(s), packed to bf16 pairs; the sums of pairs into rs
+__device__ __forceinline__ void exp32(const float (&s)[32], uint32_t (&p)[16], float (&rs)[4]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float p0 = fast_exp2(s[2 * i]), p1 = fast_exp2(s[2 * i + 1]);
+    add2(rs[2 * (i & 1)], rs[2 * (i & 1) + 1], p0, p1);
+    p[i] = pack_bf16(p0, p1);
+  }
 }
 
 // a prefill entry written by the plan kernel, read through L2
@@ -207,6 +304,15 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
       "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])                              \
       : "memory")
 
+#define PKV_ST16U(taddr, v)                                                                    \
+  asm volatile(                                                                                \
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12," \
+      "%13,%14,%15,%16};\n" ::"r"(taddr),                                                     \
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),  \
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),        \
+      "r"(v[15])                                                                               \
+      : "memory")
+
 #define PKV_LD16(taddr, v)                                                                     \
   asm volatile(                                                                                \
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13," \
@@ -224,7 +330,7 @@ __device__ __forceinline__ void tmem_wait_st() {
 }
 
 // kScored: a window, a prefix (runtime), and per instance a cap, a bias.
-template <bool kScored, bool kCap, bool kBias>
+template <bool kScored, Cap kCap, bool kBias>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, AttnArgs a, Workspace ws) {
@@ -358,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       // lane p < pages(j) holds the block id of page p of tile j
-      auto tile_key = [&](int j) { return tile_key0<kBias>(it, j); };
+      auto tile_key = [&](int j) { return tile_key0<kScored, kBias>(it, j); };
       auto tile_pages = [&](int key) { return min(8, (it.L - key + 15) / 16); };
       // first key any row of the item sees (its tiles start at this key's page)
       const int vlow = kScored ? first_key(it.ctx + it.qt * kPreTileQ, a.score.window) : 0;
@@ -536,9 +642,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = qd * 32 + lane;  // == TMEM lane
     const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
     float* xch = reinterpret_cast<float*>(smem + kOffXch);
+    const float sl2 = a.scale * kLog2e;
     const ScoreParams sp = score_params(a);
-    // the factor from what load_scores leaves to log2 units
-    const float smul = kCap || kBias ? 1.f : a.scale * kLog2e;
+    const CapForm cf = cap_form(sp);
     uint32_t s_cnt[2] = {0, 0}, x_cnt = 0;
     bool ok = true;
     // this lane's value out, the other warp's value for the same row back
@@ -574,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float m_used[2] = {-INFINITY, -INFINITY}, l_part[2] = {0.f, 0.f};
       for (int j = 0; j < it.nkv && ok; ++j) {
-        const int key0 = tile_key0<kBias>(it, j) + 64 * hf;  // key of my first column
+        const int key0 = tile_key0<kScored, kBias>(it, j) + 64 * hf;  // key of my first column
         const int lim = qpos - key0;   // my columns <= lim are visible
         const int low = rlow - key0;   // (scored) and >= low
         const bool masked = !__all_sync(0xffffffffu, lim >= 63 && (!kScored || low <= 0));
@@ -585,40 +691,119 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_after();
           const uint32_t t_s = tmem + x * 128 + 64 * hf + lane_off;
+          if constexpr (kCap == kFixedCap) {
+            // Fixed-reference softmax: a capped logit lies within +-cap2, so
+            // exp2(y - cap2 / 2) lies within 2^(-3/2 cap2) and 2^(cap2 / 2),
+            // inside fp32's and bf16's exponents for cap2 <= 80 (caps up to
+            // 55) with room for the sums: no maximum, no exchange between the
+            // two warps of a row, no rescaling, and P goes out 32 columns at
+            // a time.
+            float rs[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
+              float s[32];
+              uint32_t p[16];
+              PKV_LD32(t_s + 32 * c, s);
+              tmem_wait_ld();
+              logits32<true, false>(s, sp, cf, -0.5f * sp.cap2, masked, lim - 32 * c,
+                                    low - 32 * c, valid_row, 0.f, 0.f, false);
+              exp32(s, p, rs);
+              PKV_ST16U(t_s + 16 * c, p);
+            }
+            l_part[x] += (rs[0] + rs[1]) + (rs[2] + rs[3]);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_PF + x));
+            continue;
+          }
+          if constexpr (kCap == kAnyCap || kBias) {
+            // Running maximum as below, the logits formed 32 columns at a
+            // time: P stays in registers until the maximum is agreed on.
+            const float sl = x ? slope2[1] : slope2[0];
+            const float d0 = (float)(rpos - key0);
+            auto logits = [&](float(&s)[32], int c, float nm) {
+              PKV_LD32(t_s + 32 * c, s);
+              tmem_wait_ld();
+              logits32<kCap != kNoCap, kBias>(s, sp, cf, nm, masked, lim - 32 * c, low - 32 * c,
+                                              valid_row, sl, d0 - 32.f * c, it.prefix > 0);
+            };
+            float alpha = 1.f;
+            bool resc = false, maxed = j == 0;
+            uint32_t p[2][16];
+            float rs[4];
+            for (;;) {
+              if (maxed) {
+                float pm = -INFINITY;
+#pragma unroll 1
+                for (int c = 0; c < 2; ++c) {
+                  float s[32];
+                  logits(s, c, 0.f);
+#pragma unroll
+                  for (int i = 0; i < 32; i += 2) pm = max3f(pm, s[i], s[i + 1]);
+                }
+                const float po = exchange(pm);
+                if (!ok) break;
+                const float mt = hf == 0 ? fmaxf(pm, po) : fmaxf(po, pm);
+                resc = mt > m_used[x] + kRescaleThreshold;
+                if (resc) {
+                  alpha = fast_exp2(m_used[x] - mt);  // 0 on the row's first keys
+                  m_used[x] = mt;
+                }
+              }
+              rs[0] = rs[1] = rs[2] = rs[3] = 0.f;
+              // (a row that has seen no key yet has no maximum: 0 is its reference)
+              const float nm = m_used[x] == -INFINITY ? 0.f : -m_used[x];
+#pragma unroll 1
+              for (int c = 0; c < 2; ++c) {
+                float s[32];
+                if (c == 1) {
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) p[0][i] = p[1][i];
+                }
+                logits(s, c, nm);
+                exp32(s, p[1], rs);
+              }
+              if (maxed) break;
+              const float tot = (rs[0] + rs[1]) + (rs[2] + rs[3]);
+              // a row that sees its first key in a later tile takes the max
+              // pass until it has a maximum
+              const float mine =
+                  valid_row && (!(tot <= 256.f) || m_used[x] == -INFINITY) ? 1.f : 0.f;
+              const float other = exchange(mine);
+              if (!ok) break;
+              maxed = __any_sync(0xffffffffu, mine + other > 0.f);
+              if (!maxed) break;
+            }
+            if (!ok) break;
+            PKV_ST16U(t_s, p[0]);
+            PKV_ST16U(t_s + 16, p[1]);
+            l_part[x] = l_part[x] * alpha + ((rs[0] + rs[1]) + (rs[2] + rs[3]));
+            if (j > 0 && __any_sync(0xffffffffu, resc)) {
+              const uint32_t t_o = tmem + 256 + x * 128 + 64 * hf + lane_off;
+#pragma unroll 1
+              for (int ch = 0; ch < 4; ++ch) {
+                float ov[16];
+                PKV_LD16(t_o + ch * 16, ov);
+                tmem_wait_ld();
+                uint32_t ou[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) ou[i] = __float_as_uint(ov[i] * alpha);
+                PKV_ST16U(t_o + ch * 16, ou);
+              }
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_PF + x));
+            continue;
+          }
           // my 64 scores of the row in registers (one wait), then P in place
           float sv[64];
           auto load_scores = [&]() {
             PKV_LD32(t_s + 0, (sv + 0));
             PKV_LD32(t_s + 32, (sv + 32));
             tmem_wait_ld();
-            if (kCap) {
-              // one form for the warp, by the keys its rows see (the others,
-              // and the rows past the request's, may hold anything)
-              float big = 0.f;
-              if (masked) {
-#pragma unroll
-                for (int i = 0; i < 64; ++i)
-                  big = fmaxf(big, i <= lim && i >= low ? fabsf(sv[i]) : 0.f);
-              } else {
-#pragma unroll
-                for (int i = 0; i < 64; ++i) big = fmaxf(big, fabsf(sv[i]));
-              }
-              if (!valid_row) big = 0.f;
-              if (__all_sync(0xffffffffu, big * sp.k <= 1.f)) {
-#pragma unroll
-                for (int i = 0; i < 64; ++i) sv[i] = capped_poly(sv[i], sp);
-              } else {
-#pragma unroll
-                for (int i = 0; i < 64; ++i) sv[i] = capped_exp(sv[i], sp);
-              }
-            }
-            if (kBias) {
-#pragma unroll
-              for (int i = 0; i < 64; ++i) {
-                const float v = kCap ? sv[i] : sv[i] * sp.lin;
-                sv[i] = fmaf(-(x ? slope2[1] : slope2[0]), fabsf((float)(rpos - key0 - i)), v);
-              }
-            }
             if (masked) {
 #pragma unroll
               for (int i = 0; i < 64; ++i)
@@ -636,7 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               float x0, x1;
-              fma2(x0, x1, sv[2 * i], sv[2 * i + 1], smul, smul, nm, nm);
+              fma2(x0, x1, sv[2 * i], sv[2 * i + 1], sl2, sl2, nm, nm);
               const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
               add2(rs[2 * (i & 1)], rs[2 * (i & 1) + 1], p0, p1);
               sv[i] = __uint_as_float(pack_bf16(p0, p1));
@@ -679,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float po = exchange(pm);
             if (!ok) break;
             // (both warps form the same value: the halves in a fixed order)
-            const float mt = (hf == 0 ? fmaxf(pm, po) : fmaxf(po, pm)) * smul;
+            const float mt = (hf == 0 ? fmaxf(pm, po) : fmaxf(po, pm)) * sl2;
             resc = mt > m_used[x] + kRescaleThreshold;
             if (resc) {
               alpha = fast_exp2(m_used[x] - mt);  // 0 on the first tile
@@ -825,7 +1010,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   combine_splits(a, ws, blockIdx.x * (kThreads / 32) + warp, gridDim.x * (kThreads / 32));
 }
 
-template <bool kScored, bool kCap, bool kBias>
+template <bool kScored, Cap kCap, bool kBias>
 cudaError_t launch_prefill_as(const AttnArgs& a, const Workspace& ws, int sms, cudaStream_t st) {
   static std::atomic<bool> attr[kMaxAttrDevices];
   auto* kernel = prefill_kernel<kScored, kCap, kBias>;
@@ -841,12 +1026,15 @@ cudaError_t launch_prefill_as(const AttnArgs& a, const Workspace& ws, int sms, c
 }  // namespace
 
 cudaError_t launch_prefill(const AttnArgs& a, const Workspace& ws, int sms, cudaStream_t st) {
-  if (!a.score.on) return launch_prefill_as<false, false, false>(a, ws, sms, st);
-  if (a.score.softcap > 0.f)
-    return a.score.slopes ? launch_prefill_as<true, true, true>(a, ws, sms, st)
-                          : launch_prefill_as<true, true, false>(a, ws, sms, st);
-  return a.score.slopes ? launch_prefill_as<true, false, true>(a, ws, sms, st)
-                        : launch_prefill_as<true, false, false>(a, ws, sms, st);
+  if (!a.score.on) return launch_prefill_as<false, kNoCap, false>(a, ws, sms, st);
+  if (a.score.softcap > 0.f) {
+    if (a.score.slopes) return launch_prefill_as<true, kAnyCap, true>(a, ws, sms, st);
+    return a.score.softcap * dev::kLog2e <= kFixedCap2
+               ? launch_prefill_as<true, kFixedCap, false>(a, ws, sms, st)
+               : launch_prefill_as<true, kAnyCap, false>(a, ws, sms, st);
+  }
+  return a.score.slopes ? launch_prefill_as<true, kNoCap, true>(a, ws, sms, st)
+                        : launch_prefill_as<true, kNoCap, false>(a, ws, sms, st);
 }
 
 }  // namespace pkv
