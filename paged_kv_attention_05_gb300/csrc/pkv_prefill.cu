@@ -44,6 +44,8 @@
 //               through a per-warp staging area (whole 64-byte row pieces).
 // Every mbarrier wait is bounded; on expiry the kernel records
 // PKV_DEV_ERR_TIMEOUT, stops issuing work, frees its TMEM and returns.
+#include <type_traits>
+
 #include "pkv_combine.cuh"
 #include "pkv_device.cuh"
 
@@ -60,6 +62,7 @@ constexpr int kTileBytes = 2 * kHalfBytes;        // a Q, K or V tile: 32 KB
 constexpr int kPageBoxBytes = 16 * 128;           // one 16-slot x 64-dim box
 constexpr int kTmemCols = 512;
 constexpr float kRescaleThreshold = 8.0f;         // log2 units
+constexpr float kMaxSum = 0x1p40f;                // scored calls: sum of a row over a pair of blocks
 
 // shared-memory layout (offsets from a 1024-byte aligned base)
 constexpr int kOffQ = 0;                          // Q_a | Q_b
@@ -120,90 +123,6 @@ __device__ __forceinline__ int tile_key0(const Item& it, int j) {
   return it.base + t * kTileK;
 }
 
-// 32 raw products s = q.K (columns i of one row) to logits in log2 units, with
-// nm added: the cap and the bias applied, -inf outside low <= i <= lim when
-// `masked` (columns there may hold anything).  d0: distance of column 0's key.
-// The cap takes the cheapest form that serves the warp's visible scores (x =
-// s * scale / cap): |x| <= 1/4, s times a degree-2 polynomial in s^2 whose
-// coefficients hold the powers of scale / cap (5.5e-7 relative error, four
-// packed operations a pair); |x| <= 1, the polynomial of capped_poly; else
-// the exponential form.  (A switch of the whole warp per 32 columns: the code
-// of all three stays small enough for the instruction cache, which an
-// unrolled row of 64 outgrew: 2.2 ms against X for the large capped prefill.)
-struct CapForm {
-  float a0, a1, a2, wlim;  // the degree-2 form; s^2 <= wlim selects it
-};
-__device__ __forceinline__ CapForm cap_form(const ScoreParams& sp) {
-  CapForm c;
-  const float k2 = sp.k * sp.k;
-  c.a0 = sp.lin;
-  c.a1 = sp.lin * -0.33324572f * k2;
-  c.a2 = sp.lin * 0.12876421f * k2 * k2;
-  // (outside this range of k a power of it or of s could leave fp32's)
-  c.wlim = sp.k >= 0x1p-24f && sp.k <= 0x1p24f ? 0.0625f / k2 : -1.f;
-  return c;
-}
-template <bool kCap, bool kBias>
-__device__ __forceinline__ void logits32(float (&s)[32], const ScoreParams& sp, const CapForm& cf,
-                                         float nm, bool masked, int lim, int low, bool valid_row,
-                                         float slope2, float d0, bool sym) {
-  if (kCap) {
-    if (masked) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) s[i] = i <= lim && i >= low ? s[i] : 0.f;
-    }
-    float wm = 0.f;
-#pragma unroll
-    for (int i = 0; i < 32; i += 2) wm = max3f(wm, fabsf(s[i]), fabsf(s[i + 1]));
-    if (!valid_row) wm = 0.f;
-    const float w1 = wm * sp.k;
-    if (__all_sync(0xffffffffu, wm * wm <= cf.wlim)) {
-#pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        float w0, wq, q0, q1;
-        mul2(w0, wq, s[i], s[i + 1], s[i], s[i + 1]);
-        fma2(q0, q1, w0, wq, cf.a2, cf.a2, cf.a1, cf.a1);
-        fma2(q0, q1, q0, q1, w0, wq, cf.a0, cf.a0);
-        fma2(s[i], s[i + 1], s[i], s[i + 1], q0, q1, nm, nm);
-      }
-    } else if (__all_sync(0xffffffffu, w1 <= 1.f)) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) s[i] = capped_poly(s[i], sp) + nm;
-    } else {
-      const float c2 = sp.cap2 + nm;
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        s[i] = fmaf(-2.f * sp.cap2, fast_rcp(1.f + fast_exp2(s[i] * sp.mul)), c2);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; i += 2)
-      fma2(s[i], s[i + 1], s[i], s[i + 1], sp.lin, sp.lin, nm, nm);
-  }
-  if (kBias) {
-    if (sym) {  // a prefix: keys after the row's position too
-#pragma unroll
-      for (int i = 0; i < 32; ++i) s[i] = fmaf(-slope2, fabsf(d0 - (float)i), s[i]);
-    } else {
-      const float b0 = -slope2 * d0;
-#pragma unroll
-      for (int i = 0; i < 32; ++i) s[i] += fmaf(slope2, (float)i, b0);
-    }
-  }
-  if (masked) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) s[i] = i <= lim && i >= low ? s[i] : -INFINITY;
-  }
-}
-// p = exp2(s), packed to bf16 pairs; the sums of pairs into rs
-__device__ __forceinline__ void exp32(const float (&s)[32], uint32_t (&p)[16], float (&rs)[4]) {
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float p0 = fast_exp2(s[2 * i]), p1 = fast_exp2(s[2 * i + 1]);
-    add2(rs[2 * (i & 1)], rs[2 * (i & 1) + 1], p0, p1);
-    p[i] = pack_bf16(p0, p1);
-  }
-}
 
 // a prefill entry written by the plan kernel, read through L2
 __device__ __forceinline__ PreEntry load_entry(const PreEntry* p) {
@@ -329,8 +248,167 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
 }
 
-// kScored: a window, a prefix (runtime), and per instance a cap, a bias.
-template <bool kScored, Cap kCap, bool kBias>
+// The cap's forms (x = s * scale / cap).  Up to |x| = 1/2, s times a
+// polynomial of degree 3 in s^2 whose coefficients hold the powers of scale /
+// cap, two columns at a time (7.2e-7 relative error as computed; fitted like
+// capped_poly); past that capped_exp.  Where scale / cap is so small or large
+// that a power of it or of s could leave fp32's range (a cap of thousands),
+// capped_poly serves |x| <= 1.
+struct CapForm {
+  f32x2 a[4];   // pairs: formed at each use they cost two moves an operation
+  float limit;  // largest s^2; -1: not in range
+};
+__device__ __forceinline__ CapForm cap_form(const ScoreParams& sp) {
+  CapForm c;
+  const float k2 = sp.k * sp.k;
+  const bool in_range = sp.k >= 0x1p-20f && sp.k <= 0x1p20f;
+  const float a[4] = {sp.lin, sp.lin * -0.33328161f * k2, sp.lin * 0.13205360f * k2 * k2,
+                      sp.lin * -0.04475065f * k2 * k2 * k2};
+#pragma unroll
+  for (int n = 0; n < 4; ++n) c.a[n] = pair(a[n], a[n]);
+  c.limit = in_range ? 0.25f / k2 : -1.f;
+  return c;
+}
+// s -> cap2 * tanh(x) + nm for 32 columns, by one form (0: polynomial, 1:
+// exponential); the largest s^2 max'ed into big (form 0).
+template <int kForm>
+__device__ __forceinline__ void cap32(float (&s)[32], const ScoreParams& sp, const CapForm& cf,
+                                      float nm, float& big) {
+  if (kForm == 1) {
+    const float c2 = sp.cap2 + nm;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      s[i] = fmaf(-2.f * sp.cap2, fast_rcp(1.f + fast_exp2(s[i] * sp.mul)), c2);
+    return;
+  }
+  const f32x2 nm2 = pair(nm, nm);
+  float m0 = 0.f, m1 = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const f32x2 v = pair(s[2 * i], s[2 * i + 1]), w = mul2(v, v);
+    float w0, w1;
+    split(w, w0, w1);
+    if (i & 1) m1 = max3f(m1, w0, w1); else m0 = max3f(m0, w0, w1);
+    const f32x2 q = fma2(fma2(fma2(w, cf.a[3], cf.a[2]), w, cf.a[1]), w, cf.a[0]);
+    split(fma2(v, q, nm2), s[2 * i], s[2 * i + 1]);
+  }
+  big = max3f(big, m0, m1);
+}
+// Adds the bias slope2 * (i - d0) to 32 columns (d0: distance of the first
+// one's key) or, without a cap, forms s * lin + nm + bias: four pairs stepped
+// by eight columns (three additions at most: their roundings stay below 2^-22
+// of the bias).  kSym: a column past d0 counts its distance too.
+template <bool kCapped, bool kSym>
+__device__ __forceinline__ void bias32(float (&s)[32], float lin, float nm, float slope2,
+                                       float d0) {
+  f32x2 b[4];
+  const float b0 = kCapped ? -slope2 * d0 : fmaf(-slope2, d0, nm);
+  const f32x2 b8 = pair(8.f * slope2, 8.f * slope2), lin2 = pair(lin, lin);
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    b[k] = pair(fmaf(slope2, 2.f * k, b0), fmaf(slope2, 2.f * k + 1.f, b0));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const f32x2 v = pair(s[2 * i], s[2 * i + 1]);
+    split(kCapped ? add2(v, b[i & 3]) : fma2(v, lin2, b[i & 3]), s[2 * i], s[2 * i + 1]);
+    if (i < 12) b[i & 3] = add2(b[i & 3], b8);
+  }
+  if (kSym) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s[i] -= 2.f * slope2 * fmaxf((float)i - d0, 0.f);
+  }
+}
+// 32 raw products s = q.K (columns of one row) to logits in log2 units + nm,
+// the cap by the given form.
+template <Cap kCap, bool kBias, bool kSym, int kForm>
+__device__ __forceinline__ void logits32(float (&s)[32], const ScoreParams& sp, const CapForm& cf,
+                                         float nm, float slope2, float d0, float& big) {
+  if (kCap != kNoCap) cap32<kForm>(s, sp, cf, nm, big);
+  if (kBias) {
+    bias32<kCap != kNoCap, kSym>(s, sp.lin, nm, slope2, d0);
+  } else if (kCap == kNoCap) {
+    const f32x2 lin2 = pair(sp.lin, sp.lin), nm2 = pair(nm, nm);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      split(fma2(pair(s[2 * i], s[2 * i + 1]), lin2, nm2), s[2 * i], s[2 * i + 1]);
+  }
+}
+// The same for any block: the form by the warp's visible scores, -inf outside
+// low <= i <= lim when `edge` (columns there may hold anything).
+template <Cap kCap, bool kBias, bool kSym>
+__device__ __forceinline__ void logits32_any(float (&s)[32], const ScoreParams& sp,
+                                             const CapForm& cf, float nm, bool edge, int lim,
+                                             int low, bool valid_row, float slope2, float d0) {
+  float big = 0.f;
+  if (kCap == kNoCap) {
+    logits32<kCap, kBias, kSym, 0>(s, sp, cf, nm, slope2, d0, big);
+  } else {
+    if (edge) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) s[i] = i <= lim && i >= low ? s[i] : 0.f;
+    }
+    float m0 = 0.f, m1 = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+      m0 = max3f(m0, fabsf(s[i]), fabsf(s[i + 1]));
+      m1 = max3f(m1, fabsf(s[i + 2]), fabsf(s[i + 3]));
+    }
+    const float m = valid_row ? fmaxf(m0, m1) : 0.f;
+    if (__all_sync(0xffffffffu, m * m <= cf.limit)) {
+      logits32<kCap, kBias, kSym, 0>(s, sp, cf, nm, slope2, d0, big);
+    } else if (kCap == kAnyCap && __all_sync(0xffffffffu, m * sp.k <= 1.f)) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) s[i] = capped_poly(s[i], sp) + nm;
+      if (kBias) bias32<true, kSym>(s, sp.lin, nm, slope2, d0);
+    } else {
+      logits32<kCap, kBias, kSym, 1>(s, sp, cf, nm, slope2, d0, big);
+    }
+  }
+  if (edge) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s[i] = i <= lim && i >= low ? s[i] : -INFINITY;
+  }
+}
+// p = exp2(s), packed to bf16 pairs; the sums of pairs into rs
+__device__ __forceinline__ void exp32(const float (&s)[32], uint32_t (&p)[16], f32x2 (&rs)[2]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float p0 = fast_exp2(s[2 * i]), p1 = fast_exp2(s[2 * i + 1]);
+    rs[i & 1] = add2(rs[i & 1], pair(p0, p1));
+    p[i] = pack_bf16(p0, p1);
+  }
+}
+// 16 TMEM columns of fp32 (bf16 pairs) times alpha
+__device__ __forceinline__ void rescale16(uint32_t t, float alpha) {
+  float v[16];
+  uint32_t u[16];
+  PKV_LD16(t, v);
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(v[i] * alpha);
+  PKV_ST16U(t, u);
+}
+__device__ __forceinline__ void rescale16_bf16(uint32_t t, float alpha) {
+  float v[16];
+  uint32_t u[16];
+  PKV_LD16(t, v);
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t w = __float_as_uint(v[i]);
+    u[i] = pack_bf16(__uint_as_float(w << 16) * alpha, __uint_as_float(w & 0xFFFF0000u) * alpha);
+  }
+  PKV_ST16U(t, u);
+}
+__device__ __forceinline__ float total(const f32x2 (&rs)[2]) {
+  float a, b;
+  split(add2(rs[0], rs[1]), a, b);
+  return a + b;
+}
+
+// kScored: a window, a prefix (runtime), and per instance a cap, a bias (kSym:
+// that may meet keys after a row's position, with a prefix).
+template <bool kScored, Cap kCap, bool kBias, bool kSym>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, AttnArgs a, Workspace ws) {
@@ -370,10 +448,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) mbar_init(bar(i), 1);
     for (int x = 0; x < 2; ++x) {
-      mbar_init(bar(B_PF + x), 8);  // one arrival per softmax warp (each writes half of P)
+      mbar_init(bar(B_PF + x), kScored ? 4 : 8);  // one arrival per softmax warp of the tile
       mbar_init(bar(B_OE + x), 4);  // one arrival per epilogue warp
-      mbar_init(bar(B_LF + x), 8);  // one arrival per softmax warp
-      mbar_init(sbase + kOffBarLF1 + 8 * x, 8);
+      mbar_init(bar(B_LF + x), kScored ? 4 : 8);  // one arrival per softmax warp of the tile
+      mbar_init(sbase + kOffBarLF1 + 8 * x, kScored ? 4 : 8);
       mbar_init(bar(B_IE + x), 1 + 8 + 4);  // MMA warp, softmax warps, epilogue warps
     }
     for (int i = 0; i < 4; ++i) mbar_init(bar(B_XP + i), 2);
@@ -557,13 +635,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         s_cnt[x]++;
       };
       // O_x (+)= P_x V_c  (P_x: bf16 pairs, keys 0-63 in columns 0-31 and keys
-      // 64-127 in columns 64-95 of S_x: each half where its own scores were)
+      // 64-127 in columns 64-95 of S_x: each half where its own scores were;
+      // in a scored call each 32 keys where their scores were)
       auto issue_pv = [&](int x, uint32_t c, bool acc) {
         const uint64_t db = (c & 1) ? dv1 : dv0;
         const uint32_t d = tmem + 256 + x * 128, pa = tmem + x * 128;
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          mma_ts(d, pa + (kk >> 2) * 64 + (kk & 3) * 8, db + ((kk * 16 * 128) >> 4), id_o,
+          mma_ts(d, pa + (kScored ? (kk >> 1) * 32 + (kk & 1) * 8 : (kk >> 2) * 64 + (kk & 3) * 8), db + ((kk * 16 * 128) >> 4), id_o,
                  (acc || kk > 0) ? 1u : 0u);
       };
       bool ok = true;
@@ -627,7 +706,214 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
+  } else if (kScored && warp < 10) {
+    if constexpr (kScored) {
+    // ------------- softmax of a scored call: a row per thread, four warps per tile -------------
+    // Warps 2-5 serve tile a of every item, 6-9 tile b, each its 32 rows
+    // whole, in four blocks of 32 columns; the two tiles' softmaxes run beside
+    // each other, and no row needs another warp's values.  P of a block goes
+    // where its scores began (16 packed columns).  Two paths:
+    //   quick: pairs of blocks that every row of the warp sees, the running
+    //     maximum at hand and the form of the cap foreseen: straight code,
+    //     checked at its end, and redone if the check fails (P has not left
+    //     the registers, the scores are still in TMEM);
+    //   block: any block of 32 columns, masks, new maxima, in a loop.
+    // 8 prompts of 2048 tokens, 64 heads over 8: without options 452 us,
+    // bias 475, cap 608, window of 1024 389 (plain call 500; with
+    // scores of three times the size its repeated maxima take it to 648).
+    // The cap is bound by the two warps a sub-partition has for its
+    // arithmetic: five packed operations a pair of scores where the others
+    // take one to two.  Measured and not kept: a row's 128 or 64 columns in
+    // straight code with all forms of the cap in place (730 to 2229 us for
+    // the cap: instruction-cache misses); two warps a row as in the plain
+    // call, in loops of 32 columns (cap 573, bias 718); two warps a row and
+    // tile, 16 in all (cap 537 to 548, bias 794 to 825: 80 registers a thread
+    // spill); four warps a row (cap 566, bias 746).
+    const int x = (warp - 2) >> 2;  // my query tile
+    const int qd = warp & 3;
+    const int row = qd * 32 + lane;  // == TMEM lane
+    const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
+    float* lsum = reinterpret_cast<float*>(smem + kOffLsum);
+    const ScoreParams sp = score_params(a);
+    const CapForm cf = cap_form(sp);
+    const uint32_t t_s = tmem + x * 128 + lane_off, t_o = tmem + 256 + x * 128 + lane_off;
+    uint32_t s_cnt = 0;
+    // The quick path's form of the cap: the exponential for the next eight
+    // items after a score past the polynomial's range; kBlocks: none.
+    constexpr int kBlocks = 2;
+    int form = kCap != kNoCap && cf.limit < 0.f ? kBlocks : 0, hold = 0;
+    bool ok = true;
+    for (uint32_t it_cnt = 0; ok; ++it_cnt) {
+      const int slot = it_cnt & 1;
+      if (!mbar_wait_warp(bar(B_IF + slot), (it_cnt >> 1) & 1, abort, ws.err)) break;
+      const Item it = items[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_IE + slot));
+      if (it.r < 0) break;
+      if (x == 1 && it.hb < 0) continue;  // an item of one tile
+      const int qrow = it.qt * kPreTileQ + row;  // row inside the request
+      const bool valid_row = qrow < it.n;
+      // rows past the request's take the last row's position; they take part
+      // in no decision, and their results are dropped
+      const int rpos = it.ctx + (valid_row ? qrow : it.n - 1);
+      const int last = max(rpos, it.prefix - 1);           // last visible key
+      const int first = first_key(rpos, a.score.window);   // first visible key
+      const float slope2 = kBias ? __ldg(a.score.slopes + (x ? it.hb : it.ha)) * kLog2e : 0.f;
+      // The reference (log2 units) that the exponentials are taken against.
+      // Fixed: a capped logit lies within +-cap2, so with half the cap and the
+      // row's largest bias (0, its own key's, or with a negative slope its
+      // furthest key's) exp2(y - ref) of the key of that bias lies within
+      // 2^(-3/2 cap2) and 2^(cap2 / 2), inside fp32's and bf16's exponents for
+      // cap2 <= 80 (caps up to 55) with room for the sums.  Else the running
+      // maximum, rounded up to a whole number, so that rescaling is exact; it
+      // follows the scores only when a block's sum passes kMaxSum: bf16 keeps
+      // its precision over fp32's exponents, so a reference below the maximum
+      // costs none, and 2^40 leaves the sums room to 2^127.
+      float ref = kCap == kFixedCap ? 0.5f * sp.cap2 - fminf(0.f, slope2) *
+                                          (float)max(rpos - first, last - rpos)
+                                    : -INFINITY;
+      float l = 0.f;
+      if (form == 1 && --hold <= 0) form = 0;
+      for (int j = 0; j < it.nkv; ++j) {
+        const int key0 = tile_key0<kScored, kBias>(it, j);
+        const int lim = last - key0, low = first - key0;  // low <= column <= lim is visible
+        // blocks c1 .. c2 - 1 are seen whole by every row of the warp
+        const int c1 = (__reduce_max_sync(0xffffffffu, low) + 31) >> 5;
+        const int c2 = min(4, (__reduce_min_sync(0xffffffffu, lim) + 1) >> 5);
+        if (!mbar_wait_warp(bar(B_SF + x), s_cnt++ & 1, abort, ws.err)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t done = 0;  // blocks whose P is written
+        bool tried = false;
+        for (;;) {
+          // the block path: before the quick one only where a row has no
+          // maximum yet, after it whatever is left
+          const bool have = __all_sync(0xffffffffu, ref != -INFINITY || !valid_row);
+          if (tried || !have || form == kBlocks) {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              if ((done >> c) & 1) continue;
+              float s[32];
+              uint32_t p[16];
+              const int lc = lim - 32 * c, wc = low - 32 * c;
+              if (__all_sync(0xffffffffu, lc < 0 || wc > 31)) {  // no row sees any
+#pragma unroll
+                for (int i = 0; i < 16; ++i) p[i] = 0;
+              } else {
+                const bool edge = !__all_sync(0xffffffffu, lc >= 31 && wc <= 0);
+                const float nm = kCap == kFixedCap ? -ref : 0.f;
+                PKV_LD32(t_s + 32 * c, s);
+                tmem_wait_ld();
+                logits32_any<kCap, kBias, kSym>(s, sp, cf, nm, edge, lc, wc, valid_row, slope2,
+                                                (float)(rpos - key0 - 32 * c));
+                if (kCap != kFixedCap) {
+                  float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+                  for (int i = 0; i < 32; i += 4) {
+                    m0 = max3f(m0, s[i], s[i + 1]);
+                    m1 = max3f(m1, s[i + 2], s[i + 3]);
+                  }
+                  const float m = fmaxf(m0, m1);
+                  const bool up = m > ref + kRescaleThreshold;
+                  if (__any_sync(0xffffffffu, up)) {
+                    // the reference moves up by k whole units (a row without
+                    // one: everything so far of it is zero)
+                    const float to = up ? ceilf(m) : ref;
+                    const float k = up ? to - ref : 0.f;
+                    const float alpha =
+                        k < 126.f ? __int_as_float((127 - (int)k) << 23) : 0.f;
+                    l *= alpha;
+                    ref = to;
+                    tmem_wait_st();
+                    if (j > 0) {
+                      // (PV of the tile before is complete: S of this one is)
+#pragma unroll 1
+                      for (int ch = 0; ch < 8; ++ch) rescale16(t_o + ch * 16, alpha);
+                    }
+#pragma unroll 1
+                    for (int e = 0; e < 4; ++e)
+                      if ((done >> e) & 1) rescale16_bf16(t_s + 32 * e, alpha);
+                  }
+                  const float r0 = ref == -INFINITY ? 0.f : ref;  // (no key seen yet)
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) s[i] -= r0;
+                }
+                f32x2 rs[2] = {0, 0};
+                exp32(s, p, rs);
+                l += total(rs);
+              }
+              PKV_ST16U(t_s + 32 * c, p);
+              done |= 1u << c;
+              // (the rest by the quick path, once each row has a maximum)
+              if (!tried && form != kBlocks && c2 > c1 &&
+                  __all_sync(0xffffffffu, ref != -INFINITY || !valid_row))
+                break;
+            }
+          }
+          if (done == 15u) break;
+          if (tried) continue;
+          tried = true;
+          // the quick path: pairs of blocks, none of them done yet
+#pragma unroll 1
+          for (int h = 0; h < 2 && form != kBlocks;) {
+            if (2 * h < c1 || 2 * h + 2 > c2 || ((done >> (2 * h)) & 3) != 0) {
+              ++h;
+              continue;
+            }
+            uint32_t p[2][16];
+            f32x2 rs[2] = {0, 0};
+            float big = 0.f;
+            auto go = [&](auto f) {
+              float s[2][32];
+              PKV_LD32(t_s + 64 * h, s[0]);
+              PKV_LD32(t_s + 64 * h + 32, s[1]);
+              tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                logits32<kCap, kBias, kSym, decltype(f)::value>(
+                    s[c], sp, cf, -ref, slope2, (float)(rpos - key0 - 64 * h - 32 * c), big);
+                exp32(s[c], p[c], rs);
+              }
+            };
+            if (kCap == kNoCap || form == 0)
+              go(std::integral_constant<int, 0>());
+            else
+              go(std::integral_constant<int, 1>());
+            const float sum = total(rs);
+            if (kCap != kNoCap && form == 0 &&
+                !__all_sync(0xffffffffu, big <= cf.limit || !valid_row)) {
+              form = 1;
+              hold = 8;
+              continue;
+            }
+            if (kCap != kFixedCap && !__all_sync(0xffffffffu, sum <= kMaxSum || !valid_row)) {
+              ++h;  // (a new maximum: the block path's)
+              continue;
+            }
+            l += sum;
+            PKV_ST16U(t_s + 64 * h, p[0]);
+            PKV_ST16U(t_s + 64 * h + 32, p[1]);
+            done |= 3u << (2 * h);
+            ++h;
+          }
+          if (done == 15u) break;
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_PF + x));
+      }
+      if (!ok) break;
+      // the row sums of the item, for the epilogue (see the plain call's)
+      lsum[((it_cnt & 1) * 2 + x) * 2 * 128 + row] = l;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(lf_bar(it_cnt, x));
+    }
+    }
   } else if (warp < 10) {
+    if constexpr (!kScored) {
     // ------------------- softmax: two warps per row, a column half each -------------------
     // Warp w reads TMEM lanes 32 * (w % 4) .. + 31 (its 32 rows, one per
     // thread) and key columns 64 * hf .. 64 * hf + 63, hf = (w - 2) / 4, of
@@ -643,8 +929,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
     float* xch = reinterpret_cast<float*>(smem + kOffXch);
     const float sl2 = a.scale * kLog2e;
-    const ScoreParams sp = score_params(a);
-    const CapForm cf = cap_form(sp);
     uint32_t s_cnt[2] = {0, 0}, x_cnt = 0;
     bool ok = true;
     // this lane's value out, the other warp's value for the same row back
@@ -668,22 +952,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nx = it.hb >= 0 ? 2 : 1;
       const int qrow = it.qt * kPreTileQ + row;  // row inside the request
       const bool valid_row = qrow < it.n;
-      // last visible key; in a scored call rows past the request's repeat its
-      // last row, so that they take part in no decision of their own
-      const int rpos = it.ctx + (valid_row ? qrow : it.n - 1);
-      const int qpos = kScored ? max(rpos, it.prefix - 1) : (valid_row ? it.ctx + qrow : 0);
-      const int rlow = kScored ? first_key(rpos, a.score.window) : 0;  // first visible key
-      float slope2[2] = {0.f, 0.f};
-      if (kBias) {
-        slope2[0] = __ldg(a.score.slopes + it.ha) * kLog2e;
-        if (it.hb >= 0) slope2[1] = __ldg(a.score.slopes + it.hb) * kLog2e;
-      }
+      const int qpos = valid_row ? it.ctx + qrow : 0;  // last visible key
       float m_used[2] = {-INFINITY, -INFINITY}, l_part[2] = {0.f, 0.f};
       for (int j = 0; j < it.nkv && ok; ++j) {
-        const int key0 = tile_key0<kScored, kBias>(it, j) + 64 * hf;  // key of my first column
-        const int lim = qpos - key0;   // my columns <= lim are visible
-        const int low = rlow - key0;   // (scored) and >= low
-        const bool masked = !__all_sync(0xffffffffu, lim >= 63 && (!kScored || low <= 0));
+        const int lim = qpos - j * kTileK - 64 * hf;  // my columns <= lim are visible
+        const bool masked = !__all_sync(0xffffffffu, lim >= 63);
         for (int x = 0; x < nx && ok; ++x) {
           if (!mbar_wait_warp(bar(B_SF + x), s_cnt[x]++ & 1, abort, ws.err)) {
             ok = false;
@@ -691,113 +964,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_after();
           const uint32_t t_s = tmem + x * 128 + 64 * hf + lane_off;
-          if constexpr (kCap == kFixedCap) {
-            // Fixed-reference softmax: a capped logit lies within +-cap2, so
-            // exp2(y - cap2 / 2) lies within 2^(-3/2 cap2) and 2^(cap2 / 2),
-            // inside fp32's and bf16's exponents for cap2 <= 80 (caps up to
-            // 55) with room for the sums: no maximum, no exchange between the
-            // two warps of a row, no rescaling, and P goes out 32 columns at
-            // a time.
-            float rs[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-            for (int c = 0; c < 2; ++c) {
-              float s[32];
-              uint32_t p[16];
-              PKV_LD32(t_s + 32 * c, s);
-              tmem_wait_ld();
-              logits32<true, false>(s, sp, cf, -0.5f * sp.cap2, masked, lim - 32 * c,
-                                    low - 32 * c, valid_row, 0.f, 0.f, false);
-              exp32(s, p, rs);
-              PKV_ST16U(t_s + 16 * c, p);
-            }
-            l_part[x] += (rs[0] + rs[1]) + (rs[2] + rs[3]);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_PF + x));
-            continue;
-          }
-          if constexpr (kCap == kAnyCap || kBias) {
-            // Running maximum as below, the logits formed 32 columns at a
-            // time: P stays in registers until the maximum is agreed on.
-            const float sl = x ? slope2[1] : slope2[0];
-            const float d0 = (float)(rpos - key0);
-            auto logits = [&](float(&s)[32], int c, float nm) {
-              PKV_LD32(t_s + 32 * c, s);
-              tmem_wait_ld();
-              logits32<kCap != kNoCap, kBias>(s, sp, cf, nm, masked, lim - 32 * c, low - 32 * c,
-                                              valid_row, sl, d0 - 32.f * c, it.prefix > 0);
-            };
-            float alpha = 1.f;
-            bool resc = false, maxed = j == 0;
-            uint32_t p[2][16];
-            float rs[4];
-            for (;;) {
-              if (maxed) {
-                float pm = -INFINITY;
-#pragma unroll 1
-                for (int c = 0; c < 2; ++c) {
-                  float s[32];
-                  logits(s, c, 0.f);
-#pragma unroll
-                  for (int i = 0; i < 32; i += 2) pm = max3f(pm, s[i], s[i + 1]);
-                }
-                const float po = exchange(pm);
-                if (!ok) break;
-                const float mt = hf == 0 ? fmaxf(pm, po) : fmaxf(po, pm);
-                resc = mt > m_used[x] + kRescaleThreshold;
-                if (resc) {
-                  alpha = fast_exp2(m_used[x] - mt);  // 0 on the row's first keys
-                  m_used[x] = mt;
-                }
-              }
-              rs[0] = rs[1] = rs[2] = rs[3] = 0.f;
-              // (a row that has seen no key yet has no maximum: 0 is its reference)
-              const float nm = m_used[x] == -INFINITY ? 0.f : -m_used[x];
-#pragma unroll 1
-              for (int c = 0; c < 2; ++c) {
-                float s[32];
-                if (c == 1) {
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) p[0][i] = p[1][i];
-                }
-                logits(s, c, nm);
-                exp32(s, p[1], rs);
-              }
-              if (maxed) break;
-              const float tot = (rs[0] + rs[1]) + (rs[2] + rs[3]);
-              // a row that sees its first key in a later tile takes the max
-              // pass until it has a maximum
-              const float mine =
-                  valid_row && (!(tot <= 256.f) || m_used[x] == -INFINITY) ? 1.f : 0.f;
-              const float other = exchange(mine);
-              if (!ok) break;
-              maxed = __any_sync(0xffffffffu, mine + other > 0.f);
-              if (!maxed) break;
-            }
-            if (!ok) break;
-            PKV_ST16U(t_s, p[0]);
-            PKV_ST16U(t_s + 16, p[1]);
-            l_part[x] = l_part[x] * alpha + ((rs[0] + rs[1]) + (rs[2] + rs[3]));
-            if (j > 0 && __any_sync(0xffffffffu, resc)) {
-              const uint32_t t_o = tmem + 256 + x * 128 + 64 * hf + lane_off;
-#pragma unroll 1
-              for (int ch = 0; ch < 4; ++ch) {
-                float ov[16];
-                PKV_LD16(t_o + ch * 16, ov);
-                tmem_wait_ld();
-                uint32_t ou[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) ou[i] = __float_as_uint(ov[i] * alpha);
-                PKV_ST16U(t_o + ch * 16, ou);
-              }
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_PF + x));
-            continue;
-          }
           // my 64 scores of the row in registers (one wait), then P in place
           float sv[64];
           auto load_scores = [&]() {
@@ -806,8 +972,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_ld();
             if (masked) {
 #pragma unroll
-              for (int i = 0; i < 64; ++i)
-                sv[i] = (i <= lim && (!kScored || i >= low)) ? sv[i] : -INFINITY;
+              for (int i = 0; i < 64; ++i) sv[i] = (i <= lim) ? sv[i] : -INFINITY;
             }
           };
           // p = exp2(s * scale * log2(e) - m) two columns at a time (packed
@@ -816,8 +981,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float rs[4];
           auto exp_pack = [&](float m) {
             rs[0] = rs[1] = rs[2] = rs[3] = 0.f;
-            // (a row that has seen no key yet has no maximum: 0 is its reference)
-            const float nm = kScored && m == -INFINITY ? 0.f : -m;
+            const float nm = -m;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               float x0, x1;
@@ -838,11 +1002,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!need_max) {
             exp_pack(m_used[x]);
             const float tot = (rs[0] + rs[1]) + (rs[2] + rs[3]);
-            float mine = (tot <= 256.f) ? 0.f : 1.f;
-            // a window's or a reversed order's row may see its first key in
-            // any tile: it takes the max pass until it has a maximum
-            if (kScored && m_used[x] == -INFINITY) mine = 1.f;
-            if (kScored && !valid_row) mine = 0.f;
+            const float mine = (tot <= 256.f) ? 0.f : 1.f;
             const float other = exchange(mine);
             if (!ok) break;
             need_max = __any_sync(0xffffffffu, mine + other > 0.f);
@@ -906,6 +1066,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(lf_bar(it_cnt, x));
       }
     }
+    }
   } else {
     // ------------------ epilogue: one warp per TMEM lane quarter ------------------
     // Warp w (10..13) owns rows 32 * (w % 4) .. + 31 of both output tiles.  When
@@ -941,7 +1102,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const float* ls = lsum + ((it_cnt & 1) * 2 + x) * 2 * 128;
-        const float inv = 1.f / (ls[row] + ls[128 + row]);  // the two column halves' sums
+        // the two column halves' sums (one sum in a scored call)
+        const float inv = 1.f / (kScored ? ls[row] : ls[row] + ls[128 + row]);
         const uint32_t t_o = tmem + 256 + x * 128 + lane_off;
         const int h = x == 0 ? it.ha : it.hb;
         const int row_base = it.qt * kPreTileQ + qd * 32;  // the warp's first row
@@ -1010,10 +1172,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   combine_splits(a, ws, blockIdx.x * (kThreads / 32) + warp, gridDim.x * (kThreads / 32));
 }
 
-template <bool kScored, Cap kCap, bool kBias>
+template <bool kScored, Cap kCap, bool kBias, bool kSym>
 cudaError_t launch_prefill_as(const AttnArgs& a, const Workspace& ws, int sms, cudaStream_t st) {
   static std::atomic<bool> attr[kMaxAttrDevices];
-  auto* kernel = prefill_kernel<kScored, kCap, kBias>;
+  auto* kernel = prefill_kernel<kScored, kCap, kBias, kSym>;
   if (cudaError_t e = smem_attr_once(kernel, kSmemBytes, attr)) return e;
   CUtensorMap tq, tk, tv;
   if (!make_rows_map(&tq, a.q, a.q_rows, a.hq, a.q_stride, 1, kPreTileQ) ||
@@ -1026,15 +1188,21 @@ cudaError_t launch_prefill_as(const AttnArgs& a, const Workspace& ws, int sms, c
 }  // namespace
 
 cudaError_t launch_prefill(const AttnArgs& a, const Workspace& ws, int sms, cudaStream_t st) {
-  if (!a.score.on) return launch_prefill_as<false, kNoCap, false>(a, ws, sms, st);
-  if (a.score.softcap > 0.f) {
-    if (a.score.slopes) return launch_prefill_as<true, kAnyCap, true>(a, ws, sms, st);
-    return a.score.softcap * dev::kLog2e <= kFixedCap2
-               ? launch_prefill_as<true, kFixedCap, false>(a, ws, sms, st)
-               : launch_prefill_as<true, kAnyCap, false>(a, ws, sms, st);
+  const ScoreArgs& sc = a.score;
+  if (!sc.on) return launch_prefill_as<false, kNoCap, false, false>(a, ws, sms, st);
+  const bool bias = sc.slopes != nullptr, sym = bias && sc.prefix != nullptr;
+  if (sc.softcap > 0.f) {
+    const float k = a.scale / sc.softcap;  // (its sixth power in the polynomial form)
+    if (sc.softcap * dev::kLog2e <= kFixedCap2 && k >= 0x1p-20f && k <= 0x1p20f)
+      return sym    ? launch_prefill_as<true, kFixedCap, true, true>(a, ws, sms, st)
+             : bias ? launch_prefill_as<true, kFixedCap, true, false>(a, ws, sms, st)
+                    : launch_prefill_as<true, kFixedCap, false, false>(a, ws, sms, st);
+    return bias ? launch_prefill_as<true, kAnyCap, true, true>(a, ws, sms, st)
+                : launch_prefill_as<true, kAnyCap, false, false>(a, ws, sms, st);
   }
-  return a.score.slopes ? launch_prefill_as<true, kNoCap, true>(a, ws, sms, st)
-                        : launch_prefill_as<true, kNoCap, false>(a, ws, sms, st);
+  return sym    ? launch_prefill_as<true, kNoCap, true, true>(a, ws, sms, st)
+         : bias ? launch_prefill_as<true, kNoCap, true, false>(a, ws, sms, st)
+                : launch_prefill_as<true, kNoCap, false, false>(a, ws, sms, st);
 }
 
 }  // namespace pkv
