@@ -98,11 +98,12 @@ def _check(rc):
 
 _torch = None
 _raw_stream = None  # () -> the current device's current stream handle, as an int
+_get_device = None  # () -> the current device's index
 
 
 def _T():
     """torch, imported on first use (the binding loads without it)."""
-    global _torch, _raw_stream
+    global _torch, _raw_stream, _get_device
     if _torch is None:
         import torch
         get_dev = getattr(torch._C, "_cuda_getDevice", None)
@@ -111,6 +112,12 @@ def _T():
             _raw_stream = lambda: get_raw(get_dev())  # noqa: E731
         else:
             _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+        # (a build or machine without CUDA has no current device, and no tensor on one)
+        _get_device = torch.cuda.current_device
+        if not torch.cuda.is_available():
+            _get_device = lambda: -2  # noqa: E731
+        elif get_dev is not None:
+            _get_device = get_dev
         _torch = torch
     return _torch
 
@@ -246,68 +253,99 @@ def _caches(key_cache, value_cache, dtype):
     return key_cache.shape
 
 
-def _on_current_device(*named):
-    """Checks (tensor, name, dtype) triples: the dtype, and that each tensor
-    lives on the current CUDA device, whose stream the call enqueues on.
-    Tensors that are None are skipped."""
-    torch = _T()
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -2
+def _name_culprit(*named):
+    """Raises for the first of these (tensor, name, dtype) triples that is no
+    tensor of that dtype on the current CUDA device, whose stream the call
+    enqueues on (None stands for an optional tensor left out)."""
+    dev = _get_device()
     for t, name, dtype in named:
         if t is None:
             continue
-        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_cuda:
-            _require(t, dtype, name)
+        _require(t, dtype, name)
         if t.get_device() != dev:
             raise ValueError("%s is on cuda:%d, the current device is cuda:%d" %
                              (name, t.get_device(), dev))
 
 
-def _heads3(t, name):
-    """(rows, heads, row stride) of a [rows, heads, 128] tensor."""
-    if t.dim() != 3:
-        raise ValueError("%s must be [rows, heads, head_size]" % name)
-    rows, heads, _ = t.shape
-    return rows, heads, _rows3(t, name)
-
-
 def _write_rope(q, k, v, positions, cos_sin, key_cache, value_cache, slot_mapping, q_out,
                 interleaved, q_weight, k_weight, weight_offset, eps, n_tokens, stream, scales):
-    torch = _T()
+    torch = _torch or _T()
     bf16 = torch.bfloat16
     cache = torch.int8 if scales else bf16
-    _on_current_device((q, "q", bf16), (k, "k", bf16), (v, "v", bf16), (q_out, "q_out", bf16),
-                       (key_cache, "key_cache", cache), (value_cache, "value_cache", cache),
-                       (cos_sin, "cos_sin", torch.float32), (positions, "positions", torch.int64),
-                       (slot_mapping, "slot_mapping", torch.int64), (q_weight, "q_weight", bf16),
-                       (k_weight, "k_weight", bf16))
-    nb, bs, hkv, d = _caches(key_cache, value_cache, cache)
-    qr, hq, qs = _heads3(q, "q")
-    qor, hqo, qos = _heads3(q_out, "q_out")
-    kr, hk, ks = _heads3(k, "k")
-    vr, hv, vs = _heads3(v, "v")
-    if hqo != hq or hk != hkv or hv != hkv or not (q.shape[2] == q_out.shape[2] == k.shape[2] ==
-                                                   v.shape[2] == d):
+    # every check in one pass of plain attribute reads (a small step's time is
+    # this function's); a failing one is named afterwards
+    try:
+        dev = _get_device()
+        good = (q.dtype is bf16 and k.dtype is bf16 and v.dtype is bf16 and q_out.dtype is bf16 and
+                key_cache.dtype is cache and value_cache.dtype is cache and
+                cos_sin.dtype is torch.float32 and positions.dtype is torch.int64 and
+                slot_mapping.dtype is torch.int64 and
+                dev == q.get_device() == k.get_device() == v.get_device() == q_out.get_device() ==
+                key_cache.get_device() == value_cache.get_device() == cos_sin.get_device() ==
+                positions.get_device() == slot_mapping.get_device())
+        qw = kw = None
+        if q_weight is not None:
+            good = good and q_weight.dtype is bf16 and dev == q_weight.get_device()
+            qw = q_weight.data_ptr()
+        if k_weight is not None:
+            good = good and k_weight.dtype is bf16 and dev == k_weight.get_device()
+            kw = k_weight.data_ptr()
+    except AttributeError:
+        good = False
+    if not good:
+        _name_culprit((q, "q", bf16), (k, "k", bf16), (v, "v", bf16), (q_out, "q_out", bf16),
+                      (key_cache, "key_cache", cache), (value_cache, "value_cache", cache),
+                      (cos_sin, "cos_sin", torch.float32), (positions, "positions", torch.int64),
+                      (slot_mapping, "slot_mapping", torch.int64), (q_weight, "q_weight", bf16),
+                      (k_weight, "k_weight", bf16))
+        raise ValueError("arguments must be tensors on the current CUDA device")
+    cs = key_cache.shape
+    if len(cs) != 4 or cs != value_cache.shape or not (key_cache.is_contiguous() and
+                                                       value_cache.is_contiguous()):
+        _caches(key_cache, value_cache, cache)
+    nb, bs, hkv, d = cs
+    try:
+        rows, hq, qd = q.shape
+        orows, ohq, od = q_out.shape
+        krows, hk, kd = k.shape
+        vrows, hv, vd = v.shape
+        qs, q1, q2 = q.stride()
+        os_, o1, o2 = q_out.stride()
+        ks, k1, k2 = k.stride()
+        vs, v1, v2 = v.stride()
+        far, rot = cos_sin.shape
+        n, = slot_mapping.shape
+        npos, = positions.shape
+    except ValueError:
+        raise ValueError("q, k, v and q_out must be [rows, heads, head_size], cos_sin "
+                         "[max_positions, rotary_dim], positions and slot_mapping "
+                         "one-dimensional") from None
+    if not (qd == od == kd == vd == d and ohq == hq and hk == hv == hkv):
         raise ValueError("q and q_out must have the same heads, k and v those of the caches, all "
                          "head_size %d" % d)
+    if not (q2 == o2 == k2 == v2 == 1 and q1 == o1 == k1 == v1 == d):
+        raise ValueError("q, k, v and q_out must have contiguous rows")
+    if not (cos_sin.is_contiguous() and slot_mapping.is_contiguous() and
+            positions.is_contiguous()):
+        raise ValueError("cos_sin, slot_mapping and positions must be contiguous")
     for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if t is not None and (t.shape != (d,) or not t.is_contiguous()):
             raise ValueError("%s must be a contiguous [head_size]" % name)
-    if cos_sin.dim() != 2 or not cos_sin.is_contiguous():
-        raise ValueError("cos_sin must be a contiguous [max_positions, rotary_dim]")
-    if not (slot_mapping.is_contiguous() and positions.is_contiguous()):
-        raise ValueError("slot_mapping and positions must be contiguous")
-    n = slot_mapping.shape[0] if n_tokens is None else int(n_tokens)
-    if n > min(slot_mapping.shape[0], positions.shape[0], qr, qor, kr, vr):
-        raise ValueError("n_tokens exceeds the rows of q/k/v/q_out/positions/slot_mapping")
-    L = load()
+    if n_tokens is not None:
+        if int(n_tokens) > n:
+            raise ValueError("n_tokens exceeds the rows of slot_mapping")
+        n = int(n_tokens)
+    if n > rows or n > orows or n > krows or n > vrows or n > npos:
+        raise ValueError("n_tokens exceeds the rows of q/k/v/q_out/positions")
+    L = _lib or load()
     fn = L.pkv_write_rope_int8 if scales else L.pkv_write_rope
-    _check(fn(q.data_ptr(), qs, hq, k.data_ptr(), ks, v.data_ptr(), vs,
-              None if q_weight is None else q_weight.data_ptr(),
-              None if k_weight is None else k_weight.data_ptr(), weight_offset, eps,
-              cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], 1 if interleaved else 0,
-              positions.data_ptr(), q_out.data_ptr(), qos, key_cache.data_ptr(),
-              value_cache.data_ptr(), *scales, nb, bs, hkv, d, slot_mapping.data_ptr(), n,
-              _stream(stream)))
+    rc = fn(q.data_ptr(), qs, hq, k.data_ptr(), ks, v.data_ptr(), vs, qw, kw, weight_offset, eps,
+            cos_sin.data_ptr(), far, rot, 1 if interleaved else 0, positions.data_ptr(),
+            q_out.data_ptr(), os_, key_cache.data_ptr(), value_cache.data_ptr(), *scales, nb, bs,
+            hkv, d, slot_mapping.data_ptr(), n,
+            _raw_stream() if stream is None else _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def pkv_write_rope(q, k, v, positions, cos_sin, key_cache, value_cache, slot_mapping, q_out,
@@ -388,43 +426,72 @@ def pkv_attention_scored(q, key_cache, value_cache, query_start_loc, seq_lens, b
     """pkv_attention with modified scores: softcap * tanh(s / softcap), the
     bias -alibi_slopes[head] * distance (fp32 [Hq]), a sliding window of keys
     and a prefix (int32 [num_reqs]) that every row sees; see include/pkv.h."""
-    torch = _T()
+    torch = _torch or _T()
     bf16, i32 = torch.bfloat16, torch.int32
-    _on_current_device((q, "q", bf16), (key_cache, "key_cache", bf16),
-                       (value_cache, "value_cache", bf16), (out, "out", bf16),
-                       (query_start_loc, "query_start_loc", i32), (seq_lens, "seq_lens", i32),
-                       (block_table, "block_table", i32),
-                       (alibi_slopes, "alibi_slopes", torch.float32),
-                       (prefix_lens, "prefix_lens", i32))
-    nb, bs, hkv, d = _caches(key_cache, value_cache, bf16)
-    rows, hq, qs = _heads3(q, "q")
-    orows, ohq, os_ = _heads3(out, "out")
-    if orows < rows or ohq != hq or out.shape[2] != d or q.shape[2] != d:
+    try:  # (see _write_rope)
+        dev = _get_device()
+        good = (q.dtype is bf16 and key_cache.dtype is bf16 and value_cache.dtype is bf16 and
+                out.dtype is bf16 and query_start_loc.dtype is i32 and seq_lens.dtype is i32 and
+                block_table.dtype is i32 and
+                dev == q.get_device() == key_cache.get_device() == value_cache.get_device() ==
+                out.get_device() == query_start_loc.get_device() == seq_lens.get_device() ==
+                block_table.get_device())
+        slopes = prefix = None
+        if alibi_slopes is not None:
+            good = good and alibi_slopes.dtype is torch.float32 and dev == alibi_slopes.get_device()
+            slopes = alibi_slopes.data_ptr()
+        if prefix_lens is not None:
+            good = good and prefix_lens.dtype is i32 and dev == prefix_lens.get_device()
+            prefix = prefix_lens.data_ptr()
+    except AttributeError:
+        good = False
+    if not good:
+        _name_culprit((q, "q", bf16), (key_cache, "key_cache", bf16),
+                      (value_cache, "value_cache", bf16), (out, "out", bf16),
+                      (query_start_loc, "query_start_loc", i32), (seq_lens, "seq_lens", i32),
+                      (block_table, "block_table", i32),
+                      (alibi_slopes, "alibi_slopes", torch.float32),
+                      (prefix_lens, "prefix_lens", i32))
+        raise ValueError("arguments must be tensors on the current CUDA device")
+    cs = key_cache.shape
+    if len(cs) != 4 or cs != value_cache.shape or not (key_cache.is_contiguous() and
+                                                       value_cache.is_contiguous()):
+        _caches(key_cache, value_cache, bf16)
+    nb, bs, hkv, d = cs
+    try:
+        rows, hq, qd = q.shape
+        orows, ohq, od = out.shape
+        qs, q1, q2 = q.stride()
+        os_, o1, o2 = out.stride()
+    except ValueError:
+        raise ValueError("q and out must be [rows, num_heads, head_size]") from None
+    if orows < rows or ohq != hq or od != d or qd != d:
         raise ValueError("q and out must be [rows, num_heads, %d] with as many rows of out" % d)
+    if not (q2 == o2 == 1 and q1 == o1 == d):
+        raise ValueError("q and out must have contiguous rows")
     num_reqs, window = int(num_reqs), int(window)
-    for t, name in ((query_start_loc, "query_start_loc"), (seq_lens, "seq_lens"),
-                    (block_table, "block_table"), (alibi_slopes, "alibi_slopes"),
-                    (prefix_lens, "prefix_lens")):
-        if t is not None and not t.is_contiguous():
-            raise ValueError("%s must be contiguous" % name)
-    two = block_table.dim() == 2
-    if not two and (block_table.dim() != 1 or num_reqs > 1):
+    bts = block_table.shape
+    if len(bts) != 2 and (len(bts) != 1 or num_reqs > 1):
         raise ValueError("block_table must be [num_reqs, width]")
+    if not (query_start_loc.is_contiguous() and seq_lens.is_contiguous() and
+            block_table.is_contiguous()):
+        raise ValueError("query_start_loc, seq_lens and block_table must be contiguous")
     if num_reqs > 0 and (query_start_loc.numel() < num_reqs + 1 or seq_lens.numel() < num_reqs or
-                         (two and block_table.shape[0] < num_reqs) or
-                         (prefix_lens is not None and prefix_lens.numel() < num_reqs)):
+                         (len(bts) == 2 and bts[0] < num_reqs)):
         raise ValueError("metadata shorter than num_reqs")
-    if alibi_slopes is not None and alibi_slopes.shape != (hq,):
-        raise ValueError("alibi_slopes must be [num_heads]")
+    if slopes is not None and (alibi_slopes.shape != (hq,) or not alibi_slopes.is_contiguous()):
+        raise ValueError("alibi_slopes must be a contiguous [num_heads]")
+    if prefix is not None and (prefix_lens.numel() < num_reqs or not prefix_lens.is_contiguous()):
+        raise ValueError("prefix_lens must be contiguous, one per request")
     if not -1 <= window < 1 << 31 or num_reqs >= 1 << 31:
         raise ValueError("window or num_reqs out of range")
-    _check(load().pkv_attention_scored(
+    rc = (_lib or load()).pkv_attention_scored(
         q.data_ptr(), qs, rows, hq, key_cache.data_ptr(), value_cache.data_ptr(), nb, bs, hkv, d,
-        query_start_loc.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(),
-        block_table.shape[-1], num_reqs, scale, softcap, window,
-        None if alibi_slopes is None else alibi_slopes.data_ptr(),
-        None if prefix_lens is None else prefix_lens.data_ptr(), out.data_ptr(), os_,
-        _stream(stream)))
+        query_start_loc.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), bts[-1], num_reqs,
+        scale, softcap, window, slopes, prefix, out.data_ptr(), os_,
+        _raw_stream() if stream is None else _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def pkv_plan(q_rows, num_heads, num_kv_heads, query_start_loc, seq_lens, block_table_width,
