@@ -148,6 +148,7 @@ struct RopeArgs {
   void* kc;
   void* vc;
   float k_scale, v_scale;    // int8 caches
+  float k_rcp, v_rcp;        // their rounded reciprocals, 0: divide (set by the launcher)
   int64_t num_slots;
   int hkv;
   const int64_t* slots;

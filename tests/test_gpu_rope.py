@@ -218,6 +218,56 @@ def test_bad_slots_and_positions_are_skipped_and_reported():
     c.check()
 
 
+@pytest.mark.parametrize("scale", [0.03125, 1 / 3, 0.0123, 127.0, 3.0, 1e-3, 2.0 ** -40, 5e-25,
+                                   1e25, 1e-37])
+def test_value_codes_are_those_of_write_int8(scale):
+    """Every bf16 bit pattern as a value, at scales with and without exact
+    halves between codes: the same codes as pkv_write_int8's, bit for bit
+    (ties, infinities, NaN and tiny values among them)."""
+    hkv, n = 4, 128
+    v = torch.arange(-32768, 32768, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    v = v.view(n, hkv, D).cuda()
+    q = torch.zeros((n, 4, D), dtype=torch.bfloat16, device="cuda")
+    slots = torch.arange(n, device="cuda")
+    pos, tab = torch.zeros(n, dtype=torch.int64, device="cuda"), table(1, 64).cuda()
+    caches = [torch.full((n // 16, 16, hkv, D), 99, dtype=torch.int8, device="cuda")
+              for _ in range(4)]
+    pkv.pkv_write_int8(v, v, caches[0], caches[1], slots, scale, scale)
+    # (position 0 rotates by nothing: the keys' codes are the plain ones too,
+    # but for an infinity times a sine of zero, which is no number)
+    pkv.pkv_write_rope_int8(q, v, v, pos, tab, caches[2], caches[3], slots, scale, scale, q)
+    assert pkv.pkv_get_error() == 0
+    assert torch.equal(caches[1], caches[3])
+    finite = v.float().isfinite()
+    pair = finite.clone()
+    pair[..., :32] &= finite[..., 32:64]
+    pair[..., 32:64] &= finite[..., :32]
+    assert torch.equal(caches[0].view(n, hkv, D)[pair], caches[2].view(n, hkv, D)[pair])
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("hq,hkv,rot,il", [(64, 8, 128, False), (32, 8, 64, True), (7, 5, 96, False),
+                                           (32, 32, 128, True), (1, 1, 16, False)])
+def test_larger_steps(hq, hkv, rot, il, int8):
+    """Steps long enough for the streaming form, whose warps take many units of
+    one token after another, with padding and bad tokens in between."""
+    n = 9000 if hq + hkv < 20 else 4500
+    c = Case(n, hq, hkv, rot, il, qn=True, kn=True, int8=int8, seed=n)
+    c.dev[2][7::13] = -1                     # padding inside the batch
+    c.dev[0][5::101] = c.table.shape[0]      # positions past the table
+    c.run()
+    assert pkv.pkv_get_error() == pkv.DEV_ERR_BITS["POSITION"]
+    left_out = torch.zeros(n, dtype=torch.bool)
+    left_out[7::13] = True
+    left_out[5::101] = True
+    assert torch.isnan(c.q_out[left_out.cuda()].float()).all()
+    keep = (~left_out).nonzero().view(-1)
+    c.q_out, c.n = c.q_out[keep.cuda()], keep.numel()
+    c.host = [t[keep] for t in c.host]
+    c.pos, c.slots = c.pos[keep], c.slots[keep]
+    c.check()
+
+
 def test_no_tokens():
     c = Case(4, 4, 2)
     c.run(n_tokens=0)
