@@ -45,6 +45,7 @@
 // shares the plan, the work units and the merge.
 #include "pkv_combine.cuh"
 #include "pkv_device.cuh"
+#include "pkv_score.cuh"
 
 namespace pkv {
 namespace {
@@ -135,17 +136,31 @@ __device__ __forceinline__ uint32_t mask_pair(uint32_t v, int tok_lo, int valid)
   const uint32_t hi = tok_lo + 1 < valid ? 0xFFFF0000u : 0u;
   return v & (lo | hi);
 }
-// keep the halves whose key index is at least `first`
-__device__ __forceinline__ uint32_t mask_pair_low(uint32_t v, int tok_lo, int first) {
-  const uint32_t lo = tok_lo >= first ? 0x0000FFFFu : 0u;
-  const uint32_t hi = tok_lo + 1 >= first ? 0xFFFF0000u : 0u;
-  return v & (lo | hi);
+// Zeroes the V rows of a page in shared memory (st: its stage) whose slots are
+// below `first`: the keys before a window in its first page, whose V must not
+// reach the product.  (By every warp that reads the page, each before its own
+// reads; once a unit, where masks in the product's loop cost every step.)
+__device__ __forceinline__ void zero_v_rows(uint8_t* st, int first, int lane) {
+  const int rows = min(first, kBlockSize);
+  for (int i = lane; i < rows * 16; i += 32)
+    *reinterpret_cast<uint4*>(st + (2 + (i & 1)) * kBox + (i >> 4) * 128 + ((i >> 1) & 7) * 16) =
+        make_uint4(0, 0, 0, 0);
+  fence_async_smem();  // (the stage is refilled by TMA)
+  __syncwarp();
 }
+
+// Instances: the plain call; a scored one; a scored one with a cap that
+// fixed_reference() holds for.  (For the warp pairs below, whose chain of
+// dependent steps sets the pace, the fixed reference takes the maximum, its
+// four exchanges and the rescaling vote out of each step: 32 decodes of 32,769
+// keys, one KV head, cap 50: 117 -> X us.)
+enum Mode { kPlain, kRunning, kFixedRef };
 
 // What a scored call does to one query row of a decode unit.
 struct RowScore {
   int pos, low;  // the row's position; first key it sees
   float slope2;  // bias slope, log2 units
+  float top;     // its largest bias (max_bias)
 };
 // The row at position pos of request r, head h; *vis (keys it sees end here)
 // grows to the request's prefix, clipped to the unit.
@@ -155,43 +170,78 @@ __device__ __forceinline__ RowScore row_score(const AttnArgs& a, int r, int pos,
   s.pos = pos;
   s.low = first_key(pos, a.score.window);
   s.slope2 = a.score.slopes ? __ldg(a.score.slopes + h) * kLog2e : 0.f;
-  if (a.score.prefix) *vis = max(*vis, min(k1, __ldg(a.score.prefix + r)));
+  int last = pos;
+  if (a.score.prefix) {
+    const int p = __ldg(a.score.prefix + r);
+    *vis = max(*vis, min(k1, p));
+    last = max(pos, p - 1);  // (past the last key: a larger bound does no harm)
+  }
+  s.top = max_bias(s.slope2, pos, s.low, last);
   return s;
 }
-// A step's raw products q.K (n registers) to logits in log2 units, the cap
-// applied: one form for the whole warp, chosen by the keys its rows see
-// (seen(i, e): register e of tile i), since the others may hold anything.
-template <int n, class Seen>
-__device__ __forceinline__ void cap_scores(const ScoreParams& sp, float (&s)[n][4], Seen&& seen) {
-  if (!sp.cap) {
+// The raw products q.K of a step's keys, tile nt of eight keys at key0 + 8 nt +
+// (e & 1), rows e >> 1 of the thread, to logits in log2 units: cap, bias, and
+// -inf for the keys a row does not see (any: some row of the unit sees not all
+// of the step's keys).  One form of the cap for the warp, chosen by the keys
+// its rows see, since the others may hold anything.
+// Fixed reference: minus it.
+template <int kTiles, bool kFixed>
+__device__ __forceinline__ void step_logits(const AttnArgs& a, const ScoreParams& sp,
+                                            const CapForm& cf, float (&s2)[kTiles][4],
+                                            const RowScore (&rs)[2], int vis0, int vis1, int key0,
+                                            bool any) {
+  float(&s)[4 * kTiles] = reinterpret_cast<float(&)[4 * kTiles]>(s2);
+  auto seen = [&](int i) {
+    const int j = key0 + 8 * (i >> 2) + (i & 1);
+    return (i & 2) ? j >= rs[1].low && j < vis1 : j >= rs[0].low && j < vis0;
+  };
+  const float nm = kFixed ? -0.5f * sp.cap2 : 0.f;
+  if (kFixed || sp.cap) {
+    float m0 = 0.f, m1 = 0.f;
+    if (any) {
 #pragma unroll
-    for (int i = 0; i < 4 * n; ++i) s[i >> 2][i & 3] *= sp.lin;
-    return;
-  }
-  float big = 0.f;
+      for (int i = 0; i < 4 * kTiles; ++i) s[i] = seen(i) ? s[i] : 0.f;
+    }
 #pragma unroll
-  for (int i = 0; i < 4 * n; ++i)
-    big = fmaxf(big, seen(i >> 2, i & 3) ? fabsf(s[i >> 2][i & 3]) : 0.f);
-  if (__all_sync(0xffffffffu, big * sp.k <= 1.f)) {
+    for (int i = 0; i < 4 * kTiles; i += 4) {
+      m0 = max3f(m0, fabsf(s[i]), fabsf(s[i + 1]));
+      m1 = max3f(m1, fabsf(s[i + 2]), fabsf(s[i + 3]));
+    }
+    const float m = fmaxf(m0, m1);
+    float big = 0.f;
+    if (__all_sync(0xffffffffu, m * m <= cf.limit)) {
+      cap_values<0>(s, sp, cf, nm, big);
+    } else if (!kFixed && cf.limit < 0.f && __all_sync(0xffffffffu, m * sp.k <= 1.f)) {
 #pragma unroll
-    for (int i = 0; i < 4 * n; ++i) s[i >> 2][i & 3] = capped_poly(s[i >> 2][i & 3], sp);
+      for (int i = 0; i < 4 * kTiles; ++i) s[i] = capped_poly(s[i], sp);
+    } else {
+      cap_values<1>(s, sp, cf, nm, big);
+    }
   } else {
 #pragma unroll
-    for (int i = 0; i < 4 * n; ++i) s[i >> 2][i & 3] = capped_exp(s[i >> 2][i & 3], sp);
+    for (int i = 0; i < 4 * kTiles; ++i) s[i] *= sp.lin;
+  }
+  if (a.score.slopes) {
+    const float d[2] = {(float)(rs[0].pos - key0), (float)(rs[1].pos - key0)};
+#pragma unroll
+    for (int i = 0; i < 4 * kTiles; ++i) {
+      const int r = (i >> 1) & 1;
+      if (kFixed) s[i] -= rs[r].top;
+      s[i] = fmaf(-rs[r].slope2, fabsf(d[r] - (float)(8 * (i >> 2) + (i & 1))), s[i]);
+    }
+  }
+  if (any) {
+#pragma unroll
+    for (int i = 0; i < 4 * kTiles; ++i) s[i] = seen(i) ? s[i] : -INFINITY;
   }
 }
-// The logit x of key j with the row's bias; -inf where the row does not see
-// the key.
-__device__ __forceinline__ float scored_logit(const RowScore& rs, float x, int j, int vis) {
-  x = fmaf(-rs.slope2, fabsf((float)(rs.pos - j)), x);
-  return j >= rs.low && j < vis ? x : -INFINITY;
-}
 
-template <bool kScored>
+template <int kMode>
 __global__ void __launch_bounds__(Cfg::kThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, AttnArgs a, Workspace ws) {
   using C = Cfg;
+  constexpr bool kScored = kMode != kPlain, kFixed = kMode == kFixedRef;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~(uintptr_t)1023);
@@ -228,6 +278,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
   const uint64_t pol = l2_evict_first();  // K/V pages are read once
   const float sl2 = a.scale * kLog2e;
   const ScoreParams sp = score_params(a);
+  const CapForm cf = cap_form(sp);
   const int gid = lane >> 2, tig = lane & 3;
   const int mi = lane >> 3, rr = lane & 7;
   uint32_t page_cnt = 0;
@@ -288,6 +339,12 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         rs[hrow] = row_score(a, un.r, un.ctx + ti, row < nrows ? ug * G + row % G : ug * G, k1,
                              &vis[hrow]);
     }
+    // every row of the unit sees the keys from all_lo up to all_hi
+    int all_lo = 0, all_hi = 0;
+    if (kScored) {
+      all_lo = __reduce_max_sync(0xffffffffu, max(rs[0].low, rs[1].low));
+      all_hi = __reduce_min_sync(0xffffffffu, min(vis[0], vis[1]));
+    }
 
     // page p of the unit into stage (page_cnt + p) % kStages; the stage's
     // previous page was consumed by this warp already (program order)
@@ -326,6 +383,10 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[dn][e] = 0.f;
     float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+    if (kFixed) {
+      m_run[0] = 0.5f * sp.cap2 + rs[0].top;
+      m_run[1] = 0.5f * sp.cap2 + rs[1].top;
+    }
 
     bool ok = true;
     for (int p = 0; p < npages; ++p) {
@@ -360,10 +421,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       {
         float xs[2][4];
         if (kScored)
-          cap_scores(sp, sacc, [&](int nt, int e) {
-            const int j = pos0 + nt * 8 + tig * 2 + (e & 1);
-            return j >= rs[e >> 1].low && j < vis[e >> 1];
-          });
+          step_logits<2, kFixed>(a, sp, cf, sacc, rs, vis[0], vis[1], pos0 + tig * 2,
+                         pos0 < all_lo || pos0 + 16 > all_hi);
         float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
@@ -371,38 +430,40 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           for (int e = 0; e < 4; ++e) {
             const int tok = nt * 8 + tig * 2 + (e & 1);
             if (kScored)
-              xs[nt][e] = scored_logit(rs[e >> 1], sacc[nt][e], pos0 + tok, vis[e >> 1]);
+              xs[nt][e] = sacc[nt][e];
             else
               xs[nt][e] = pos0 + tok < vis[e >> 1] ? sacc[nt][e] * sl2 : -INFINITY;
           }
           mx0 = fmaxf(mx0, fmaxf(xs[nt][0], xs[nt][1]));
           mx1 = fmaxf(mx1, fmaxf(xs[nt][2], xs[nt][3]));
         }
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
-        const bool up0 = mx0 > m_run[0] + 8.f, up1 = mx1 > m_run[1] + 8.f;
-        if (__any_sync(0xffffffffu, up0 || up1)) {
-          const float n0 = up0 ? mx0 : m_run[0], n1 = up1 ? mx1 : m_run[1];
-          // (a row that did not grow keeps factor 1: its maximum may still be -inf)
-          const float al0 = up0 ? fast_exp2(m_run[0] - n0) : 1.f;
-          const float al1 = up1 ? fast_exp2(m_run[1] - n1) : 1.f;
-          m_run[0] = n0;
-          m_run[1] = n1;
-          l_run[0] *= al0;
-          l_run[1] *= al1;
+        if (!kFixed) {
+          mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
+          mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
+          mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
+          mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
+          const bool up0 = mx0 > m_run[0] + 8.f, up1 = mx1 > m_run[1] + 8.f;
+          if (__any_sync(0xffffffffu, up0 || up1)) {
+            const float n0 = up0 ? mx0 : m_run[0], n1 = up1 ? mx1 : m_run[1];
+            // (a row that did not grow keeps factor 1: its maximum may still be -inf)
+            const float al0 = up0 ? fast_exp2(m_run[0] - n0) : 1.f;
+            const float al1 = up1 ? fast_exp2(m_run[1] - n1) : 1.f;
+            m_run[0] = n0;
+            m_run[1] = n1;
+            l_run[0] *= al0;
+            l_run[1] *= al1;
 #pragma unroll
-          for (int dn = 0; dn < 16; ++dn) {
-            o[dn][0] *= al0;
-            o[dn][1] *= al0;
-            o[dn][2] *= al1;
-            o[dn][3] *= al1;
+            for (int dn = 0; dn < 16; ++dn) {
+              o[dn][0] *= al0;
+              o[dn][1] *= al0;
+              o[dn][2] *= al1;
+              o[dn][3] *= al1;
+            }
           }
         }
         // a row with no visible key yet keeps m = -inf: use 0 as its reference
-        const float c0 = m_run[0] == -INFINITY ? 0.f : m_run[0];
-        const float c1 = m_run[1] == -INFINITY ? 0.f : m_run[1];
+        const float c0 = kFixed || m_run[0] == -INFINITY ? 0.f : m_run[0];
+        const float c1 = kFixed || m_run[1] == -INFINITY ? 0.f : m_run[1];
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
           xs[nt][0] = fast_exp2(xs[nt][0] - c0);
@@ -419,6 +480,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       }
 
       // O += P V (V rows read transposed); V of keys past the unit zeroed
+      if (kScored && pos0 < vlow) zero_v_rows(smem + (st - sbase), vlow - pos0, lane);
 #pragma unroll
       for (int dn = 0; dn < 16; dn += 2) {
         uint32_t b0, b1, b2, b3;
@@ -429,12 +491,6 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           b2 = mask_pair(b2, 2 * tig, valid);
           b1 = mask_pair(b1, 8 + 2 * tig, valid);
           b3 = mask_pair(b3, 8 + 2 * tig, valid);
-        }
-        if (kScored && pos0 < vlow) {  // the first page of a window
-          b0 = mask_pair_low(b0, 2 * tig, vlow - pos0);
-          b2 = mask_pair_low(b2, 2 * tig, vlow - pos0);
-          b1 = mask_pair_low(b1, 8 + 2 * tig, vlow - pos0);
-          b3 = mask_pair_low(b3, 8 + 2 * tig, vlow - pos0);
         }
         mma_bf16(o[dn], pa, b0, b1);
         mma_bf16(o[dn + 1], pa, b2, b3);
@@ -517,11 +573,12 @@ struct CfgP {
 };
 static_assert(CfgP::kSmem <= 232448, "shared memory per CTA");
 
-template <bool kScored>
+template <int kMode>
 __global__ void __launch_bounds__(CfgP::kThreads, 1)
     decode_pair_kernel(const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, AttnArgs a, Workspace ws) {
   using C = CfgP;
+  constexpr bool kScored = kMode != kPlain, kFixed = kMode == kFixedRef;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~(uintptr_t)1023);
@@ -559,6 +616,7 @@ __global__ void __launch_bounds__(CfgP::kThreads, 1)
   const uint64_t pol = l2_evict_first();  // K/V pages are read once
   const float sl2 = a.scale * kLog2e;
   const ScoreParams sp = score_params(a);
+  const CapForm cf = cap_form(sp);
   const int gid = lane >> 2, tig = lane & 3;
   const int mi = lane >> 3, rr = lane & 7;
   const int roff = 16 * tile;  // this warp's rows (heads of the group)
@@ -681,6 +739,10 @@ __global__ void __launch_bounds__(CfgP::kThreads, 1)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[dn][e] = 0.f;
     float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+    if (kFixed) {
+      m_run[0] = 0.5f * sp.cap2 + rs[0].top;
+      m_run[1] = 0.5f * sp.cap2 + rs[1].top;
+    }
 
     for (int j = 0; j < nsteps; ++j) {
       const uint32_t x = step_cnt + j;
@@ -721,10 +783,8 @@ __global__ void __launch_bounds__(CfgP::kThreads, 1)
       {
         float xs[4][4];
         if (kScored)
-          cap_scores(sp, sacc, [&](int nt, int e) {
-            const int j = pos0 + nt * 8 + tig * 2 + (e & 1);
-            return j >= rs[e >> 1].low && j < vis;
-          });
+          step_logits<4, kFixed>(a, sp, cf, sacc, rs, vis, vis, pos0 + tig * 2,
+                         pos0 < vlow || pos0 + 32 > vis);
         float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
@@ -732,36 +792,38 @@ __global__ void __launch_bounds__(CfgP::kThreads, 1)
           for (int e = 0; e < 4; ++e) {
             const int tok = nt * 8 + tig * 2 + (e & 1);
             if (kScored)
-              xs[nt][e] = scored_logit(rs[e >> 1], sacc[nt][e], pos0 + tok, vis);
+              xs[nt][e] = sacc[nt][e];
             else
               xs[nt][e] = pos0 + tok < vis ? sacc[nt][e] * sl2 : -INFINITY;
           }
           mx0 = fmaxf(mx0, fmaxf(xs[nt][0], xs[nt][1]));
           mx1 = fmaxf(mx1, fmaxf(xs[nt][2], xs[nt][3]));
         }
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
-        const bool up0 = mx0 > m_run[0] + 8.f, up1 = mx1 > m_run[1] + 8.f;
-        if (__any_sync(0xffffffffu, up0 || up1)) {
-          const float n0 = up0 ? mx0 : m_run[0], n1 = up1 ? mx1 : m_run[1];
-          const float al0 = up0 ? fast_exp2(m_run[0] - n0) : 1.f;
-          const float al1 = up1 ? fast_exp2(m_run[1] - n1) : 1.f;
-          m_run[0] = n0;
-          m_run[1] = n1;
-          l_run[0] *= al0;
-          l_run[1] *= al1;
+        if (!kFixed) {
+          mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
+          mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
+          mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
+          mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
+          const bool up0 = mx0 > m_run[0] + 8.f, up1 = mx1 > m_run[1] + 8.f;
+          if (__any_sync(0xffffffffu, up0 || up1)) {
+            const float n0 = up0 ? mx0 : m_run[0], n1 = up1 ? mx1 : m_run[1];
+            const float al0 = up0 ? fast_exp2(m_run[0] - n0) : 1.f;
+            const float al1 = up1 ? fast_exp2(m_run[1] - n1) : 1.f;
+            m_run[0] = n0;
+            m_run[1] = n1;
+            l_run[0] *= al0;
+            l_run[1] *= al1;
 #pragma unroll
-          for (int dn = 0; dn < 16; ++dn) {
-            o[dn][0] *= al0;
-            o[dn][1] *= al0;
-            o[dn][2] *= al1;
-            o[dn][3] *= al1;
+            for (int dn = 0; dn < 16; ++dn) {
+              o[dn][0] *= al0;
+              o[dn][1] *= al0;
+              o[dn][2] *= al1;
+              o[dn][3] *= al1;
+            }
           }
         }
-        const float c0 = m_run[0] == -INFINITY ? 0.f : m_run[0];
-        const float c1 = m_run[1] == -INFINITY ? 0.f : m_run[1];
+        const float c0 = kFixed || m_run[0] == -INFINITY ? 0.f : m_run[0];
+        const float c1 = kFixed || m_run[1] == -INFINITY ? 0.f : m_run[1];
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
           xs[nt][0] = fast_exp2(xs[nt][0] - c0);
@@ -782,6 +844,8 @@ __global__ void __launch_bounds__(CfgP::kThreads, 1)
 
       // O += P V (V rows read transposed), one k-step of 16 keys per page;
       // V of keys past the unit zeroed
+      if (kScored && pos0 < vlow)  // (the first page: the window starts in it)
+        zero_v_rows(smem + (sa[0] - sbase), vlow - pos0, lane);
 #pragma unroll
       for (int pg = 0; pg < 2; ++pg)
 #pragma unroll
@@ -795,13 +859,6 @@ __global__ void __launch_bounds__(CfgP::kThreads, 1)
             b2 = mask_pair(b2, 2 * tig, valid[pg]);
             b1 = mask_pair(b1, 8 + 2 * tig, valid[pg]);
             b3 = mask_pair(b3, 8 + 2 * tig, valid[pg]);
-          }
-          if (kScored && pos0 < vlow) {  // the first page of a window
-            const int first = vlow - pos0 - pg * kBlockSize;
-            b0 = mask_pair_low(b0, 2 * tig, first);
-            b2 = mask_pair_low(b2, 2 * tig, first);
-            b1 = mask_pair_low(b1, 8 + 2 * tig, first);
-            b3 = mask_pair_low(b3, 8 + 2 * tig, first);
           }
           mma_bf16(o[dn], pa[pg], b0, b1);
           mma_bf16(o[dn + 1], pa[pg], b2, b3);
@@ -864,30 +921,30 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(AttnArgs a, Wo
   combine_splits(a, ws, blockIdx.x * kWarpsPerBlock + (threadIdx.x >> 5), gridDim.x * kWarpsPerBlock);
 }
 
-template <bool kScored>
+template <int kMode>
 cudaError_t launch_one_tile(const AttnArgs& a, const Workspace& ws, int sms, cudaStream_t st) {
   using C = Cfg;
   static std::atomic<bool> attr[kMaxAttrDevices];
-  if (cudaError_t e = smem_attr_once(decode_kernel<kScored>, C::kSmem, attr)) return e;
+  if (cudaError_t e = smem_attr_once(decode_kernel<kMode>, C::kSmem, attr)) return e;
   const int G = a.hq / a.hkv;
   CUtensorMap tq, tk, tv;
   if (!make_rows_map(&tq, a.q, a.q_rows, a.hq, a.q_stride, G, 1) ||
       !make_cache_map(&tk, a.kc, a.num_blocks, a.hkv) ||
       !make_cache_map(&tv, a.vc, a.num_blocks, a.hkv))
     return cudaErrorInvalidValue;
-  return launch_dependent(decode_kernel<kScored>, dim3(sms), dim3(C::kThreads), C::kSmem, st, tq, tk,
+  return launch_dependent(decode_kernel<kMode>, dim3(sms), dim3(C::kThreads), C::kSmem, st, tq, tk,
                           tv, a, ws);
 }
 
-template <bool kScored>
+template <int kMode>
 cudaError_t launch_pair(const AttnArgs& a, const Workspace& ws, int sms, cudaStream_t st) {
   static std::atomic<bool> attr[kMaxAttrDevices];
-  if (cudaError_t e = smem_attr_once(decode_pair_kernel<kScored>, CfgP::kSmem, attr)) return e;
+  if (cudaError_t e = smem_attr_once(decode_pair_kernel<kMode>, CfgP::kSmem, attr)) return e;
   CUtensorMap tk, tv;  // (query rows: plain loads, 16-byte aligned by the API's checks)
   if (!make_cache_map(&tk, a.kc, a.num_blocks, a.hkv) ||
       !make_cache_map(&tv, a.vc, a.num_blocks, a.hkv))
     return cudaErrorInvalidValue;
-  return launch_dependent(decode_pair_kernel<kScored>, dim3(sms), dim3(CfgP::kThreads), CfgP::kSmem, st,
+  return launch_dependent(decode_pair_kernel<kMode>, dim3(sms), dim3(CfgP::kThreads), CfgP::kSmem, st,
                           tk, tv, a, ws);
 }
 
@@ -900,9 +957,13 @@ int decode_workers(int group, int kv_int8, int sms) {
 cudaError_t launch_decode(const AttnArgs& a, const Workspace& ws, int sms, cudaStream_t st) {
   const int G = a.hq / a.hkv;
   if (a.kv_int8) return launch_decode_i8(a, ws, sms, st);
-  if (a.score.on)
-    return G <= 16 ? launch_one_tile<true>(a, ws, sms, st) : launch_pair<true>(a, ws, sms, st);
-  return G <= 16 ? launch_one_tile<false>(a, ws, sms, st) : launch_pair<false>(a, ws, sms, st);
+  const bool one = G <= 16;
+  if (!a.score.on)
+    return one ? launch_one_tile<kPlain>(a, ws, sms, st) : launch_pair<kPlain>(a, ws, sms, st);
+  if (fixed_reference(a))
+    return one ? launch_one_tile<kFixedRef>(a, ws, sms, st)
+               : launch_pair<kFixedRef>(a, ws, sms, st);
+  return one ? launch_one_tile<kRunning>(a, ws, sms, st) : launch_pair<kRunning>(a, ws, sms, st);
 }
 
 cudaError_t launch_combine(const AttnArgs& a, const Workspace& ws, int sms, cudaStream_t st) {

@@ -146,43 +146,6 @@ __device__ __forceinline__ float fast_rcp(float x) {
   return y;
 }
 
-// The score modification of a scored call, from the raw product s = q.K to a
-// logit in log2 units: s * lin without a cap (lin = scale * log2(e)); with
-// one, cap2 * tanh(x), x = s * scale / cap, cap2 = cap * log2(e), in two forms:
-//   capped_exp, any x: tanh(x) = 1 - 2 / (1 + e^(2x)), one exponential (its
-//     overflow and underflow give +-1) and one reciprocal; an absolute error
-//     of about 2^-22 of the cap, whatever the size of x;
-//   capped_poly, |x| <= 1: x times a degree-6 polynomial in x^2 with constant
-//     term 1, fitted to tanh(x) / x for the smallest largest relative error
-//     (5.5e-8, 1.6e-7 as computed in fp32): a relative error, so that a cap
-//     far above the logits leaves their own precision.
-// The kernels take capped_poly where a warp's scores allow it.
-struct ScoreParams {
-  float lin, k, mul, cap2;  // k = scale / cap, mul = 2 log2(e) k
-  bool cap;
-};
-__device__ __forceinline__ ScoreParams score_params(const AttnArgs& a) {
-  ScoreParams p;
-  p.cap = a.score.softcap > 0.f;
-  p.lin = a.scale * kLog2e;
-  p.k = p.cap ? a.scale / a.score.softcap : 0.f;
-  p.mul = 2.f * kLog2e * p.k;
-  p.cap2 = a.score.softcap * kLog2e;
-  return p;
-}
-__device__ __forceinline__ float capped_exp(float s, const ScoreParams& p) {
-  return fmaf(-2.f * p.cap2, fast_rcp(1.f + fast_exp2(s * p.mul)), p.cap2);
-}
-__device__ __forceinline__ float capped_poly(float s, const ScoreParams& p) {
-  const float x = s * p.k, u = x * x;
-  float c = fmaf(0.0010582346f, u, -0.0062592492f);
-  c = fmaf(c, u, 0.0203596614f);
-  c = fmaf(c, u, -0.0534986593f);
-  c = fmaf(c, u, 0.1332640797f);
-  c = fmaf(c, u, -0.3333298564f);
-  return s * p.lin * fmaf(c, u, 1.f);
-}
-
 // max(a, b, c) in one instruction
 __device__ __forceinline__ float max3f(float a, float b, float c) {
   float d;

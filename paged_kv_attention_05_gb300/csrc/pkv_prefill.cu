@@ -48,6 +48,7 @@
 
 #include "pkv_combine.cuh"
 #include "pkv_device.cuh"
+#include "pkv_score.cuh"
 
 namespace pkv {
 namespace {
@@ -102,10 +103,8 @@ struct Item {
   int ctx, nkv, base, prefix;  // first key of the tiles; keys every row sees (scored)
 };
 
-// What an instance does to the scores.  kFixed: a cap of at most
-// kFixedCap2 log2 units (see fixed-reference softmax below).
+// What an instance does to the scores.  kFixedCap: fixed_reference() holds.
 enum Cap { kNoCap, kAnyCap, kFixedCap };
-constexpr float kFixedCap2 = 80.f;
 
 // First key of the j-th tile an item processes.  With a distance bias the
 // tiles run from the diagonal back: the bias falls with distance, so a row's
@@ -248,52 +247,6 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
 }
 
-// The cap's forms (x = s * scale / cap).  Up to |x| = 1/2, s times a
-// polynomial of degree 3 in s^2 whose coefficients hold the powers of scale /
-// cap, two columns at a time (7.2e-7 relative error as computed; fitted like
-// capped_poly); past that capped_exp.  Where scale / cap is so small or large
-// that a power of it or of s could leave fp32's range (a cap of thousands),
-// capped_poly serves |x| <= 1.
-struct CapForm {
-  f32x2 a[4];   // pairs: formed at each use they cost two moves an operation
-  float limit;  // largest s^2; -1: not in range
-};
-__device__ __forceinline__ CapForm cap_form(const ScoreParams& sp) {
-  CapForm c;
-  const float k2 = sp.k * sp.k;
-  const bool in_range = sp.k >= 0x1p-20f && sp.k <= 0x1p20f;
-  const float a[4] = {sp.lin, sp.lin * -0.33328161f * k2, sp.lin * 0.13205360f * k2 * k2,
-                      sp.lin * -0.04475065f * k2 * k2 * k2};
-#pragma unroll
-  for (int n = 0; n < 4; ++n) c.a[n] = pair(a[n], a[n]);
-  c.limit = in_range ? 0.25f / k2 : -1.f;
-  return c;
-}
-// s -> cap2 * tanh(x) + nm for 32 columns, by one form (0: polynomial, 1:
-// exponential); the largest s^2 max'ed into big (form 0).
-template <int kForm>
-__device__ __forceinline__ void cap32(float (&s)[32], const ScoreParams& sp, const CapForm& cf,
-                                      float nm, float& big) {
-  if (kForm == 1) {
-    const float c2 = sp.cap2 + nm;
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      s[i] = fmaf(-2.f * sp.cap2, fast_rcp(1.f + fast_exp2(s[i] * sp.mul)), c2);
-    return;
-  }
-  const f32x2 nm2 = pair(nm, nm);
-  float m0 = 0.f, m1 = 0.f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const f32x2 v = pair(s[2 * i], s[2 * i + 1]), w = mul2(v, v);
-    float w0, w1;
-    split(w, w0, w1);
-    if (i & 1) m1 = max3f(m1, w0, w1); else m0 = max3f(m0, w0, w1);
-    const f32x2 q = fma2(fma2(fma2(w, cf.a[3], cf.a[2]), w, cf.a[1]), w, cf.a[0]);
-    split(fma2(v, q, nm2), s[2 * i], s[2 * i + 1]);
-  }
-  big = max3f(big, m0, m1);
-}
 // Adds the bias slope2 * (i - d0) to 32 columns (d0: distance of the first
 // one's key) or, without a cap, forms s * lin + nm + bias: four pairs stepped
 // by eight columns (three additions at most: their roundings stay below 2^-22
@@ -323,7 +276,7 @@ __device__ __forceinline__ void bias32(float (&s)[32], float lin, float nm, floa
 template <Cap kCap, bool kBias, bool kSym, int kForm>
 __device__ __forceinline__ void logits32(float (&s)[32], const ScoreParams& sp, const CapForm& cf,
                                          float nm, float slope2, float d0, float& big) {
-  if (kCap != kNoCap) cap32<kForm>(s, sp, cf, nm, big);
+  if (kCap != kNoCap) cap_values<kForm>(s, sp, cf, nm, big);
   if (kBias) {
     bias32<kCap != kNoCap, kSym>(s, sp.lin, nm, slope2, d0);
   } else if (kCap == kNoCap) {
@@ -759,18 +712,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int last = max(rpos, it.prefix - 1);           // last visible key
       const int first = first_key(rpos, a.score.window);   // first visible key
       const float slope2 = kBias ? __ldg(a.score.slopes + (x ? it.hb : it.ha)) * kLog2e : 0.f;
-      // The reference (log2 units) that the exponentials are taken against.
-      // Fixed: a capped logit lies within +-cap2, so with half the cap and the
-      // row's largest bias (0, its own key's, or with a negative slope its
-      // furthest key's) exp2(y - ref) of the key of that bias lies within
-      // 2^(-3/2 cap2) and 2^(cap2 / 2), inside fp32's and bf16's exponents for
-      // cap2 <= 80 (caps up to 55) with room for the sums.  Else the running
-      // maximum, rounded up to a whole number, so that rescaling is exact; it
-      // follows the scores only when a block's sum passes kMaxSum: bf16 keeps
-      // its precision over fp32's exponents, so a reference below the maximum
-      // costs none, and 2^40 leaves the sums room to 2^127.
-      float ref = kCap == kFixedCap ? 0.5f * sp.cap2 - fminf(0.f, slope2) *
-                                          (float)max(rpos - first, last - rpos)
+      // The reference (log2 units) that the exponentials are taken against:
+      // fixed (see fixed_reference), or the running maximum, rounded up to a
+      // whole number, so that rescaling is exact; it follows the scores only
+      // when a block's sum passes kMaxSum: bf16 keeps its precision over fp32's
+      // exponents, so a reference below the maximum costs none, and 2^40 leaves
+      // the sums room to 2^127.
+      float ref = kCap == kFixedCap ? 0.5f * sp.cap2 + max_bias(slope2, rpos, first, last)
                                     : -INFINITY;
       float l = 0.f;
       if (form == 1 && --hold <= 0) form = 0;
@@ -1192,8 +1140,7 @@ cudaError_t launch_prefill(const AttnArgs& a, const Workspace& ws, int sms, cuda
   if (!sc.on) return launch_prefill_as<false, kNoCap, false, false>(a, ws, sms, st);
   const bool bias = sc.slopes != nullptr, sym = bias && sc.prefix != nullptr;
   if (sc.softcap > 0.f) {
-    const float k = a.scale / sc.softcap;  // (its sixth power in the polynomial form)
-    if (sc.softcap * dev::kLog2e <= kFixedCap2 && k >= 0x1p-20f && k <= 0x1p20f)
+    if (dev::fixed_reference(a))
       return sym    ? launch_prefill_as<true, kFixedCap, true, true>(a, ws, sms, st)
              : bias ? launch_prefill_as<true, kFixedCap, true, false>(a, ws, sms, st)
                     : launch_prefill_as<true, kFixedCap, false, false>(a, ws, sms, st);

@@ -346,9 +346,11 @@ cudaError_t launch_rope_as(const RopeArgs& a, int sms, cudaStream_t st) {
   constexpr int kWarps = kRopeThreads / 32;
   const int rows = a.hq + 2 * a.hkv;
   const int64_t streamed = a.n_tokens * ((rows + 4 * kRopeGroups - 1) / (4 * kRopeGroups));
-  // The streaming form once its units give every resident warp one; a step of
-  // fewer tokens is spread over four times the warps instead.
-  if (streamed >= (int64_t)sms * kRopeCtas * kWarps && streamed < (1LL << 30)) {
+  // The streaming form from ten units an SM (sixteen warps are resident); a
+  // step of fewer tokens is spread over four times the warps instead.  Measured
+  // (64 / 8 heads, norms; straight, streamed, us): 128 tokens 3.0, 4.7; 256
+  // (8.4 units an SM) 4.6, 4.8; 400 (13) 8.2, 6.0; 1600 22.5, 17.8.
+  if (streamed >= (int64_t)sms * 10 && streamed < (1LL << 30)) {
     static std::atomic<bool> attr[kMaxAttrDevices];
     auto* kernel = rope_stream_kernel<kInt8, kNorm, kInterleaved>;
     if (cudaError_t e = smem_attr_once(kernel, kRopeSmem, attr)) return e;
