@@ -136,15 +136,19 @@ __device__ __forceinline__ uint32_t mask_pair(uint32_t v, int tok_lo, int valid)
   const uint32_t hi = tok_lo + 1 < valid ? 0xFFFF0000u : 0u;
   return v & (lo | hi);
 }
-// Zeroes the V rows of a page in shared memory (st: its stage) whose slots are
-// below `first`: the keys before a window in its first page, whose V must not
-// reach the product.  (By every warp that reads the page, each before its own
-// reads; once a unit, where masks in the product's loop cost every step.)
-__device__ __forceinline__ void zero_v_rows(uint8_t* st, int first, int lane) {
-  const int rows = min(first, kBlockSize);
-  for (int i = lane; i < rows * 16; i += 32)
-    *reinterpret_cast<uint4*>(st + (2 + (i & 1)) * kBox + (i >> 4) * 128 + ((i >> 1) & 7) * 16) =
-        make_uint4(0, 0, 0, 0);
+// Zeroes the V rows of a page in shared memory (st: its stage) outside slots
+// first .. end - 1: the keys before a window in its first page and past the
+// unit in its last, whose V must not reach the product.  (By every warp that
+// reads the page, each before its own reads; at most twice a unit, where masks
+// in the product's loop cost every step: 117 against 98 us for 32 decodes of
+// 32,769 keys with one KV head.)
+__device__ __forceinline__ void zero_v_rows(uint8_t* st, int first, int end, int lane) {
+  for (int i = lane; i < kBlockSize * 16; i += 32) {
+    const int row = i >> 4;
+    if (row < first || row >= end)
+      *reinterpret_cast<uint4*>(st + (2 + (i & 1)) * kBox + row * 128 + ((i >> 1) & 7) * 16) =
+          make_uint4(0, 0, 0, 0);
+  }
   fence_async_smem();  // (the stage is refilled by TMA)
   __syncwarp();
 }
@@ -153,7 +157,7 @@ __device__ __forceinline__ void zero_v_rows(uint8_t* st, int first, int lane) {
 // fixed_reference() holds for.  (For the warp pairs below, whose chain of
 // dependent steps sets the pace, the fixed reference takes the maximum, its
 // four exchanges and the rescaling vote out of each step: 32 decodes of 32,769
-// keys, one KV head, cap 50: 117 -> X us.)
+// keys, one KV head, cap 50: 117 -> 98 us with the two changes.)
 enum Mode { kPlain, kRunning, kFixedRef };
 
 // What a scored call does to one query row of a decode unit.
@@ -480,13 +484,14 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       }
 
       // O += P V (V rows read transposed); V of keys past the unit zeroed
-      if (kScored && pos0 < vlow) zero_v_rows(smem + (st - sbase), vlow - pos0, lane);
+      if (kScored && (pos0 < vlow || valid < kBlockSize))
+        zero_v_rows(smem + (st - sbase), vlow - pos0, valid, lane);
 #pragma unroll
       for (int dn = 0; dn < 16; dn += 2) {
         uint32_t b0, b1, b2, b3;
         ldsm_x4_t(st + (2 + (dn >> 3)) * kBox + sw128(rr + ((mi & 1) << 3), (dn & 7) + (mi >> 1)),
                   b0, b1, b2, b3);
-        if (valid < 16) {
+        if (!kScored && valid < 16) {
           b0 = mask_pair(b0, 2 * tig, valid);
           b2 = mask_pair(b2, 2 * tig, valid);
           b1 = mask_pair(b1, 8 + 2 * tig, valid);
@@ -844,8 +849,10 @@ __global__ void __launch_bounds__(CfgP::kThreads, 1)
 
       // O += P V (V rows read transposed), one k-step of 16 keys per page;
       // V of keys past the unit zeroed
-      if (kScored && pos0 < vlow)  // (the first page: the window starts in it)
-        zero_v_rows(smem + (sa[0] - sbase), vlow - pos0, lane);
+      if (kScored && (pos0 < vlow || valid[1] < kBlockSize)) {
+        zero_v_rows(smem + (sa[0] - sbase), vlow - pos0, valid[0], lane);
+        if (two) zero_v_rows(smem + (sa[1] - sbase), vlow - pos0 - kBlockSize, valid[1], lane);
+      }
 #pragma unroll
       for (int pg = 0; pg < 2; ++pg)
 #pragma unroll
@@ -854,7 +861,7 @@ __global__ void __launch_bounds__(CfgP::kThreads, 1)
           ldsm_x4_t(sa[pg] + (2 + (dn >> 3)) * kBox +
                         sw128(rr + ((mi & 1) << 3), (dn & 7) + (mi >> 1)),
                     b0, b1, b2, b3);
-          if (valid[pg] < 16) {
+          if (!kScored && valid[pg] < 16) {
             b0 = mask_pair(b0, 2 * tig, valid[pg]);
             b2 = mask_pair(b2, 2 * tig, valid[pg]);
             b1 = mask_pair(b1, 8 + 2 * tig, valid[pg]);
