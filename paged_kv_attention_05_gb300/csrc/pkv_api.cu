@@ -165,6 +165,35 @@ Sizes sizes_for(int64_t reqs, int64_t q_rows, int64_t bt_width, int hq, int hkv)
   return z;
 }
 
+void set_score_form(AttnArgs& a) {
+  ScoreArgs& s = a.score;
+  const double log2e = 1.4426950408889634, lin = a.scale * log2e;
+  auto both = [](double x) {
+    const float f = (float)x;
+    uint32_t u;
+    memcpy(&u, &f, 4);
+    return (unsigned long long)u << 32 | u;
+  };
+  s.lin = (float)lin;
+  s.lin2 = both(lin);
+  if (!(s.softcap > 0.f)) return;
+  const double k = (double)a.scale / s.softcap, k2 = k * k;
+  s.k = (float)k;
+  s.mul = (float)(2 * log2e * k);
+  s.cap2 = (float)(s.softcap * log2e);
+  const double c2[3] = {1, -0.33324572443962097, 0.12876421213150024};
+  const double c3[4] = {1, -0.33328160643577576, 0.13205359876155853, -0.0447506457567215};
+  double p = lin;
+  for (int n = 0; n < 4; ++n, p *= k2) {
+    if (n < 3) s.deg2[n] = both(p * c2[n]);
+    s.deg3[n] = both(p * c3[n]);
+  }
+  if (k >= 0x1p-20 && k <= 0x1p20) {
+    s.limit2 = (float)(0.0625 / k2);
+    s.limit3 = (float)(0.25 / k2);
+  }
+}
+
 // Room for the plan's one-wave split of a small batch: as many decode units
 // as the decode grid has workers, each with up to one unit's query rows of
 // partial results (the plan takes a chunk shorter than kMinChunk only where
@@ -506,6 +535,7 @@ int run_locked(DeviceState* s, const void* q, int64_t q_row_stride, const void* 
   a.k_scale = kv_int8 ? k_scale : 1.f;
   a.v_scale = kv_int8 ? v_scale : 1.f;
   a.score = score;
+  if (score.on) set_score_form(a);
   // Decode first.  When the step also has prefill work, the decode grid
   // leaves some SMs to it at once and the prefill grid (its programmatic
   // dependent) runs its items there beside the decode units; the prefill

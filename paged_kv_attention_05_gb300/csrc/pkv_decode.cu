@@ -190,8 +190,7 @@ __device__ __forceinline__ RowScore row_score(const AttnArgs& a, int r, int pos,
 // its rows see, since the others may hold anything.
 // Fixed reference: minus it.
 template <int kTiles, bool kFixed>
-__device__ __forceinline__ void step_logits(const AttnArgs& a, const ScoreParams& sp,
-                                            const CapForm& cf, float (&s2)[kTiles][4],
+__device__ __forceinline__ void step_logits(const ScoreArgs& sp, float (&s2)[kTiles][4],
                                             const RowScore (&rs)[2], int vis0, int vis1, int key0,
                                             bool any) {
   float(&s)[4 * kTiles] = reinterpret_cast<float(&)[4 * kTiles]>(s2);
@@ -200,7 +199,7 @@ __device__ __forceinline__ void step_logits(const AttnArgs& a, const ScoreParams
     return (i & 2) ? j >= rs[1].low && j < vis1 : j >= rs[0].low && j < vis0;
   };
   const float nm = kFixed ? -0.5f * sp.cap2 : 0.f;
-  if (kFixed || sp.cap) {
+  if (kFixed || sp.softcap > 0.f) {
     float m0 = 0.f, m1 = 0.f;
     if (any) {
 #pragma unroll
@@ -213,19 +212,19 @@ __device__ __forceinline__ void step_logits(const AttnArgs& a, const ScoreParams
     }
     const float m = fmaxf(m0, m1);
     float big = 0.f;
-    if (__all_sync(0xffffffffu, m * m <= cf.limit)) {
-      cap_values<0>(s, sp, cf, nm, big);
-    } else if (!kFixed && cf.limit < 0.f && __all_sync(0xffffffffu, m * sp.k <= 1.f)) {
+    if (__all_sync(0xffffffffu, m * m <= sp.limit3)) {
+      cap_values<kDeg3>(s, sp, nm, big);
+    } else if (!kFixed && sp.limit3 < 0.f && __all_sync(0xffffffffu, m * sp.k <= 1.f)) {
 #pragma unroll
       for (int i = 0; i < 4 * kTiles; ++i) s[i] = capped_poly(s[i], sp);
     } else {
-      cap_values<1>(s, sp, cf, nm, big);
+      cap_values<kExp>(s, sp, nm, big);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 4 * kTiles; ++i) s[i] *= sp.lin;
   }
-  if (a.score.slopes) {
+  if (sp.slopes) {
     const float d[2] = {(float)(rs[0].pos - key0), (float)(rs[1].pos - key0)};
 #pragma unroll
     for (int i = 0; i < 4 * kTiles; ++i) {
@@ -281,8 +280,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
   const int n_units = ws.hdr->n_dec_units;
   const uint64_t pol = l2_evict_first();  // K/V pages are read once
   const float sl2 = a.scale * kLog2e;
-  const ScoreParams sp = score_params(a);
-  const CapForm cf = cap_form(sp);
+  const ScoreArgs& sp = a.score;
   const int gid = lane >> 2, tig = lane & 3;
   const int mi = lane >> 3, rr = lane & 7;
   uint32_t page_cnt = 0;
@@ -425,7 +423,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       {
         float xs[2][4];
         if (kScored)
-          step_logits<2, kFixed>(a, sp, cf, sacc, rs, vis[0], vis[1], pos0 + tig * 2,
+          step_logits<2, kFixed>(sp, sacc, rs, vis[0], vis[1], pos0 + tig * 2,
                          pos0 < all_lo || pos0 + 16 > all_hi);
         float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
@@ -620,8 +618,7 @@ __global__ void __launch_bounds__(CfgP::kThreads, 1)
   const int n_units = ws.hdr->n_dec_units;
   const uint64_t pol = l2_evict_first();  // K/V pages are read once
   const float sl2 = a.scale * kLog2e;
-  const ScoreParams sp = score_params(a);
-  const CapForm cf = cap_form(sp);
+  const ScoreArgs& sp = a.score;
   const int gid = lane >> 2, tig = lane & 3;
   const int mi = lane >> 3, rr = lane & 7;
   const int roff = 16 * tile;  // this warp's rows (heads of the group)
@@ -788,7 +785,7 @@ __global__ void __launch_bounds__(CfgP::kThreads, 1)
       {
         float xs[4][4];
         if (kScored)
-          step_logits<4, kFixed>(a, sp, cf, sacc, rs, vis, vis, pos0 + tig * 2,
+          step_logits<4, kFixed>(sp, sacc, rs, vis, vis, pos0 + tig * 2,
                          pos0 < vlow || pos0 + 32 > vis);
         float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll

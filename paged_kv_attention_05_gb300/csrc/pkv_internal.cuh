@@ -166,7 +166,16 @@ struct ScoreArgs {
   int window = 0;                   // 0: none
   const float* slopes = nullptr;    // [hq], or null
   const int32_t* prefix = nullptr;  // [num_reqs], or null
+  // what the kernels take of scale and softcap (pkv_score.cuh; set_score_form):
+  // as kernel arguments they sit in the constant bank, pairs ready for the
+  // packed instructions, and take no registers
+  float lin = 0.f, k = 0.f, mul = 0.f, cap2 = 0.f;
+  float limit2 = -1.f, limit3 = -1.f;
+  unsigned long long deg2[3] = {}, deg3[4] = {}, lin2 = 0;
 };
+struct AttnArgs;
+// Fills those from a.scale and a.score.softcap.
+void set_score_form(AttnArgs& a);
 
 // First key any row of a request sees, rounded down to its page: the keys a
 // decode request's units cover start here (ctx = keys before its first row).

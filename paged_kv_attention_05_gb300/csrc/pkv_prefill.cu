@@ -55,7 +55,14 @@ namespace {
 
 using namespace dev;
 
-constexpr int kThreads = 448;                     // 14 warps
+// Warps: producer, MMA issuer, softmax, four of epilogue.  8 softmax warps in
+// the plain call (two a row quarter, both query tiles in turn) and in scored
+// calls with a running maximum (one a row quarter and tile), 16 with a fixed
+// reference (two a row quarter and tile).
+__host__ __device__ constexpr int soft_warps(bool fixed_ref) { return fixed_ref ? 16 : 8; }
+__host__ __device__ constexpr int threads_of(bool fixed_ref) {
+  return 32 * (2 + soft_warps(fixed_ref) + 4);  // 448, 704
+}
 constexpr int kStages = 2;
 constexpr int kTileK = 128;                       // keys per KV tile
 constexpr int kHalfBytes = 128 * 128;             // 128 rows x 64 bf16
@@ -252,18 +259,18 @@ __device__ __forceinline__ void tmem_wait_st() {
 // by eight columns (three additions at most: their roundings stay below 2^-22
 // of the bias).  kSym: a column past d0 counts its distance too.
 template <bool kCapped, bool kSym>
-__device__ __forceinline__ void bias32(float (&s)[32], float lin, float nm, float slope2,
-                                       float d0) {
+__device__ __forceinline__ void bias32(float (&s)[32], const ScoreArgs& sp, float nm,
+                                       float slope2, float d0) {
   f32x2 b[4];
   const float b0 = kCapped ? -slope2 * d0 : fmaf(-slope2, d0, nm);
-  const f32x2 b8 = pair(8.f * slope2, 8.f * slope2), lin2 = pair(lin, lin);
+  const f32x2 b8 = pair(8.f * slope2, 8.f * slope2);
 #pragma unroll
   for (int k = 0; k < 4; ++k)
     b[k] = pair(fmaf(slope2, 2.f * k, b0), fmaf(slope2, 2.f * k + 1.f, b0));
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const f32x2 v = pair(s[2 * i], s[2 * i + 1]);
-    split(kCapped ? add2(v, b[i & 3]) : fma2(v, lin2, b[i & 3]), s[2 * i], s[2 * i + 1]);
+    split(kCapped ? add2(v, b[i & 3]) : fma2(v, sp.lin2, b[i & 3]), s[2 * i], s[2 * i + 1]);
     if (i < 12) b[i & 3] = add2(b[i & 3], b8);
   }
   if (kSym) {
@@ -273,30 +280,30 @@ __device__ __forceinline__ void bias32(float (&s)[32], float lin, float nm, floa
 }
 // 32 raw products s = q.K (columns of one row) to logits in log2 units + nm,
 // the cap by the given form.
-template <Cap kCap, bool kBias, bool kSym, int kForm>
-__device__ __forceinline__ void logits32(float (&s)[32], const ScoreParams& sp, const CapForm& cf,
-                                         float nm, float slope2, float d0, float& big) {
-  if (kCap != kNoCap) cap_values<kForm>(s, sp, cf, nm, big);
+template <Cap kCap, bool kBias, bool kSym, Form kForm>
+__device__ __forceinline__ void logits32(float (&s)[32], const ScoreArgs& sp, float nm,
+                                         float slope2, float d0, float& big) {
+  if (kCap != kNoCap) cap_values<kForm>(s, sp, nm, big);
   if (kBias) {
-    bias32<kCap != kNoCap, kSym>(s, sp.lin, nm, slope2, d0);
+    bias32<kCap != kNoCap, kSym>(s, sp, nm, slope2, d0);
   } else if (kCap == kNoCap) {
-    const f32x2 lin2 = pair(sp.lin, sp.lin), nm2 = pair(nm, nm);
+    const f32x2 nm2 = pair(nm, nm);
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-      split(fma2(pair(s[2 * i], s[2 * i + 1]), lin2, nm2), s[2 * i], s[2 * i + 1]);
+      split(fma2(pair(s[2 * i], s[2 * i + 1]), sp.lin2, nm2), s[2 * i], s[2 * i + 1]);
   }
 }
-// The same for any block: the form by the warp's visible scores, -inf outside
-// low <= i <= lim when `edge` (columns there may hold anything).
-template <Cap kCap, bool kBias, bool kSym>
-__device__ __forceinline__ void logits32_any(float (&s)[32], const ScoreParams& sp,
-                                             const CapForm& cf, float nm, bool edge, int lim,
-                                             int low, bool valid_row, float slope2, float d0) {
+// The same, the form of the cap by the warp's visible scores.  kEdge: -inf
+// outside low <= i <= lim (columns there may hold anything).
+template <Cap kCap, bool kBias, bool kSym, bool kEdge>
+__device__ __forceinline__ void logits32_any(float (&s)[32], const ScoreArgs& sp, float nm,
+                                             int lim, int low, bool valid_row, float slope2,
+                                             float d0) {
   float big = 0.f;
   if (kCap == kNoCap) {
-    logits32<kCap, kBias, kSym, 0>(s, sp, cf, nm, slope2, d0, big);
+    logits32<kCap, kBias, kSym, kDeg2>(s, sp, nm, slope2, d0, big);
   } else {
-    if (edge) {
+    if (kEdge) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) s[i] = i <= lim && i >= low ? s[i] : 0.f;
     }
@@ -307,17 +314,19 @@ __device__ __forceinline__ void logits32_any(float (&s)[32], const ScoreParams& 
       m1 = max3f(m1, fabsf(s[i + 2]), fabsf(s[i + 3]));
     }
     const float m = valid_row ? fmaxf(m0, m1) : 0.f;
-    if (__all_sync(0xffffffffu, m * m <= cf.limit)) {
-      logits32<kCap, kBias, kSym, 0>(s, sp, cf, nm, slope2, d0, big);
+    if (__all_sync(0xffffffffu, m * m <= sp.limit2)) {
+      logits32<kCap, kBias, kSym, kDeg2>(s, sp, nm, slope2, d0, big);
+    } else if (__all_sync(0xffffffffu, m * m <= sp.limit3)) {
+      logits32<kCap, kBias, kSym, kDeg3>(s, sp, nm, slope2, d0, big);
     } else if (kCap == kAnyCap && __all_sync(0xffffffffu, m * sp.k <= 1.f)) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) s[i] = capped_poly(s[i], sp) + nm;
-      if (kBias) bias32<true, kSym>(s, sp.lin, nm, slope2, d0);
+      if (kBias) bias32<true, kSym>(s, sp, nm, slope2, d0);
     } else {
-      logits32<kCap, kBias, kSym, 1>(s, sp, cf, nm, slope2, d0, big);
+      logits32<kCap, kBias, kSym, kExp>(s, sp, nm, slope2, d0, big);
     }
   }
-  if (edge) {
+  if (kEdge) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) s[i] = i <= lim && i >= low ? s[i] : -INFINITY;
   }
@@ -362,7 +371,7 @@ __device__ __forceinline__ float total(const f32x2 (&rs)[2]) {
 // kScored: a window, a prefix (runtime), and per instance a cap, a bias (kSym:
 // that may meet keys after a row's position, with a prefix).
 template <bool kScored, Cap kCap, bool kBias, bool kSym>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads_of(kCap == kFixedCap), 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, AttnArgs a, Workspace ws) {
   // This grid is the programmatic dependent of the decode grid, which
@@ -372,6 +381,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the kernels before it wrote is read through L2 (ld.global.cg).  The split
   // decode results are merged at the end, once the decode grid has finished
   // (so this grid finishing implies that every kernel before it has).
+  constexpr int kSoft = soft_warps(kCap == kFixedCap), kThreads = threads_of(kCap == kFixedCap);
+  constexpr int kHalves = kScored ? kSoft / 8 : 2;  // softmax warps that share a row
   const int n_pre = __ldcg(&ws.hdr->n_pre_entries);
   if (n_pre == 0) {  // a step without prefill work (every CTA agrees)
     grid_dep_wait();
@@ -401,11 +412,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) mbar_init(bar(i), 1);
     for (int x = 0; x < 2; ++x) {
-      mbar_init(bar(B_PF + x), kScored ? 4 : 8);  // one arrival per softmax warp of the tile
+      mbar_init(bar(B_PF + x), 4 * kHalves);  // one arrival per softmax warp of the tile
       mbar_init(bar(B_OE + x), 4);  // one arrival per epilogue warp
-      mbar_init(bar(B_LF + x), kScored ? 4 : 8);  // one arrival per softmax warp of the tile
-      mbar_init(sbase + kOffBarLF1 + 8 * x, kScored ? 4 : 8);
-      mbar_init(bar(B_IE + x), 1 + 8 + 4);  // MMA warp, softmax warps, epilogue warps
+      mbar_init(bar(B_LF + x), 4 * kHalves);  // one arrival per softmax warp of the tile
+      mbar_init(sbase + kOffBarLF1 + 8 * x, 4 * kHalves);
+      mbar_init(bar(B_IE + x), 1 + kSoft + 4);  // MMA warp, softmax warps, epilogue warps
     }
     for (int i = 0; i < 4; ++i) mbar_init(bar(B_XP + i), 2);
     ctl[1] = 0;
@@ -659,42 +670,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (kScored && warp < 10) {
+  } else if (kScored && warp < 2 + kSoft) {
     if constexpr (kScored) {
-    // ------------- softmax of a scored call: a row per thread, four warps per tile -------------
-    // Warps 2-5 serve tile a of every item, 6-9 tile b, each its 32 rows
-    // whole, in four blocks of 32 columns; the two tiles' softmaxes run beside
-    // each other, and no row needs another warp's values.  P of a block goes
-    // where its scores began (16 packed columns).  Two paths:
-    //   quick: pairs of blocks that every row of the warp sees, the running
-    //     maximum at hand and the form of the cap foreseen: straight code,
-    //     checked at its end, and redone if the check fails (P has not left
-    //     the registers, the scores are still in TMEM);
-    //   block: any block of 32 columns, masks, new maxima, in a loop.
-    // 8 prompts of 2048 tokens, 64 heads over 8: without options 452 us,
-    // bias 475, cap 608, window of 1024 389 (plain call 500; with
-    // scores of three times the size its repeated maxima take it to 648).
-    // The cap is bound by the two warps a sub-partition has for its
-    // arithmetic: five packed operations a pair of scores where the others
-    // take one to two.  Measured and not kept: a row's 128 or 64 columns in
-    // straight code with all forms of the cap in place (730 to 2229 us for
-    // the cap: instruction-cache misses); two warps a row as in the plain
-    // call, in loops of 32 columns (cap 573, bias 718); two warps a row and
-    // tile, 16 in all (cap 537 to 548, bias 794 to 825: 80 registers a thread
-    // spill); four warps a row (cap 566, bias 746).
-    const int x = (warp - 2) >> 2;  // my query tile
+    // ------------- softmax of a scored call: a set of warps for each query tile -------------
+    // The first half of the softmax warps serves tile a of every item, the
+    // second tile b: the two tiles' softmaxes run beside each other.  P of a
+    // block of 32 columns goes where its scores began (16 packed columns).
+    //   Fixed reference: 16 warps, each 64 columns (hf) of its 32 rows in two
+    //     rounds; nothing passes between the warps of a row.
+    //   Running maximum: 8 warps, each its 32 rows whole, so that no row needs
+    //     another warp's values.  Quick path: pairs of blocks that every row of
+    //     the warp sees, the maximum at hand and the form of the cap foreseen:
+    //     straight code, checked at its end, and redone if the check fails (P
+    //     has not left the registers, the scores are still in TMEM).  Block
+    //     path: any block, masks, new maxima, in a loop.
+    // 8 prompts of 2048 tokens, 64 heads over 8, us: without options 452, bias
+    // 475, cap 526 (scores past a quarter of the cap 602, past half 760),
+    // window of 1024 389; the plain call 500 (with scores of three times the
+    // size its repeated maxima take it to 648).  Bound, with the cap, by the
+    // softmax warps' issue slots (a packed operation takes two) and the chain S
+    // -> P -> P.V of a tile.  Measured and not kept, for the cap: a row's 128
+    // or 64 columns in straight code with all of its forms in place (730 to
+    // 2229: instruction-cache misses); two warps a row as in the plain call
+    // (573); four warps a row and tile (566); a row per thread (530 to 608); a
+    // quick path checked at its end with 16 warps (584); prefetched rounds of 16
+    // columns (601).  For the bias: two warps a row that exchange maxima (718
+    // to 825: 80 registers a thread spill).
+    const int x = (warp - 2) / (4 * kHalves);  // my query tile
+    const int hf = kHalves == 1 ? 0 : ((warp - 2) >> 2) & 1;
+    const int b0 = 2 * hf;  // my first block of 32 columns
     const int qd = warp & 3;
     const int row = qd * 32 + lane;  // == TMEM lane
     const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
     float* lsum = reinterpret_cast<float*>(smem + kOffLsum);
-    const ScoreParams sp = score_params(a);
-    const CapForm cf = cap_form(sp);
-    const uint32_t t_s = tmem + x * 128 + lane_off, t_o = tmem + 256 + x * 128 + lane_off;
+    const ScoreArgs& sp = a.score;
+    const uint32_t t_s = tmem + x * 128 + 32 * b0 + lane_off;
+    const uint32_t t_o = tmem + 256 + x * 128 + lane_off;
     uint32_t s_cnt = 0;
     // The quick path's form of the cap: the exponential for the next eight
     // items after a score past the polynomial's range; kBlocks: none.
     constexpr int kBlocks = 2;
-    int form = kCap != kNoCap && cf.limit < 0.f ? kBlocks : 0, hold = 0;
+    int form = kCap == kAnyCap && sp.limit3 < 0.f ? kBlocks : 0, hold = 0;
     bool ok = true;
     for (uint32_t it_cnt = 0; ok; ++it_cnt) {
       const int slot = it_cnt & 1;
@@ -723,26 +739,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       float l = 0.f;
       if (form == 1 && --hold <= 0) form = 0;
       for (int j = 0; j < it.nkv; ++j) {
-        const int key0 = tile_key0<kScored, kBias>(it, j);
+        const int key0 = tile_key0<kScored, kBias>(it, j) + 32 * b0;  // key of my first column
         const int lim = last - key0, low = first - key0;  // low <= column <= lim is visible
-        // blocks c1 .. c2 - 1 are seen whole by every row of the warp
-        const int c1 = (__reduce_max_sync(0xffffffffu, low) + 31) >> 5;
-        const int c2 = min(4, (__reduce_min_sync(0xffffffffu, lim) + 1) >> 5);
         if (!mbar_wait_warp(bar(B_SF + x), s_cnt++ & 1, abort, ws.err)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        uint32_t done = 0;  // blocks whose P is written
-        bool tried = false;
-        for (;;) {
-          // the block path: before the quick one only where a row has no
-          // maximum yet, after it whatever is left
-          const bool have = __all_sync(0xffffffffu, ref != -INFINITY || !valid_row);
-          if (tried || !have || form == kBlocks) {
+        if constexpr (kCap == kFixedCap) {
+          // (one vote a tile, and a loop without masks for most: votes and
+          // branches of a block's own cost a tenth)
+          if (__all_sync(0xffffffffu, lim >= 63 && low <= 0)) {
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              if ((done >> c) & 1) continue;
+            for (int c = 0; c < 2; ++c) {
+              float s[32];
+              uint32_t p[16];
+              f32x2 rs[2] = {0, 0};
+              PKV_LD32(t_s + 32 * c, s);
+              tmem_wait_ld();
+              logits32_any<kCap, kBias, kSym, false>(s, sp, -ref, 0, 0, valid_row, slope2,
+                                                     (float)(rpos - key0 - 32 * c));
+              exp32(s, p, rs);
+              PKV_ST16U(t_s + 32 * c, p);
+              l += total(rs);
+            }
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
               float s[32];
               uint32_t p[16];
               const int lc = lim - 32 * c, wc = low - 32 * c;
@@ -750,13 +773,42 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) p[i] = 0;
               } else {
-                const bool edge = !__all_sync(0xffffffffu, lc >= 31 && wc <= 0);
-                const float nm = kCap == kFixedCap ? -ref : 0.f;
+                f32x2 rs[2] = {0, 0};
                 PKV_LD32(t_s + 32 * c, s);
                 tmem_wait_ld();
-                logits32_any<kCap, kBias, kSym>(s, sp, cf, nm, edge, lc, wc, valid_row, slope2,
-                                                (float)(rpos - key0 - 32 * c));
-                if (kCap != kFixedCap) {
+                logits32_any<kCap, kBias, kSym, true>(s, sp, -ref, lc, wc, valid_row, slope2,
+                                                      (float)(rpos - key0 - 32 * c));
+                exp32(s, p, rs);
+                l += total(rs);
+              }
+              PKV_ST16U(t_s + 32 * c, p);
+            }
+          }
+        } else {
+          // blocks c1 .. c2 - 1 are seen whole by every row of the warp
+          const int c1 = (__reduce_max_sync(0xffffffffu, low) + 31) >> 5;
+          const int c2 = min(4, (__reduce_min_sync(0xffffffffu, lim) + 1) >> 5);
+          uint32_t done = 0;  // blocks whose P is written
+          bool tried = false;
+          for (;;) {
+            // the block path: before the quick one only where a row has no
+            // maximum yet, after it whatever is left
+            const bool have = __all_sync(0xffffffffu, ref != -INFINITY || !valid_row);
+            if (tried || !have || form == kBlocks) {
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                if ((done >> c) & 1) continue;
+                float s[32];
+                uint32_t p[16];
+                const int lc = lim - 32 * c, wc = low - 32 * c;
+                if (__all_sync(0xffffffffu, lc < 0 || wc > 31)) {  // no row sees any
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) p[i] = 0;
+                } else {
+                  PKV_LD32(t_s + 32 * c, s);
+                  tmem_wait_ld();
+                  logits32_any<kCap, kBias, kSym, true>(s, sp, 0.f, lc, wc, valid_row, slope2,
+                                                        (float)(rpos - key0 - 32 * c));
                   float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
                   for (int i = 0; i < 32; i += 4) {
@@ -787,66 +839,65 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const float r0 = ref == -INFINITY ? 0.f : ref;  // (no key seen yet)
 #pragma unroll
                   for (int i = 0; i < 32; ++i) s[i] -= r0;
+                  f32x2 rs[2] = {0, 0};
+                  exp32(s, p, rs);
+                  l += total(rs);
                 }
-                f32x2 rs[2] = {0, 0};
-                exp32(s, p, rs);
-                l += total(rs);
+                PKV_ST16U(t_s + 32 * c, p);
+                done |= 1u << c;
+                // (the rest by the quick path, once each row has a maximum)
+                if (!tried && form != kBlocks && c2 > c1 &&
+                    __all_sync(0xffffffffu, ref != -INFINITY || !valid_row))
+                  break;
               }
-              PKV_ST16U(t_s + 32 * c, p);
-              done |= 1u << c;
-              // (the rest by the quick path, once each row has a maximum)
-              if (!tried && form != kBlocks && c2 > c1 &&
-                  __all_sync(0xffffffffu, ref != -INFINITY || !valid_row))
-                break;
             }
-          }
-          if (done == 15u) break;
-          if (tried) continue;
-          tried = true;
-          // the quick path: pairs of blocks, none of them done yet
+            if (done == 15u) break;
+            if (tried) continue;
+            tried = true;
+            // the quick path: pairs of blocks, none of them done yet
 #pragma unroll 1
-          for (int h = 0; h < 2 && form != kBlocks;) {
-            if (2 * h < c1 || 2 * h + 2 > c2 || ((done >> (2 * h)) & 3) != 0) {
-              ++h;
-              continue;
-            }
-            uint32_t p[2][16];
-            f32x2 rs[2] = {0, 0};
-            float big = 0.f;
-            auto go = [&](auto f) {
-              float s[2][32];
-              PKV_LD32(t_s + 64 * h, s[0]);
-              PKV_LD32(t_s + 64 * h + 32, s[1]);
-              tmem_wait_ld();
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                logits32<kCap, kBias, kSym, decltype(f)::value>(
-                    s[c], sp, cf, -ref, slope2, (float)(rpos - key0 - 64 * h - 32 * c), big);
-                exp32(s[c], p[c], rs);
+            for (int h = 0; h < 4 && form != kBlocks;) {
+              if (h < c1 || h + 2 > c2 || ((done >> h) & 3) != 0) {
+                h += 2;
+                continue;
               }
-            };
-            if (kCap == kNoCap || form == 0)
-              go(std::integral_constant<int, 0>());
-            else
-              go(std::integral_constant<int, 1>());
-            const float sum = total(rs);
-            if (kCap != kNoCap && form == 0 &&
-                !__all_sync(0xffffffffu, big <= cf.limit || !valid_row)) {
-              form = 1;
-              hold = 8;
-              continue;
+              uint32_t p[2][16];
+              f32x2 rs[2] = {0, 0};
+              float big = 0.f;
+              auto go = [&](auto f) {
+                float s[2][32];
+                PKV_LD32(t_s + 32 * h, s[0]);
+                PKV_LD32(t_s + 32 * h + 32, s[1]);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                  logits32<kCap, kBias, kSym, decltype(f)::value>(
+                      s[c], sp, -ref, slope2, (float)(rpos - key0 - 32 * (h + c)), big);
+                  exp32(s[c], p[c], rs);
+                }
+              };
+              if (kCap == kNoCap || form == 0)
+                go(std::integral_constant<Form, kDeg3>());
+              else
+                go(std::integral_constant<Form, kExp>());
+              const float sum = total(rs);
+              if (kCap != kNoCap && form == 0 &&
+                  !__all_sync(0xffffffffu, big <= sp.limit3 || !valid_row)) {
+                form = 1;
+                hold = 8;
+                continue;
+              }
+              // (past kMaxSum a new maximum is needed: the block path's)
+              if (__all_sync(0xffffffffu, sum <= kMaxSum || !valid_row)) {
+                l += sum;
+                PKV_ST16U(t_s + 32 * h, p[0]);
+                PKV_ST16U(t_s + 32 * h + 32, p[1]);
+                done |= 3u << h;
+              }
+              h += 2;
             }
-            if (kCap != kFixedCap && !__all_sync(0xffffffffu, sum <= kMaxSum || !valid_row)) {
-              ++h;  // (a new maximum: the block path's)
-              continue;
-            }
-            l += sum;
-            PKV_ST16U(t_s + 64 * h, p[0]);
-            PKV_ST16U(t_s + 64 * h + 32, p[1]);
-            done |= 3u << (2 * h);
-            ++h;
+            if (done == 15u) break;
           }
-          if (done == 15u) break;
         }
         tmem_wait_st();
         tc_fence_before();
@@ -855,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // the row sums of the item, for the epilogue (see the plain call's)
-      lsum[((it_cnt & 1) * 2 + x) * 2 * 128 + row] = l;
+      lsum[(((it_cnt & 1) * 2 + x) * 2 + hf) * 128 + row] = l;
       __syncwarp();
       if (lane == 0) mbar_arrive(lf_bar(it_cnt, x));
     }
@@ -1017,7 +1068,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------ epilogue: one warp per TMEM lane quarter ------------------
-    // Warp w (10..13) owns rows 32 * (w % 4) .. + 31 of both output tiles.  When
+    // Warp w (the last four) owns rows 32 * (w % 4) .. + 31 of both output tiles.  When
     // O_x is final (its last P.V done) and both partial row sums are in, the
     // warp reads the 128-column row block out of TMEM in two halves,
     // normalises them and packs them to bf16 in registers, and releases O_x as
@@ -1030,7 +1081,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = qd * 32 + lane;  // == TMEM lane
     const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
     const float* lsum = reinterpret_cast<const float*>(smem + kOffLsum);
-    const uint32_t stg = sbase + kOffStage + (warp - 10) * kStageWarp;
+    const uint32_t stg = sbase + kOffStage + (warp - 2 - kSoft) * kStageWarp;
     uint32_t o_cnt[2] = {0, 0};
     for (uint32_t it_cnt = 0;; ++it_cnt) {
       const int slot = it_cnt & 1;
@@ -1050,8 +1101,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const float* ls = lsum + ((it_cnt & 1) * 2 + x) * 2 * 128;
-        // the two column halves' sums (one sum in a scored call)
-        const float inv = 1.f / (kScored ? ls[row] : ls[row] + ls[128 + row]);
+        // the sums of the warps that shared the row
+        const float inv = 1.f / (kHalves == 1 ? ls[row] : ls[row] + ls[128 + row]);
         const uint32_t t_o = tmem + 256 + x * 128 + lane_off;
         const int h = x == 0 ? it.ha : it.hb;
         const int row_base = it.qt * kPreTileQ + qd * 32;  // the warp's first row
@@ -1130,7 +1181,7 @@ cudaError_t launch_prefill_as(const AttnArgs& a, const Workspace& ws, int sms, c
       !make_cache_map(&tk, a.kc, a.num_blocks, a.hkv) ||
       !make_cache_map(&tv, a.vc, a.num_blocks, a.hkv))
     return cudaErrorInvalidValue;
-  return launch_dependent(kernel, dim3(sms), dim3(kThreads), kSmemBytes, st, tq, tk, tv, a, ws);
+  return launch_dependent(kernel, dim3(sms), dim3(threads_of(kCap == kFixedCap)), kSmemBytes, st, tq, tk, tv, a, ws);
 }
 
 }  // namespace
