@@ -166,19 +166,19 @@ struct RowScore {
   float slope2;  // bias slope, log2 units
   float top;     // its largest bias (max_bias)
 };
-// The row at position pos of request r, head h; *vis (keys it sees end here)
-// grows to the request's prefix, clipped to the unit.
-__device__ __forceinline__ RowScore row_score(const AttnArgs& a, int r, int pos, int h, int k1,
-                                              int* vis) {
+// The row at position pos of request r (L keys), head h; *vis (keys it sees end
+// here) grows to the request's prefix, clipped to the unit.
+__device__ __forceinline__ RowScore row_score(const AttnArgs& a, int r, int L, int pos, int h,
+                                              int k1, int* vis) {
   RowScore s;
   s.pos = pos;
   s.low = first_key(pos, a.score.window);
   s.slope2 = a.score.slopes ? __ldg(a.score.slopes + h) * kLog2e : 0.f;
   int last = pos;
   if (a.score.prefix) {
-    const int p = __ldg(a.score.prefix + r);
+    const int p = clip_prefix(__ldg(a.score.prefix + r), L);
     *vis = max(*vis, min(k1, p));
-    last = max(pos, p - 1);  // (past the last key: a larger bound does no harm)
+    last = max(pos, p - 1);
   }
   s.top = max_bias(s.slope2, pos, s.low, last);
   return s;
@@ -338,8 +338,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       const int ti = row < nrows ? row / G : qn - 1;
       vis[hrow] = min(k1, un.ctx + ti + 1);
       if (kScored)
-        rs[hrow] = row_score(a, un.r, un.ctx + ti, row < nrows ? ug * G + row % G : ug * G, k1,
-                             &vis[hrow]);
+        rs[hrow] = row_score(a, un.r, un.ctx + qn, un.ctx + ti,
+                             row < nrows ? ug * G + row % G : ug * G, k1, &vis[hrow]);
     }
     // every row of the unit sees the keys from all_lo up to all_hi
     int all_lo = 0, all_hi = 0;
@@ -714,7 +714,8 @@ __global__ void __launch_bounds__(CfgP::kThreads, 1)
     if (kScored) {
 #pragma unroll
       for (int hrow = 0; hrow < 2; ++hrow)
-        rs[hrow] = row_score(a, un.r, un.ctx, ug * G + min(roff + gid + 8 * hrow, G - 1), k1, &vis);
+        rs[hrow] = row_score(a, un.r, un.ctx + 1, un.ctx,
+                             ug * G + min(roff + gid + 8 * hrow, G - 1), k1, &vis);
     }
     // the A fragments of the warp's 16 query rows (heads roff + gid and
     // roff + gid + 8 of the group; k-step k: dimensions 16k + 2tig, + 1 in

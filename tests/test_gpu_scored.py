@@ -211,6 +211,17 @@ def test_slopes(kind):
     run_and_check(W.build(W.custom(ctx, n, 8, 2, seed=21)), kind, slopes=s)
 
 
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (32, 1)])
+def test_slopes_of_either_sign_under_a_cap(hq, hkv):
+    """The fixed reference covers a bias that grows with distance: long rows,
+    prefixes up to the largest integer, windows, steep slopes of both signs."""
+    slopes = torch.linspace(-0.5, 0.5, hq)
+    for pre, window in ((None, 0), ([2 ** 31 - 1, 5, 2 ** 31 - 1, 700, 0], 0), (None, 90)):
+        ctx, n = [900, 300, 0, 200, 3000], [1, 1, 150, 140, 1]
+        run_and_check(W.build(W.custom(ctx, n, hq, hkv, seed=22)), "prefix %s" % pre,
+                      softcap=20.0, slopes=slopes, prefix=pre, window=window)
+
+
 def test_prefixes():
     """No prefix, negative, a part, the whole request, more than it: prompts,
     a chunk whose prefix runs past it, and decodes."""
@@ -335,6 +346,23 @@ def test_refusals():
         assert e.value.code == -1
     torch.cuda.synchronize()
     assert torch.isnan(ds.out.float()).all() and pkv.pkv_get_error() == 0
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """With another device current (made up: the tests have one), the call's
+    tensors are not on it, and nothing is enqueued."""
+    from paged_kv_attention_05_gb300 import _binding
+    ds = DeviceStep(W.build(W.custom([10], [1], 4, 2, seed=94)))
+    call(ds)
+    torch.cuda.synchronize()
+    launches = pkv.pkv_launch_count()
+    monkeypatch.setattr(_binding, "_get_device", lambda: 1)
+    with pytest.raises(ValueError, match="cuda:0.*current device is cuda:1"):
+        call(ds)
+    with pytest.raises(ValueError, match="cuda:0.*current device is cuda:1"):
+        pkv.pkv_write_rope(ds.q, ds.k, ds.v, ds.slot_mapping, torch.zeros(20, 128, device="cuda"),
+                           ds.key_cache, ds.value_cache, ds.slot_mapping, ds.q)
+    assert pkv.pkv_launch_count() == launches
 
 
 def test_another_stream_and_a_replayed_graph():
