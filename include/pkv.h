@@ -34,7 +34,9 @@
  *     device workspace per device (step plan, split-KV partial results and
  *     the device error word).  It is allocated on first use, or beforehand by
  *     pkv_reserve_workspace (needed before CUDA-graph capture, since no
- *     allocation may happen while a stream is being captured).
+ *     allocation may happen while a stream is being captured).  Growing it
+ *     leaves the old one allocated when a captured call holds its address, so
+ *     that the graph can still be replayed.
  *   - Errors found on the host (null pointers, sizes, geometry, alignment)
  *     return a negative PKV_ERR_* code before anything is enqueued: no buffer
  *     is touched.  pkv_last_error_string() describes the last such error of

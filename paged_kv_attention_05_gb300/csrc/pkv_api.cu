@@ -24,6 +24,7 @@ struct DeviceState {
   int* err = nullptr;  // device error word
   void* ws = nullptr;  // workspace
   size_t ws_bytes = 0;
+  bool ws_in_graph = false;  // a captured call holds its address
   // the step plan held in the workspace (pkv_plan / pkv_attention): its
   // geometry and the carve of the workspace it was written with
   bool plan_valid = false;
@@ -121,7 +122,10 @@ int ensure_workspace(DeviceState* s, const Sizes& z, cudaStream_t st, Workspace*
                   need);
     cudaError_t e = cudaDeviceSynchronize();  // the old workspace may still be in use
     if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
-    if (s->ws) cudaFree(s->ws);
+    // (a graph that was captured on the old workspace goes on using it when it
+    // is replayed: it is kept then, for as long as the process lives)
+    if (s->ws && !s->ws_in_graph) cudaFree(s->ws);
+    s->ws_in_graph = false;
     s->ws = nullptr;
     s->ws_bytes = 0;
     s->plan_valid = false;  // the plan lived in the old workspace
@@ -135,6 +139,14 @@ int ensure_workspace(DeviceState* s, const Sizes& z, cudaStream_t st, Workspace*
   // carve for the capacity actually held, scaled from the request
   *ws = carve_workspace(s->ws, z, s->err);
   return PKV_OK;
+}
+
+// Called wherever work that holds the workspace's address is enqueued.
+void note_capture(DeviceState* s, cudaStream_t st) {
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  if (!s->ws_in_graph && st != nullptr && cudaStreamIsCapturing(st, &cap) == cudaSuccess &&
+      cap != cudaStreamCaptureStatusNone)
+    s->ws_in_graph = true;
 }
 
 int check_geometry(int32_t block_size, int32_t hkv, int32_t head_size) {
@@ -493,6 +505,7 @@ int plan_locked(DeviceState* s, int64_t q_rows, int32_t num_heads, int32_t num_k
   a.num_reqs = num_reqs;
   a.kv_int8 = kv_int8;
   a.score = score;
+  note_capture(s, st);
   cudaError_t e = traced(1, st, [&] { return launch_plan(a, ws, workers, st); });
   if (e != cudaSuccess) return cuda_fail(e, "plan launch");
   // an int8 plan leaves prefill-class requests out, a scored one the keys
@@ -513,6 +526,7 @@ int run_locked(DeviceState* s, const void* q, int64_t q_row_stride, const void* 
                const void* value_cache, int64_t num_blocks, const int32_t* block_table,
                float scale, void* out, int64_t out_row_stride, int kv_int8, float k_scale,
                float v_scale, const ScoreArgs& score, cudaStream_t st) {
+  note_capture(s, st);
   Workspace ws = carve_workspace(s->ws, s->plan_sizes, s->err);
   AttnArgs a{};
   a.q = static_cast<const uint16_t*>(q);

@@ -401,6 +401,32 @@ def test_another_stream_and_a_replayed_graph():
     assert_near(ds.out[:206], ref, tol, "replayed")
 
 
+def test_a_graph_outlives_a_larger_workspace():
+    """A graph captured on one workspace is replayed after a later call needed a
+    larger one: the old one is still there, and the results are the graph's."""
+    ds = DeviceStep(W.build(W.custom([700, 0], [1, 200], 8, 2, seed=98)))
+    ds.write()
+    ref, tol = reference(ds, softcap=30.0)
+    call(ds, softcap=30.0)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(ds, softcap=30.0)
+    size = lambda r: pkv.pkv_workspace_size(r, 4096, 2048, 32, 8, pkv.pkv_num_sms())["bytes"]  # noqa: E731
+    reqs = 64
+    while size(reqs) < 1 << 28:
+        reqs *= 2
+    pkv.pkv_reserve_workspace(reqs, 4096, 2048, 32, 8)
+    filler = torch.full((1 << 28,), 255, dtype=torch.uint8, device="cuda")  # takes freed memory
+    ds.out.fill_(float("nan"))
+    g.replay()
+    torch.cuda.synchronize()
+    assert pkv.pkv_get_error() == 0
+    assert_near(ds.out[:201], ref, tol, "replayed")
+    assert int(filler.min()) == 255
+    call(ds, softcap=30.0)
+    assert_near(ds.out[:201], ref, tol, "on the larger workspace")
+
+
 def test_the_same_bits_every_time():
     ctx, n = [0, 700, 3000, 61], [300, 1, 1, 4]
     ds = DeviceStep(W.build(W.custom(ctx, n, 8, 2, seed=96)))
