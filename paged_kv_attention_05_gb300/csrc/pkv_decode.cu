@@ -111,12 +111,13 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
 __device__ __forceinline__ bool leaves_sm_to_prefill(const AttnArgs& a, const Workspace& ws,
                                                      int units_per_cta) {
   const int G = a.hq / a.hkv;
-  const int per_entry = G % 2 == 0 ? a.hq / 2 : a.hq;  // items (query head pairs) per entry
+  const bool single = single_head_items(a, ws.hdr->n_pre_entries, gridDim.x);
+  const int per_entry = G % 2 == 0 && !single ? a.hq / 2 : a.hq;  // items per entry
   const int items = ws.hdr->n_pre_entries * per_entry;
   if (items == 0) return false;
   const long long steps = (long long)ws.hdr->pre_tiles * per_entry;
   const int longest = max(ws.hdr->pre_max_tiles, 1);
-  const int cap = min(items, (int)gridDim.x / 2);
+  const int cap = single ? items : min(items, (int)gridDim.x / 2);
   int p = (int)min((long long)cap, (steps + longest - 1) / longest);
   const int spare = (int)gridDim.x - (ws.hdr->n_dec_units + units_per_cta - 1) / units_per_cta;
   if (spare > p) p = min(cap, spare);

@@ -406,7 +406,8 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap), 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.hq / a.hkv;
-  const bool pairs = (G % 2) == 0;  // two heads of one KV head per item
+  // two heads of one KV head per item
+  const bool pairs = (G % 2) == 0 && !(kScored && single_head_items(a, n_pre, gridDim.x));
   const int per_entry = pairs ? a.hq / 2 : a.hq;
 
   if (tid == 0) {

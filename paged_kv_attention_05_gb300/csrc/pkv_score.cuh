@@ -76,5 +76,13 @@ __device__ __forceinline__ float max_bias(float slope2, int pos, int first, int 
   return -fminf(0.f, slope2) * (float)max(pos - first, last - pos);
 }
 
+// Whether a scored call's prefill items are single query heads: where even so
+// they leave a quarter of the SMs idle, two heads of an item would only wait
+// for each other.  (A prompt of 300 tokens, 32 heads: 16.8 us, in pairs 18.9; of
+// 17 tokens 13.3, 14.0.)
+__device__ __forceinline__ bool single_head_items(const AttnArgs& a, int n_pre, int sms) {
+  return a.score.on && (long long)n_pre * a.hq * 4 <= 3LL * sms;
+}
+
 }  // namespace dev
 }  // namespace pkv
