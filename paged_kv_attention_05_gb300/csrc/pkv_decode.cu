@@ -473,13 +473,22 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           xs[nt][1] = fast_exp2(xs[nt][1] - c0);
           xs[nt][2] = fast_exp2(xs[nt][2] - c1);
           xs[nt][3] = fast_exp2(xs[nt][3] - c1);
-          l_run[0] += xs[nt][0] + xs[nt][1];
-          l_run[1] += xs[nt][2] + xs[nt][3];
+          if (!kScored) {
+            l_run[0] += xs[nt][0] + xs[nt][1];
+            l_run[1] += xs[nt][2] + xs[nt][3];
+          }
         }
         pa[0] = pack_bf16(xs[0][0], xs[0][1]);
         pa[1] = pack_bf16(xs[0][2], xs[0][3]);
         pa[2] = pack_bf16(xs[1][0], xs[1][1]);
         pa[3] = pack_bf16(xs[1][2], xs[1][3]);
+        if (kScored) {  // the sums of the rounded weights (see the prefill's exp32)
+          float r[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) add_bf16x2(r[2 * (i & 1)], r[2 * (i & 1) + 1], pa[i]);
+          l_run[0] += r[0] + r[1];
+          l_run[1] += r[2] + r[3];
+        }
       }
 
       // O += P V (V rows read transposed); V of keys past the unit zeroed
@@ -834,8 +843,10 @@ __global__ void __launch_bounds__(CfgP::kThreads, 1)
           xs[nt][1] = fast_exp2(xs[nt][1] - c0);
           xs[nt][2] = fast_exp2(xs[nt][2] - c1);
           xs[nt][3] = fast_exp2(xs[nt][3] - c1);
-          l_run[0] += xs[nt][0] + xs[nt][1];
-          l_run[1] += xs[nt][2] + xs[nt][3];
+          if (!kScored) {
+            l_run[0] += xs[nt][0] + xs[nt][1];
+            l_run[1] += xs[nt][2] + xs[nt][3];
+          }
         }
 #pragma unroll
         for (int pg = 0; pg < 2; ++pg) {
@@ -843,6 +854,13 @@ __global__ void __launch_bounds__(CfgP::kThreads, 1)
           pa[pg][1] = pack_bf16(xs[2 * pg][2], xs[2 * pg][3]);
           pa[pg][2] = pack_bf16(xs[2 * pg + 1][0], xs[2 * pg + 1][1]);
           pa[pg][3] = pack_bf16(xs[2 * pg + 1][2], xs[2 * pg + 1][3]);
+          if (kScored) {  // the sums of the rounded weights
+            float r[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) add_bf16x2(r[2 * (i & 1)], r[2 * (i & 1) + 1], pa[pg][i]);
+            l_run[0] += r[0] + r[1];
+            l_run[1] += r[2] + r[3];
+          }
         }
       }
 

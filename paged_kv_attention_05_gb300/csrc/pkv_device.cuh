@@ -206,6 +206,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+// s0 += the low bf16 of w, s1 += the high one (fp32 sums, exact conversions)
+__device__ __forceinline__ void add_bf16x2(float& s0, float& s1, uint32_t w) {
+  asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %2;\n add.rn.f32.bf16 %0, lo, %0;\n"
+      " add.rn.f32.bf16 %1, hi, %1;\n}\n"
+      : "+f"(s0), "+f"(s1)
+      : "r"(w));
+}
+
 // Byte offset of element (row, col) in a tile of 64-column (128-byte) rows
 // stored with the 128-byte swizzle of TMA / UMMA: the 16-byte chunk index is
 // XOR-ed with the row index modulo 8 (base 1024-byte aligned).

@@ -3,11 +3,14 @@ window, prefix and their combinations, on the decode path (every group size,
 several tokens, split keys) and the prefill path (ragged tiles, chunks), with
 NaN in every cache slot that no request holds.
 
-Tolerance, per output value, with A = sum_j softmax_j |V_j| of its row and
-column: the bf16 output is off by half a step (2^-8 of the value); each
-probability is rounded to bf16 before it meets V (2^-8 A); the fp32 sums over
-keys are off by less than 2^-14 A; and a logit off by d changes the average by
-at most 2 d A.  d: the product of 128 terms in fp32, 128 * 2^-24 times scale *
+Tolerance, per output value o, with A = sum_j softmax_j |V_j| of its row and
+column: the bf16 output is off by half a step (2^-8 |o|); each probability w_j
+is rounded to bf16, w_j (1 + e_j) with |e_j| <= 2^-8, before it meets V and
+before it enters the sum that divides, so that to first order
+  sum w_j (1 + e_j) V_j / sum w_j (1 + e_j) - o = sum w_j e_j (V_j - o),
+at most 2^-8 (A + |o|) (the second order, 2^-16 A, is inside the next term); the
+fp32 sums over keys are off by less than 2^-14 A; and a logit off by d changes
+the average by at most 2 d A.  d: the product of 128 terms in fp32, 128 * 2^-24 times scale *
 sum |q||K| (2^-16 with the scaling and the exponent's argument), plus 2^-20 of
 the cap and of the largest visible bias (identities in fp32 with two
 approximations of 2^-22 each)."""
@@ -65,7 +68,7 @@ def reference(ds, softcap=0.0, window=0, slopes=None, prefix=None):
             w = torch.softmax(s, -1)
             o, A = w @ v, w @ v.abs()
             out[a:b, g * G:(g + 1) * G] = o.transpose(0, 1)
-            tol[a:b, g * G:(g + 1) * G] = (2.0 ** -8 * o.abs() + A *
+            tol[a:b, g * G:(g + 1) * G] = (2.0 ** -7 * o.abs() + A *
                                            (2.0 ** -8 + 2.0 ** -14 + 2 * d[..., None])).transpose(0, 1)
     return out, tol
 
