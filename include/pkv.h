@@ -138,7 +138,7 @@ int pkv_write(const void* k, int64_t k_row_stride, const void* v, int64_t v_row_
  *                 pkv_attention.  q_out may be q with the same row stride
  *                 (in place); any other overlap is not allowed.
  *   k, v, caches, slot_mapping, n_tokens  as in pkv_write; num_heads is any
- *                 positive count (no relation to num_kv_heads is needed).
+ *                 count from 1 to 32767 (no relation to num_kv_heads).
  *   q_weight,     bf16 [head_size], or NULL: that side is not normalised.
  *   k_weight      weight_offset is added to both (0; 1 for models that store
  *                 w - 1).  eps >= 0.
@@ -173,6 +173,36 @@ int pkv_write_rope_int8(const void* q, int64_t q_row_stride, int32_t num_heads, 
                         void* value_cache, float k_scale, float v_scale, int64_t num_blocks,
                         int32_t block_size, int32_t num_kv_heads, int32_t head_size,
                         const int64_t* slot_mapping, int64_t n_tokens, void* stream);
+
+/*
+ * pkv_write_rope_packed — pkv_write_rope (int8 = 0; k_scale and v_scale are not
+ * read) or pkv_write_rope_int8 (int8 = 1) with the arguments in a struct, for
+ * bindings that pay for every argument they pass.
+ */
+typedef struct {
+  const void* q;
+  int64_t q_row_stride;
+  const void* k;
+  int64_t k_row_stride;
+  const void* v;
+  int64_t v_row_stride;
+  const void* q_weight;
+  const void* k_weight;
+  const float* cos_sin;
+  int64_t max_positions;
+  const int64_t* positions;
+  void* q_out;
+  int64_t q_out_row_stride;
+  void* key_cache;
+  void* value_cache;
+  int64_t num_blocks;
+  const int64_t* slot_mapping;
+  int64_t n_tokens;
+  void* stream;
+  int32_t num_heads, num_kv_heads, head_size, block_size, rotary_dim, interleaved;
+  float weight_offset, eps, k_scale, v_scale;
+} pkv_write_rope_args;
+int pkv_write_rope_packed(const pkv_write_rope_args* args, int32_t int8);
 
 /*
  * pkv_attention — varlen causal attention over the paged cache for a packed
@@ -255,7 +285,7 @@ int pkv_attention(const void* q, int64_t q_row_stride, int64_t q_rows, int32_t n
  * finite: the rows that do not see it weigh it with an exact zero.
  *
  * Other arguments, layouts, checks, alignment and errors are those of
- * pkv_attention (bf16 caches; any query_len; the plan reads prefix_lens when
+ * pkv_attention (out must not overlap q; bf16 caches; any query_len; the plan reads prefix_lens when
  * it reads query_start_loc).  The call makes its own plan in the shared
  * workspace (pkv_reserve_workspace covers it); the plan does not serve
  * pkv_attention_planned.  As with every call that uses the workspace, calls
@@ -270,6 +300,28 @@ int pkv_attention_scored(const void* q, int64_t q_row_stride, int64_t q_rows, in
                          float scale, float softcap, int32_t window, const float* alibi_slopes,
                          const int32_t* prefix_lens, void* out, int64_t out_row_stride,
                          void* stream);
+
+/* pkv_attention_scored with the arguments in a struct (see
+ * pkv_write_rope_packed). */
+typedef struct {
+  const void* q;
+  int64_t q_row_stride, q_rows;
+  const void* key_cache;
+  const void* value_cache;
+  int64_t num_blocks;
+  const int32_t* query_start_loc;
+  const int32_t* seq_lens;
+  const int32_t* block_table;
+  int64_t block_table_width;
+  const float* alibi_slopes;
+  const int32_t* prefix_lens;
+  void* out;
+  int64_t out_row_stride;
+  void* stream;
+  int32_t num_heads, num_kv_heads, head_size, block_size, num_reqs, window;
+  float scale, softcap;
+} pkv_attention_scored_args;
+int pkv_attention_scored_packed(const pkv_attention_scored_args* args);
 
 /*
  * pkv_plan / pkv_attention_planned — one step plan serving every layer.

@@ -1,6 +1,7 @@
 """ctypes marshalling for libpkv.so (argument checks and pointers only)."""
 import ctypes
 import os
+import struct
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(PKG, "libpkv.so")
@@ -22,7 +23,8 @@ EXPORTS = ["pkv_write", "pkv_attention", "pkv_reserve_workspace", "pkv_get_error
            "pkv_last_error_string", "pkv_num_sms", "pkv_trace_enable", "pkv_trace_read",
            "pkv_launch_count", "pkv_prepare_step", "pkv_write_int8", "pkv_attention_int8",
            "pkv_plan", "pkv_attention_planned", "pkv_workspace_size", "pkv_write_rope",
-           "pkv_write_rope_int8", "pkv_attention_scored"]
+           "pkv_write_rope_int8", "pkv_attention_scored", "pkv_write_rope_packed",
+           "pkv_attention_scored_packed"]
 TRACE_KINDS = ["write", "plan", "decode", "prefill", "combine", "prepare"]
 
 
@@ -54,6 +56,10 @@ def load():
     L.pkv_attention_scored.restype = ctypes.c_int
     L.pkv_attention_scored.argtypes = [vp, i64, i64, i32, vp, vp, i64, i32, i32, i32, vp, vp, vp,
                                        i64, i32, f32, f32, i32, vp, vp, vp, i64, vp]
+    L.pkv_write_rope_packed.restype = ctypes.c_int
+    L.pkv_write_rope_packed.argtypes = [ctypes.c_char_p, ctypes.c_int]
+    L.pkv_attention_scored_packed.restype = ctypes.c_int
+    L.pkv_attention_scored_packed.argtypes = [ctypes.c_char_p]
     L.pkv_write_int8.restype = ctypes.c_int
     L.pkv_write_int8.argtypes = [vp, i64, vp, i64, vp, vp, f32, f32, i64, i32, i32, i32, vp, i64,
                                  vp]
@@ -253,6 +259,13 @@ def _caches(key_cache, value_cache, dtype):
     return key_cache.shape
 
 
+# The structs of the packed calls (pkv_write_rope_args, pkv_attention_scored_args
+# of include/pkv.h): packed by one call and passed as one argument, they cost
+# 0.5 us where two dozen ctypes arguments cost 2.2.
+_ROPE_ARGS = struct.Struct("=19q6i4f")
+_SCORED_ARGS = struct.Struct("=15q6i2f")
+
+
 def _name_culprit(*named):
     """Raises for the first of these (tensor, name, dtype) triples that is no
     tensor of that dtype on the current CUDA device, whose stream the call
@@ -283,7 +296,7 @@ def _write_rope(q, k, v, positions, cos_sin, key_cache, value_cache, slot_mappin
                 dev == q.get_device() == k.get_device() == v.get_device() == q_out.get_device() ==
                 key_cache.get_device() == value_cache.get_device() == cos_sin.get_device() ==
                 positions.get_device() == slot_mapping.get_device())
-        qw = kw = None
+        qw = kw = 0
         if q_weight is not None:
             good = good and q_weight.dtype is bf16 and dev == q_weight.get_device()
             qw = q_weight.data_ptr()
@@ -337,13 +350,16 @@ def _write_rope(q, k, v, positions, cos_sin, key_cache, value_cache, slot_mappin
         n = int(n_tokens)
     if n > rows or n > orows or n > krows or n > vrows or n > npos:
         raise ValueError("n_tokens exceeds the rows of q/k/v/q_out/positions")
-    L = _lib or load()
-    fn = L.pkv_write_rope_int8 if scales else L.pkv_write_rope
-    rc = fn(q.data_ptr(), qs, hq, k.data_ptr(), ks, v.data_ptr(), vs, qw, kw, weight_offset, eps,
-            cos_sin.data_ptr(), far, rot, 1 if interleaved else 0, positions.data_ptr(),
-            q_out.data_ptr(), os_, key_cache.data_ptr(), value_cache.data_ptr(), *scales, nb, bs,
-            hkv, d, slot_mapping.data_ptr(), n,
-            _raw_stream() if stream is None else _stream(stream))
+    try:
+        args = _ROPE_ARGS.pack(
+            q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, qw, kw, cos_sin.data_ptr(), far,
+            positions.data_ptr(), q_out.data_ptr(), os_, key_cache.data_ptr(),
+            value_cache.data_ptr(), nb, slot_mapping.data_ptr(), n,
+            _raw_stream() if stream is None else _stream(stream), hq, hkv, d, bs, rot,
+            1 if interleaved else 0, weight_offset, eps, *(scales or (0.0, 0.0)))
+    except (struct.error, OverflowError) as e:
+        raise ValueError("an argument is out of range: %s" % e) from None
+    rc = (_lib or load()).pkv_write_rope_packed(args, 1 if scales else 0)
     if rc:
         _check(rc)
 
@@ -436,7 +452,7 @@ def pkv_attention_scored(q, key_cache, value_cache, query_start_loc, seq_lens, b
                 dev == q.get_device() == key_cache.get_device() == value_cache.get_device() ==
                 out.get_device() == query_start_loc.get_device() == seq_lens.get_device() ==
                 block_table.get_device())
-        slopes = prefix = None
+        slopes = prefix = 0
         if alibi_slopes is not None:
             good = good and alibi_slopes.dtype is torch.float32 and dev == alibi_slopes.get_device()
             slopes = alibi_slopes.data_ptr()
@@ -479,17 +495,22 @@ def pkv_attention_scored(q, key_cache, value_cache, query_start_loc, seq_lens, b
     if num_reqs > 0 and (query_start_loc.numel() < num_reqs + 1 or seq_lens.numel() < num_reqs or
                          (len(bts) == 2 and bts[0] < num_reqs)):
         raise ValueError("metadata shorter than num_reqs")
-    if slopes is not None and (alibi_slopes.shape != (hq,) or not alibi_slopes.is_contiguous()):
+    if alibi_slopes is not None and (alibi_slopes.shape != (hq,) or
+                                     not alibi_slopes.is_contiguous()):
         raise ValueError("alibi_slopes must be a contiguous [num_heads]")
-    if prefix is not None and (prefix_lens.numel() < num_reqs or not prefix_lens.is_contiguous()):
+    if prefix_lens is not None and (prefix_lens.numel() < num_reqs or
+                                    not prefix_lens.is_contiguous()):
         raise ValueError("prefix_lens must be contiguous, one per request")
-    if not -1 <= window < 1 << 31 or num_reqs >= 1 << 31:
-        raise ValueError("window or num_reqs out of range")
-    rc = (_lib or load()).pkv_attention_scored(
-        q.data_ptr(), qs, rows, hq, key_cache.data_ptr(), value_cache.data_ptr(), nb, bs, hkv, d,
-        query_start_loc.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), bts[-1], num_reqs,
-        scale, softcap, window, slopes, prefix, out.data_ptr(), os_,
-        _raw_stream() if stream is None else _stream(stream))
+    try:
+        args = _SCORED_ARGS.pack(
+            q.data_ptr(), qs, rows, key_cache.data_ptr(), value_cache.data_ptr(), nb,
+            query_start_loc.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), bts[-1],
+            slopes, prefix, out.data_ptr(), os_,
+            _raw_stream() if stream is None else _stream(stream), hq, hkv, d, bs, num_reqs,
+            window, scale, softcap)
+    except (struct.error, OverflowError) as e:
+        raise ValueError("an argument is out of range: %s" % e) from None
+    rc = (_lib or load()).pkv_attention_scored_packed(args)
     if rc:
         _check(rc)
 

@@ -333,91 +333,82 @@ extern "C" int pkv_write_int8(const void* k, int64_t k_row_stride, const void* v
 
 namespace {
 
-// pkv_write_rope and pkv_write_rope_int8: the arguments in a (all but the
-// error word), checked and enqueued.
-int write_rope_common(RopeArgs a, bool int8, int64_t num_blocks, int32_t block_size,
-                      int32_t head_size, void* stream) {
+// pkv_write_rope, pkv_write_rope_int8 and pkv_write_rope_packed.
+int write_rope_common(const pkv_write_rope_args& p, bool int8) {
   g_msg[0] = 0;
-  int rc = check_geometry(block_size, a.hkv, head_size);
+  int rc = check_geometry(p.block_size, p.num_kv_heads, p.head_size);
   if (rc) return rc;
-  if (a.hq <= 0 || a.hq > 32767) return fail(PKV_ERR_ARG, "num_heads %d", a.hq);
-  if (a.n_tokens < 0) return fail(PKV_ERR_ARG, "n_tokens %lld < 0", (long long)a.n_tokens);
-  if (num_blocks < 1) return fail(PKV_ERR_ARG, "num_blocks %lld < 1", (long long)num_blocks);
-  if (a.rotary_dim < 16 || a.rotary_dim > kHeadSize || a.rotary_dim % 16)
+  if (p.num_heads <= 0 || p.num_heads > 32767)
+    return fail(PKV_ERR_ARG, "num_heads %d (1 to 32767)", p.num_heads);
+  if (p.n_tokens < 0) return fail(PKV_ERR_ARG, "n_tokens %lld < 0", (long long)p.n_tokens);
+  if (p.num_blocks < 1) return fail(PKV_ERR_ARG, "num_blocks %lld < 1", (long long)p.num_blocks);
+  if (p.rotary_dim < 16 || p.rotary_dim > kHeadSize || p.rotary_dim % 16)
     return fail(PKV_ERR_UNSUPPORTED, "rotary_dim %d (a multiple of 16 from 16 to %d)",
-                a.rotary_dim, kHeadSize);
-  if (a.max_positions < 1)
-    return fail(PKV_ERR_ARG, "max_positions %lld < 1", (long long)a.max_positions);
-  if (a.q_weight || a.k_weight) {
-    if (!(a.eps >= 0.f && a.eps < INFINITY)) return fail(PKV_ERR_ARG, "eps must be finite, >= 0");
-    if (!(fabsf(a.weight_offset) < INFINITY))
+                p.rotary_dim, kHeadSize);
+  if (p.max_positions < 1)
+    return fail(PKV_ERR_ARG, "max_positions %lld < 1", (long long)p.max_positions);
+  if (p.q_weight || p.k_weight) {
+    if (!(p.eps >= 0.f && p.eps < INFINITY)) return fail(PKV_ERR_ARG, "eps must be finite, >= 0");
+    if (!(fabsf(p.weight_offset) < INFINITY))
       return fail(PKV_ERR_ARG, "weight_offset must be finite");
   }
-  if (int8 && !(a.k_scale > 0.f && a.v_scale > 0.f && a.k_scale < INFINITY &&
-                a.v_scale < INFINITY))
+  if (int8 && !(p.k_scale > 0.f && p.v_scale > 0.f && p.k_scale < INFINITY &&
+                p.v_scale < INFINITY))
     return fail(PKV_ERR_ARG, "k_scale and v_scale must be finite and positive");
-  if (a.n_tokens == 0) return PKV_OK;
-  if (!a.q || !a.k || !a.v || !a.table || !a.positions || !a.q_out || !a.kc || !a.vc || !a.slots)
+  if (p.n_tokens == 0) return PKV_OK;
+  if (!p.q || !p.k || !p.v || !p.cos_sin || !p.positions || !p.q_out || !p.key_cache ||
+      !p.value_cache || !p.slot_mapping)
     return fail(PKV_ERR_ARG, "null pointer argument");
-  const int64_t qrow = (int64_t)a.hq * kHeadSize, row = (int64_t)a.hkv * kHeadSize;
-  if (a.q_stride < qrow || a.q_out_stride < qrow || a.k_stride < row || a.v_stride < row)
+  const int64_t qrow = (int64_t)p.num_heads * kHeadSize, row = (int64_t)p.num_kv_heads * kHeadSize;
+  if (p.q_row_stride < qrow || p.q_out_row_stride < qrow || p.k_row_stride < row ||
+      p.v_row_stride < row)
     return fail(PKV_ERR_ARG, "row stride below heads * head_size (q, q_out: %lld, k, v: %lld)",
                 (long long)qrow, (long long)row);
-  if (!aligned16(a.q) || !aligned16(a.k) || !aligned16(a.v) || !aligned16(a.q_out) ||
-      !aligned16(a.kc) || !aligned16(a.vc) || !aligned16(a.table) || !aligned16(a.q_weight) ||
-      !aligned16(a.k_weight) || (a.q_stride % 8) || (a.k_stride % 8) || (a.v_stride % 8) ||
-      (a.q_out_stride % 8))
+  if (!aligned16(p.q) || !aligned16(p.k) || !aligned16(p.v) || !aligned16(p.q_out) ||
+      !aligned16(p.key_cache) || !aligned16(p.value_cache) || !aligned16(p.cos_sin) ||
+      !aligned16(p.q_weight) || !aligned16(p.k_weight) || (p.q_row_stride % 8) ||
+      (p.k_row_stride % 8) || (p.v_row_stride % 8) || (p.q_out_row_stride % 8))
     return fail(PKV_ERR_ALIGN, "q/k/v/q_out/caches/cos_sin/weights must be 16-byte aligned with "
                                "row strides * 2 a multiple of 16 bytes");
-  a.num_slots = num_blocks * kBlockSize;
   std::lock_guard<std::mutex> lock(g_mu);
   DeviceState* s = nullptr;
   rc = current_state(&s);
   if (rc) return rc;
+  RopeArgs a{};
+  a.q = static_cast<const uint16_t*>(p.q);
+  a.q_stride = p.q_row_stride;
+  a.hq = p.num_heads;
+  a.k = static_cast<const uint16_t*>(p.k);
+  a.k_stride = p.k_row_stride;
+  a.v = static_cast<const uint16_t*>(p.v);
+  a.v_stride = p.v_row_stride;
+  a.q_weight = static_cast<const uint16_t*>(p.q_weight);
+  a.k_weight = static_cast<const uint16_t*>(p.k_weight);
+  a.weight_offset = p.weight_offset;
+  a.eps = p.eps;
+  a.table = p.cos_sin;
+  a.max_positions = p.max_positions;
+  a.rotary_dim = p.rotary_dim;
+  a.interleaved = p.interleaved != 0;
+  a.positions = p.positions;
+  a.q_out = static_cast<uint16_t*>(p.q_out);
+  a.q_out_stride = p.q_out_row_stride;
+  a.kc = p.key_cache;
+  a.vc = p.value_cache;
+  a.k_scale = p.k_scale;
+  a.v_scale = p.v_scale;
+  a.num_slots = p.num_blocks * kBlockSize;
+  a.hkv = p.num_kv_heads;
+  a.slots = p.slot_mapping;
+  a.n_tokens = p.n_tokens;
   a.err = s->err;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaStream_t st = static_cast<cudaStream_t>(p.stream);
   cudaError_t e = traced(0, st, [&] { return launch_write_rope(a, int8, s->sms, st); });
   if (e != cudaSuccess) return cuda_fail(e, "pkv_write_rope launch");
   return PKV_OK;
 }
 
 }  // namespace
-
-extern "C" int pkv_write_rope(const void* q, int64_t q_row_stride, int32_t num_heads,
-                              const void* k, int64_t k_row_stride, const void* v,
-                              int64_t v_row_stride, const void* q_weight, const void* k_weight,
-                              float weight_offset, float eps, const float* cos_sin,
-                              int64_t max_positions, int32_t rotary_dim, int32_t interleaved,
-                              const int64_t* positions, void* q_out, int64_t q_out_row_stride,
-                              void* key_cache, void* value_cache, int64_t num_blocks,
-                              int32_t block_size, int32_t num_kv_heads, int32_t head_size,
-                              const int64_t* slot_mapping, int64_t n_tokens, void* stream) {
-  RopeArgs a{};
-  a.q = static_cast<const uint16_t*>(q);
-  a.q_stride = q_row_stride;
-  a.hq = num_heads;
-  a.k = static_cast<const uint16_t*>(k);
-  a.k_stride = k_row_stride;
-  a.v = static_cast<const uint16_t*>(v);
-  a.v_stride = v_row_stride;
-  a.q_weight = static_cast<const uint16_t*>(q_weight);
-  a.k_weight = static_cast<const uint16_t*>(k_weight);
-  a.weight_offset = weight_offset;
-  a.eps = eps;
-  a.table = cos_sin;
-  a.max_positions = max_positions;
-  a.rotary_dim = rotary_dim;
-  a.interleaved = interleaved != 0;
-  a.positions = positions;
-  a.q_out = static_cast<uint16_t*>(q_out);
-  a.q_out_stride = q_out_row_stride;
-  a.kc = key_cache;
-  a.vc = value_cache;
-  a.hkv = num_kv_heads;
-  a.slots = slot_mapping;
-  a.n_tokens = n_tokens;
-  return write_rope_common(a, false, num_blocks, block_size, head_size, stream);
-}
 
 extern "C" int pkv_write_rope_int8(const void* q, int64_t q_row_stride, int32_t num_heads,
                                    const void* k, int64_t k_row_stride, const void* v,
@@ -430,33 +421,37 @@ extern "C" int pkv_write_rope_int8(const void* q, int64_t q_row_stride, int32_t 
                                    float k_scale, float v_scale, int64_t num_blocks,
                                    int32_t block_size, int32_t num_kv_heads, int32_t head_size,
                                    const int64_t* slot_mapping, int64_t n_tokens, void* stream) {
-  RopeArgs a{};
-  a.q = static_cast<const uint16_t*>(q);
-  a.q_stride = q_row_stride;
-  a.hq = num_heads;
-  a.k = static_cast<const uint16_t*>(k);
-  a.k_stride = k_row_stride;
-  a.v = static_cast<const uint16_t*>(v);
-  a.v_stride = v_row_stride;
-  a.q_weight = static_cast<const uint16_t*>(q_weight);
-  a.k_weight = static_cast<const uint16_t*>(k_weight);
-  a.weight_offset = weight_offset;
-  a.eps = eps;
-  a.table = cos_sin;
-  a.max_positions = max_positions;
-  a.rotary_dim = rotary_dim;
-  a.interleaved = interleaved != 0;
-  a.positions = positions;
-  a.q_out = static_cast<uint16_t*>(q_out);
-  a.q_out_stride = q_out_row_stride;
-  a.kc = key_cache;
-  a.vc = value_cache;
-  a.k_scale = k_scale;
-  a.v_scale = v_scale;
-  a.hkv = num_kv_heads;
-  a.slots = slot_mapping;
-  a.n_tokens = n_tokens;
-  return write_rope_common(a, true, num_blocks, block_size, head_size, stream);
+  const pkv_write_rope_args p = {q, q_row_stride, k, k_row_stride, v, v_row_stride, q_weight,
+                                 k_weight, cos_sin, max_positions, positions, q_out,
+                                 q_out_row_stride, key_cache, value_cache, num_blocks,
+                                 slot_mapping, n_tokens, stream, num_heads, num_kv_heads,
+                                 head_size, block_size, rotary_dim, interleaved, weight_offset,
+                                 eps, k_scale, v_scale};
+  return write_rope_common(p, true);
+}
+
+extern "C" int pkv_write_rope(const void* q, int64_t q_row_stride, int32_t num_heads,
+                              const void* k, int64_t k_row_stride, const void* v,
+                              int64_t v_row_stride, const void* q_weight, const void* k_weight,
+                              float weight_offset, float eps, const float* cos_sin,
+                              int64_t max_positions, int32_t rotary_dim, int32_t interleaved,
+                              const int64_t* positions, void* q_out, int64_t q_out_row_stride,
+                              void* key_cache, void* value_cache, int64_t num_blocks,
+                              int32_t block_size, int32_t num_kv_heads, int32_t head_size,
+                              const int64_t* slot_mapping, int64_t n_tokens, void* stream) {
+  const pkv_write_rope_args p = {q, q_row_stride, k, k_row_stride, v, v_row_stride, q_weight,
+                                 k_weight, cos_sin, max_positions, positions, q_out,
+                                 q_out_row_stride, key_cache, value_cache, num_blocks,
+                                 slot_mapping, n_tokens, stream, num_heads, num_kv_heads,
+                                 head_size, block_size, rotary_dim, interleaved, weight_offset,
+                                 eps, 0.f, 0.f};
+  return write_rope_common(p, false);
+}
+
+extern "C" int pkv_write_rope_packed(const pkv_write_rope_args* args, int32_t int8) {
+  g_msg[0] = 0;
+  if (!args) return fail(PKV_ERR_ARG, "args is null");
+  return write_rope_common(*args, int8 != 0);
 }
 
 namespace {
@@ -740,6 +735,17 @@ extern "C" int pkv_attention_scored(const void* q, int64_t q_row_stride, int64_t
                           block_size, num_kv_heads, head_size, query_start_loc, seq_lens,
                           block_table, block_table_width, num_reqs, scale, out, out_row_stride,
                           stream, 0, 1.f, 1.f, score);
+}
+
+extern "C" int pkv_attention_scored_packed(const pkv_attention_scored_args* p) {
+  g_msg[0] = 0;
+  if (!p) return fail(PKV_ERR_ARG, "args is null");
+  return pkv_attention_scored(p->q, p->q_row_stride, p->q_rows, p->num_heads, p->key_cache,
+                              p->value_cache, p->num_blocks, p->block_size, p->num_kv_heads,
+                              p->head_size, p->query_start_loc, p->seq_lens, p->block_table,
+                              p->block_table_width, p->num_reqs, p->scale, p->softcap, p->window,
+                              p->alibi_slopes, p->prefix_lens, p->out, p->out_row_stride,
+                              p->stream);
 }
 
 extern "C" int pkv_reserve_workspace(int32_t max_reqs, int64_t max_q_rows,

@@ -331,6 +331,7 @@ def test_refusals():
         q=ds.q, key_cache=ds.key_cache, value_cache=ds.value_cache, query_start_loc=ds.qsl,
         seq_lens=ds.seq_lens, block_table=ds.block_table, num_reqs=2, scale=0.1, out=ds.out), **kw))
     for bad in (dict(alibi_slopes=torch.ones(7, device="cuda")),
+                dict(alibi_slopes=torch.ones(0, device="cuda")),
                 dict(alibi_slopes=torch.ones(16, device="cuda")[::2]),
                 dict(prefix_lens=torch.ones(1, dtype=torch.int32, device="cuda")),
                 dict(alibi_slopes=torch.ones(8)), dict(window=2 ** 31), dict(num_reqs=3),

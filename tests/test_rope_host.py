@@ -53,6 +53,58 @@ def test_int8_scales_must_be_finite_and_positive(lib):
         assert call(lib, True, v_scale=s) == -1
 
 
+def test_packed_structs_match_the_header():
+    """The binding's struct formats against the C compiler's layout."""
+    import os
+    import subprocess
+    import tempfile
+    from paged_kv_attention_05_gb300 import _binding as b
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src = r"""
+#include <stddef.h>
+#include <stdio.h>
+#include "pkv.h"
+int main(void) {
+  printf("%zu %zu %zu %zu %zu %zu\n", sizeof(pkv_write_rope_args),
+         offsetof(pkv_write_rope_args, num_heads), offsetof(pkv_write_rope_args, v_scale),
+         sizeof(pkv_attention_scored_args), offsetof(pkv_attention_scored_args, num_heads),
+         offsetof(pkv_attention_scored_args, softcap));
+  return 0;
+}
+"""
+    with tempfile.TemporaryDirectory() as d:
+        exe = os.path.join(d, "t")
+        subprocess.run(["gcc", "-std=c99", "-I", os.path.join(root, "include"), "-x", "c", "-",
+                        "-o", exe], input=src, text=True, check=True)
+        got = [int(x) for x in subprocess.run([exe], capture_output=True, text=True,
+                                              check=True).stdout.split()]
+    assert got == [b._ROPE_ARGS.size, 19 * 8, b._ROPE_ARGS.size - 4,
+                   b._SCORED_ARGS.size, 15 * 8, b._SCORED_ARGS.size - 4]
+
+
+def test_packed_calls_check_like_the_others(lib):
+    assert lib.pkv_write_rope_packed(None, 0) == -1
+    assert lib.pkv_attention_scored_packed(None) == -1
+    from paged_kv_attention_05_gb300 import _binding as b
+    ok = dict(heads=(32, 8, 128, 16, 128, 0))
+    pack = lambda heads, n=4, sc=0.1: b._ROPE_ARGS.pack(  # noqa: E731
+        FAKE, 4096, FAKE, 1024, FAKE, 1024, 0, 0, FAKE, 100, FAKE, FAKE, 4096, FAKE, FAKE, 10,
+        FAKE, n, 0, *heads, 0.0, 1e-6, sc, 0.1)
+    assert lib.pkv_write_rope_packed(pack(n=0, **ok), 0) == 0
+    assert lib.pkv_write_rope_packed(pack(n=-1, **ok), 0) == -1
+    assert lib.pkv_write_rope_packed(pack((32, 8, 64, 16, 128, 0)), 0) == -2
+    assert lib.pkv_write_rope_packed(pack((32, 8, 128, 16, 24, 0)), 1) == -2
+    assert lib.pkv_write_rope_packed(pack(sc=0.0, n=0, **ok), 1) == -1
+    assert lib.pkv_write_rope_packed(pack(sc=0.0, n=0, **ok), 0) == 0
+    scored = lambda heads, scale=0.1, cap=0.0: b._SCORED_ARGS.pack(  # noqa: E731
+        FAKE, 4096, 4, FAKE, FAKE, 10, FAKE, FAKE, FAKE, 4, 0, 0, FAKE, 4096, 0, *heads, scale,
+        cap)
+    assert lib.pkv_attention_scored_packed(scored((32, 8, 128, 16, 0, 0))) == 0
+    assert lib.pkv_attention_scored_packed(scored((30, 8, 128, 16, 2, 0))) == -2
+    assert lib.pkv_attention_scored_packed(scored((32, 8, 128, 16, 2, -1))) == -1
+    assert lib.pkv_attention_scored_packed(scored((32, 8, 128, 16, 2, 0), cap=-1.0)) == -1
+
+
 def test_no_tokens_is_not_an_error(lib):
     assert call(lib, n=0, q=None, k=None, v=None, sm=None) == 0
     assert call(lib, True, n=0) == 0
