@@ -21,12 +21,13 @@
  *     stream is finishing, but it writes no global memory, and reads none
  *     that that work produces, until that work has finished.  One
  *     refinement: the step plan of the attention calls and of pkv_plan reads
- *     query_start_loc and seq_lens (and prefix_lens) as soon as its kernel starts, which is after the kernel before it on
- *     the stream has finished, or, when that kernel is a cache write's
- *     (pkv_write*) or another plan's, after everything before that kernel
- *     has finished: so enqueue the metadata before the write (as a
- *     step does), or from a kernel launched without programmatic
- *     serialisation.  Within a bf16 attention call that has prefill work,
+ *     query_start_loc and seq_lens (and prefix_lens) as soon as its kernel
+ *     starts, which is after the kernel before it on the stream has finished,
+ *     or, when that kernel is a cache write's (pkv_write*), another plan's or
+ *     the last of a pkv_attention_scored call's, after everything enqueued
+ *     before that kernel's call has finished: so enqueue the metadata before
+ *     the write (as a step does), or from a kernel launched without
+ *     programmatic serialisation.  Within a bf16 attention call that has prefill work,
  *     the decode kernel leaves some SMs to the prefill kernel, whose items
  *     run there beside the decode units.
  *   - The caller owns every buffer it passes; the library keeps no pointer to

@@ -352,10 +352,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(AttnArgs a, Workspac
   // pass 2: per-request offsets (block scans), then the work lists written
   // cooperatively: consecutive threads write consecutive entries, each
   // finding its request by binary search over the chunk's offsets
-  __shared__ int s_off_u[kPlanThreads + 1], s_off_t[kPlanThreads + 1], s_off_q[kPlanThreads + 1];
-  __shared__ int s_off_f[kPlanThreads], s_off_l[kPlanThreads];  // full chunks, last piece
-  __shared__ int s_off_p[kPlanThreads], s_len[kPlanThreads], s_n[kPlanThreads];
-  __shared__ int s_q0[kPlanThreads];
+  // (one int per thread each, three of them one more: plan_smem)
+  extern __shared__ int s_plan[];
+  int *s_off_u = s_plan, *s_off_t = s_off_u + nt + 1, *s_off_q = s_off_t + nt + 1;
+  int *s_off_f = s_off_q + nt + 1, *s_off_l = s_off_f + nt;  // full chunks, last piece
+  int *s_off_p = s_off_l + nt, *s_len = s_off_p + nt, *s_n = s_len + nt, *s_q0 = s_n + nt;
   __shared__ int s_max_rows;
   if (tid == 0) s_max_rows = 0;
   __syncthreads();
@@ -489,6 +490,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(AttnArgs a, Workspac
   }
 }
 
+// Shared memory of a plan CTA, by its threads: a small one fits beside the
+// prefill kernel's CTA, so that the plan of the next scored call starts while
+// the last one's merge still runs.
+constexpr size_t plan_smem(int threads) { return (9 * (size_t)threads + 3) * sizeof(int); }
+
 }  // namespace
 
 cudaError_t launch_plan(const AttnArgs& a, const Workspace& ws, int dec_grid, cudaStream_t st) {
@@ -499,7 +505,7 @@ cudaError_t launch_plan(const AttnArgs& a, const Workspace& ws, int dec_grid, cu
   const int want = (std::min(a.num_reqs, threads) + warps - 1) / warps;
   const int grid = std::max(1, std::min(16, want));
   return launch_dependent(a.score.on ? plan_kernel<true> : plan_kernel<false>, dim3(grid),
-                          dim3(threads), 0, st, a, ws, dec_grid);
+                          dim3(threads), plan_smem(threads), st, a, ws, dec_grid);
 }
 
 }  // namespace pkv

@@ -383,6 +383,10 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap), 1)
   // (so this grid finishing implies that every kernel before it has).
   constexpr int kSoft = soft_warps(kCap == kFixedCap), kThreads = threads_of(kCap == kFixedCap);
   constexpr int kHalves = kScored ? kSoft / 8 : 2;  // softmax warps that share a row
+  // (a scored call lets the next kernel, usually another call's plan or cache
+  // write, set up meanwhile: everything before this kernel has finished or, as
+  // the decode grid, writes only what those wait for)
+  if (kScored) grid_dep_launch();
   const int n_pre = __ldcg(&ws.hdr->n_pre_entries);
   if (n_pre == 0) {  // a step without prefill work (every CTA agrees)
     grid_dep_wait();

@@ -405,6 +405,43 @@ def test_another_stream_and_a_replayed_graph():
     assert_near(ds.out[:206], ref, tol, "replayed")
 
 
+def test_calls_back_to_back_without_a_wait():
+    """Each call's plan starts while the one before still runs; different steps
+    (decodes that are split and merged, prompts, both), the cache write, the
+    plain call and metadata changed by ordinary kernels in between, enqueued
+    without a synchronisation, give the bits that they give alone."""
+    specs = [([20000, 300], [1, 1]), ([0, 129, 540], [298, 1, 1]), ([40], [1]),
+             ([0, 700], [400, 130])]
+    steps = [DeviceStep(W.build(W.custom(c, n, 8, 2, seed=100 + i)))
+             for i, (c, n) in enumerate(specs)]
+    alone = []
+    for ds in steps:
+        ds.write()
+        call(ds, softcap=30.0)
+        torch.cuda.synchronize()
+        alone.append(ds.out.clone())
+    torch.cuda.synchronize()
+    got = []
+    for turn in range(40):
+        ds = steps[turn % 4]
+        if turn % 3 == 1:
+            ds.write()
+        if turn % 5 == 2:
+            ds.attention()
+        if turn % 7 == 3:      # the lengths are gone and come back, in stream order
+            keep = ds.seq_lens.clone()
+            ds.seq_lens.zero_()
+            ds.seq_lens.copy_(keep)
+        call(ds, softcap=30.0)
+        if turn % 4 == 1:
+            call(ds, softcap=30.0)
+        got.append(ds.out.clone())
+    assert pkv.pkv_get_error() == 0
+    for turn, out in enumerate(got):
+        n = int(steps[turn % 4].step.query_start_loc[-1])
+        assert torch.equal(out[:n], alone[turn % 4][:n]), "turn %d" % turn
+
+
 def test_a_graph_outlives_a_larger_workspace():
     """A graph captured on one workspace is replayed after a later call needed a
     larger one: the old one is still there, and the results are the graph's."""
