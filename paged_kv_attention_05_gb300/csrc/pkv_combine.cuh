@@ -17,18 +17,32 @@ namespace dev {
 // multi-token row) contributes nothing; the first split always holds key 0.
 // Rows are (query token, head in group); pairs with fewer rows than the
 // largest skip the rest.
+// What a warp reads of the plan for that: the header's counts and its first
+// pair.  (The plan's lists are read through L2: the plan kernel ran two
+// launches before this one.)
+struct CombineStart {
+  int max_rows, n_items;
+  SplitPair first;
+};
+__device__ __forceinline__ SplitPair load_pair(const Workspace& ws, int i) {
+  const int4 w0 = __ldcg(reinterpret_cast<const int4*>(ws.pairs + i));
+  const int4 w1 = __ldcg(reinterpret_cast<const int4*>(ws.pairs + i) + 1);
+  return SplitPair{w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+}
+__device__ __forceinline__ CombineStart combine_start(const Workspace& ws, int warp_id) {
+  CombineStart s{};
+  s.max_rows = __ldcg(&ws.hdr->max_rows);
+  s.n_items = __ldcg(&ws.hdr->n_pairs) * s.max_rows;
+  if (warp_id < s.n_items) s.first = load_pair(ws, warp_id / s.max_rows);
+  return s;
+}
 __device__ __forceinline__ void combine_splits(const AttnArgs& a, const Workspace& ws, int warp_id,
-                                               int n_warps) {
+                                               int n_warps, const CombineStart& start) {
   const int G = a.hq / a.hkv;
-  // (the plan's lists are read through L2: the plan kernel ran two launches
-  // before this one)
-  const int max_rows = __ldcg(&ws.hdr->max_rows);
-  const int n_items = __ldcg(&ws.hdr->n_pairs) * max_rows;
+  const int max_rows = start.max_rows, n_items = start.n_items;
   const int lane = threadIdx.x & 31;
   for (int item = warp_id; item < n_items; item += n_warps) {
-    const int4 pw0 = __ldcg(reinterpret_cast<const int4*>(ws.pairs + item / max_rows));
-    const int4 pw1 = __ldcg(reinterpret_cast<const int4*>(ws.pairs + item / max_rows) + 1);
-    const SplitPair sp{pw0.x, pw0.y, pw0.z, pw0.w, pw1.x, pw1.y, pw1.z, pw1.w};
+    const SplitPair sp = item == warp_id ? start.first : load_pair(ws, item / max_rows);
     const int row = item % max_rows;
     const int q0 = sp.q0;
     const int rows = sp.qn * G;
@@ -57,6 +71,10 @@ __device__ __forceinline__ void combine_splits(const AttnArgs& a, const Workspac
     *reinterpret_cast<uint2*>(orow) =
         make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
   }
+}
+__device__ __forceinline__ void combine_splits(const AttnArgs& a, const Workspace& ws, int warp_id,
+                                               int n_warps) {
+  combine_splits(a, ws, warp_id, n_warps, combine_start(ws, warp_id));
 }
 
 }  // namespace dev

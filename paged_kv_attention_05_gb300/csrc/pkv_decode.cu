@@ -107,28 +107,50 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
 // the grid has (units_per_cta at a time each), the spare SMs would idle
 // anyway: P then grows up to one per item (still at most half of the SMs).
 // Every CTA computes the same from the plan header (read after the plan
-// wait).
-__device__ __forceinline__ bool leaves_sm_to_prefill(const AttnArgs& a, const Workspace& ws,
-                                                     int units_per_cta) {
+// wait): P.
+__device__ __forceinline__ int sms_to_prefill(const AttnArgs& a, const Workspace& ws,
+                                              int units_per_cta) {
   const int G = a.hq / a.hkv;
   const bool single = single_head_items(a, ws.hdr->n_pre_entries, gridDim.x);
   const int per_entry = G % 2 == 0 && !single ? a.hq / 2 : a.hq;  // items per entry
   const int items = ws.hdr->n_pre_entries * per_entry;
-  if (items == 0) return false;
+  if (items == 0) return 0;
   const long long steps = (long long)ws.hdr->pre_tiles * per_entry;
   const int longest = max(ws.hdr->pre_max_tiles, 1);
   const int cap = single ? items : min(items, (int)gridDim.x / 2);
   int p = (int)min((long long)cap, (steps + longest - 1) / longest);
   const int spare = (int)gridDim.x - (ws.hdr->n_dec_units + units_per_cta - 1) / units_per_cta;
   if (spare > p) p = min(cap, spare);
-  return (int)blockIdx.x < max(p, 1);
+  return max(p, 1);
 }
-
 // a work unit written by the plan kernel
 __device__ __forceinline__ DecUnit load_unit(const DecUnit* p) {
   const int4 w0 = __ldcg(reinterpret_cast<const int4*>(p));
   const int4 w1 = __ldcg(reinterpret_cast<const int4*>(p) + 1);
   return DecUnit{w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+}
+
+// A scored call gives each worker (of `per_cta` in a CTA) its first unit by its
+// index, spread over the CTAs, loaded together with the plan header, and lets
+// the cursor count on from there: two dependent reads less before the first
+// page is asked for (the guess that no SM is left to prefill is put right).
+struct FirstUnit {
+  int index, after;  // after: units given out so
+  DecUnit unit;
+};
+__device__ __forceinline__ FirstUnit first_unit(const AttnArgs& a, const Workspace& ws, int worker,
+                                                int per_cta, int* prefill_sms) {
+  FirstUnit f;
+  f.index = worker * gridDim.x + blockIdx.x;  // (the list has room for a unit a worker)
+  f.unit = load_unit(ws.units + f.index);
+  const int p = sms_to_prefill(a, ws, per_cta);
+  f.after = (gridDim.x - p) * per_cta;
+  if (p > 0) {
+    f.index = worker * (gridDim.x - p) + blockIdx.x - p;
+    if ((int)blockIdx.x >= p) f.unit = load_unit(ws.units + f.index);
+  }
+  *prefill_sms = p;
+  return f;
 }
 
 // keep the bf16 halves of a register whose key index is below `valid`
@@ -275,7 +297,13 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
   // the set-up above overlaps the plan kernel; the work list is read after it
   grid_dep_wait();
   grid_dep_launch();
-  if (leaves_sm_to_prefill(a, ws, C::kWarps) || ws.hdr->n_dec_units == 0) return;
+  int left = 0;
+  FirstUnit mine{};
+  if (kScored)
+    mine = first_unit(a, ws, warp, C::kWarps, &left);
+  else
+    left = sms_to_prefill(a, ws, C::kWarps);
+  if ((int)blockIdx.x < left || ws.hdr->n_dec_units == 0) return;
   __syncthreads();
 
   const int n_units = ws.hdr->n_dec_units;
@@ -287,11 +315,13 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
   uint32_t page_cnt = 0;
 
   for (uint32_t unit_cnt = 0;; ++unit_cnt) {
-    int u = 0;
-    if (lane == 0) u = atomicAdd(&ws.hdr->dec_counter, 1);
-    u = __shfl_sync(0xffffffffu, u, 0);
+    int u = mine.index;
+    if (!kScored || unit_cnt > 0) {
+      if (lane == 0) u = mine.after + atomicAdd(&ws.hdr->dec_counter, 1);
+      u = __shfl_sync(0xffffffffu, u, 0);
+    }
     if (u >= n_units || *abort) break;
-    const DecUnit un = load_unit(ws.units + u);
+    const DecUnit un = kScored && unit_cnt == 0 ? mine.unit : load_unit(ws.units + u);
     const int ug = un.gq & 0xFFFF;  // KV head
     const int uqn = un.gq >> 16;    // query tokens of the request
     const int k0 = un.k0, k1 = un.k1;
@@ -622,7 +652,13 @@ __global__ void __launch_bounds__(CfgP::kThreads, 1)
   // the set-up above overlaps the plan kernel; the work list is read after it
   grid_dep_wait();
   grid_dep_launch();
-  if (leaves_sm_to_prefill(a, ws, C::kPairs) || ws.hdr->n_dec_units == 0) return;
+  int left = 0;
+  FirstUnit mine{};
+  if (kScored)
+    mine = first_unit(a, ws, pair, C::kPairs, &left);
+  else
+    left = sms_to_prefill(a, ws, C::kPairs);
+  if ((int)blockIdx.x < left || ws.hdr->n_dec_units == 0) return;
   __syncthreads();
 
   const int n_units = ws.hdr->n_dec_units;
@@ -639,17 +675,20 @@ __global__ void __launch_bounds__(CfgP::kThreads, 1)
     int u = 0;
     if (tile == 0) {
       if (lane == 0) {
-        u = atomicAdd(&ws.hdr->dec_counter, 1);
+        u = kScored && unit_cnt == 0 ? mine.index
+                                     : mine.after + atomicAdd(&ws.hdr->dec_counter, 1);
         uslot[slot] = u;
         mbar_arrive(unit_bar(slot));
       }
       u = __shfl_sync(0xffffffffu, u, 0);
+    } else if (kScored && unit_cnt == 0) {
+      u = mine.index;  // (handed over all the same: the barrier's phases count units)
     } else {
       if (!mbar_wait_warp(unit_bar(slot), (unit_cnt >> 1) & 1, abort, ws.err)) break;
       u = uslot[slot];
     }
     if (u >= n_units || *abort) break;
-    const DecUnit un = load_unit(ws.units + u);
+    const DecUnit un = kScored && unit_cnt == 0 ? mine.unit : load_unit(ws.units + u);
     const int ug = un.gq & 0xFFFF;  // KV head
     const int k0 = un.k0, k1 = un.k1;
     const int p0 = k0 / kBlockSize;

@@ -389,9 +389,13 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap), 1)
   if (kScored) grid_dep_launch();
   const int n_pre = __ldcg(&ws.hdr->n_pre_entries);
   if (n_pre == 0) {  // a step without prefill work (every CTA agrees)
+    // (a scored call reads its part of the plan before the wait)
+    const int id = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    CombineStart start{};
+    if (kScored) start = combine_start(ws, id);
     grid_dep_wait();
-    combine_splits(a, ws, blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5),
-                   gridDim.x * (kThreads / 32));
+    if (!kScored) start = combine_start(ws, id);
+    combine_splits(a, ws, id, gridDim.x * (kThreads / 32), start);
     return;
   }
   extern __shared__ uint8_t smem_raw[];
@@ -446,9 +450,15 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap), 1)
     // while the current item is being issued, and each tile's block ids one
     // tile ahead; a load only stalls at its first use.
     uint32_t tile_cnt = 0, vt_uses[kStages] = {0, 0}, qx_cnt[2] = {0, 0};
-    int w_nxt = 0;
-    if (lane == 0) w_nxt = atomicAdd(&ws.hdr->pre_counter, 1);
-    w_nxt = __shfl_sync(0xffffffffu, w_nxt, 0);
+    // (a scored call without decode units has every CTA at once: the first
+    // item of each is its index, and the cursor counts on from there)
+    const bool own_first = kScored && __ldcg(&ws.hdr->n_dec_units) == 0;
+    const int after = own_first ? (int)gridDim.x : 0;
+    int w_nxt = (int)blockIdx.x;
+    if (!own_first) {
+      if (lane == 0) w_nxt = atomicAdd(&ws.hdr->pre_counter, 1);
+      w_nxt = __shfl_sync(0xffffffffu, w_nxt, 0);
+    }
     const PreEntry none{-1, 0, 0, 0, 0, 0, 0, 0};
     PreEntry e_nxt = w_nxt < n_items ? load_entry(ws.pre + w_nxt / per_entry) : none;
     for (uint32_t it_cnt = 0;; ++it_cnt) {
@@ -487,7 +497,7 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap), 1)
         mbar_arrive(bar(B_IF + slot));
       }
       // the next item's cursor and entry (consumed after this item)
-      if (lane == 0) w_nxt = atomicAdd(&ws.hdr->pre_counter, 1);
+      if (lane == 0) w_nxt = after + atomicAdd(&ws.hdr->pre_counter, 1);
       w_nxt = __shfl_sync(0xffffffffu, w_nxt, 0);
       e_nxt = w_nxt < n_items ? load_entry(ws.pre + w_nxt / per_entry) : none;
       const int* btrow = a.bt + (int64_t)it.r * a.bt_width;
