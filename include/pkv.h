@@ -25,11 +25,12 @@
  *     starts, which is after the kernel before it on the stream has finished,
  *     or, when that kernel is a cache write's (pkv_write*), another plan's or
  *     the last of a pkv_attention_scored call's, after everything enqueued
- *     before that kernel's call has finished: so enqueue the metadata before
- *     the write (as a step does), or from a kernel launched without
- *     programmatic serialisation.  Within a bf16 attention call that has prefill work,
- *     the decode kernel leaves some SMs to the prefill kernel, whose items
- *     run there beside the decode units.
+ *     before the run of such calls that it ends (they write none of the
+ *     three): so enqueue the metadata before the write (as a step does), or
+ *     from a kernel launched without programmatic serialisation.  Within a
+ *     bf16 attention call that has prefill work, the decode kernel leaves
+ *     some SMs to the prefill kernel, whose items run there beside the decode
+ *     units.
  *   - The caller owns every buffer it passes; the library keeps no pointer to
  *     any of them after the call returns.  The library owns one grow-only
  *     device workspace per device (step plan, split-KV partial results and
@@ -277,7 +278,7 @@ int pkv_attention(const void* q, int64_t q_row_stride, int64_t q_rows, int32_t n
  *                 fp32's range (else PKV_ERR_ARG).
  *   window        >= 0; 0: no window; 1: each row sees only its own key (and
  *                 the prefix keys after it, when there is a prefix).
- *   alibi_slopes  fp32 [num_heads] device, or NULL.
+ *   alibi_slopes  fp32 [num_heads] device, finite, of either sign, or NULL.
  *   prefix_lens   int32 [num_reqs] device, or NULL; negative counts as 0.
  * Pages that lie wholly before a request's window (keys before
  * max(0, ctx - window + 1)) are not read, nor are their block_table entries,
@@ -286,9 +287,9 @@ int pkv_attention(const void* q, int64_t q_row_stride, int64_t q_rows, int32_t n
  * finite: the rows that do not see it weigh it with an exact zero.
  *
  * Other arguments, layouts, checks, alignment and errors are those of
- * pkv_attention (out must not overlap q; bf16 caches; any query_len; the plan reads prefix_lens when
- * it reads query_start_loc).  The call makes its own plan in the shared
- * workspace (pkv_reserve_workspace covers it); the plan does not serve
+ * pkv_attention (out must not overlap q; bf16 caches; any query_len; the plan
+ * reads prefix_lens when it reads query_start_loc).  The call makes its own
+ * plan in the shared workspace (pkv_reserve_workspace covers it); the plan does not serve
  * pkv_attention_planned.  As with every call that uses the workspace, calls
  * on one device must not overlap on the GPU (two streams, two captured
  * graphs replayed at once): they share one plan and one set of partials.

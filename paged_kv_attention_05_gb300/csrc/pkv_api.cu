@@ -521,7 +521,6 @@ int run_locked(DeviceState* s, const void* q, int64_t q_row_stride, const void* 
                const void* value_cache, int64_t num_blocks, const int32_t* block_table,
                float scale, void* out, int64_t out_row_stride, int kv_int8, float k_scale,
                float v_scale, const ScoreArgs& score, cudaStream_t st) {
-  note_capture(s, st);
   Workspace ws = carve_workspace(s->ws, s->plan_sizes, s->err);
   AttnArgs a{};
   a.q = static_cast<const uint16_t*>(q);
@@ -674,6 +673,7 @@ extern "C" int pkv_attention_planned(const void* q, int64_t q_row_stride, int32_
   PlanHeader* hdr = carve_workspace(s->ws, s->plan_sizes, s->err).hdr;
   static_assert(offsetof(PlanHeader, pre_counter) == offsetof(PlanHeader, dec_counter) + 4,
                 "adjacent cursors");
+  note_capture(s, st);
   cudaError_t e = cudaMemsetAsync(&hdr->dec_counter, 0, 2 * sizeof(int), st);
   if (e != cudaSuccess) return cuda_fail(e, "cursor reset");
   return run_locked(s, q, q_row_stride, key_cache, value_cache, num_blocks, block_table, scale,

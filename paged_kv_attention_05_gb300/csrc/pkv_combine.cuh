@@ -8,17 +8,8 @@
 namespace pkv {
 namespace dev {
 
-// Merge of split results: one (split pair, query row) per warp (warp_id of
-// n_warps in the grid), four output columns per lane, the splits merged in
-// one pass with the online-softmax identity the decode loop uses between
-// pages (a running max M; the sum and the output so far are scaled by
-// exp2(M_old - M_new) when it grows).  A
-// split that saw no key of the row (m = -inf: only later splits of a
-// multi-token row) contributes nothing; the first split always holds key 0.
-// Rows are (query token, head in group); pairs with fewer rows than the
-// largest skip the rest.
-// What a warp reads of the plan for that: the header's counts and its first
-// pair.  (The plan's lists are read through L2: the plan kernel ran two
+// What a warp reads of the plan for the merge: the header's counts and its
+// first pair.  (The plan's lists are read through L2: the plan kernel ran two
 // launches before this one.)
 struct CombineStart {
   int max_rows, n_items;
@@ -36,6 +27,15 @@ __device__ __forceinline__ CombineStart combine_start(const Workspace& ws, int w
   if (warp_id < s.n_items) s.first = load_pair(ws, warp_id / s.max_rows);
   return s;
 }
+// Merge of split results: one (split pair, query row) per warp (warp_id of
+// n_warps in the grid), four output columns per lane, the splits merged in
+// one pass with the online-softmax identity the decode loop uses between
+// pages (a running max M; the sum and the output so far are scaled by
+// exp2(M_old - M_new) when it grows).  A
+// split that saw no key of the row (m = -inf: only later splits of a
+// multi-token row) contributes nothing; the first split always holds key 0.
+// Rows are (query token, head in group); pairs with fewer rows than the
+// largest skip the rest.
 __device__ __forceinline__ void combine_splits(const AttnArgs& a, const Workspace& ws, int warp_id,
                                                int n_warps, const CombineStart& start) {
   const int G = a.hq / a.hkv;

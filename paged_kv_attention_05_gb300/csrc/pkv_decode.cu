@@ -42,7 +42,9 @@
 //     end of the prefill kernel's launch for bf16 calls, in the combine
 //     kernel below for int8 calls.  Every mbarrier wait is bounded.
 // The int8-cache variant of the decode kernel is in pkv_decode_i8.cu; it
-// shares the plan, the work units and the merge.
+// shares the plan, the work units and the merge.  pkv_attention_scored runs
+// instances of the two kernels here with its scores in step_logits (see Mode);
+// its units begin at the page of the first key that a row's window lets it see.
 #include "pkv_combine.cuh"
 #include "pkv_device.cuh"
 #include "pkv_score.cuh"
@@ -95,23 +97,25 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Whether this CTA leaves its SM to the prefill grid, launched after this
-// one as its programmatic dependent: when the step has prefill items, the
-// first P CTAs of the decode grid exit at once, so that the prefill items
-// run on their SMs beside the decode units on the others (the prefill kernel
-// does not wait for this grid before its items).  P is the number of SMs on
+// How many SMs are left to the prefill grid, launched after this one as its
+// programmatic dependent: when the step has prefill items, the first P CTAs
+// of the decode grid exit at once, so that the prefill items run on their SMs
+// beside the decode units on the others (the prefill kernel does not wait for
+// this grid before its items).  P is the number of SMs on
 // which the prefill's key-tile steps (items x tiles) fit into the longest
 // item's chain, at most one per item and half of the SMs: fewer would
 // lengthen the prefill, more would take SMs the decode units need and sit
 // idle once the items are done.  When the decode units fill fewer CTAs than
 // the grid has (units_per_cta at a time each), the spare SMs would idle
-// anyway: P then grows up to one per item (still at most half of the SMs).
+// anyway: P then grows up to one per item (still at most half of the SMs; the
+// single-head items of a scored call take an SM each, see single_head_items).
 // Every CTA computes the same from the plan header (read after the plan
-// wait): P.
+// wait): P, 0 without prefill items.
+template <bool kScored>
 __device__ __forceinline__ int sms_to_prefill(const AttnArgs& a, const Workspace& ws,
                                               int units_per_cta) {
   const int G = a.hq / a.hkv;
-  const bool single = single_head_items(a, ws.hdr->n_pre_entries, gridDim.x);
+  const bool single = kScored && single_head_items(a, ws.hdr->n_pre_entries, gridDim.x);
   const int per_entry = G % 2 == 0 && !single ? a.hq / 2 : a.hq;  // items per entry
   const int items = ws.hdr->n_pre_entries * per_entry;
   if (items == 0) return 0;
@@ -123,6 +127,11 @@ __device__ __forceinline__ int sms_to_prefill(const AttnArgs& a, const Workspace
   if (spare > p) p = min(cap, spare);
   return max(p, 1);
 }
+__device__ __forceinline__ bool leaves_sm_to_prefill(const AttnArgs& a, const Workspace& ws,
+                                                     int units_per_cta) {
+  return (int)blockIdx.x < sms_to_prefill<false>(a, ws, units_per_cta);
+}
+
 // a work unit written by the plan kernel
 __device__ __forceinline__ DecUnit load_unit(const DecUnit* p) {
   const int4 w0 = __ldcg(reinterpret_cast<const int4*>(p));
@@ -143,7 +152,7 @@ __device__ __forceinline__ FirstUnit first_unit(const AttnArgs& a, const Workspa
   FirstUnit f;
   f.index = worker * gridDim.x + blockIdx.x;  // (the list has room for a unit a worker)
   f.unit = load_unit(ws.units + f.index);
-  const int p = sms_to_prefill(a, ws, per_cta);
+  const int p = sms_to_prefill<true>(a, ws, per_cta);
   f.after = (gridDim.x - p) * per_cta;
   if (p > 0) {
     f.index = worker * (gridDim.x - p) + blockIdx.x - p;
@@ -297,13 +306,14 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
   // the set-up above overlaps the plan kernel; the work list is read after it
   grid_dep_wait();
   grid_dep_launch();
-  int left = 0;
   FirstUnit mine{};
-  if (kScored)
+  if constexpr (kScored) {
+    int left = 0;
     mine = first_unit(a, ws, warp, C::kWarps, &left);
-  else
-    left = sms_to_prefill(a, ws, C::kWarps);
-  if ((int)blockIdx.x < left || ws.hdr->n_dec_units == 0) return;
+    if ((int)blockIdx.x < left || ws.hdr->n_dec_units == 0) return;
+  } else {
+    if (leaves_sm_to_prefill(a, ws, C::kWarps) || ws.hdr->n_dec_units == 0) return;
+  }
   __syncthreads();
 
   const int n_units = ws.hdr->n_dec_units;
@@ -455,7 +465,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         float xs[2][4];
         if (kScored)
           step_logits<2, kFixed>(sp, sacc, rs, vis[0], vis[1], pos0 + tig * 2,
-                         pos0 < all_lo || pos0 + 16 > all_hi);
+                                 pos0 < all_lo || pos0 + 16 > all_hi);
         float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
@@ -652,13 +662,14 @@ __global__ void __launch_bounds__(CfgP::kThreads, 1)
   // the set-up above overlaps the plan kernel; the work list is read after it
   grid_dep_wait();
   grid_dep_launch();
-  int left = 0;
   FirstUnit mine{};
-  if (kScored)
+  if constexpr (kScored) {
+    int left = 0;
     mine = first_unit(a, ws, pair, C::kPairs, &left);
-  else
-    left = sms_to_prefill(a, ws, C::kPairs);
-  if ((int)blockIdx.x < left || ws.hdr->n_dec_units == 0) return;
+    if ((int)blockIdx.x < left || ws.hdr->n_dec_units == 0) return;
+  } else {
+    if (leaves_sm_to_prefill(a, ws, C::kPairs) || ws.hdr->n_dec_units == 0) return;
+  }
   __syncthreads();
 
   const int n_units = ws.hdr->n_dec_units;
@@ -836,7 +847,7 @@ __global__ void __launch_bounds__(CfgP::kThreads, 1)
         float xs[4][4];
         if (kScored)
           step_logits<4, kFixed>(sp, sacc, rs, vis, vis, pos0 + tig * 2,
-                         pos0 < vlow || pos0 + 32 > vis);
+                                 pos0 < vlow || pos0 + 32 > vis);
         float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
@@ -1007,8 +1018,8 @@ cudaError_t launch_pair(const AttnArgs& a, const Workspace& ws, int sms, cudaStr
   if (!make_cache_map(&tk, a.kc, a.num_blocks, a.hkv) ||
       !make_cache_map(&tv, a.vc, a.num_blocks, a.hkv))
     return cudaErrorInvalidValue;
-  return launch_dependent(decode_pair_kernel<kMode>, dim3(sms), dim3(CfgP::kThreads), CfgP::kSmem, st,
-                          tk, tv, a, ws);
+  return launch_dependent(decode_pair_kernel<kMode>, dim3(sms), dim3(CfgP::kThreads), CfgP::kSmem,
+                          st, tk, tv, a, ws);
 }
 
 }  // namespace

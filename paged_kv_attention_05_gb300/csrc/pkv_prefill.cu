@@ -42,6 +42,9 @@
 //               64-column halves, divide by the row sum, release O_x to the
 //               next item's first P.V and write the bf16 rows to global memory
 //               through a per-warp staging area (whole 64-byte row pieces).
+// pkv_attention_scored runs instances with softmax warps of their own kind (8
+// or 16, a set for each query tile; described there), whose key tiles start at
+// the window's first page; the other roles are the same.
 // Every mbarrier wait is bounded; on expiry the kernel records
 // PKV_DEV_ERR_TIMEOUT, stops issuing work, frees its TMEM and returns.
 #include <type_traits>
@@ -128,7 +131,6 @@ __device__ __forceinline__ int tile_key0(const Item& it, int j) {
     t = j + 1 < it.nkv ? j + 1 : 0;
   return it.base + t * kTileK;
 }
-
 
 // a prefill entry written by the plan kernel, read through L2
 __device__ __forceinline__ PreEntry load_entry(const PreEntry* p) {
@@ -621,8 +623,9 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap), 1)
         const uint32_t d = tmem + 256 + x * 128, pa = tmem + x * 128;
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          mma_ts(d, pa + (kScored ? (kk >> 1) * 32 + (kk & 1) * 8 : (kk >> 2) * 64 + (kk & 3) * 8), db + ((kk * 16 * 128) >> 4), id_o,
-                 (acc || kk > 0) ? 1u : 0u);
+          mma_ts(d,
+                 pa + (kScored ? (kk >> 1) * 32 + (kk & 1) * 8 : (kk >> 2) * 64 + (kk & 3) * 8),
+                 db + ((kk * 16 * 128) >> 4), id_o, (acc || kk > 0) ? 1u : 0u);
       };
       bool ok = true;
       for (uint32_t it_cnt = 0; ok; ++it_cnt) {
@@ -699,12 +702,13 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap), 1)
     //     straight code, checked at its end, and redone if the check fails (P
     //     has not left the registers, the scores are still in TMEM).  Block
     //     path: any block, masks, new maxima, in a loop.
-    // 8 prompts of 2048 tokens, 64 heads over 8, us: without options 452, bias
-    // 475, cap 526 (scores past a quarter of the cap 602, past half 760),
-    // window of 1024 389; the plain call 500 (with scores of three times the
-    // size its repeated maxima take it to 648).  Bound, with the cap, by the
+    // 8 prompts of 2048 tokens, 64 heads over 8, us: without options 471, bias
+    // 502, cap 539 (scores past a quarter of the cap 602, past half 758),
+    // window of 1024 407; the plain call 495 (with scores of three times the
+    // size its repeated maxima take it to 653).  Bound, with the cap, by the
     // softmax warps' issue slots (a packed operation takes two) and the chain S
-    // -> P -> P.V of a tile.  Measured and not kept, for the cap: a row's 128
+    // -> P -> P.V of a tile.  Measured and not kept, for the cap (526 at the
+    // time, with row sums of the unrounded weights): a row's 128
     // or 64 columns in straight code with all of its forms in place (730 to
     // 2229: instruction-cache misses); two warps a row as in the plain call
     // (573); four warps a row and tile (566); a row per thread (530 to 608); a
@@ -1188,7 +1192,8 @@ cudaError_t launch_prefill_as(const AttnArgs& a, const Workspace& ws, int sms, c
       !make_cache_map(&tk, a.kc, a.num_blocks, a.hkv) ||
       !make_cache_map(&tv, a.vc, a.num_blocks, a.hkv))
     return cudaErrorInvalidValue;
-  return launch_dependent(kernel, dim3(sms), dim3(threads_of(kCap == kFixedCap)), kSmemBytes, st, tq, tk, tv, a, ws);
+  return launch_dependent(kernel, dim3(sms), dim3(threads_of(kCap == kFixedCap)), kSmemBytes, st,
+                          tq, tk, tv, a, ws);
 }
 
 }  // namespace

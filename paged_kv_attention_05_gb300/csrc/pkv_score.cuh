@@ -65,7 +65,7 @@ __device__ __forceinline__ void cap_values(float (&s)[kN], const ScoreArgs& sp, 
 // + max_bias, exp2(y - reference) is at most 2^(cap2 / 2), and at least 2^(-3/2
 // cap2) for the key of that bias: inside fp32's and bf16's exponents for cap2 <=
 // 80 (caps up to 55) with room for the sums.  No maximum is looked for then and
-// nothing is rescaled. 
+// nothing is rescaled.
 constexpr float kFixedCap2 = 80.f;
 inline bool fixed_reference(const AttnArgs& a) {
   return a.score.softcap > 0.f && a.score.cap2 <= kFixedCap2 && a.score.limit3 > 0.f;
@@ -81,7 +81,7 @@ __device__ __forceinline__ float max_bias(float slope2, int pos, int first, int 
 // for each other.  (A prompt of 300 tokens, 32 heads: 16.8 us, in pairs 18.9; of
 // 17 tokens 13.3, 14.0.)
 __device__ __forceinline__ bool single_head_items(const AttnArgs& a, int n_pre, int sms) {
-  return a.score.on && (long long)n_pre * a.hq * 4 <= 3LL * sms;
+  return (long long)n_pre * a.hq * 4 <= 3LL * sms;
 }
 
 }  // namespace dev
