@@ -78,8 +78,8 @@ __device__ __forceinline__ float max_bias(float slope2, int pos, int first, int 
 
 // Whether a scored call's prefill items are single query heads: where even so
 // they leave a quarter of the SMs idle, two heads of an item would only wait
-// for each other.  (A prompt of 300 tokens, 32 heads: 16.8 us, in pairs 18.9; of
-// 17 tokens 13.3, 14.0.)
+// for each other.  (32 heads, cap 30, us a call, single and in pairs: a prompt
+// of 17 tokens 11.5, 12.7; 64 tokens 12.1, 13.5; 300 tokens 14.9, 16.6.)
 __device__ __forceinline__ bool single_head_items(const AttnArgs& a, int n_pre, int sms) {
   return (long long)n_pre * a.hq * 4 <= 3LL * sms;
 }
