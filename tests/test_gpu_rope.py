@@ -377,3 +377,30 @@ def test_rotated_step_then_attention_matches_the_oracle():
     got = out.float().cpu().numpy().astype(np.float64)
     assert_close(got[:300], ref[:300], "rotated step")
     assert np.isnan(got[300:]).all()
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_the_calls_of_plain_arguments(int8):
+    """pkv_write_rope and pkv_write_rope_int8 themselves (the binding passes a
+    struct): the same bits, two different weights and every stride its own."""
+    from paged_kv_attention_05_gb300 import _binding
+    c = Case(40, 6, 3, rot=96, interleaved=True, qn=True, kn=True, offset=1.0, pad=2, int8=int8)
+    c.run()
+    c.check()
+    want = [t.clone() for t in (c.q_out, c.kc, c.vc)]
+    wide = torch.full((c.rows, c.hq + 1, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    kc, vc = c.kc0.cuda(), c.vc0.cuda()
+    k = torch.nn.functional.pad(c.k, (0, 0, 0, 2)).contiguous()
+    p = [t.data_ptr() for t in (c.q, k, c.v, *c.w, c.dev[1], c.dev[0], wide, kc, vc, c.dev[2])]
+    head = (p[0], c.q.stride(0), c.hq, p[1], k.stride(0), p[2], c.v.stride(0), p[3], p[4], 1.0,
+            1e-6, p[5], c.table.shape[0], c.rot, 1, p[6], p[7], wide.stride(0), p[8], p[9])
+    tail = (kc.shape[0], 16, c.hkv, D, p[10], c.rows, torch.cuda.current_stream().cuda_stream)
+    lib = _binding.load()
+    if int8:
+        assert lib.pkv_write_rope_int8(*head, c.ks, c.vs, *tail) == 0
+    else:
+        assert lib.pkv_write_rope(*head, *tail) == 0
+    assert pkv.pkv_get_error() == 0
+    assert torch.isnan(wide[:, c.hq].float()).all()
+    for got, ref in zip((wide[:, :c.hq].contiguous(), kc, vc), want):
+        assert torch.equal(got.view(torch.int8), ref.contiguous().view(torch.int8))

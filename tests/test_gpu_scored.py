@@ -506,3 +506,26 @@ def test_layers_of_a_step_together():
         ref, tol = reference(ds, **opt)
         assert_near(ds.out[:300], ref, tol, str(opt))
         assert torch.isnan(ds.out[300:].float()).all()
+
+
+def test_the_call_of_plain_arguments():
+    """pkv_attention_scored itself (the binding passes a struct): the same bits,
+    with all four options and a row stride of its own for out."""
+    from paged_kv_attention_05_gb300 import _binding
+    ds = DeviceStep(W.build(W.custom([300, 0, 77, 500], [1, 140, 3, 1], 8, 2, seed=12)))
+    ds.write()
+    opt = dict(softcap=20.0, window=90, slopes=slopes_for(8), prefix=[10, 100, 0, 501])
+    call(ds, **opt)
+    n = int(ds.step.query_start_loc[-1])
+    sl = opt["slopes"].cuda()
+    px = torch.tensor(opt["prefix"], dtype=torch.int32).cuda()
+    wide = torch.full((ds.out.shape[0], 9, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+    t = [x.data_ptr() for x in (ds.q, ds.key_cache, ds.value_cache, ds.qsl, ds.seq_lens,
+                                ds.block_table, sl, px, wide)]
+    rc = _binding.load().pkv_attention_scored(
+        t[0], ds.q.stride(0), ds.q.shape[0], 8, t[1], t[2], ds.key_cache.shape[0], 16, 2, D, t[3],
+        t[4], t[5], ds.block_table.shape[1], ds.step.num_reqs, ds.step.scale, 20.0, 90, t[6], t[7],
+        t[8], wide.stride(0), torch.cuda.current_stream().cuda_stream)
+    assert rc == 0 and pkv.pkv_get_error() == 0
+    assert torch.isnan(wide[:, 8].float()).all()
+    assert torch.equal(wide[:n, :8].contiguous().view(torch.int16), ds.out[:n].view(torch.int16))
