@@ -177,7 +177,7 @@ Sizes sizes_for(int64_t reqs, int64_t q_rows, int64_t bt_width, int hq, int hkv)
   return z;
 }
 
-void set_score_form(AttnArgs& a) {
+void set_score_form(ScoredArgs& a) {
   ScoreArgs& s = a.score;
   const double log2e = 1.4426950408889634, lin = a.scale * log2e;
   auto both = [](double x) {
@@ -490,7 +490,7 @@ int plan_locked(DeviceState* s, int64_t q_rows, int32_t num_heads, int32_t num_k
   Workspace ws;
   int rc = ensure_workspace(s, z, st, &ws);
   if (rc) return rc;
-  AttnArgs a{};
+  ScoredArgs a{};
   a.q_rows = q_rows;
   a.hq = num_heads;
   a.hkv = num_kv_heads;
@@ -522,7 +522,7 @@ int run_locked(DeviceState* s, const void* q, int64_t q_row_stride, const void* 
                float scale, void* out, int64_t out_row_stride, int kv_int8, float k_scale,
                float v_scale, const ScoreArgs& score, cudaStream_t st) {
   Workspace ws = carve_workspace(s->ws, s->plan_sizes, s->err);
-  AttnArgs a{};
+  ScoredArgs a{};
   a.q = static_cast<const uint16_t*>(q);
   a.q_stride = q_row_stride;
   a.q_rows = s->plan_q_rows;

@@ -200,15 +200,15 @@ struct RowScore {
 };
 // The row at position pos of request r (L keys), head h; *vis (keys it sees end
 // here) grows to the request's prefix, clipped to the unit.
-__device__ __forceinline__ RowScore row_score(const AttnArgs& a, int r, int L, int pos, int h,
+__device__ __forceinline__ RowScore row_score(const ScoreArgs& sp, int r, int L, int pos, int h,
                                               int k1, int* vis) {
   RowScore s;
   s.pos = pos;
-  s.low = first_key(pos, a.score.window);
-  s.slope2 = a.score.slopes ? __ldg(a.score.slopes + h) * kLog2e : 0.f;
+  s.low = first_key(pos, sp.window);
+  s.slope2 = sp.slopes ? __ldg(sp.slopes + h) * kLog2e : 0.f;
   int last = pos;
-  if (a.score.prefix) {
-    const int p = clip_prefix(__ldg(a.score.prefix + r), L);
+  if (sp.prefix) {
+    const int p = clip_prefix(__ldg(sp.prefix + r), L);
     *vis = max(*vis, min(k1, p));
     last = max(pos, p - 1);
   }
@@ -274,7 +274,8 @@ __device__ __forceinline__ void step_logits(const ScoreArgs& sp, float (&s2)[kTi
 template <int kMode>
 __global__ void __launch_bounds__(Cfg::kThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                  const __grid_constant__ CUtensorMap tm_v, AttnArgs a, Workspace ws) {
+                  const __grid_constant__ CUtensorMap tm_v, ArgsOf<kMode != kPlain> a,
+                  Workspace ws) {
   using C = Cfg;
   constexpr bool kScored = kMode != kPlain, kFixed = kMode == kFixedRef;
   extern __shared__ uint8_t smem_raw[];
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
   const int n_units = ws.hdr->n_dec_units;
   const uint64_t pol = l2_evict_first();  // K/V pages are read once
   const float sl2 = a.scale * kLog2e;
-  const ScoreArgs& sp = a.score;
+  const ScoreArgs& sp = score_of(a);
   const int gid = lane >> 2, tig = lane & 3;
   const int mi = lane >> 3, rr = lane & 7;
   uint32_t page_cnt = 0;
@@ -372,14 +373,14 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     // head) sees keys < ctx + i + 1, clipped to the unit
     int vis[2];
     RowScore rs[2];
-    const int vlow = kScored ? first_key(un.ctx, a.score.window) : 0;  // no row sees keys below
+    const int vlow = kScored ? first_key(un.ctx, sp.window) : 0;  // no row sees keys below
 #pragma unroll
     for (int hrow = 0; hrow < 2; ++hrow) {
       const int row = (lane >> 2) + hrow * 8;
       const int ti = row < nrows ? row / G : qn - 1;
       vis[hrow] = min(k1, un.ctx + ti + 1);
       if (kScored)
-        rs[hrow] = row_score(a, un.r, un.ctx + qn, un.ctx + ti,
+        rs[hrow] = row_score(sp, un.r, un.ctx + qn, un.ctx + ti,
                              row < nrows ? ug * G + row % G : ug * G, k1, &vis[hrow]);
     }
     // every row of the unit sees the keys from all_lo up to all_hi
@@ -629,7 +630,8 @@ static_assert(CfgP::kSmem <= 232448, "shared memory per CTA");
 template <int kMode>
 __global__ void __launch_bounds__(CfgP::kThreads, 1)
     decode_pair_kernel(const __grid_constant__ CUtensorMap tm_k,
-                       const __grid_constant__ CUtensorMap tm_v, AttnArgs a, Workspace ws) {
+                       const __grid_constant__ CUtensorMap tm_v, ArgsOf<kMode != kPlain> a,
+                       Workspace ws) {
   using C = CfgP;
   constexpr bool kScored = kMode != kPlain, kFixed = kMode == kFixedRef;
   extern __shared__ uint8_t smem_raw[];
@@ -675,7 +677,7 @@ __global__ void __launch_bounds__(CfgP::kThreads, 1)
   const int n_units = ws.hdr->n_dec_units;
   const uint64_t pol = l2_evict_first();  // K/V pages are read once
   const float sl2 = a.scale * kLog2e;
-  const ScoreArgs& sp = a.score;
+  const ScoreArgs& sp = score_of(a);
   const int gid = lane >> 2, tig = lane & 3;
   const int mi = lane >> 3, rr = lane & 7;
   const int roff = 16 * tile;  // this warp's rows (heads of the group)
@@ -770,11 +772,11 @@ __global__ void __launch_bounds__(CfgP::kThreads, 1)
     // every row sees keys < ctx + 1, clipped to the unit
     int vis = min(k1, un.ctx + 1);
     RowScore rs[2];
-    const int vlow = kScored ? first_key(un.ctx, a.score.window) : 0;
+    const int vlow = kScored ? first_key(un.ctx, sp.window) : 0;
     if (kScored) {
 #pragma unroll
       for (int hrow = 0; hrow < 2; ++hrow)
-        rs[hrow] = row_score(a, un.r, un.ctx + 1, un.ctx,
+        rs[hrow] = row_score(sp, un.r, un.ctx + 1, un.ctx,
                              ug * G + min(roff + gid + 8 * hrow, G - 1), k1, &vis);
     }
     // the A fragments of the warp's 16 query rows (heads roff + gid and
@@ -996,7 +998,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(AttnArgs a, Wo
 }
 
 template <int kMode>
-cudaError_t launch_one_tile(const AttnArgs& a, const Workspace& ws, int sms, cudaStream_t st) {
+cudaError_t launch_one_tile(const ScoredArgs& a, const Workspace& ws, int sms, cudaStream_t st) {
   using C = Cfg;
   static std::atomic<bool> attr[kMaxAttrDevices];
   if (cudaError_t e = smem_attr_once(decode_kernel<kMode>, C::kSmem, attr)) return e;
@@ -1011,7 +1013,7 @@ cudaError_t launch_one_tile(const AttnArgs& a, const Workspace& ws, int sms, cud
 }
 
 template <int kMode>
-cudaError_t launch_pair(const AttnArgs& a, const Workspace& ws, int sms, cudaStream_t st) {
+cudaError_t launch_pair(const ScoredArgs& a, const Workspace& ws, int sms, cudaStream_t st) {
   static std::atomic<bool> attr[kMaxAttrDevices];
   if (cudaError_t e = smem_attr_once(decode_pair_kernel<kMode>, CfgP::kSmem, attr)) return e;
   CUtensorMap tk, tv;  // (query rows: plain loads, 16-byte aligned by the API's checks)
@@ -1028,7 +1030,7 @@ int decode_workers(int group, int kv_int8, int sms) {
   return sms * (kv_int8 ? decode_i8_warps(group) : (group <= 16 ? Cfg::kWarps : CfgP::kPairs));
 }
 
-cudaError_t launch_decode(const AttnArgs& a, const Workspace& ws, int sms, cudaStream_t st) {
+cudaError_t launch_decode(const ScoredArgs& a, const Workspace& ws, int sms, cudaStream_t st) {
   const int G = a.hq / a.hkv;
   if (a.kv_int8) return launch_decode_i8(a, ws, sms, st);
   const bool one = G <= 16;

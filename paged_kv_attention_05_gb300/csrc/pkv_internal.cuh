@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 #include <utility>
 
 #include "pkv.h"
@@ -173,10 +174,6 @@ struct ScoreArgs {
   float limit2 = -1.f, limit3 = -1.f;
   unsigned long long deg2[3] = {}, deg3[4] = {}, lin2 = 0;
 };
-struct AttnArgs;
-// Fills those from a.scale and a.score.softcap.
-void set_score_form(AttnArgs& a);
-
 // First key any row of a request sees, rounded down to its page: the keys a
 // decode request's units cover start here (ctx = keys before its first row).
 __host__ __device__ inline int first_key(int ctx, int window) {
@@ -212,8 +209,19 @@ struct AttnArgs {
   int kv_int8;
   float k_scale;
   float v_scale;
+};
+
+// The launchers take the arguments with the scores'; the kernels of the plain
+// calls get them without (168 bytes less to pass at each launch).
+struct ScoredArgs : AttnArgs {
   ScoreArgs score;
 };
+template <bool kScored>
+using ArgsOf = std::conditional_t<kScored, ScoredArgs, AttnArgs>;
+__host__ __device__ inline const ScoreArgs& score_of(const ScoredArgs& a) { return a.score; }
+__host__ __device__ inline ScoreArgs score_of(const AttnArgs&) { return ScoreArgs(); }
+// Fills what the kernels take of scale and softcap.
+void set_score_form(ScoredArgs& a);
 
 // TMA descriptors (pkv_tma.cu).  rows map: [rows, heads, 128] bf16 with a row
 // stride, box = 64 columns x box_heads x box_rows; cache map: [num_blocks, 16,
@@ -244,8 +252,8 @@ struct PrepArgs {
 };
 cudaError_t launch_prepare(const PrepArgs& p, int sms, cudaStream_t st);
 
-cudaError_t launch_plan(const AttnArgs& a, const Workspace& ws, int dec_grid, cudaStream_t st);
-cudaError_t launch_decode(const AttnArgs& a, const Workspace& ws, int sms, cudaStream_t st);
+cudaError_t launch_plan(const ScoredArgs& a, const Workspace& ws, int dec_grid, cudaStream_t st);
+cudaError_t launch_decode(const ScoredArgs& a, const Workspace& ws, int sms, cudaStream_t st);
 // the decode path over int8 caches (pkv_decode_i8.cu)
 cudaError_t launch_decode_i8(const AttnArgs& a, const Workspace& ws, int sms, cudaStream_t st);
 cudaError_t launch_combine(const AttnArgs& a, const Workspace& ws, int sms, cudaStream_t st);
@@ -253,7 +261,7 @@ cudaError_t launch_combine(const AttnArgs& a, const Workspace& ws, int sms, cuda
 // and cache type; the plan sizes its split chunks for this many.
 int decode_workers(int group, int kv_int8, int sms);
 int decode_i8_warps(int group);
-cudaError_t launch_prefill(const AttnArgs& a, const Workspace& ws, int sms, cudaStream_t st);
+cudaError_t launch_prefill(const ScoredArgs& a, const Workspace& ws, int sms, cudaStream_t st);
 
 // Programmatic dependent launch.  The cache write and the attention kernels
 // (plan, decode, prefill; the merge for int8 calls) are launched with programmatic stream

@@ -138,7 +138,7 @@ extern "C" int pkv_attention_noalloc(const void* q, int64_t q_row_stride, int64_
   Sizes zc = with_wave_room(z, q_rows, group, decode_workers(group, 0, sms));
   if (workspace_bytes(zc) > kScratchBytes) zc = z;
   Workspace ws = carve_workspace(scratch, zc, err);
-  AttnArgs a;
+  ScoredArgs a;
   a.q = static_cast<const uint16_t*>(q);
   a.q_stride = q_row_stride;
   a.q_rows = q_rows;

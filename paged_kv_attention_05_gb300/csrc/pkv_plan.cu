@@ -107,7 +107,7 @@ struct ReqInfo {
 };
 
 template <bool kScored>
-__device__ ReqInfo classify(const AttnArgs& a, int r) {
+__device__ ReqInfo classify(const ArgsOf<kScored>& a, int r) {
   ReqInfo ri{0, 0, 0, 0, 0, 0};
   const int q0 = __ldcg(a.qsl + r), q1 = __ldcg(a.qsl + r + 1), L = __ldcg(a.seq_lens + r);
   int bad = 0;
@@ -124,7 +124,7 @@ __device__ ReqInfo classify(const AttnArgs& a, int r) {
   ri.n = q1 - q0;
   ri.L = L;
   ri.q0 = q0;
-  if (kScored) ri.kb = first_page_key(ri.L - ri.n, a.score.window);
+  if (kScored) ri.kb = first_page_key(ri.L - ri.n, score_of(a).window);
   // decode: the query tokens x heads of a KV head fit one decode unit's rows
   // (speculative / multi-token decode included); prefill: anything longer
   const int G = a.hq / a.hkv;
@@ -139,14 +139,14 @@ __device__ ReqInfo classify(const AttnArgs& a, int r) {
 // The keys a prefill entry reads: rows 128 t .. of a request of n rows, L keys
 // and (scored calls) a prefix clipped to L; *base = first key, page aligned.
 template <bool kScored>
-__device__ __forceinline__ int entry_tiles(const AttnArgs& a, int n, int L, int t, int prefix,
-                                           int* base) {
+__device__ __forceinline__ int entry_tiles(const ArgsOf<kScored>& a, int n, int L, int t,
+                                           int prefix, int* base) {
   const int ctx = L - n;
   int hi = ctx + min(kPreTileQ * (t + 1), n);
   *base = 0;
   if (kScored) {
     hi = max(hi, prefix);
-    *base = first_page_key(ctx + kPreTileQ * t, a.score.window);
+    *base = first_page_key(ctx + kPreTileQ * t, score_of(a).window);
   }
   return (hi - *base + kPreTileQ - 1) / kPreTileQ;
 }
@@ -154,7 +154,7 @@ __device__ __forceinline__ int entry_tiles(const AttnArgs& a, int n, int L, int 
 __host__ __device__ constexpr int plan_ints(int threads) { return 9 * threads + 3; }
 
 template <bool kScored>
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(AttnArgs a, Workspace ws,
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(ArgsOf<kScored> a, Workspace ws,
                                                             int dec_grid) {
   __shared__ int4 smem33[33], smem33b[33];
   __shared__ long long red[32];
@@ -188,7 +188,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(AttnArgs a, Workspac
     } else if (ri.kind == 2) {
       // query tile t (rows up to min(128 (t + 1), n)) reads ctx + its last row
       // keys; the last tile reads them all
-      const int pfx = kScored && a.score.prefix ? clip_prefix(__ldcg(a.score.prefix + r), ri.L) : 0;
+      const int32_t* prefix = score_of(a).prefix;
+      const int pfx = kScored && prefix ? clip_prefix(__ldcg(prefix + r), ri.L) : 0;
       for (int t = 0; t * kPreTileQ < ri.n; ++t) {
         int base;
         const int tiles = entry_tiles<kScored>(a, ri.n, ri.L, t, pfx, &base);
@@ -427,7 +428,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(AttnArgs a, Workspac
       const int cnt_u = s_off_u[lo + 1] - s_off_u[lo];
       if (cnt_u == 0) continue;
       const int L = s_len[lo], qn = s_n[lo];
-      const int kb = kScored ? first_page_key(L - qn, a.score.window) : 0;
+      const int kb = kScored ? first_page_key(L - qn, score_of(a).window) : 0;
       const int nsplit = (L - kb + chunk - 1) / chunk, nfull = (L - kb) / chunk;
       for (int rem = ln; rem < cnt_u; rem += 32) {
         const int sp = rem / a.hkv, g = rem - sp * a.hkv;
@@ -456,8 +457,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(AttnArgs a, Workspac
       const int t = (n + kPreTileQ - 1) / kPreTileQ - 1 - (i - s_off_t[lo]);
       const int64_t idx = (int64_t)pre_carry + i;
       if (idx >= ws.max_pre) break;
-      const int pfx =
-          kScored && a.score.prefix ? clip_prefix(__ldcg(a.score.prefix + base + lo), L) : 0;
+      const int32_t* prefix = score_of(a).prefix;
+      const int pfx = kScored && prefix ? clip_prefix(__ldcg(prefix + base + lo), L) : 0;
       int kb;
       const int tiles = entry_tiles<kScored>(a, n, L, t, pfx, &kb);
       int4* dst = reinterpret_cast<int4*>(ws.pre + idx);
@@ -509,15 +510,18 @@ constexpr size_t plan_smem(bool scored, int threads) {
 
 }  // namespace
 
-cudaError_t launch_plan(const AttnArgs& a, const Workspace& ws, int dec_grid, cudaStream_t st) {
+cudaError_t launch_plan(const ScoredArgs& a, const Workspace& ws, int dec_grid, cudaStream_t st) {
   // a thread per request of a chunk (whole warps, at most 1024); one warp
   // of the grid per request of the first chunk, at most 16 CTAs
   const int threads = std::min(kPlanThreads, std::max(32, (a.num_reqs + 31) / 32 * 32));
   const int warps = threads / 32;
   const int want = (std::min(a.num_reqs, threads) + warps - 1) / warps;
   const int grid = std::max(1, std::min(16, want));
-  return launch_dependent(a.score.on ? plan_kernel<true> : plan_kernel<false>, dim3(grid),
-                          dim3(threads), plan_smem(a.score.on, threads), st, a, ws, dec_grid);
+  auto launch = [&](auto* kernel) {
+    return launch_dependent(kernel, dim3(grid), dim3(threads), plan_smem(a.score.on, threads), st, a,
+                            ws, dec_grid);
+  };
+  return a.score.on ? launch(plan_kernel<true>) : launch(plan_kernel<false>);
 }
 
 }  // namespace pkv

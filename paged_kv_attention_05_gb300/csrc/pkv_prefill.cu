@@ -375,7 +375,8 @@ __device__ __forceinline__ void rescale16_bf16(uint32_t t, float alpha) {
 template <bool kScored, Cap kCap, bool kBias, bool kSym>
 __global__ void __launch_bounds__(threads_of(kCap == kFixedCap), 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                   const __grid_constant__ CUtensorMap tm_v, AttnArgs a, Workspace ws) {
+                   const __grid_constant__ CUtensorMap tm_v, ArgsOf<kScored> a,
+                   Workspace ws) {
   // This grid is the programmatic dependent of the decode grid, which
   // triggers it after its own wait for the plan kernel: the plan is complete
   // when any CTA here runs, so the items start without waiting for the decode
@@ -526,7 +527,7 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap), 1)
       auto tile_key = [&](int j) { return tile_key0<kScored, kBias>(it, j); };
       auto tile_pages = [&](int key) { return min(8, (it.L - key + 15) / 16); };
       // first key any row of the item sees (its tiles start at this key's page)
-      const int vlow = kScored ? first_key(it.ctx + it.qt * kPreTileQ, a.score.window) : 0;
+      const int vlow = kScored ? first_key(it.ctx + it.qt * kPreTileQ, score_of(a).window) : 0;
       int blk_nxt = lane < tile_pages(tile_key(0)) ? __ldcg(btrow + (tile_key(0) >> 4) + lane) : 0;
       for (int j = 0; ok && j < it.nkv; ++j) {
         const uint32_t c = tile_cnt++;
@@ -722,7 +723,7 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap), 1)
     const int row = qd * 32 + lane;  // == TMEM lane
     const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
     float* lsum = reinterpret_cast<float*>(smem + kOffLsum);
-    const ScoreArgs& sp = a.score;
+    const ScoreArgs& sp = score_of(a);
     const uint32_t t_s = tmem + x * 128 + 32 * b0 + lane_off;
     const uint32_t t_o = tmem + 256 + x * 128 + lane_off;
     uint32_t s_cnt = 0;
@@ -745,8 +746,8 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap), 1)
       // in no decision, and their results are dropped
       const int rpos = it.ctx + (valid_row ? qrow : it.n - 1);
       const int last = max(rpos, it.prefix - 1);           // last visible key
-      const int first = first_key(rpos, a.score.window);   // first visible key
-      const float slope2 = kBias ? __ldg(a.score.slopes + (x ? it.hb : it.ha)) * kLog2e : 0.f;
+      const int first = first_key(rpos, sp.window);   // first visible key
+      const float slope2 = kBias ? __ldg(sp.slopes + (x ? it.hb : it.ha)) * kLog2e : 0.f;
       // The reference (log2 units) that the exponentials are taken against:
       // fixed (see fixed_reference), or the running maximum, rounded up to a
       // whole number, so that rescaling is exact; it follows the scores only
@@ -1183,7 +1184,7 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap), 1)
 }
 
 template <bool kScored, Cap kCap, bool kBias, bool kSym>
-cudaError_t launch_prefill_as(const AttnArgs& a, const Workspace& ws, int sms, cudaStream_t st) {
+cudaError_t launch_prefill_as(const ScoredArgs& a, const Workspace& ws, int sms, cudaStream_t st) {
   static std::atomic<bool> attr[kMaxAttrDevices];
   auto* kernel = prefill_kernel<kScored, kCap, kBias, kSym>;
   if (cudaError_t e = smem_attr_once(kernel, kSmemBytes, attr)) return e;
@@ -1198,7 +1199,7 @@ cudaError_t launch_prefill_as(const AttnArgs& a, const Workspace& ws, int sms, c
 
 }  // namespace
 
-cudaError_t launch_prefill(const AttnArgs& a, const Workspace& ws, int sms, cudaStream_t st) {
+cudaError_t launch_prefill(const ScoredArgs& a, const Workspace& ws, int sms, cudaStream_t st) {
   const ScoreArgs& sc = a.score;
   if (!sc.on) return launch_prefill_as<false, kNoCap, false, false>(a, ws, sms, st);
   const bool bias = sc.slopes != nullptr, sym = bias && sc.prefix != nullptr;

@@ -67,7 +67,7 @@ __device__ __forceinline__ void cap_values(float (&s)[kN], const ScoreArgs& sp, 
 // 80 (caps up to 55) with room for the sums.  No maximum is looked for then and
 // nothing is rescaled.
 constexpr float kFixedCap2 = 80.f;
-inline bool fixed_reference(const AttnArgs& a) {
+inline bool fixed_reference(const ScoredArgs& a) {
   return a.score.softcap > 0.f && a.score.cap2 <= kFixedCap2 && a.score.limit3 > 0.f;
 }
 // The largest -slope2 * |pos - j| over the keys first <= j <= last that a row at
