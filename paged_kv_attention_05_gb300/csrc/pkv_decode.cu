@@ -109,8 +109,15 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
 // the grid has (units_per_cta at a time each), the spare SMs would idle
 // anyway: P then grows up to one per item (still at most half of the SMs; the
 // single-head items of a scored call take an SM each, see single_head_items).
+// A scored call leaves fewer where its decodes take so long that the prefill
+// ends in their time all the same (kTilesPerStep: decode tiles of 128 keys, 64
+// KB, that all SMs read in the 3 us of a prefill step).  128 decodes of up to
+// 4096 keys beside a prompt of 1000 tokens: 200 -> 185 us; 64 decodes with 32 KV
+// heads beside two of 500: 436 -> 368; the prefill given half of that time 186,
+// 365, but 100 decodes beside two chunks of 700: 173 against 150.
 // Every CTA computes the same from the plan header (read after the plan
 // wait): P, 0 without prefill items.
+constexpr int kTilesPerStep = 320;
 template <bool kScored>
 __device__ __forceinline__ int sms_to_prefill(const AttnArgs& a, const Workspace& ws,
                                               int units_per_cta) {
@@ -124,7 +131,12 @@ __device__ __forceinline__ int sms_to_prefill(const AttnArgs& a, const Workspace
   const int cap = single ? items : min(items, (int)gridDim.x / 2);
   int p = (int)min((long long)cap, (steps + longest - 1) / longest);
   const int spare = (int)gridDim.x - (ws.hdr->n_dec_units + units_per_cta - 1) / units_per_cta;
-  if (spare > p) p = min(cap, spare);
+  if (spare > p) {
+    p = min(cap, spare);
+  } else if (kScored) {
+    const int room = ws.hdr->dec_tiles / kTilesPerStep - longest;
+    if (room > 0) p = min(p, (int)((steps + room - 1) / room));
+  }
   return max(p, 1);
 }
 __device__ __forceinline__ bool leaves_sm_to_prefill(const AttnArgs& a, const Workspace& ws,

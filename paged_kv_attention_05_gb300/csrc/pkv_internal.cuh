@@ -67,7 +67,8 @@ struct PlanHeader {
   int max_rows;     // most query rows of one split pair (qn * G)
   int pre_tiles;    // 128-key tiles of all prefill entries (one query head pair each)
   int pre_max_tiles;  // key tiles of the longest prefill entry
-  int pad[7];
+  int dec_tiles;    // 128-key tiles of all decode (request, KV head) pairs (scored calls)
+  int pad[6];
 };
 
 // Device pointers into the per-device workspace.

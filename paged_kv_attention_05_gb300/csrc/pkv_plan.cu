@@ -495,6 +495,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ArgsOf<kScored> a, W
     ws.hdr->max_rows = s_max_rows;
     ws.hdr->pre_tiles = red_t[0];
     ws.hdr->pre_max_tiles = red_m[0];
+    if (kScored) ws.hdr->dec_tiles = (int)min(total_keys * a.hkv / 128, (long long)INT_MAX);
   }
 }
 

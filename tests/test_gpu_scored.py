@@ -529,3 +529,14 @@ def test_the_call_of_plain_arguments():
     assert rc == 0 and pkv.pkv_get_error() == 0
     assert torch.isnan(wide[:, 8].float()).all()
     assert torch.equal(wide[:n, :8].contiguous().view(torch.int16), ds.out[:n].view(torch.int16))
+
+
+@pytest.mark.parametrize("name", ["off", "cap", "cap+bias+window+prefix"])
+@pytest.mark.parametrize("hq,hkv", [(16, 8), (32, 1), (9, 3)])
+def test_long_decodes_beside_a_short_prompt(hq, hkv, name):
+    """Many keys to decode and few to prefill: the SMs left to the prefill are a
+    few, which take several items each."""
+    n_dec = 24 * 8 // hkv if hkv > 1 else 40
+    ctx = [4000 + 3 * i for i in range(n_dec)] + [0, 60]
+    run_and_check(W.build(W.custom(ctx, [1] * n_dec + [300, 130], hq, hkv, seed=hq)), name,
+                  **options(name, hq, n_dec + 2, prefix=250))
