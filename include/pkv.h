@@ -284,7 +284,8 @@ int pkv_attention(const void* q, int64_t q_row_stride, int64_t q_rows, int32_t n
  * max(0, ctx - window + 1)) are not read, nor are their block_table entries,
  * so a cache that frees them may leave anything there.  A masked key's K may
  * hold anything.  V of a key that some row of the same request sees must be
- * finite: the rows that do not see it weigh it with an exact zero.
+ * finite: the rows that do not see it weigh it with an exact zero; and below
+ * 2^28 in size under a cap (the sums over keys are unnormalised fp32 ones).
  *
  * Other arguments, layouts, checks, alignment and errors are those of
  * pkv_attention (out must not overlap q; bf16 caches; any query_len; the plan

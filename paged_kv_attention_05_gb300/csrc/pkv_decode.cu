@@ -232,7 +232,7 @@ __device__ __forceinline__ RowScore row_score(const ScoreArgs& sp, int r, int L,
 // -inf for the keys a row does not see (any: some row of the unit sees not all
 // of the step's keys).  One form of the cap for the warp, chosen by the keys
 // its rows see, since the others may hold anything.
-// Fixed reference: minus it.
+// Fixed reference: minus it (see fixed_reference()).
 template <int kTiles, bool kFixed>
 __device__ __forceinline__ void step_logits(const ScoreArgs& sp, float (&s2)[kTiles][4],
                                             const RowScore (&rs)[2], int vis0, int vis1, int key0,
@@ -242,7 +242,6 @@ __device__ __forceinline__ void step_logits(const ScoreArgs& sp, float (&s2)[kTi
     const int j = key0 + 8 * (i >> 2) + (i & 1);
     return (i & 2) ? j >= rs[1].low && j < vis1 : j >= rs[0].low && j < vis0;
   };
-  const float nm = kFixed ? -0.5f * sp.cap2 : 0.f;
   if (kFixed || sp.softcap > 0.f) {
     float m0 = 0.f, m1 = 0.f;
     if (any) {
@@ -257,12 +256,12 @@ __device__ __forceinline__ void step_logits(const ScoreArgs& sp, float (&s2)[kTi
     const float m = fmaxf(m0, m1);
     float big = 0.f;
     if (__all_sync(0xffffffffu, m * m <= sp.limit3)) {
-      cap_values<kDeg3>(s, sp, nm, big);
+      cap_values<kDeg3>(s, sp, 0.f, big);
     } else if (!kFixed && sp.limit3 < 0.f && __all_sync(0xffffffffu, m * sp.k <= 1.f)) {
 #pragma unroll
       for (int i = 0; i < 4 * kTiles; ++i) s[i] = capped_poly(s[i], sp);
     } else {
-      cap_values<kExp>(s, sp, nm, big);
+      cap_values<kExp>(s, sp, 0.f, big);
     }
   } else {
 #pragma unroll
@@ -440,8 +439,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       for (int e = 0; e < 4; ++e) o[dn][e] = 0.f;
     float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
     if (kFixed) {
-      m_run[0] = 0.5f * sp.cap2 + rs[0].top;
-      m_run[1] = 0.5f * sp.cap2 + rs[1].top;
+      m_run[0] = rs[0].top;
+      m_run[1] = rs[1].top;
     }
 
     bool ok = true;
@@ -817,8 +816,8 @@ __global__ void __launch_bounds__(CfgP::kThreads, 1)
       for (int e = 0; e < 4; ++e) o[dn][e] = 0.f;
     float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
     if (kFixed) {
-      m_run[0] = 0.5f * sp.cap2 + rs[0].top;
-      m_run[1] = 0.5f * sp.cap2 + rs[1].top;
+      m_run[0] = rs[0].top;
+      m_run[1] = rs[1].top;
     }
 
     for (int j = 0; j < nsteps; ++j) {

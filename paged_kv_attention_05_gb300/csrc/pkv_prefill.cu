@@ -754,8 +754,7 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap), 1)
       // when a block's sum passes kMaxSum: bf16 keeps its precision over fp32's
       // exponents, so a reference below the maximum costs none, and 2^40 leaves
       // the sums room to 2^127.
-      float ref = kCap == kFixedCap ? 0.5f * sp.cap2 + max_bias(slope2, rpos, first, last)
-                                    : -INFINITY;
+      float ref = kCap == kFixedCap ? max_bias(slope2, rpos, first, last) : -INFINITY;
       float l = 0.f;
       if (form == 1 && --hold <= 0) form = 0;
       for (int j = 0; j < it.nkv; ++j) {

@@ -61,11 +61,18 @@ __device__ __forceinline__ void cap_values(float (&s)[kN], const ScoreArgs& sp, 
 }
 
 // Fixed-reference softmax.  A capped logit lies within +-cap2 (log2 units), and
-// a row's own bias term at most max_bias above it.  With the reference cap2 / 2
-// + max_bias, exp2(y - reference) is at most 2^(cap2 / 2), and at least 2^(-3/2
-// cap2) for the key of that bias: inside fp32's and bf16's exponents for cap2 <=
-// 80 (caps up to 55) with room for the sums.  No maximum is looked for then and
-// nothing is rescaled.
+// a row's own bias term at most max_bias above zero.  Taken against max_bias
+// alone, the weight of the key of that bias is between 2^-cap2 and 2^cap2, so
+// that no maximum is looked for and nothing is rescaled.  What cap2 <= 80 (caps up
+// to 55) leaves of fp32's exponents (bf16 has the same):
+//   below: a row's largest weight is at least 2^-80, and exp2 flushes below
+//     2^-126, so that a key further along the bias counts down to 2^-46 of it
+//     (2^19 keys less than that are 2^-27 of the sum), and the products of the
+//     largest with V keep all their bits for |V| >= 2^-46;
+//   above: a sum of 2^19 weights of 2^80 is 2^99: |V| up to 2^28.
+// (With half of cap2 more, the weights begin at 2^-120: at cap 55.4, with scores
+// at the cap's lower end, a bias loses all beyond six binades, 1.4% of a row's
+// weight at a slope of 0.02, and an output of V around 2^-30 is 78% off.)
 constexpr float kFixedCap2 = 80.f;
 inline bool fixed_reference(const ScoredArgs& a) {
   return a.score.softcap > 0.f && a.score.cap2 <= kFixedCap2 && a.score.limit3 > 0.f;
