@@ -278,7 +278,8 @@ int pkv_attention(const void* q, int64_t q_row_stride, int64_t q_rows, int32_t n
  *                 fp32's range (else PKV_ERR_ARG).
  *   window        >= 0; 0: no window; 1: each row sees only its own key (and
  *                 the prefix keys after it, when there is a prefix).
- *   alibi_slopes  fp32 [num_heads] device, finite, of either sign, or NULL.
+ *   alibi_slopes  fp32 [num_heads] device, of either sign, up to 1e30 in size,
+ *                 or NULL.
  *   prefix_lens   int32 [num_reqs] device, or NULL; negative counts as 0.
  * Pages that lie wholly before a request's window (keys before
  * max(0, ctx - window + 1)) are not read, nor are their block_table entries,

@@ -208,7 +208,7 @@ enum Mode { kPlain, kRunning, kFixedRef };
 struct RowScore {
   int pos, low;  // the row's position; first key it sees
   float slope2;  // bias slope, log2 units
-  float top;     // its largest bias (max_bias)
+  float from;    // fixed reference: distance its bias is counted from (bias_from)
 };
 // The row at position pos of request r (L keys), head h; *vis (keys it sees end
 // here) grows to the request's prefix, clipped to the unit.
@@ -224,7 +224,7 @@ __device__ __forceinline__ RowScore row_score(const ScoreArgs& sp, int r, int L,
     *vis = max(*vis, min(k1, p));
     last = max(pos, p - 1);
   }
-  s.top = max_bias(s.slope2, pos, s.low, last);
+  s.from = bias_from(s.slope2, pos, s.low, last);
   return s;
 }
 // The raw products q.K of a step's keys, tile nt of eight keys at key0 + 8 nt +
@@ -232,7 +232,7 @@ __device__ __forceinline__ RowScore row_score(const ScoreArgs& sp, int r, int L,
 // -inf for the keys a row does not see (any: some row of the unit sees not all
 // of the step's keys).  One form of the cap for the warp, chosen by the keys
 // its rows see, since the others may hold anything.
-// Fixed reference: minus it (see fixed_reference()).
+// Fixed reference: the bias counted from rs.from.
 template <int kTiles, bool kFixed>
 __device__ __forceinline__ void step_logits(const ScoreArgs& sp, float (&s2)[kTiles][4],
                                             const RowScore (&rs)[2], int vis0, int vis1, int key0,
@@ -272,8 +272,8 @@ __device__ __forceinline__ void step_logits(const ScoreArgs& sp, float (&s2)[kTi
 #pragma unroll
     for (int i = 0; i < 4 * kTiles; ++i) {
       const int r = (i >> 1) & 1;
-      if (kFixed) s[i] -= rs[r].top;
-      s[i] = fmaf(-rs[r].slope2, fabsf(d[r] - (float)(8 * (i >> 2) + (i & 1))), s[i]);
+      const float dist = fabsf(d[r] - (float)(8 * (i >> 2) + (i & 1)));
+      s[i] = fmaf(-rs[r].slope2, kFixed ? dist - rs[r].from : dist, s[i]);
     }
   }
   if (any) {
@@ -438,10 +438,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[dn][e] = 0.f;
     float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
-    if (kFixed) {
-      m_run[0] = rs[0].top;
-      m_run[1] = rs[1].top;
-    }
+    if (kFixed) m_run[0] = m_run[1] = 0.f;
 
     bool ok = true;
     for (int p = 0; p < npages; ++p) {
@@ -815,10 +812,7 @@ __global__ void __launch_bounds__(CfgP::kThreads, 1)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[dn][e] = 0.f;
     float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
-    if (kFixed) {
-      m_run[0] = rs[0].top;
-      m_run[1] = rs[1].top;
-    }
+    if (kFixed) m_run[0] = m_run[1] = 0.f;
 
     for (int j = 0; j < nsteps; ++j) {
       const uint32_t x = step_cnt + j;

@@ -256,38 +256,57 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
 }
 
-// Adds the bias slope2 * (i - d0) to 32 columns (d0: distance of the first
-// one's key) or, without a cap, forms s * lin + nm + bias: four pairs stepped
-// by eight columns (three additions at most: their roundings stay below 2^-22
-// of the bias).  kSym: a column past d0 counts its distance too.
+// Adds the bias -slope2 * (distance - from) to 32 columns (d0: distance of the
+// first one's key; from: see bias_from) or, without a cap, forms s * lin + nm +
+// bias.  Capped: the distances in four pairs stepped by eight columns, exact whole
+// numbers.  Without a cap: the biases stepped instead (one operation less; three
+// additions at most, whose roundings stay below 2^-22 of the bias).  kSym: a
+// column past d0 counts its distance too.
 template <bool kCapped, bool kSym>
 __device__ __forceinline__ void bias32(float (&s)[32], const ScoreArgs& sp, float nm,
-                                       float slope2, float d0) {
+                                       float slope2, float d0, float from) {
+  if (kSym) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      if (!kCapped)
+        split(fma2(pair(s[i], s[i + 1]), sp.lin2, pair(nm, nm)), s[i], s[i + 1]);
+#pragma unroll
+      for (int k = i; k < i + 2; ++k) s[k] = fmaf(-slope2, fabsf((float)k - d0) - from, s[k]);
+    }
+    return;
+  }
   f32x2 b[4];
-  const float b0 = kCapped ? -slope2 * d0 : fmaf(-slope2, d0, nm);
+  if (kCapped) {
+    const f32x2 m = pair(slope2, slope2), e8 = pair(8.f, 8.f);
+    const float e0 = from - d0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) b[k] = pair(e0 + 2.f * k, e0 + (2.f * k + 1.f));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      split(fma2(b[i & 3], m, pair(s[2 * i], s[2 * i + 1])), s[2 * i], s[2 * i + 1]);
+      if (i < 12) b[i & 3] = add2(b[i & 3], e8);
+    }
+    return;
+  }
+  const float b0 = fmaf(-slope2, d0, nm);
   const f32x2 b8 = pair(8.f * slope2, 8.f * slope2);
 #pragma unroll
   for (int k = 0; k < 4; ++k)
     b[k] = pair(fmaf(slope2, 2.f * k, b0), fmaf(slope2, 2.f * k + 1.f, b0));
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const f32x2 v = pair(s[2 * i], s[2 * i + 1]);
-    split(kCapped ? add2(v, b[i & 3]) : fma2(v, sp.lin2, b[i & 3]), s[2 * i], s[2 * i + 1]);
+    split(fma2(pair(s[2 * i], s[2 * i + 1]), sp.lin2, b[i & 3]), s[2 * i], s[2 * i + 1]);
     if (i < 12) b[i & 3] = add2(b[i & 3], b8);
-  }
-  if (kSym) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) s[i] -= 2.f * slope2 * fmaxf((float)i - d0, 0.f);
   }
 }
 // 32 raw products s = q.K (columns of one row) to logits in log2 units + nm,
 // the cap by the given form.
 template <Cap kCap, bool kBias, bool kSym, Form kForm>
 __device__ __forceinline__ void logits32(float (&s)[32], const ScoreArgs& sp, float nm,
-                                         float slope2, float d0, float& big) {
+                                         float slope2, float d0, float from, float& big) {
   if (kCap != kNoCap) cap_values<kForm>(s, sp, nm, big);
   if (kBias) {
-    bias32<kCap != kNoCap, kSym>(s, sp, nm, slope2, d0);
+    bias32<kCap != kNoCap, kSym>(s, sp, nm, slope2, d0, from);
   } else if (kCap == kNoCap) {
     const f32x2 nm2 = pair(nm, nm);
 #pragma unroll
@@ -300,10 +319,10 @@ __device__ __forceinline__ void logits32(float (&s)[32], const ScoreArgs& sp, fl
 template <Cap kCap, bool kBias, bool kSym, bool kEdge>
 __device__ __forceinline__ void logits32_any(float (&s)[32], const ScoreArgs& sp, float nm,
                                              int lim, int low, bool valid_row, float slope2,
-                                             float d0) {
+                                             float d0, float from) {
   float big = 0.f;
   if (kCap == kNoCap) {
-    logits32<kCap, kBias, kSym, kDeg2>(s, sp, nm, slope2, d0, big);
+    logits32<kCap, kBias, kSym, kDeg2>(s, sp, nm, slope2, d0, from, big);
   } else {
     if (kEdge) {
 #pragma unroll
@@ -317,15 +336,15 @@ __device__ __forceinline__ void logits32_any(float (&s)[32], const ScoreArgs& sp
     }
     const float m = valid_row ? fmaxf(m0, m1) : 0.f;
     if (__all_sync(0xffffffffu, m * m <= sp.limit2)) {
-      logits32<kCap, kBias, kSym, kDeg2>(s, sp, nm, slope2, d0, big);
+      logits32<kCap, kBias, kSym, kDeg2>(s, sp, nm, slope2, d0, from, big);
     } else if (__all_sync(0xffffffffu, m * m <= sp.limit3)) {
-      logits32<kCap, kBias, kSym, kDeg3>(s, sp, nm, slope2, d0, big);
+      logits32<kCap, kBias, kSym, kDeg3>(s, sp, nm, slope2, d0, from, big);
     } else if (kCap == kAnyCap && __all_sync(0xffffffffu, m * sp.k <= 1.f)) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) s[i] = capped_poly(s[i], sp) + nm;
-      if (kBias) bias32<true, kSym>(s, sp, nm, slope2, d0);
+      if (kBias) bias32<true, kSym>(s, sp, nm, slope2, d0, from);
     } else {
-      logits32<kCap, kBias, kSym, kExp>(s, sp, nm, slope2, d0, big);
+      logits32<kCap, kBias, kSym, kExp>(s, sp, nm, slope2, d0, from, big);
     }
   }
   if (kEdge) {
@@ -754,7 +773,8 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap), 1)
       // when a block's sum passes kMaxSum: bf16 keeps its precision over fp32's
       // exponents, so a reference below the maximum costs none, and 2^40 leaves
       // the sums room to 2^127.
-      float ref = kCap == kFixedCap ? max_bias(slope2, rpos, first, last) : -INFINITY;
+      float ref = kCap == kFixedCap ? 0.f : -INFINITY;
+      const float from = kCap == kFixedCap ? bias_from(slope2, rpos, first, last) : 0.f;
       float l = 0.f;
       if (form == 1 && --hold <= 0) form = 0;
       for (int j = 0; j < it.nkv; ++j) {
@@ -775,8 +795,8 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap), 1)
               uint32_t p[16];
               PKV_LD32(t_s + 32 * c, s);
               tmem_wait_ld();
-              logits32_any<kCap, kBias, kSym, false>(s, sp, -ref, 0, 0, valid_row, slope2,
-                                                     (float)(rpos - key0 - 32 * c));
+              logits32_any<kCap, kBias, kSym, false>(s, sp, 0.f, 0, 0, valid_row, slope2,
+                                                     (float)(rpos - key0 - 32 * c), from);
               l += exp32(s, p);
               PKV_ST16U(t_s + 32 * c, p);
             }
@@ -792,8 +812,8 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap), 1)
               } else {
                 PKV_LD32(t_s + 32 * c, s);
                 tmem_wait_ld();
-                logits32_any<kCap, kBias, kSym, true>(s, sp, -ref, lc, wc, valid_row, slope2,
-                                                      (float)(rpos - key0 - 32 * c));
+                logits32_any<kCap, kBias, kSym, true>(s, sp, 0.f, lc, wc, valid_row, slope2,
+                                                      (float)(rpos - key0 - 32 * c), from);
                 l += exp32(s, p);
               }
               PKV_ST16U(t_s + 32 * c, p);
@@ -823,7 +843,7 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap), 1)
                   PKV_LD32(t_s + 32 * c, s);
                   tmem_wait_ld();
                   logits32_any<kCap, kBias, kSym, true>(s, sp, 0.f, lc, wc, valid_row, slope2,
-                                                        (float)(rpos - key0 - 32 * c));
+                                                        (float)(rpos - key0 - 32 * c), 0.f);
                   float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
                   for (int i = 0; i < 32; i += 4) {
@@ -884,7 +904,7 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap), 1)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                   logits32<kCap, kBias, kSym, decltype(f)::value>(
-                      s[c], sp, -ref, slope2, (float)(rpos - key0 - 32 * (h + c)), big);
+                      s[c], sp, -ref, slope2, (float)(rpos - key0 - 32 * (h + c)), 0.f, big);
                   sum += exp32(s[c], p[c]);
                 }
               };

@@ -61,10 +61,11 @@ __device__ __forceinline__ void cap_values(float (&s)[kN], const ScoreArgs& sp, 
 }
 
 // Fixed-reference softmax.  A capped logit lies within +-cap2 (log2 units), and
-// a row's own bias term at most max_bias above zero.  Taken against max_bias
-// alone, the weight of the key of that bias is between 2^-cap2 and 2^cap2, so
-// that no maximum is looked for and nothing is rescaled.  What cap2 <= 80 (caps up
-// to 55) leaves of fp32's exponents (bf16 has the same):
+// the bias is counted from the row's visible key that has the most of it (see
+// bias_from), where it is zero.  The weight exp2 of the sum is then between
+// 2^-cap2 and 2^cap2 at that key and lower at the others, so that no maximum is
+// looked for and nothing is rescaled.  What cap2 <= 80 (caps up to 55) leaves of
+// fp32's exponents (bf16 has the same):
 //   below: a row's largest weight is at least 2^-80, and exp2 flushes below
 //     2^-126, so that a key further along the bias counts down to 2^-46 of it
 //     (2^19 keys less than that are 2^-27 of the sum), and the products of the
@@ -77,10 +78,14 @@ constexpr float kFixedCap2 = 80.f;
 inline bool fixed_reference(const ScoredArgs& a) {
   return a.score.softcap > 0.f && a.score.cap2 <= kFixedCap2 && a.score.limit3 > 0.f;
 }
-// The largest -slope2 * |pos - j| over the keys first <= j <= last that a row at
-// pos sees (its own among them).
-__device__ __forceinline__ float max_bias(float slope2, int pos, int first, int last) {
-  return -fminf(0.f, slope2) * (float)max(pos - first, last - pos);
+// The distance that the bias of a row at pos is counted from, -slope2 * (|pos -
+// j| - from): its own (0), or, with a bias that grows with distance, the farthest
+// of the keys first .. last that it sees.  Distances are whole numbers below
+// 2^20, so that their difference is exact and the bias never positive, however
+// steep the slope (a bias and its largest value, rounded one by one, are 2^12
+// apart at a slope of 10^8).
+__device__ __forceinline__ float bias_from(float slope2, int pos, int first, int last) {
+  return slope2 < 0.f ? (float)max(pos - first, last - pos) : 0.f;
 }
 
 // Whether a scored call's prefill items are single query heads: where even so

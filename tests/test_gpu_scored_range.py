@@ -82,3 +82,35 @@ def test_saturated_scores_with_small_and_large_values(hq, hkv, cap, v_scale, sig
     ds = saturated(STEP[0], n, hq, hkv, SIGNS[signs], v_scale=v_scale, seed=hq)
     check(ds, "no bias", softcap=cap)
     check(ds, "window", softcap=cap, window=100)
+
+
+@pytest.mark.parametrize("opt", [dict(), dict(softcap=20.0), dict(softcap=55.0),
+                                 dict(softcap=200.0)], ids=str)
+@pytest.mark.parametrize("slope", [1e4, 1e8, 1e30, -1e4, -1e8, -1e30])
+@pytest.mark.parametrize("hq,hkv", [(6, 2), (32, 1)])
+def test_slopes_steep_enough_to_leave_one_key(hq, hkv, slope, opt):
+    """The next key lies 1e4 below or more, scores differ by 400 at most: the row's
+    one key is its own, or the farthest that it sees, with weight one, and the
+    output that key's V to the bit (a bf16 value times a weight, divided by that
+    weight in fp32, rounds back to it)."""
+    ctx, n = [0, 300, 5000, 64, 300], [300, 140, 1, 3 if hkv == 2 else 1, 1]
+    ds = DeviceStep(W.build(W.custom(ctx, n, hq, hkv, seed=77)))
+    ds.write()
+    slopes = torch.full((hq,), slope)
+    # an even prefix: no row is as far from its last key as from key 0
+    for window, prefix in ((0, None), (50, None), (0, [250, 400, 0, 66, 40])):
+        ds.out.fill_(float("nan"))
+        call(ds, slopes=slopes, window=window, prefix=prefix, **opt)
+        assert pkv.pkv_get_error() == 0
+        at = 0
+        for r, (c, m) in enumerate(zip(ctx, n)):
+            keys = []
+            for p in range(c, c + m):
+                hi = max(p + 1, min(prefix[r], c + m)) if prefix else p + 1
+                lo = max(0, p - window + 1) if window else 0
+                keys.append(p if slope > 0 else (lo if p - lo > hi - 1 - p else hi - 1))
+            j = torch.tensor(keys, device="cuda")
+            want = ds.value_cache[ds.block_table[r].long()[j // 16], j % 16]
+            want = want.repeat_interleave(hq // hkv, dim=1)
+            assert torch.equal(ds.out[at:at + m], want), (window, prefix, r)
+            at += m
