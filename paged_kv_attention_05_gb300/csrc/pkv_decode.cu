@@ -695,13 +695,22 @@ __global__ void __launch_bounds__(CfgP::kThreads, 1)
     const int slot = unit_cnt & 1;
     int u = 0;
     if (tile == 0) {
-      if (lane == 0) {
+      if (lane == 0)
         u = kScored && unit_cnt == 0 ? mine.index
                                      : mine.after + atomicAdd(&ws.hdr->dec_counter, 1);
+      u = __shfl_sync(0xffffffffu, u, 0);
+      // The slot held the unit before last: the other warp has taken it once it
+      // has released the step before last, a step of that unit or a later one.
+      // (Units of one step would otherwise let this warp run ahead and hand over
+      // two units before the other takes one: the barrier, two phases on, never
+      // shows it the first.  The stage's own refill waits for the same release.)
+      if (unit_cnt >= 2 && !mbar_wait_warp(empty_bar(step_cnt % C::kStages),
+                                           ((step_cnt / C::kStages) - 1) & 1, abort, ws.err))
+        break;
+      if (lane == 0) {
         uslot[slot] = u;
         mbar_arrive(unit_bar(slot));
       }
-      u = __shfl_sync(0xffffffffu, u, 0);
     } else if (kScored && unit_cnt == 0) {
       u = mine.index;  // (handed over all the same: the barrier's phases count units)
     } else {
