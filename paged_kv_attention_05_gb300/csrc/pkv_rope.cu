@@ -240,8 +240,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const RopeArgs
 // Larger steps: a warp takes a unit of 4 * kRopeGroups rows of a token at a
 // time and copies the rows and the table entry of the units ahead into shared
 // memory (cp.async, its own ring of kRopeStages) while it works on the present
-// one, so that it keeps bytes in flight whatever its arithmetic takes; the slot
-// and position of the unit after those are loaded a step earlier still.
+// one, so that it keeps bytes in flight whatever its arithmetic takes; the
+// position of the unit after those is loaded a step earlier still, and its slot,
+// which says whether there is a position to load, a step before that.
 constexpr int kRopeGroups = 4;   // of four rows
 constexpr int kRopeStages = 3;
 constexpr int kRopeCtas = 2;     // an SM
@@ -268,17 +269,18 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_stream_kernel(co
   uint8_t* ring = smem + (threadIdx.x >> 5) * kRopeStages * kRopeStage;
   const uint32_t ring32 = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
   const uint32_t nwarps = (gridDim.x * blockDim.x) >> 5;
-  const uint32_t units = (uint32_t)a.n_tokens * per_token;  // (the launcher: below 2^31)
+  const uint32_t units = (uint32_t)a.n_tokens * per_token;  // (the launcher: below 2^30)
 
-  // the raw slot and position of unit w, used a step after they are asked for
-  int64_t slot_raw = -1, pos_raw = 0;
-  auto ask = [&](uint32_t w) {
-    slot_raw = -1;
-    if (w < units) {
-      const uint32_t tok = w / per_token;
-      slot_raw = __ldg(a.slots + tok);
-      pos_raw = __ldg(a.positions + tok);
-    }
+  // the raw slot and position of unit `ahead`, and the slot of the unit after it
+  // (padding behind the last unit)
+  int64_t slot_raw = -1, pos_raw = 0, slot_next = -1;
+  auto slot_of = [&](uint32_t w) -> int64_t {
+    return w < units ? __ldg(a.slots + w / per_token) : -1;
+  };
+  auto advance = [&](uint32_t w) {  // w: the unit that comes ahead
+    slot_raw = slot_next;
+    if (slot_raw >= 0) pos_raw = __ldg(a.positions + w / per_token);
+    slot_next = slot_of(w + nwarps);
   };
   // copies unit w into a stage, by its raw slot and position
   auto fetch = [&](uint32_t w, int stage) {
@@ -305,18 +307,18 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_stream_kernel(co
   };
 
   uint32_t w = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, ahead = w;
+  slot_next = slot_of(ahead);
+  advance(ahead);
 #pragma unroll
-  for (int s = 0; s < kRopeStages - 1; ++s, ahead += nwarps) {
-    ask(ahead);
+  for (int s = 0; s < kRopeStages - 1; ++s) {
     fetch(ahead, s);
+    advance(ahead += nwarps);
   }
-  ask(ahead);
   for (int stage = 0; w < units; w += nwarps) {
     int to = stage + kRopeStages - 1;
     if (to >= kRopeStages) to -= kRopeStages;
     fetch(ahead, to);
-    ahead += nwarps;
-    ask(ahead);
+    advance(ahead += nwarps);
     asm volatile("cp.async.wait_group %0;\n" ::"n"(kRopeStages - 1) : "memory");
     __syncwarp();  // (the table entry and the slot came from other lanes)
     const uint8_t* st = ring + stage * kRopeStage;
