@@ -157,15 +157,15 @@ def _per_row(t):
 
 
 def _rows3(t, name):
-    """Row stride of a [rows, heads, 128] tensor whose per-row block is contiguous."""
+    """Row stride of a [rows, heads, 128] tensor whose per-row block is contiguous
+    (of one head or one row, that dimension's stride addresses nothing)."""
     st, sh = t.stride(), t.shape
     if len(st) == 2:
         if st[1] != 1:
             raise ValueError("%s: last dimension must be contiguous" % name)
-        return st[0]
-    if len(st) != 3 or st[2] != 1 or st[1] != sh[2]:
+    elif len(st) != 3 or st[2] != 1 or (st[1] != sh[2] and sh[1] != 1):
         raise ValueError("%s must be [rows, heads, head_size] with contiguous rows" % name)
-    return st[0]
+    return _per_row(t) if sh[0] == 1 else st[0]
 
 
 def _all_on_device(dtype, *ts):
@@ -336,7 +336,8 @@ def _write_rope(q, k, v, positions, cos_sin, key_cache, value_cache, slot_mappin
     if not (qd == od == kd == vd == d and ohq == hq and hk == hv == hkv):
         raise ValueError("q and q_out must have the same heads, k and v those of the caches, all "
                          "head_size %d" % d)
-    if not (q2 == o2 == k2 == v2 == 1 and q1 == o1 == k1 == v1 == d):
+    if not (q2 == o2 == k2 == v2 == 1 and (q1 == o1 == d or hq == 1) and
+            (k1 == v1 == d or hkv == 1)):
         raise ValueError("q, k, v and q_out must have contiguous rows")
     if not (cos_sin.is_contiguous() and slot_mapping.is_contiguous() and
             positions.is_contiguous()):
@@ -350,6 +351,9 @@ def _write_rope(q, k, v, positions, cos_sin, key_cache, value_cache, slot_mappin
         n = int(n_tokens)
     if n > rows or n > orows or n > krows or n > vrows or n > npos:
         raise ValueError("n_tokens exceeds the rows of q/k/v/q_out/positions")
+    if n == 1:  # (a single row's stride may be anything)
+        qs = os_ = hq * d
+        ks = vs = hkv * d
     try:
         args = _ROPE_ARGS.pack(
             q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, qw, kw, cos_sin.data_ptr(), far,
@@ -483,8 +487,10 @@ def pkv_attention_scored(q, key_cache, value_cache, query_start_loc, seq_lens, b
         raise ValueError("q and out must be [rows, num_heads, head_size]") from None
     if orows < rows or ohq != hq or od != d or qd != d:
         raise ValueError("q and out must be [rows, num_heads, %d] with as many rows of out" % d)
-    if not (q2 == o2 == 1 and q1 == o1 == d):
+    if not (q2 == o2 == 1 and (q1 == o1 == d or hq == 1)):
         raise ValueError("q and out must have contiguous rows")
+    if rows == 1:
+        qs = os_ = hq * d
     num_reqs, window = int(num_reqs), int(window)
     bts = block_table.shape
     if len(bts) != 2 and (len(bts) != 1 or num_reqs > 1):
