@@ -3,7 +3,8 @@ of a cap, caps at the largest that takes the fixed reference and beyond, values 
 V far from one, steep slopes.
 
 Tolerance: that of test_gpu_scored (derived there); it is proportional to the
-softmax average of |V|, so that it holds for V of any size."""
+softmax average of |V|, so that it holds for V of any size.  Where the products
+q . K are whole numbers below 2^24 they are exact in fp32 and their term goes."""
 import pytest
 import torch
 
@@ -114,3 +115,103 @@ def test_slopes_steep_enough_to_leave_one_key(hq, hkv, slope, opt):
             want = want.repeat_interleave(hq // hkv, dim=1)
             assert torch.equal(ds.out[at:at + m], want), (window, prefix, r)
             at += m
+
+
+def definition(ds, softcap, window=0, slopes=None, prefix=None):
+    """(out, tolerance) in 64 bits for exact products q . K."""
+    st = ds.step
+    hq, hkv = st.spec.hq, st.spec.hkv
+    G = hq // hkv
+    rows = int(st.query_start_loc[-1])
+    out = torch.empty(rows, hq, D, dtype=torch.float64, device="cuda")
+    tol = torch.empty_like(out)
+    scale = float(torch.tensor(st.scale, dtype=torch.float32))
+    for r in range(st.num_reqs):
+        a, b = int(st.query_start_loc[r]), int(st.query_start_loc[r + 1])
+        L = int(st.seq_lens[r])
+        p = torch.arange(L - (b - a), L, device="cuda")[:, None]
+        j = torch.arange(L, device="cuda")[None]
+        hi = torch.maximum(p + 1, torch.tensor(min(prefix[r], L) if prefix else 0, device="cuda"))
+        seen = (j < hi) & (p - j < (window or L + 1))
+        blk = ds.block_table[r].long()[j[0] // 16]
+        for h in range(hq):
+            k, v = (t[blk, j[0] % 16, h // G].double() for t in (ds.key_cache, ds.value_cache))
+            x = scale * (ds.q[a:b, h].double() @ k.T)
+            x = softcap * torch.tanh(x / softcap)
+            d = torch.full_like(x[:, 0], 2.0 ** -20 * softcap)
+            if slopes is not None:
+                bias = float(slopes[h]) * (p - j).abs().double()
+                x = x - bias
+                d = d + 2.0 ** -20 * (bias.abs() * seen).amax(-1)
+            w = torch.softmax(x.masked_fill(~seen, float("-inf")), -1)
+            out[a:b, h] = w @ v
+            tol[a:b, h] = (2.0 ** -7 * out[a:b, h].abs() + (w @ v.abs()) *
+                           (2.0 ** -8 + 2.0 ** -14 + 2 * d[:, None]))
+    return out, tol
+
+
+CAP_OPTIONS = {
+    "alone": dict(),
+    "bias": dict(slopes="falling"),
+    "bias of either sign": dict(slopes="either"),
+    "window": dict(window=150),
+    "prefix": dict(prefix=True),
+    "all": dict(slopes="either", window=150, prefix=True),
+}
+# (heads, KV heads): cached tokens, tokens: prompts and chunks, decodes of one token
+# and of several, whole and split; the second in warp pairs
+CAP_STEPS = {
+    (8, 2): ([0, 130, 2000, 500, 9000, 20000], [300, 129, 200, 4, 2, 1],
+             [250, 200, 2100, 503, 0, 20001]),
+    (32, 1): ([0, 15, 99, 700, 9000, 0, 300], [1, 1, 1, 1, 1, 70, 40],
+              [1, 16, 50, 0, 9001, 65, 310]),
+}
+
+
+def cap_options(name, hq, prefix):
+    o = dict(CAP_OPTIONS[name])
+    if "slopes" in o:
+        o["slopes"] = (torch.tensor([2.0 ** (-8.0 * (h + 1) / hq) for h in range(hq)])
+                       if o["slopes"] == "falling" else torch.linspace(-0.05, 0.05, hq))
+    if "prefix" in o:
+        o["prefix"] = prefix
+    return o
+
+
+@pytest.mark.parametrize("name", CAP_OPTIONS)
+@pytest.mark.parametrize("cap,std", [(55.45, 8.0), (55.46, 8.0), (60.0, 2.0), (60.0, 8.0),
+                                     (200.0, 13.0)])
+@pytest.mark.parametrize("heads", CAP_STEPS, ids=str)
+def test_caps_about_and_past_the_fixed_reference(heads, cap, std, name):
+    """The running reference under a cap with every other option, on every path;
+    scores of a small part of the cap, and past half of it."""
+    ctx, n, prefix = CAP_STEPS[heads]
+    ds = DeviceStep(W.build(W.custom(ctx, n, *heads, seed=int(cap), std=std)))
+    ds.write()
+    check(ds, "%s, cap %g" % (name, cap), softcap=cap, **cap_options(name, heads[0], prefix))
+
+
+@pytest.mark.parametrize("name", CAP_OPTIONS)
+@pytest.mark.parametrize("a,b", [(96, 92), (200, 132)])    # scores about 50,000 and 149,000
+@pytest.mark.parametrize("heads", CAP_STEPS, ids=str)
+def test_a_cap_of_a_hundred_thousand(heads, a, b, name):
+    """Scores of half of the cap and of one and a half, a few units apart: half of
+    the dimensions give every key the same large product, the others a small one
+    of its own, all whole numbers."""
+    hq, hkv = heads
+    ctx, n, prefix = CAP_STEPS[heads]
+    ds = DeviceStep(W.build(W.custom(ctx, n, hq, hkv, seed=9)))
+    ds.write()
+    g = torch.Generator(device="cuda").manual_seed(b)
+    ds.q[..., :64] = a
+    ds.q[..., 64:] = (torch.randint(0, 2, ds.q[..., 64:].shape, generator=g, device="cuda") *
+                      2 - 1).bfloat16()
+    ds.key_cache[..., :64] = b
+    ds.key_cache[..., 64:] = torch.randint(-12, 13, ds.key_cache[..., 64:].shape, generator=g,
+                                           device="cuda").bfloat16()
+    opt = dict(softcap=1e5, **cap_options(name, hq, prefix))
+    ref, tol = definition(ds, **opt)
+    ds.out.fill_(float("nan"))
+    call(ds, **opt)
+    assert pkv.pkv_get_error() == 0
+    assert_near(ds.out[:ref.shape[0]], ref, tol, name)
