@@ -31,11 +31,13 @@ __device__ __forceinline__ CombineStart combine_start(const Workspace& ws, int w
 // n_warps in the grid), four output columns per lane, the splits merged in
 // one pass with the online-softmax identity the decode loop uses between
 // pages (a running max M; the sum and the output so far are scaled by
-// exp2(M_old - M_new) when it grows).  A
-// split that saw no key of the row (m = -inf: only later splits of a
-// multi-token row) contributes nothing; the first split always holds key 0.
-// Rows are (query token, head in group); pairs with fewer rows than the
-// largest skip the rest.
+// exp2(M_old - M_new) when it grows).  Any split of a request of several tokens
+// may hold no key of a row, the first one too: a plain row's later splits lie past
+// its position, and a scored call's units begin at the window of the request's
+// first row, before the windows of the others.  Such a split has m = -inf (or, with
+// the fixed reference, m = 0 and a sum of zero) and contributes nothing; M stays
+// -inf, and its factor zero, until a split that has a key.  Rows are (query token,
+// head in group); pairs with fewer rows than the largest skip the rest.
 __device__ __forceinline__ void combine_splits(const AttnArgs& a, const Workspace& ws, int warp_id,
                                                int n_warps, const CombineStart& start) {
   const int G = a.hq / a.hkv;

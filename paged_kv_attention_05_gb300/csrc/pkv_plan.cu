@@ -163,9 +163,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ArgsOf<kScored> a, W
   // wait for the kernel before this one: that kernel let this grid start
   // either by finishing, or, as this library's cache write, after its own
   // wait for everything before it (it does not touch the metadata), or, as
-  // another plan kernel (pkv_plan), without writing the metadata.  The wait
-  // comes before the first write to the workspace (which that plan kernel
-  // may still be writing, or the previous step's kernels still reading), and
+  // another plan kernel (pkv_plan), without writing the metadata, or, as the
+  // prefill kernel of a scored call, at its start: that call's decode and
+  // prefill may both still run then, but its plan has finished, so that
+  // everything enqueued before it has, and neither writes the metadata.  The
+  // wait comes before the first write to the workspace (which that plan kernel
+  // may still be writing, or the kernels of the call before still reading), and
   // this grid does not finish before it: a kernel that waits for this one
   // also finds the cache write done.
   grid_dep_launch();
