@@ -111,10 +111,14 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
 // single-head items of a scored call take an SM each, see single_head_items).
 // A scored call leaves fewer where its decodes take so long that the prefill
 // ends in their time all the same (kTilesPerStep: decode tiles of 128 keys, 64
-// KB, that all SMs read in the 3 us of a prefill step).  128 decodes of up to
-// 4096 keys beside a prompt of 1000 tokens: 200 -> 185 us; 64 decodes with 32 KV
-// heads beside two of 500: 436 -> 368; the prefill given half of that time 186,
-// 365, but 100 decodes beside two chunks of 700: 173 against 150.
+// KB, that all SMs read in the 3 us of a prefill step; a step of scores past half
+// of a cap takes 4.5).  128 decodes of up to 4096 keys beside a prompt of 1000
+// tokens, 100 of up to 3000 beside two chunks of 700, and 256 of up to 2048
+// beside one of 2000 (us; 213, 320 and 480 tiles a step):
+//   cap 50, scores of rms 3  198 185 186 | 143 147 162 | 272 259 268
+//   cap 50, scores of rms 8  210 190 187 | 161 147 164 | 299 259 269
+//   bias                     199 186 188 | 146 150 173 | 272 262 277
+//   window of 1024            93  97 108 |  92 104 103 | 194 185 205
 // Every CTA computes the same from the plan header (read after the plan
 // wait): P, 0 without prefill items.
 constexpr int kTilesPerStep = 320;

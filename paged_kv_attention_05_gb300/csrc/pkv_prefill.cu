@@ -722,12 +722,17 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap), 1)
     //     straight code, checked at its end, and redone if the check fails (P
     //     has not left the registers, the scores are still in TMEM).  Block
     //     path: any block, masks, new maxima, in a loop.
-    // 8 prompts of 2048 tokens, 64 heads over 8, us: without options 471, bias
-    // 502, cap 539 (scores past a quarter of the cap 602, past half 758),
-    // window of 1024 407; the plain call 495 (with scores of three times the
-    // size its repeated maxima take it to 653).  Bound, with the cap, by the
-    // softmax warps' issue slots (a packed operation takes two) and the chain S
-    // -> P -> P.V of a tile.  Measured and not kept, for the cap (526 at the
+    // 8 prompts of 2048 tokens, 64 heads over 8, us with L2 flushed: without
+    // options 476, bias 505, window of 1024 417; cap 50 with scores of rms 3
+    // 531 (of rms 5, many past a quarter of the cap, 595; of rms 9, many past
+    // half, 762), with a bias 618, with the window 445; cap 200 679 to 753; the
+    // plain call 512 (with scores of rms 3 its repeated maxima take it to 658).
+    // The floor is 285, with the window 214.  Bound by the chain S -> P -> P.V of
+    // a tile: under cap 50 no pipe is active half of the time (tensor 45%, fma
+    // 31, alu 28, XU 22; issue slots 47) and a warp waits for a TMEM load or a
+    // barrier six of the eleven cycles between two of its instructions; scores
+    // past half of the cap lengthen it by the reciprocal and the second
+    // exponential (XU 29%).  Measured and not kept, for the cap (526 at the
     // time, with row sums of the unrounded weights): a row's 128
     // or 64 columns in straight code with all of its forms in place (730 to
     // 2229: instruction-cache misses); two warps a row as in the plain call

@@ -90,8 +90,12 @@ __device__ __forceinline__ float bias_from(float slope2, int pos, int first, int
 
 // Whether a scored call's prefill items are single query heads: where even so
 // they leave a quarter of the SMs idle, two heads of an item would only wait
-// for each other.  (32 heads, cap 30, us a call, single and in pairs: a prompt
-// of 17 tokens 11.5, 12.7; 64 tokens 12.1, 13.5; 300 tokens 14.9, 16.6.)
+// for each other.  (One prompt, us a call, single and in pairs, at 1/4, 3/4, 1 and
+// 1 1/2 items an SM; without a cap and with a bias within 1 us of these:
+//   16 heads over 2, cap 50:  14.8 16.9 | 22.4 25.0 | 28.4 29.4 | 44.4 37.6
+//   32 over 8:                13.2 15.1 | 16.7 19.0 | 20.4 21.2 | 30.1 25.6
+//   64 over 8:                12.7 14.3 | 14.1 16.2 | 17.8 17.5 | 21.1 19.4
+//   32 over 1:                13.4 15.5 | 16.7 19.2 | 20.3 21.6 | 29.8 25.6.)
 __device__ __forceinline__ bool single_head_items(const AttnArgs& a, int n_pre, int sms) {
   return (long long)n_pre * a.hq * 4 <= 3LL * sms;
 }
