@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
         pa[1] = pack_bf16(xs[0][2], xs[0][3]);
         pa[2] = pack_bf16(xs[1][0], xs[1][1]);
         pa[3] = pack_bf16(xs[1][2], xs[1][3]);
-        if (kScored) {  // the sums of the rounded weights (see the prefill's exp32)
+        if (kScored) {  // the sums of the weights as rounded (why: the prefill's exp32)
           float r[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int i = 0; i < 4; ++i) add_bf16x2(r[2 * (i & 1)], r[2 * (i & 1) + 1], pa[i]);

@@ -352,11 +352,12 @@ __device__ __forceinline__ void logits32_any(float (&s)[32], const ScoreArgs& sp
     for (int i = 0; i < 32; ++i) s[i] = i <= lim && i >= low ? s[i] : -INFINITY;
   }
 }
-// p = exp2(s), packed to bf16 pairs; returns the sum of the rounded values: the
-// weights that meet V then add up to the row sum they are divided by, so that a
-// row that one key dominates is off by no rounding of its weight (2.0e-3 instead
-// of 2.3e-3 relative error of the capped prefill's output, 1.7e-3 of it the
-// output's own rounding).
+// p = exp2(s), packed to bf16 pairs (P.V takes both its operands in V's type; a
+// weight is off by 2^-8 of itself at most, as in the plain call); returns the sum
+// of the rounded values: the weights that meet V then add up to the row sum they
+// are divided by, so that a row that one key dominates is off by no rounding of
+// its weight (2.0e-3 instead of 2.3e-3 relative error of the capped prefill's
+// output, 1.7e-3 of it the output's own rounding).
 __device__ __forceinline__ float exp32(const float (&s)[32], uint32_t (&p)[16]) {
   float r[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
