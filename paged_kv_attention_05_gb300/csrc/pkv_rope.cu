@@ -240,9 +240,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const RopeArgs
 // Larger steps: a warp takes a unit of 4 * kRopeGroups rows of a token at a
 // time and copies the rows and the table entry of the units ahead into shared
 // memory (cp.async, its own ring of kRopeStages) while it works on the present
-// one, so that it keeps bytes in flight whatever its arithmetic takes; the
-// position of the unit after those is loaded a step earlier still, and its slot,
-// which says whether there is a position to load, a step before that.
+// one, so that it keeps bytes in flight whatever its arithmetic takes; the slot
+// of the unit after those, which says whether there is anything to copy and a
+// position to load, is asked for a step earlier still.
 constexpr int kRopeGroups = 4;   // of four rows
 constexpr int kRopeStages = 3;
 constexpr int kRopeCtas = 2;     // an SM
@@ -271,26 +271,16 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_stream_kernel(co
   const uint32_t nwarps = (gridDim.x * blockDim.x) >> 5;
   const uint32_t units = (uint32_t)a.n_tokens * per_token;  // (the launcher: below 2^30)
 
-  // the raw slot and position of unit `ahead`, and the slot of the unit after it
-  // (padding behind the last unit)
-  int64_t slot_raw = -1, pos_raw = 0, slot_next = -1;
-  auto slot_of = [&](uint32_t w) -> int64_t {
-    return w < units ? __ldg(a.slots + w / per_token) : -1;
-  };
-  auto advance = [&](uint32_t w) {  // w: the unit that comes ahead
-    slot_raw = slot_next;
-    if (slot_raw >= 0) pos_raw = __ldg(a.positions + w / per_token);
-    slot_next = slot_of(w + nwarps);
-  };
-  // copies unit w into a stage, by its raw slot and position
+  int64_t slot_raw = -1;  // of unit `ahead`, used a step after it is asked for
+  auto ask = [&](uint32_t w) { slot_raw = w < units ? __ldg(a.slots + w / per_token) : -1; };
+  // copies unit w into a stage, by its raw slot; its position comes while the rows
+  // are asked for
   auto fetch = [&](uint32_t w, int stage) {
     const uint32_t tok = w / per_token;
     const int row0 = (int)(w - tok * per_token) * 4 * kRopeGroups + sub;
-    const bool ok = token_ok(a, slot_raw, pos_raw, row0 == 0 && t == 0);
-    if (lane == 0)
-      *reinterpret_cast<int64_t*>(ring + stage * kRopeStage + kRopeSlot) = ok ? slot_raw : -1;
-    if (ok) {
-      const uint32_t dst = ring32 + stage * kRopeStage + lane * 16;
+    const int64_t pos = slot_raw >= 0 ? __ldg(a.positions + tok) : 0;
+    const uint32_t dst = ring32 + stage * kRopeStage + lane * 16;
+    if (slot_raw >= 0) {
 #pragma unroll
       for (int g = 0; g < kRopeGroups; ++g) {
         const int row = row0 + 4 * g;
@@ -300,25 +290,27 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_stream_kernel(co
           copy16(dst + g * 1024 + 512, src + ln.vb * 8);
         }
       }
-      if (lane * 4 < a.rotary_dim)
-        copy16(dst + kRopeTable, a.table + pos_raw * a.rotary_dim + lane * 4);
     }
+    const bool ok = token_ok(a, slot_raw, pos, row0 == 0 && t == 0);
+    if (lane == 0)
+      *reinterpret_cast<int64_t*>(ring + stage * kRopeStage + kRopeSlot) = ok ? slot_raw : -1;
+    if (ok && lane * 4 < a.rotary_dim)
+      copy16(dst + kRopeTable, a.table + pos * a.rotary_dim + lane * 4);
     asm volatile("cp.async.commit_group;\n" ::: "memory");
   };
 
   uint32_t w = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, ahead = w;
-  slot_next = slot_of(ahead);
-  advance(ahead);
 #pragma unroll
-  for (int s = 0; s < kRopeStages - 1; ++s) {
+  for (int s = 0; s < kRopeStages - 1; ++s, ahead += nwarps) {
+    ask(ahead);
     fetch(ahead, s);
-    advance(ahead += nwarps);
   }
+  ask(ahead);
   for (int stage = 0; w < units; w += nwarps) {
     int to = stage + kRopeStages - 1;
     if (to >= kRopeStages) to -= kRopeStages;
     fetch(ahead, to);
-    advance(ahead += nwarps);
+    ask(ahead += nwarps);
     asm volatile("cp.async.wait_group %0;\n" ::"n"(kRopeStages - 1) : "memory");
     __syncwarp();  // (the table entry and the slot came from other lanes)
     const uint8_t* st = ring + stage * kRopeStage;
