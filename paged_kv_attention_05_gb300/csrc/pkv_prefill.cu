@@ -730,10 +730,10 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap), 1)
     // plain call 512 (with scores of rms 3 its repeated maxima take it to 658).
     // The floor is 285, with the window 214.  Bound by the chain S -> P -> P.V of
     // a tile: under cap 50 no pipe is active half of the time (tensor 45%, fma
-    // 31, alu 28, XU 22; issue slots 47) and a warp waits for a TMEM load or a
-    // barrier six of the eleven cycles between two of its instructions; scores
-    // past half of the cap lengthen it by the reciprocal and the second
-    // exponential (XU 29%).  Measured and not kept, for the cap (526 at the
+    // 31, alu 28, XU 22; issue slots 47) and six of the twelve cycles between two
+    // instructions of a warp are waits for data (long scoreboard); scores past
+    // half of the cap lengthen it by the reciprocal and the second exponential
+    // (XU 29%).  Measured and not kept, for the cap (526 at the
     // time, with row sums of the unrounded weights): a row's 128
     // or 64 columns in straight code with all of its forms in place (730 to
     // 2229: instruction-cache misses); two warps a row as in the plain call

@@ -344,16 +344,16 @@ cudaError_t launch_rope_as(const RopeArgs& a, int sms, cudaStream_t st) {
   // step of fewer tokens is spread over four times the warps instead.  Measured
   // at 6, 10, 14, 30 and 120 units an SM (straight, streamed; us a call by
   // events, with the rows out of the caches):
-  //   64 / 8 heads, norms:  9.1 10.7 | 12.4 12.4 | 14.8 12.8 | 20.6 16.5 | 51.7 33.3
-  //   32 / 8, no norms:     8.7 10.7 | 12.5 10.4 | 12.8 10.7 | 16.5 14.5 | 41.4 31.7
-  //   32 / 32, int8:        8.7 10.8 | 12.5 12.4 | 12.8 12.8 | 16.5 16.5 | 43.5 33.3
-  //   12 / 4, int8, norms:  8.7 10.8 | 12.8 10.8 | 12.5 11.1 | 18.0 14.8 | 39.4 33.3
-  //   8 / 1, norms:         8.7 10.7 | 12.4 10.8 | 12.4 11.0 | 16.5 14.8 | 43.5 31.2
-  //   2 / 1, norms:         8.7 10.8 |  8.7 10.5 | 10.4 11.1 | 12.8 12.7 | 25.1 23.0
-  // With the rows in L2 either is up to 29% ahead between 10 and 30 units
-  // (streamed with norms, 10.9 8.8 at 30; straight with int8, 6.8 8.8 at 20), and
+  //   64 / 8 heads, norms:  10.7 10.7 | 12.5 10.4 | 14.6 10.7 | 20.6 14.5 | 51.7 33.2
+  //   32 / 8, no norms:      8.7  8.7 | 12.4 10.7 | 12.8 10.7 | 16.5 14.5 | 41.4 31.2
+  //   32 / 32, int8:         8.7 10.8 | 12.4 12.4 | 12.8 12.8 | 16.6 16.5 | 41.8 33.3
+  //   12 / 4, int8, norms:   8.7 10.8 | 12.8 10.8 | 12.5 11.1 | 16.5 14.8 | 38.9 31.9
+  //   8 / 1, norms:          8.7 10.7 | 10.8 10.7 | 12.4 11.0 | 16.5 14.8 | 43.5 31.2
+  //   2 / 1, norms:          8.7  8.7 |  9.0  8.7 | 10.7  9.0 | 12.4 12.7 | 25.1 25.0
+  // With the rows in L2 either is up to a quarter ahead between 10 and 30 units
+  // (streamed with norms, 10.7 8.4 at 30; straight with int8, 6.9 8.5 at 20), and
   // straight is ahead up to 120 for the few rows of a 2 / 1 token, which fill a
-  // quarter of a unit (14.4 17.0).
+  // quarter of a unit (14.3 16.6).
   if (streamed >= (int64_t)sms * 10 && streamed < (1LL << 30)) {
     static std::atomic<bool> attr[kMaxAttrDevices];
     auto* kernel = rope_stream_kernel<kInt8, kNorm, kInterleaved>;
