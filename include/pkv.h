@@ -446,6 +446,139 @@ int pkv_attention_int8(const void* q, int64_t q_row_stride, int64_t q_rows, int3
                        int64_t out_row_stride, void* stream);
 
 /*
+ * pkv_write_int4 — the cache write into a cache of 4-bit codes.
+ *
+ * The notes that name int8 quantisation of the cache give no format, and none
+ * for four bits.  This library's: each token's key row and value row of each KV
+ * head has a scale and a zero of its own.  For a row x of 128 bf16 values (a NaN
+ * counts as 0, values are clamped to +-2^126): z = min x, w = max x - z in fp32,
+ * s = w / 15 rounded to bf16 (0 if w < 2^-36), code = clamp(rne((x - z) / s), 0,
+ * 15) with the IEEE fp32 quotient (0 if s = 0).  The cached value is s * code + z.
+ *
+ *   cache         uint8 [num_blocks, num_kv_heads, PKV_INT4_PAGE_BYTES],
+ *                 contiguous, 16-byte aligned: keys and values of a page (16
+ *                 slots) of a KV head in one record:
+ *                   [0, 1024)     key codes, 64 bytes a slot
+ *                   [1024, 2048)  value codes
+ *                   [2048, 2112)  key (s, z) of each slot, two bf16
+ *                   [2112, 2176)  value (s, z)
+ *                 Little-endian 32-bit word i of a row's codes holds dimensions
+ *                 8 i .. 8 i + 7, dimension 8 i + 2 a + b in bits 4 a + 16 b.
+ * Placement, padding, slot checks and the other arguments and alignment are
+ * those of pkv_write.
+ */
+#define PKV_INT4_PAGE_BYTES 2176
+int pkv_write_int4(const void* k, int64_t k_row_stride, const void* v, int64_t v_row_stride,
+                   void* cache, int64_t num_blocks, int32_t block_size, int32_t num_kv_heads,
+                   int32_t head_size, const int64_t* slot_mapping, int64_t n_tokens, void* stream);
+
+/*
+ * pkv_read_int4 — cached tokens back as bf16 rows, for instance for a prefix that
+ * moves to a bf16 cache: the cached values (s * code + z in fp32, rounded once) of
+ * slot slots[t] go to k_out[t] and v_out[t], bf16 [n_tokens, num_kv_heads,
+ * head_size] with row strides as in pkv_write.  A negative slot leaves its rows as
+ * they were, one past the pool too (PKV_DEV_ERR_SLOT_RANGE); a slot may come
+ * more than once.
+ */
+int pkv_read_int4(const void* cache, int64_t num_blocks, int32_t block_size, int32_t num_kv_heads,
+                  int32_t head_size, const int64_t* slots, int64_t n_tokens, void* k_out,
+                  int64_t k_row_stride, void* v_out, int64_t v_row_stride, void* stream);
+
+/*
+ * pkv_attention_int4 — pkv_attention over a cache of 4-bit codes written by
+ * pkv_write_int4, for every request pkv_attention takes (decodes, prompts,
+ * chunks).  Arguments, checks, errors and the rows written are those of
+ * pkv_attention with `cache` for the two caches.
+ *
+ * Decode-path requests (query_len * (num_heads / num_kv_heads) at most 16, or 32
+ * for groups above 16) multiply the codes themselves, exact in fp16, with the
+ * query rows scaled by a power of two to fp16's range, and apply each key's s and z
+ * to the products in fp32; the weights, times the value rows' s, are rounded to
+ * fp16.  Longer requests round each cached value to bf16 first.  A key that no
+ * row of its request sees may hold any bits; the values of one that some row sees
+ * must be finite (a row that does not see it weighs it with an exact zero).
+ */
+int pkv_attention_int4(const void* q, int64_t q_row_stride, int64_t q_rows, int32_t num_heads,
+                       const void* cache, int64_t num_blocks, int32_t block_size,
+                       int32_t num_kv_heads, int32_t head_size, const int32_t* query_start_loc,
+                       const int32_t* seq_lens, const int32_t* block_table,
+                       int64_t block_table_width, int32_t num_reqs, float scale, void* out,
+                       int64_t out_row_stride, void* stream);
+
+/*
+ * pkv_page_bounds, pkv_select_pages, pkv_attention_selected — attention over the
+ * pages that a cheap score selects for each query row, for decodes over long
+ * contexts:
+ *   pkv_write            the step's keys and values into the cache (bf16);
+ *   pkv_page_bounds      the smallest and largest keys of the pages it wrote;
+ *   pkv_select_pages     for each row and KV head, the pages with the best bound;
+ *   pkv_attention_selected   attention over those pages.
+ *
+ * pkv_page_bounds: for each page that a token of the call (slot_mapping[t] >= 0)
+ * lies in, bounds[block][g] = (min, max) over the keys in slots 0 .. last of the
+ * page, last the slot of the page's last token in the call, for each dimension: the
+ * keys read are the cache's, so that a page filled over several steps is complete.
+ * The tokens of a page must follow one another in the call, in the order of their
+ * slots (as those of a request do; the bounds of that page are unspecified
+ * otherwise).  A slot past the pool is skipped (PKV_DEV_ERR_SLOT_RANGE).  Keys must
+ * not be NaN.  Called after pkv_write on the same stream.
+ *   bounds        bf16 [num_blocks, num_kv_heads, 2, head_size], contiguous.
+ *   key_cache, slot_mapping, n_tokens, geometry  as in pkv_write.
+ *
+ * pkv_select_pages: row i of request r at position p = ctx + i (pkv_attention's
+ * terms) has the pages 0 .. p / 16 of its request.  With n = p / 16 + 1 <= budget
+ * it takes them all; else the first first_pages, the last last_pages, and those of
+ * the rest with the largest scores, the lower page of two equal ones,
+ *   score_j = sum over heads h of g, dimensions d of
+ *             max(q[h][d] * min_j[d], q[h][d] * max_j[d]),
+ * an upper bound of the heads' summed products with any key of the page.  The
+ * choice is that of exact scores (formed in 64 bits where fp32 leaves it open).
+ *   q             bf16 [q_rows, num_heads, head_size], row-strided.
+ *   bounds        as above, finite; of the last last_pages pages none is read.
+ *   budget        1 .. 32768 pages; 0 <= first_pages, 1 <= last_pages, together at
+ *                 most budget.
+ *   sel_table     int32 [q_rows, num_kv_heads, budget]: the block ids of the pages
+ *   (out)         taken, in the order of the pages; the rest of each list -1.
+ *   sel_lens      int32 [q_rows]: keys in them, 16 * (pages taken - 1) + p % 16 + 1
+ *   (out)         (the same for every KV head); 0 for rows past the last request
+ *                 and rows of a request that fails a metadata check, whose lists
+ *                 are left as they were.
+ * query_start_loc, seq_lens, block_table, num_reqs and their errors are
+ * pkv_attention's; a block id outside the pool is reported and its page's score
+ * unspecified.  The call keeps scores in a workspace of its own (20 bytes a
+ * block-table entry, row and KV head, at most 336 MB or one row's), grown as the
+ * other one is: call pkv_reserve_select before a capture.  As with the other
+ * workspace, calls on one device must not overlap on the GPU.
+ *
+ * pkv_attention_selected: row t, KV head g: keys 0 .. sel_lens[t] - 1 of the list of
+ * pages sel_table[t][g] (key j in slot j % 16 of page j / 16 of the list), each row
+ * of any request by itself:
+ *   out[t][h] = sum_j softmax_j(scale * q[t][h] . K_j) * V_j.
+ * A row with sel_lens[t] = 0 is not written.  A negative length, or one longer than
+ * the list, is reported (PKV_DEV_ERR_SEQ_LEN, PKV_DEV_ERR_BT_WIDTH) and its row
+ * skipped; a block id outside the pool is reported, the row unspecified.
+ *   sel_table     int32 [q_rows, num_kv_heads, sel_width], sel_width <= 32768.
+ * Other arguments are pkv_attention's; pkv_reserve_workspace with q_rows requests,
+ * q_rows rows and sel_width covers the call.
+ */
+int pkv_page_bounds(const void* key_cache, int64_t num_blocks, int32_t block_size,
+                    int32_t num_kv_heads, int32_t head_size, void* bounds,
+                    const int64_t* slot_mapping, int64_t n_tokens, void* stream);
+int pkv_select_pages(const void* q, int64_t q_row_stride, int64_t q_rows, int32_t num_heads,
+                     const void* bounds, int64_t num_blocks, int32_t block_size,
+                     int32_t num_kv_heads, int32_t head_size, const int32_t* query_start_loc,
+                     const int32_t* seq_lens, const int32_t* block_table,
+                     int64_t block_table_width, int32_t num_reqs, int32_t budget,
+                     int32_t first_pages, int32_t last_pages, int32_t* sel_table,
+                     int32_t* sel_lens, void* stream);
+int pkv_reserve_select(int64_t max_q_rows, int64_t block_table_width, int32_t num_kv_heads);
+int pkv_attention_selected(const void* q, int64_t q_row_stride, int64_t q_rows, int32_t num_heads,
+                           const void* key_cache, const void* value_cache, int64_t num_blocks,
+                           int32_t block_size, int32_t num_kv_heads, int32_t head_size,
+                           const int32_t* sel_table, int64_t sel_width, const int32_t* sel_lens,
+                           float scale, void* out, int64_t out_row_stride, void* stream);
+
+/*
  * pkv_attention_noalloc — pkv_attention for callers that cannot allocate
  * device memory.  The pages this library follows have no counterpart to it.
  *

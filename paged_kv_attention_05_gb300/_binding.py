@@ -24,7 +24,10 @@ EXPORTS = ["pkv_write", "pkv_attention", "pkv_reserve_workspace", "pkv_get_error
            "pkv_launch_count", "pkv_prepare_step", "pkv_write_int8", "pkv_attention_int8",
            "pkv_plan", "pkv_attention_planned", "pkv_workspace_size", "pkv_write_rope",
            "pkv_write_rope_int8", "pkv_attention_scored", "pkv_write_rope_packed",
-           "pkv_attention_scored_packed"]
+           "pkv_attention_scored_packed", "pkv_write_int4", "pkv_read_int4",
+           "pkv_attention_int4", "pkv_page_bounds", "pkv_select_pages", "pkv_reserve_select",
+           "pkv_attention_selected"]
+INT4_PAGE_BYTES = 2176  # PKV_INT4_PAGE_BYTES of include/pkv.h
 TRACE_KINDS = ["write", "plan", "decode", "prefill", "combine", "prepare"]
 
 
@@ -72,6 +75,23 @@ def load():
     L.pkv_write_rope.argtypes = rope + [i64, i32, i32, i32, vp, i64, vp]
     L.pkv_write_rope_int8.restype = ctypes.c_int
     L.pkv_write_rope_int8.argtypes = rope + [f32, f32, i64, i32, i32, i32, vp, i64, vp]
+    L.pkv_write_int4.restype = ctypes.c_int
+    L.pkv_write_int4.argtypes = [vp, i64, vp, i64, vp, i64, i32, i32, i32, vp, i64, vp]
+    L.pkv_read_int4.restype = ctypes.c_int
+    L.pkv_read_int4.argtypes = [vp, i64, i32, i32, i32, vp, i64, vp, i64, vp, i64, vp]
+    L.pkv_attention_int4.restype = ctypes.c_int
+    L.pkv_attention_int4.argtypes = [vp, i64, i64, i32, vp, i64, i32, i32, i32, vp, vp, vp, i64,
+                                     i32, f32, vp, i64, vp]
+    L.pkv_page_bounds.restype = ctypes.c_int
+    L.pkv_page_bounds.argtypes = [vp, i64, i32, i32, i32, vp, vp, i64, vp]
+    L.pkv_select_pages.restype = ctypes.c_int
+    L.pkv_select_pages.argtypes = [vp, i64, i64, i32, vp, i64, i32, i32, i32, vp, vp, vp, i64, i32,
+                                   i32, i32, i32, vp, vp, vp]
+    L.pkv_reserve_select.restype = ctypes.c_int
+    L.pkv_reserve_select.argtypes = [i64, i64, i32]
+    L.pkv_attention_selected.restype = ctypes.c_int
+    L.pkv_attention_selected.argtypes = [vp, i64, i64, i32, vp, vp, i64, i32, i32, i32, vp, i64,
+                                         vp, f32, vp, i64, vp]
     L.pkv_plan.restype = ctypes.c_int
     L.pkv_plan.argtypes = [i64, i32, i32, vp, vp, i64, i32, vp]
     L.pkv_attention_planned.restype = ctypes.c_int
@@ -517,6 +537,218 @@ def pkv_attention_scored(q, key_cache, value_cache, query_start_loc, seq_lens, b
     except (struct.error, OverflowError) as e:
         raise ValueError("an argument is out of range: %s" % e) from None
     rc = (_lib or load()).pkv_attention_scored_packed(args)
+    if rc:
+        _check(rc)
+
+
+def _on_device(*named):
+    """True when every (tensor, name, dtype) is a tensor of its dtype on the
+    current CUDA device, or raises for the first that is not."""
+    dev = _get_device()
+    try:
+        for t, _, dtype in named:
+            if t.dtype is not dtype or t.get_device() != dev:
+                break
+        else:
+            return
+    except AttributeError:
+        for t, name, _ in named:
+            if t is None:
+                raise TypeError("%s must be a torch.Tensor" % name) from None
+    _name_culprit(*named)
+    raise ValueError("arguments must be tensors on the current CUDA device")
+
+
+def _cache4(cache):
+    sh = cache.shape
+    if len(sh) != 3 or sh[2] != INT4_PAGE_BYTES or not cache.is_contiguous():
+        raise ValueError("cache must be a contiguous [num_blocks, num_kv_heads, %d]" %
+                         INT4_PAGE_BYTES)
+    return sh[0], sh[1]
+
+
+def _head_rows(t, name, heads, d=128):
+    """Rows and row stride of a [rows, heads, d] tensor with contiguous rows."""
+    sh, st = t.shape, t.stride()
+    if len(sh) != 3 or sh[1] != heads or sh[2] != d:
+        raise ValueError("%s must be [rows, %d, %d]" % (name, heads, d))
+    if st[2] != 1 or (st[1] != d and heads != 1):
+        raise ValueError("%s must have contiguous rows" % name)
+    return sh[0], heads * d if sh[0] == 1 else st[0]
+
+
+def _rows4(k, v, cache, slots, n_tokens, names):
+    torch = _torch or _T()
+    bf16 = torch.bfloat16
+    _on_device((k, names[0], bf16), (v, names[1], bf16), (cache, "cache", torch.uint8),
+               (slots, names[2], torch.int64))
+    nb, hkv = _cache4(cache)
+    krows, ks = _head_rows(k, names[0], hkv)
+    vrows, vs = _head_rows(v, names[1], hkv)
+    if slots.dim() != 1 or not slots.is_contiguous():
+        raise ValueError("%s must be contiguous, one-dimensional" % names[2])
+    n = slots.shape[0] if n_tokens is None else int(n_tokens)
+    if n > slots.shape[0] or n > krows or n > vrows:
+        raise ValueError("n_tokens exceeds the rows of %s/%s/%s" % names)
+    return nb, hkv, ks, vs, n
+
+
+def pkv_write_int4(k, v, cache, slot_mapping, n_tokens=None, stream=None):
+    """Quantises k/v ([n, Hkv, 128] bf16) to 4 bits, each row with a scale and a
+    zero of its own, into cache ([num_blocks, Hkv, INT4_PAGE_BYTES] uint8) at
+    slot_mapping; see include/pkv.h."""
+    nb, hkv, ks, vs, n = _rows4(k, v, cache, slot_mapping, n_tokens, ("k", "v", "slot_mapping"))
+    rc = (_lib or load()).pkv_write_int4(k.data_ptr(), ks, v.data_ptr(), vs, cache.data_ptr(), nb,
+                                         16, hkv, 128, slot_mapping.data_ptr(), n, _stream(stream))
+    if rc:
+        _check(rc)
+
+
+def pkv_read_int4(cache, slots, k_out, v_out, n_tokens=None, stream=None):
+    """The cached keys and values at slots (int64 [n]; negative: row left as it
+    is) as bf16 rows of k_out and v_out ([n, Hkv, 128])."""
+    nb, hkv, ks, vs, n = _rows4(k_out, v_out, cache, slots, n_tokens, ("k_out", "v_out", "slots"))
+    rc = (_lib or load()).pkv_read_int4(cache.data_ptr(), nb, 16, hkv, 128, slots.data_ptr(), n,
+                                        k_out.data_ptr(), ks, v_out.data_ptr(), vs,
+                                        _stream(stream))
+    if rc:
+        _check(rc)
+
+
+def _step_metadata(query_start_loc, seq_lens, block_table, num_reqs):
+    """Checks the step's metadata; returns the width of a block-table row."""
+    bts = block_table.shape
+    if len(bts) != 2 and (len(bts) != 1 or num_reqs > 1):
+        raise ValueError("block_table must be [num_reqs, width]")
+    if not (query_start_loc.is_contiguous() and seq_lens.is_contiguous() and
+            block_table.is_contiguous()):
+        raise ValueError("query_start_loc, seq_lens and block_table must be contiguous")
+    if num_reqs > 0 and (query_start_loc.numel() < num_reqs + 1 or seq_lens.numel() < num_reqs or
+                         (len(bts) == 2 and bts[0] < num_reqs)):
+        raise ValueError("metadata shorter than num_reqs")
+    return bts[-1]
+
+
+def _query_and_out(q, out):
+    if len(q.shape) != 3:
+        raise ValueError("q must be [rows, num_heads, head_size]")
+    hq = q.shape[1]
+    rows, qs = _head_rows(q, "q", hq)
+    orows, os_ = _head_rows(out, "out", hq)
+    if orows < rows:
+        raise ValueError("out must have as many rows as q")
+    if rows == 1:
+        os_ = hq * 128
+    return rows, hq, qs, os_
+
+
+def pkv_attention_int4(q, cache, query_start_loc, seq_lens, block_table, num_reqs, scale, out,
+                       stream=None):
+    """pkv_attention over a cache of 4-bit codes (pkv_write_int4), decodes and
+    prompts; see include/pkv.h."""
+    torch = _torch or _T()
+    bf16, i32 = torch.bfloat16, torch.int32
+    _on_device((q, "q", bf16), (cache, "cache", torch.uint8), (out, "out", bf16),
+               (query_start_loc, "query_start_loc", i32), (seq_lens, "seq_lens", i32),
+               (block_table, "block_table", i32))
+    nb, hkv = _cache4(cache)
+    rows, hq, qs, os_ = _query_and_out(q, out)
+    num_reqs = int(num_reqs)
+    width = _step_metadata(query_start_loc, seq_lens, block_table, num_reqs)
+    rc = (_lib or load()).pkv_attention_int4(
+        q.data_ptr(), qs, rows, hq, cache.data_ptr(), nb, 16, hkv, 128, query_start_loc.data_ptr(),
+        seq_lens.data_ptr(), block_table.data_ptr(), width, num_reqs, float(scale), out.data_ptr(),
+        os_, _stream(stream))
+    if rc:
+        _check(rc)
+
+
+def _bounds(bounds, nb, hkv, d):
+    if bounds.shape != (nb, hkv, 2, d) or not bounds.is_contiguous():
+        raise ValueError("bounds must be a contiguous [num_blocks, num_kv_heads, 2, head_size]")
+
+
+def pkv_page_bounds(key_cache, bounds, slot_mapping, n_tokens=None, stream=None):
+    """The smallest and largest keys (bounds: [num_blocks, Hkv, 2, 128] bf16) of
+    the pages that the step's tokens (slot_mapping, as in pkv_write) lie in."""
+    torch = _torch or _T()
+    _on_device((key_cache, "key_cache", torch.bfloat16), (bounds, "bounds", torch.bfloat16),
+               (slot_mapping, "slot_mapping", torch.int64))
+    cs = key_cache.shape
+    if len(cs) != 4 or not key_cache.is_contiguous():
+        raise ValueError("key_cache must be a contiguous [num_blocks, block_size, Hkv, head_size]")
+    nb, bs, hkv, d = cs
+    _bounds(bounds, nb, hkv, d)
+    if slot_mapping.dim() != 1 or not slot_mapping.is_contiguous():
+        raise ValueError("slot_mapping must be contiguous, one-dimensional")
+    n = slot_mapping.shape[0] if n_tokens is None else int(n_tokens)
+    if n > slot_mapping.shape[0]:
+        raise ValueError("n_tokens exceeds the rows of slot_mapping")
+    rc = (_lib or load()).pkv_page_bounds(key_cache.data_ptr(), nb, bs, hkv, d, bounds.data_ptr(),
+                                          slot_mapping.data_ptr(), n, _stream(stream))
+    if rc:
+        _check(rc)
+
+
+def _lists(sel_table, sel_lens, rows, hkv):
+    ss = sel_table.shape
+    if len(ss) != 3 or ss[0] < rows or ss[1] != hkv or not sel_table.is_contiguous():
+        raise ValueError("sel_table must be a contiguous [rows, num_kv_heads, pages]")
+    if sel_lens.dim() != 1 or sel_lens.shape[0] < rows or not sel_lens.is_contiguous():
+        raise ValueError("sel_lens must be contiguous, one per row")
+    return ss[2]
+
+
+def pkv_select_pages(q, bounds, query_start_loc, seq_lens, block_table, num_reqs, sel_table,
+                     sel_lens, first_pages=0, last_pages=1, stream=None):
+    """For each query row and KV head the pages with the best bound on their
+    keys' products: their block ids into sel_table ([rows, Hkv, budget] int32),
+    the keys in them into sel_lens ([rows] int32); see include/pkv.h."""
+    torch = _torch or _T()
+    bf16, i32 = torch.bfloat16, torch.int32
+    _on_device((q, "q", bf16), (bounds, "bounds", bf16), (query_start_loc, "query_start_loc", i32),
+               (seq_lens, "seq_lens", i32), (block_table, "block_table", i32),
+               (sel_table, "sel_table", i32), (sel_lens, "sel_lens", i32))
+    if len(bounds.shape) != 4:
+        raise ValueError("bounds must be a contiguous [num_blocks, num_kv_heads, 2, head_size]")
+    nb, hkv, _, d = bounds.shape
+    _bounds(bounds, nb, hkv, d)
+    if len(q.shape) != 3:
+        raise ValueError("q must be [rows, num_heads, head_size]")
+    rows, qs = _head_rows(q, "q", q.shape[1])
+    budget = _lists(sel_table, sel_lens, rows, hkv)
+    num_reqs = int(num_reqs)
+    width = _step_metadata(query_start_loc, seq_lens, block_table, num_reqs)
+    rc = (_lib or load()).pkv_select_pages(
+        q.data_ptr(), qs, rows, q.shape[1], bounds.data_ptr(), nb, 16, hkv, d,
+        query_start_loc.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), width, num_reqs,
+        budget, int(first_pages), int(last_pages), sel_table.data_ptr(), sel_lens.data_ptr(),
+        _stream(stream))
+    if rc:
+        _check(rc)
+
+
+def pkv_reserve_select(max_q_rows, block_table_width, num_kv_heads):
+    """Sizes the workspace of pkv_select_pages, as pkv_reserve_workspace does the
+    other one (needed before a CUDA-graph capture)."""
+    _check(load().pkv_reserve_select(int(max_q_rows), int(block_table_width), int(num_kv_heads)))
+
+
+def pkv_attention_selected(q, key_cache, value_cache, sel_table, sel_lens, scale, out,
+                           stream=None):
+    """Attention of each query row over the pages listed for it and each KV head
+    (pkv_select_pages); see include/pkv.h."""
+    torch = _torch or _T()
+    bf16, i32 = torch.bfloat16, torch.int32
+    _on_device((q, "q", bf16), (key_cache, "key_cache", bf16), (value_cache, "value_cache", bf16),
+               (sel_table, "sel_table", i32), (sel_lens, "sel_lens", i32), (out, "out", bf16))
+    nb, bs, hkv, d = _caches(key_cache, value_cache, bf16)
+    rows, hq, qs, os_ = _query_and_out(q, out)
+    width = _lists(sel_table, sel_lens, rows, hkv)
+    rc = (_lib or load()).pkv_attention_selected(
+        q.data_ptr(), qs, rows, hq, key_cache.data_ptr(), value_cache.data_ptr(), nb, bs, hkv, d,
+        sel_table.data_ptr(), width, sel_lens.data_ptr(), float(scale), out.data_ptr(), os_,
+        _stream(stream))
     if rc:
         _check(rc)
 

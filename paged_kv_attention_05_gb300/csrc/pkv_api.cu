@@ -31,6 +31,10 @@ struct DeviceState {
   int64_t plan_q_rows = 0, plan_bt_width = 0;
   int plan_hq = 0, plan_hkv = 0, plan_reqs = 0;
   Sizes plan_sizes{};
+  // pkv_select_pages' workspace
+  void* sel_ws = nullptr;
+  size_t sel_bytes = 0;
+  bool sel_in_graph = false;
 };
 
 std::mutex g_mu;
@@ -109,44 +113,55 @@ int current_state(DeviceState** out) {
   return PKV_OK;
 }
 
-// Makes sure the workspace holds at least `z`; allocation only outside capture.
+// Grows *buf to `need` bytes and a quarter more, zeroed; allocation only outside
+// capture.  *grown tells whether it did.
+int ensure_buffer(void** buf, size_t* bytes, bool* in_graph, size_t need, const char* reserve,
+                  cudaStream_t st, bool* grown) {
+  *grown = false;
+  if (need <= *bytes) return PKV_OK;
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  if (st != nullptr) cudaStreamIsCapturing(st, &cap);
+  if (cap != cudaStreamCaptureStatusNone)
+    return fail(PKV_ERR_ARG,
+                "workspace of %zu bytes needed while the stream is being captured; call "
+                "%s before capture",
+                need, reserve);
+  cudaError_t e = cudaDeviceSynchronize();  // the old workspace may still be in use
+  if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
+  // (a graph that was captured on the old workspace goes on using it when it
+  // is replayed: it is kept then, for as long as the process lives)
+  if (*buf && !*in_graph) cudaFree(*buf);
+  *in_graph = false;
+  *buf = nullptr;
+  *bytes = 0;
+  *grown = true;
+  const size_t grow = need + need / 4;
+  e = cudaMalloc(buf, grow);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(workspace)");
+  e = cudaMemset(*buf, 0, grow);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaMemset(workspace)");
+  *bytes = grow;
+  return PKV_OK;
+}
+
+// Makes sure the workspace holds at least `z`.
 int ensure_workspace(DeviceState* s, const Sizes& z, cudaStream_t st, Workspace* ws) {
-  const size_t need = workspace_bytes(z);
-  if (need > s->ws_bytes) {
-    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    if (st != nullptr) cudaStreamIsCapturing(st, &cap);
-    if (cap != cudaStreamCaptureStatusNone)
-      return fail(PKV_ERR_ARG,
-                  "workspace of %zu bytes needed while the stream is being captured; call "
-                  "pkv_reserve_workspace before capture",
-                  need);
-    cudaError_t e = cudaDeviceSynchronize();  // the old workspace may still be in use
-    if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
-    // (a graph that was captured on the old workspace goes on using it when it
-    // is replayed: it is kept then, for as long as the process lives)
-    if (s->ws && !s->ws_in_graph) cudaFree(s->ws);
-    s->ws_in_graph = false;
-    s->ws = nullptr;
-    s->ws_bytes = 0;
-    s->plan_valid = false;  // the plan lived in the old workspace
-    const size_t grow = need + need / 4;
-    e = cudaMalloc(&s->ws, grow);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(workspace)");
-    e = cudaMemset(s->ws, 0, grow);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaMemset(workspace)");
-    s->ws_bytes = grow;
-  }
+  bool grown = false;
+  const int rc = ensure_buffer(&s->ws, &s->ws_bytes, &s->ws_in_graph, workspace_bytes(z),
+                               "pkv_reserve_workspace", st, &grown);
+  if (grown) s->plan_valid = false;  // the plan lived in the old workspace
+  if (rc) return rc;
   // carve for the capacity actually held, scaled from the request
   *ws = carve_workspace(s->ws, z, s->err);
   return PKV_OK;
 }
 
 // Called wherever work that holds the workspace's address is enqueued.
-void note_capture(DeviceState* s, cudaStream_t st) {
+void note_capture(bool* in_graph, cudaStream_t st) {
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-  if (!s->ws_in_graph && st != nullptr && cudaStreamIsCapturing(st, &cap) == cudaSuccess &&
+  if (!*in_graph && st != nullptr && cudaStreamIsCapturing(st, &cap) == cudaSuccess &&
       cap != cudaStreamCaptureStatusNone)
-    s->ws_in_graph = true;
+    *in_graph = true;
 }
 
 int check_geometry(int32_t block_size, int32_t hkv, int32_t head_size) {
@@ -481,9 +496,9 @@ int check_meta(int64_t q_rows, int32_t num_heads, int32_t num_kv_heads,
 // Builds the step plan into the device workspace (state lock held).
 int plan_locked(DeviceState* s, int64_t q_rows, int32_t num_heads, int32_t num_kv_heads,
                 const int32_t* query_start_loc, const int32_t* seq_lens,
-                int64_t block_table_width, int32_t num_reqs, int kv_int8, const ScoreArgs& score,
-                cudaStream_t st) {
-  const int workers = decode_workers(num_heads / num_kv_heads, kv_int8, s->sms);
+                int64_t block_table_width, int32_t num_reqs, int kv, const ScoreArgs& score,
+                int sel, cudaStream_t st) {
+  const int workers = decode_workers(num_heads / num_kv_heads, kv, s->sms);
   const Sizes z = with_wave_room(
       sizes_for(num_reqs, q_rows, block_table_width, num_heads, num_kv_heads), q_rows,
       num_heads / num_kv_heads, workers);
@@ -498,14 +513,16 @@ int plan_locked(DeviceState* s, int64_t q_rows, int32_t num_heads, int32_t num_k
   a.seq_lens = seq_lens;
   a.bt_width = block_table_width;
   a.num_reqs = num_reqs;
-  a.kv_int8 = kv_int8;
+  a.kv = kv;
   a.score = score;
-  note_capture(s, st);
+  a.sel = sel;
+  note_capture(&s->ws_in_graph, st);
   cudaError_t e = traced(1, st, [&] { return launch_plan(a, ws, workers, st); });
   if (e != cudaSuccess) return cuda_fail(e, "plan launch");
-  // an int8 plan leaves prefill-class requests out, a scored one the keys
-  // before its window: neither can serve a planned call
-  s->plan_valid = !kv_int8 && !score.on;
+  // an int8 plan leaves prefill-class requests out, a scored one the keys before
+  // its window, one of selected pages has rows for requests, and an int4 one
+  // splits for other workers: none can serve a planned call
+  s->plan_valid = kv == kBf16 && !score.on && !sel;
   s->plan_q_rows = q_rows;
   s->plan_bt_width = block_table_width;
   s->plan_hq = num_heads;
@@ -519,8 +536,8 @@ int plan_locked(DeviceState* s, int64_t q_rows, int32_t num_heads, int32_t num_k
 // held; the plan's geometry is the caller's).
 int run_locked(DeviceState* s, const void* q, int64_t q_row_stride, const void* key_cache,
                const void* value_cache, int64_t num_blocks, const int32_t* block_table,
-               float scale, void* out, int64_t out_row_stride, int kv_int8, float k_scale,
-               float v_scale, const ScoreArgs& score, cudaStream_t st) {
+               float scale, void* out, int64_t out_row_stride, int kv, float k_scale,
+               float v_scale, const ScoreArgs& score, int sel, cudaStream_t st) {
   Workspace ws = carve_workspace(s->ws, s->plan_sizes, s->err);
   ScoredArgs a{};
   a.q = static_cast<const uint16_t*>(q);
@@ -539,21 +556,23 @@ int run_locked(DeviceState* s, const void* q, int64_t q_row_stride, const void* 
   a.scale = scale;
   a.out = static_cast<uint16_t*>(out);
   a.out_stride = out_row_stride;
-  a.kv_int8 = kv_int8;
-  a.k_scale = kv_int8 ? k_scale : 1.f;
-  a.v_scale = kv_int8 ? v_scale : 1.f;
+  a.kv = kv;
+  a.k_scale = kv == kInt8 ? k_scale : 1.f;
+  a.v_scale = kv == kInt8 ? v_scale : 1.f;
   a.score = score;
+  a.sel = sel;
+  a.bt_more = sel ? a.hkv - 1 : 0;
   if (score.on) set_score_form(a);
   // Decode first.  When the step also has prefill work, the decode grid
   // leaves some SMs to it at once and the prefill grid (its programmatic
   // dependent) runs its items there beside the decode units; the prefill
   // kernel merges the split decode results at its end, once the decode grid
   // has finished (see pkv_decode.cu and pkv_prefill.cu).  An int8 call has no
-  // prefill work (the plan reports such requests): its merge is a launch of
-  // its own.
+  // prefill work (the plan reports such requests), nor has one of selected pages:
+  // their merge is a launch of its own.
   cudaError_t e = traced(2, st, [&] { return launch_decode(a, ws, s->sms, st); });
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
-  if (kv_int8) {
+  if (kv == kInt8 || sel) {
     e = traced(4, st, [&] { return launch_combine(a, ws, s->sms, st); });
     if (e != cudaSuccess) return cuda_fail(e, "combine launch");
   } else {
@@ -582,15 +601,16 @@ int check_buffers(const void* q, int64_t q_row_stride, int32_t num_heads, const 
   return PKV_OK;
 }
 
-// pkv_attention and pkv_attention_int8: kv_int8 = 0 for bf16 caches, 1 for
-// int8 codes with the two scales (decode-class requests only).
+// The attention calls that make their own plan: kv tells what the cache holds
+// (KvType; the two scales are an int8 cache's), sel that the rows have lists of
+// pages of their own (AttnArgs).
 int attention_common(const void* q, int64_t q_row_stride, int64_t q_rows, int32_t num_heads,
                      const void* key_cache, const void* value_cache, int64_t num_blocks,
                      int32_t block_size, int32_t num_kv_heads, int32_t head_size,
                      const int32_t* query_start_loc, const int32_t* seq_lens,
                      const int32_t* block_table, int64_t block_table_width, int32_t num_reqs,
-                     float scale, void* out, int64_t out_row_stride, void* stream, int kv_int8,
-                     float k_scale, float v_scale, const ScoreArgs& score = ScoreArgs()) {
+                     float scale, void* out, int64_t out_row_stride, void* stream, int kv,
+                     float k_scale, float v_scale, const ScoreArgs& score = ScoreArgs(), int sel = 0) {
   g_msg[0] = 0;
   int rc = check_geometry(block_size, num_kv_heads, head_size);
   if (rc) return rc;
@@ -602,7 +622,7 @@ int attention_common(const void* q, int64_t q_row_stride, int64_t q_rows, int32_
   rc = check_buffers(q, q_row_stride, num_heads, key_cache, value_cache, num_blocks, block_table,
                      scale, out, out_row_stride);
   if (rc) return rc;
-  if (kv_int8 && !(k_scale > 0.f && v_scale > 0.f && k_scale < INFINITY && v_scale < INFINITY))
+  if (kv == kInt8 && !(k_scale > 0.f && v_scale > 0.f && k_scale < INFINITY && v_scale < INFINITY))
     return fail(PKV_ERR_ARG, "k_scale and v_scale must be finite and positive");
 
   std::lock_guard<std::mutex> lock(g_mu);
@@ -611,10 +631,10 @@ int attention_common(const void* q, int64_t q_row_stride, int64_t q_rows, int32_
   if (rc) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   rc = plan_locked(s, q_rows, num_heads, num_kv_heads, query_start_loc, seq_lens,
-                   block_table_width, num_reqs, kv_int8, score, st);
+                   block_table_width, num_reqs, kv, score, sel, st);
   if (rc) return rc;
   return run_locked(s, q, q_row_stride, key_cache, value_cache, num_blocks, block_table, scale,
-                    out, out_row_stride, kv_int8, k_scale, v_scale, score, st);
+                    out, out_row_stride, kv, k_scale, v_scale, score, sel, st);
 }
 
 }  // namespace
@@ -640,7 +660,7 @@ extern "C" int pkv_plan(int64_t q_rows, int32_t num_heads, int32_t num_kv_heads,
     return PKV_OK;
   }
   return plan_locked(s, q_rows, num_heads, num_kv_heads, query_start_loc, seq_lens,
-                     block_table_width, num_reqs, 0, ScoreArgs(),
+                     block_table_width, num_reqs, kBf16, ScoreArgs(), 0,
                      static_cast<cudaStream_t>(stream));
 }
 
@@ -673,11 +693,11 @@ extern "C" int pkv_attention_planned(const void* q, int64_t q_row_stride, int32_
   PlanHeader* hdr = carve_workspace(s->ws, s->plan_sizes, s->err).hdr;
   static_assert(offsetof(PlanHeader, pre_counter) == offsetof(PlanHeader, dec_counter) + 4,
                 "adjacent cursors");
-  note_capture(s, st);
+  note_capture(&s->ws_in_graph, st);
   cudaError_t e = cudaMemsetAsync(&hdr->dec_counter, 0, 2 * sizeof(int), st);
   if (e != cudaSuccess) return cuda_fail(e, "cursor reset");
   return run_locked(s, q, q_row_stride, key_cache, value_cache, num_blocks, block_table, scale,
-                    out, out_row_stride, 0, 1.f, 1.f, ScoreArgs(), st);
+                    out, out_row_stride, kBf16, 1.f, 1.f, ScoreArgs(), 0, st);
 }
 
 extern "C" int pkv_attention(const void* q, int64_t q_row_stride, int64_t q_rows,
@@ -690,7 +710,7 @@ extern "C" int pkv_attention(const void* q, int64_t q_row_stride, int64_t q_rows
   return attention_common(q, q_row_stride, q_rows, num_heads, key_cache, value_cache, num_blocks,
                           block_size, num_kv_heads, head_size, query_start_loc, seq_lens,
                           block_table, block_table_width, num_reqs, scale, out, out_row_stride,
-                          stream, 0, 1.f, 1.f);
+                          stream, kBf16, 1.f, 1.f);
 }
 
 extern "C" int pkv_attention_int8(const void* q, int64_t q_row_stride, int64_t q_rows,
@@ -704,7 +724,7 @@ extern "C" int pkv_attention_int8(const void* q, int64_t q_row_stride, int64_t q
   return attention_common(q, q_row_stride, q_rows, num_heads, key_cache, value_cache, num_blocks,
                           block_size, num_kv_heads, head_size, query_start_loc, seq_lens,
                           block_table, block_table_width, num_reqs, scale, out, out_row_stride,
-                          stream, 1, k_scale, v_scale);
+                          stream, kInt8, k_scale, v_scale);
 }
 
 extern "C" int pkv_attention_scored(const void* q, int64_t q_row_stride, int64_t q_rows,
@@ -734,7 +754,7 @@ extern "C" int pkv_attention_scored(const void* q, int64_t q_row_stride, int64_t
   return attention_common(q, q_row_stride, q_rows, num_heads, key_cache, value_cache, num_blocks,
                           block_size, num_kv_heads, head_size, query_start_loc, seq_lens,
                           block_table, block_table_width, num_reqs, scale, out, out_row_stride,
-                          stream, 0, 1.f, 1.f, score);
+                          stream, kBf16, 1.f, 1.f, score);
 }
 
 extern "C" int pkv_attention_scored_packed(const pkv_attention_scored_args* p) {
@@ -746,6 +766,250 @@ extern "C" int pkv_attention_scored_packed(const pkv_attention_scored_args* p) {
                               p->block_table_width, p->num_reqs, p->scale, p->softcap, p->window,
                               p->alibi_slopes, p->prefix_lens, p->out, p->out_row_stride,
                               p->stream);
+}
+
+namespace {
+
+// The checks that pkv_write_int4 and pkv_read_int4 share (rows: k and v, or the
+// outputs).
+int check_rows4(const void* k, int64_t k_row_stride, const void* v, int64_t v_row_stride,
+                const void* cache, int64_t num_blocks, int32_t block_size, int32_t num_kv_heads,
+                int32_t head_size, const int64_t* slots, int64_t n_tokens) {
+  int rc = check_geometry(block_size, num_kv_heads, head_size);
+  if (rc) return rc;
+  if (n_tokens < 0) return fail(PKV_ERR_ARG, "n_tokens %lld < 0", (long long)n_tokens);
+  if (num_blocks < 1) return fail(PKV_ERR_ARG, "num_blocks %lld < 1", (long long)num_blocks);
+  if (n_tokens == 0) return PKV_OK;
+  if (!k || !v || !cache || !slots) return fail(PKV_ERR_ARG, "null pointer argument");
+  const int64_t row = (int64_t)num_kv_heads * kHeadSize;
+  if (k_row_stride < row || v_row_stride < row)
+    return fail(PKV_ERR_ARG, "row stride below num_kv_heads * head_size (%lld)", (long long)row);
+  if (!aligned16(k) || !aligned16(v) || !aligned16(cache) || (k_row_stride % 8) ||
+      (v_row_stride % 8))
+    return fail(PKV_ERR_ALIGN, "rows and cache must be 16-byte aligned with row strides * 2 a "
+                               "multiple of 16 bytes");
+  return PKV_OK;
+}
+
+// The workspace of pkv_select_pages: 20 bytes a page of `rows` rows and KV heads.  A
+// launch takes at most as many rows as 2^24 pages have, so that many rows over
+// wide tables need no more than 336 MB.  (A room that never shrinks with the
+// arguments: what is reserved for large ones serves smaller ones.)
+struct SelectSizes {
+  int64_t rows;  // of a launch
+  size_t bytes;
+};
+SelectSizes select_sizes(int64_t q_rows, int64_t width, int hkv) {
+  const int64_t per_row = width * hkv, most = std::max<int64_t>(per_row, int64_t(1) << 24);
+  return {std::min(q_rows, most / per_row), (size_t)std::min(q_rows * per_row, most) * 20};
+}
+
+}  // namespace
+
+extern "C" int pkv_write_int4(const void* k, int64_t k_row_stride, const void* v,
+                              int64_t v_row_stride, void* cache, int64_t num_blocks,
+                              int32_t block_size, int32_t num_kv_heads, int32_t head_size,
+                              const int64_t* slot_mapping, int64_t n_tokens, void* stream) {
+  g_msg[0] = 0;
+  int rc = check_rows4(k, k_row_stride, v, v_row_stride, cache, num_blocks, block_size,
+                       num_kv_heads, head_size, slot_mapping, n_tokens);
+  if (rc || n_tokens == 0) return rc;
+  std::lock_guard<std::mutex> lock(g_mu);
+  DeviceState* s = nullptr;
+  rc = current_state(&s);
+  if (rc) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = traced(0, st, [&] {
+    return launch_write_int4(static_cast<const uint16_t*>(k), k_row_stride,
+                             static_cast<const uint16_t*>(v), v_row_stride,
+                             static_cast<uint8_t*>(cache), num_blocks, num_kv_heads, slot_mapping,
+                             n_tokens, s->err, s->sms, st);
+  });
+  if (e != cudaSuccess) return cuda_fail(e, "pkv_write_int4 launch");
+  return PKV_OK;
+}
+
+extern "C" int pkv_read_int4(const void* cache, int64_t num_blocks, int32_t block_size,
+                             int32_t num_kv_heads, int32_t head_size, const int64_t* slots,
+                             int64_t n_tokens, void* k_out, int64_t k_row_stride, void* v_out,
+                             int64_t v_row_stride, void* stream) {
+  g_msg[0] = 0;
+  int rc = check_rows4(k_out, k_row_stride, v_out, v_row_stride, cache, num_blocks, block_size,
+                       num_kv_heads, head_size, slots, n_tokens);
+  if (rc || n_tokens == 0) return rc;
+  std::lock_guard<std::mutex> lock(g_mu);
+  DeviceState* s = nullptr;
+  rc = current_state(&s);
+  if (rc) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = traced(0, st, [&] {
+    return launch_read_int4(static_cast<const uint8_t*>(cache), num_blocks, num_kv_heads, slots,
+                            n_tokens, static_cast<uint16_t*>(k_out), k_row_stride,
+                            static_cast<uint16_t*>(v_out), v_row_stride, s->err, s->sms, st);
+  });
+  if (e != cudaSuccess) return cuda_fail(e, "pkv_read_int4 launch");
+  return PKV_OK;
+}
+
+extern "C" int pkv_attention_int4(const void* q, int64_t q_row_stride, int64_t q_rows,
+                                  int32_t num_heads, const void* cache, int64_t num_blocks,
+                                  int32_t block_size, int32_t num_kv_heads, int32_t head_size,
+                                  const int32_t* query_start_loc, const int32_t* seq_lens,
+                                  const int32_t* block_table, int64_t block_table_width,
+                                  int32_t num_reqs, float scale, void* out, int64_t out_row_stride,
+                                  void* stream) {
+  return attention_common(q, q_row_stride, q_rows, num_heads, cache, cache, num_blocks, block_size,
+                          num_kv_heads, head_size, query_start_loc, seq_lens, block_table,
+                          block_table_width, num_reqs, scale, out, out_row_stride, stream, kInt4,
+                          1.f, 1.f);
+}
+
+extern "C" int pkv_page_bounds(const void* key_cache, int64_t num_blocks, int32_t block_size,
+                               int32_t num_kv_heads, int32_t head_size, void* bounds,
+                               const int64_t* slot_mapping, int64_t n_tokens, void* stream) {
+  g_msg[0] = 0;
+  int rc = check_geometry(block_size, num_kv_heads, head_size);
+  if (rc) return rc;
+  if (n_tokens < 0) return fail(PKV_ERR_ARG, "n_tokens %lld < 0", (long long)n_tokens);
+  if (num_blocks < 1) return fail(PKV_ERR_ARG, "num_blocks %lld < 1", (long long)num_blocks);
+  if (n_tokens == 0) return PKV_OK;
+  if (!key_cache || !bounds || !slot_mapping) return fail(PKV_ERR_ARG, "null pointer argument");
+  if (!aligned16(key_cache) || !aligned16(bounds))
+    return fail(PKV_ERR_ALIGN, "key_cache and bounds must be 16-byte aligned");
+  std::lock_guard<std::mutex> lock(g_mu);
+  DeviceState* s = nullptr;
+  rc = current_state(&s);
+  if (rc) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = traced(0, st, [&] {
+    return launch_page_bounds(static_cast<const uint16_t*>(key_cache), num_blocks, num_kv_heads,
+                              static_cast<uint16_t*>(bounds), slot_mapping, n_tokens, s->err,
+                              s->sms, st);
+  });
+  if (e != cudaSuccess) return cuda_fail(e, "pkv_page_bounds launch");
+  return PKV_OK;
+}
+
+extern "C" int pkv_select_pages(const void* q, int64_t q_row_stride, int64_t q_rows,
+                                int32_t num_heads, const void* bounds, int64_t num_blocks,
+                                int32_t block_size, int32_t num_kv_heads, int32_t head_size,
+                                const int32_t* query_start_loc, const int32_t* seq_lens,
+                                const int32_t* block_table, int64_t block_table_width,
+                                int32_t num_reqs, int32_t budget, int32_t first_pages,
+                                int32_t last_pages, int32_t* sel_table, int32_t* sel_lens,
+                                void* stream) {
+  g_msg[0] = 0;
+  int rc = check_geometry(block_size, num_kv_heads, head_size);
+  if (rc) return rc;
+  rc = check_meta(q_rows, num_heads, num_kv_heads, query_start_loc, seq_lens, block_table_width,
+                  num_reqs);
+  if (rc) return rc;
+  if (num_blocks < 1) return fail(PKV_ERR_ARG, "num_blocks %lld < 1", (long long)num_blocks);
+  if (budget < 1 || budget > kMaxBtWidth)
+    return fail(PKV_ERR_ARG, "budget %d (1 to %d pages)", budget, kMaxBtWidth);
+  if (first_pages < 0 || last_pages < 1 || (int64_t)first_pages + last_pages > budget)
+    return fail(PKV_ERR_ARG, "first_pages %d (>= 0) and last_pages %d (>= 1) must fit the budget %d",
+                first_pages, last_pages, budget);
+  if (q_rows == 0) return PKV_OK;
+  if (q_rows > INT32_MAX) return fail(PKV_ERR_UNSUPPORTED, "q_rows above 2^31");
+  if (!sel_lens) return fail(PKV_ERR_ARG, "null pointer argument");
+  if (num_reqs > 0) {
+    if (!q || !bounds || !block_table || !sel_table) return fail(PKV_ERR_ARG, "null pointer argument");
+    const int64_t row = (int64_t)num_heads * kHeadSize;
+    if (q_row_stride < row)
+      return fail(PKV_ERR_ARG, "q row stride below num_heads * head_size (%lld)", (long long)row);
+    if (!aligned16(q) || !aligned16(bounds) || (q_row_stride % 8))
+      return fail(PKV_ERR_ALIGN, "q and bounds must be 16-byte aligned with a row stride * 2 a "
+                                 "multiple of 16 bytes");
+  }
+  std::lock_guard<std::mutex> lock(g_mu);
+  DeviceState* s = nullptr;
+  rc = current_state(&s);
+  if (rc) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (num_reqs == 0) {  // no row belongs to a request
+    cudaError_t e = cudaMemsetAsync(sel_lens, 0, q_rows * sizeof(int32_t), st);
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e, "clear sel_lens");
+  }
+  SelectArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_stride = q_row_stride;
+  a.q_rows = q_rows;
+  a.hq = num_heads;
+  a.hkv = num_kv_heads;
+  a.bounds = static_cast<const uint16_t*>(bounds);
+  a.num_blocks = num_blocks;
+  a.qsl = query_start_loc;
+  a.seq_lens = seq_lens;
+  a.bt = block_table;
+  a.bt_width = block_table_width;
+  a.num_reqs = num_reqs;
+  a.budget = budget;
+  a.first = first_pages;
+  a.last = last_pages;
+  a.sel_table = sel_table;
+  a.sel_lens = sel_lens;
+  a.err = s->err;
+  const SelectSizes z = select_sizes(q_rows, block_table_width, num_kv_heads);
+  // (scores are formed unless every row's pages, or the forced ones, fill the budget)
+  const bool score = block_table_width > budget && budget > first_pages + last_pages;
+  if (score) {
+    bool grown = false;
+    rc = ensure_buffer(&s->sel_ws, &s->sel_bytes, &s->sel_in_graph, z.bytes, "pkv_reserve_select",
+                       st, &grown);
+    if (rc) return rc;
+    note_capture(&s->sel_in_graph, st);
+    uint8_t* p = static_cast<uint8_t*>(s->sel_ws);
+    const int64_t n = z.rows * num_kv_heads * block_table_width;
+    a.exact = reinterpret_cast<double*>(p);
+    a.scores = reinterpret_cast<float*>(p + n * 8);
+    a.index = reinterpret_cast<int32_t*>(p + n * 12);
+    a.largest = reinterpret_cast<float*>(p + n * 16);
+    a.largest_stride = (block_table_width + 31) / 32;
+    a.chunk_pages = select_chunk_pages(z.rows, num_kv_heads, block_table_width, s->sms);
+  }
+  for (int64_t row0 = 0; row0 < q_rows; row0 += z.rows) {
+    const int rows = (int)std::min(z.rows, q_rows - row0);
+    cudaError_t e = cudaSuccess;
+    if (score) e = traced(5, st, [&] { return launch_page_scores(a, row0, rows, s->sms, st); });
+    if (e == cudaSuccess)
+      e = traced(5, st, [&] { return launch_select(a, row0, rows, score, st); });
+    if (e != cudaSuccess) return cuda_fail(e, "pkv_select_pages launch");
+  }
+  return PKV_OK;
+}
+
+extern "C" int pkv_reserve_select(int64_t max_q_rows, int64_t block_table_width,
+                                  int32_t num_kv_heads) {
+  g_msg[0] = 0;
+  if (max_q_rows < 0 || block_table_width < 0 || block_table_width > kMaxBtWidth ||
+      num_kv_heads <= 0 || num_kv_heads > 32767)
+    return fail(PKV_ERR_ARG, "bad sizes");
+  std::lock_guard<std::mutex> lock(g_mu);
+  DeviceState* s = nullptr;
+  int rc = current_state(&s);
+  if (rc) return rc;
+  if (max_q_rows == 0 || block_table_width == 0) return PKV_OK;
+  bool grown = false;
+  return ensure_buffer(&s->sel_ws, &s->sel_bytes, &s->sel_in_graph,
+                       select_sizes(max_q_rows, block_table_width, num_kv_heads).bytes,
+                       "pkv_reserve_select", nullptr, &grown);
+}
+
+extern "C" int pkv_attention_selected(const void* q, int64_t q_row_stride, int64_t q_rows,
+                                      int32_t num_heads, const void* key_cache,
+                                      const void* value_cache, int64_t num_blocks,
+                                      int32_t block_size, int32_t num_kv_heads, int32_t head_size,
+                                      const int32_t* sel_table, int64_t sel_width,
+                                      const int32_t* sel_lens, float scale, void* out,
+                                      int64_t out_row_stride, void* stream) {
+  g_msg[0] = 0;
+  if (q_rows > INT32_MAX) return fail(PKV_ERR_UNSUPPORTED, "q_rows above 2^31");
+  // (every row is a request of one token; the plan reads no query_start_loc)
+  return attention_common(q, q_row_stride, q_rows, num_heads, key_cache, value_cache, num_blocks,
+                          block_size, num_kv_heads, head_size, sel_lens, sel_lens, sel_table,
+                          sel_width, (int32_t)q_rows, scale, out, out_row_stride, stream, kBf16,
+                          1.f, 1.f, ScoreArgs(), 1);
 }
 
 extern "C" int pkv_reserve_workspace(int32_t max_reqs, int64_t max_q_rows,

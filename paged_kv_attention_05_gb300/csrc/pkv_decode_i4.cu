@@ -1,0 +1,465 @@
+// Split-KV decode attention over the cache of 4-bit codes (pkv_attention_int4):
+// requests of one query token, or a few.  Longer ones take the prefill kernel's
+// instance for this cache; work units, split results and their merge are those of
+// the bf16 path.
+//
+// Mathematics.  K_j = s_j c_j + z_j with codes c_j and the row's own scale and zero;
+// for values t_j and y_j likewise.  A row's logits (log2 units, f = scale * log2 e):
+//   x_j = f s_j (q . c_j) + f z_j (sum_d q_d),
+// and with weights e_j = 2^(x_j - ref), over the keys:
+//   out = (sum_j (e_j t_j) c_j + sum_j e_j y_j) / sum_j e_j,
+// so that the products run on the codes, and scales and zeros are two multiply-adds a
+// score and one a weight.
+//
+// GB300 design.  A page of a KV head is one record of 2176 bytes (keys, values,
+// scales), one bulk copy into a ring of the warp's own; nothing else is read.  At
+// 6.8 TB/s an SM gets a page every 93 cycles, 372 issue slots, of which the codes'
+// way into the MMA operands may take a part:
+//   * codes as fp16 numbers without an operation besides the mask: a nibble in the
+//     low bits of a half is the subnormal c * 2^-24, one place up c * 2^-20, exact
+//     either way.  A word and the word shifted by 8, each with two masks, are the
+//     operands of 8 codes (five operations).  The power of two is undone in fp32:
+//     2^-24 at the end, and the 16 between the two masks in the query (half of its
+//     values are divided by 16), in the output by its rows.
+//   * keys and output dimensions are the MMA's 16 rows and query rows its 8 columns
+//     (S^T = K Q^T, O^T = V^T P^T): a step of 8 query rows, which groups of up to 8
+//     heads need, takes half the MMAs and accumulators of query rows in the 16-row
+//     operand.  P^T's operand is S^T's accumulator transposed, 8x8 by 8x8
+//     (movmatrix).
+//   * k order of S: a thread holds 32 consecutive dimensions of its two keys; the
+//     16 keys of a page are the MMA rows in the order kappa(m), so that the value
+//     rows that the threads of a quad read lie in different banks.
+//   * query rows are scaled by a power of two, so that their largest value is
+//     between 2^10 and 2^11 in fp16: bf16's 8 bits stay exact, whatever the range.
+//   * weights: e_j t_j is rounded to fp16 (2^-12 of itself at most).  The
+//     reference follows the largest e_j t_j of a row, not the largest e_j: fp16's range
+//     then holds every weight that counts, however large or small the value rows'
+//     scales.  It is moved only when a weight passes 2^14 (checked by one vote a
+//     page, no exchange between the lanes otherwise).
+// Keys past the unit's end get weight 0 and scale and zero 0.
+#include <cuda_fp16.h>
+
+#include "pkv_int4.cuh"
+#include "pkv_sched.cuh"
+
+namespace pkv {
+namespace {
+
+using namespace dev;
+
+constexpr int kIdRegs4 = kMaxChunk / kBlockSize / 32;
+constexpr uint32_t kNib0 = 0x000F000Fu, kNib1 = 0x00F000F0u;
+constexpr float kMaxWeight = 16384.f;  // e_j t_j that the reference is kept for
+constexpr float kMaxExp = 0x1p54f;     // e_j (of value rows with tiny or no scale)
+
+// kTiles: the most tiles of 8 query rows a unit has
+template <int kTiles>
+struct Cfg4 {
+  static constexpr int kWarps = kTiles <= 2 ? 12 : 8;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kStages = kTiles <= 2 ? 8 : 12;
+  static constexpr int kWarpBytes = kStages * kPage4;
+  static constexpr int kOffBar = kWarps * kWarpBytes;
+  static constexpr int kOffCtl = kOffBar + kWarps * kStages * 8;
+  static constexpr int kSmem = kOffCtl + 16 + 128;
+  static_assert(kSmem <= 232448, "shared memory per CTA");
+};
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(v) : "r"(addr));
+  return v;
+}
+// D += A(16x16, row) * B(16x8, col); fp16 inputs, fp32 accumulators.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// the 8x8 matrix of b16 values that the warp holds, transposed
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(d) : "r"(v));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+// One warp's view of its ring.
+struct Ring {
+  uint32_t base, bars;
+  uint32_t cnt;  // pages taken so far
+};
+
+// A unit of at most 8 * kT query rows.  Returns false when a wait gave up.
+template <int kT, int kStages>
+__device__ __forceinline__ bool run_unit(const AttnArgs& a, const Workspace& ws, const DecUnit& un,
+                                         Ring& ring, uint64_t pol, volatile int* abort) {
+  const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+  const int G = a.hq / a.hkv;
+  const int ug = un.gq & 0xFFFF;  // KV head
+  const int qn = un.gq >> 16;     // query tokens of the request
+  const int k0 = un.k0, k1 = un.k1;
+  const int p0 = k0 / kBlockSize;
+  const int npages = (k1 + kBlockSize - 1) / kBlockSize - p0;
+  const int nrows = qn * G;
+
+  // block ids of the unit, one per lane per 32 pages
+  int ids[kIdRegs4];
+  const int* btrow = table_row(a, un.r, ug) + p0;
+#pragma unroll
+  for (int j = 0; j < kIdRegs4; ++j) {
+    const int p = lane + 32 * j;
+    int blk = 0;
+    if (p < npages) {
+      blk = __ldg(btrow + p);
+      if (blk < 0 || (int64_t)blk >= a.num_blocks) {
+        atomicOr(ws.err, PKV_DEV_ERR_BLOCK_ID);
+        blk = 0;
+      }
+    }
+    ids[j] = blk;
+  }
+  // page p into its stage, by the lane that holds its id; the stage's last page was
+  // taken by this warp already (program order)
+  auto issue = [&](int p) {
+    const uint32_t s = (ring.cnt + p) % kStages;
+    int id = ids[0];
+#pragma unroll
+    for (int j = 1; j < kIdRegs4; ++j)
+      if ((p >> 5) == j) id = ids[j];
+    if (lane == (p & 31)) {
+      fence_async_smem();
+      const uint32_t bar = ring.bars + 8 * s;
+      mbar_expect_tx(bar, kPage4);
+      bulk_load_hint(ring.base + s * kPage4,
+                     reinterpret_cast<const uint8_t*>(a.kc) + ((int64_t)id * a.hkv + ug) * kPage4,
+                     kPage4, bar, pol);
+    }
+  };
+  for (int p = 0; p < kStages && p < npages; ++p) issue(p);
+
+  // Query rows: tile t has rows 8 t .. 8 t + 7 (token * G + head in group), a thread
+  // dimensions 32 tig .. + 31 of row gid.  Operand pair 2 i + h of k-step order: word
+  // i of the keys' codes, shifted by 8 h.
+  uint32_t qb[kT][8][2];
+  float fac[kT][2], off[kT][2];  // by the thread's two columns: f * 2^(24 + exponent), f * sum q
+  int vis[kT][2];                // keys the column's row sees end here
+  const float f = a.scale * kLog2e;
+#pragma unroll
+  for (int t = 0; t < kT; ++t) {
+    const int row = 8 * t + gid;
+    uint4 raw[4] = {};
+    if (row < nrows) {
+      const uint4* src = reinterpret_cast<const uint4*>(
+          a.q + (int64_t)(un.q0 + row / G) * a.q_stride + (int64_t)(ug * G + row % G) * kHeadSize +
+          32 * tig);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) raw[i] = __ldg(src + i);
+    }
+    float big = 0.f, sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        big = max3f(big, fabsf(lo16(w[j])), fabsf(hi16(w[j])));
+        sum += lo16(w[j]) + hi16(w[j]);
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+      sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
+    // q * 2^-ex, its largest value in [2^10, 2^11)
+    const int ex = max((int)(__float_as_uint(big) >> 23) - 127 - 10, -100);
+    const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+    const float rf = f * __uint_as_float((uint32_t)(127 + ex) << 23) * 0x1p24f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float m = j & 1 ? down * 0.0625f : down;
+        qb[t][2 * i + (j >> 1)][j & 1] = pack_f16(lo16(w[j]) * m, hi16(w[j]) * m);
+      }
+    }
+    const float rs = f * sum;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      fac[t][c] = __shfl_sync(0xffffffffu, rf, 4 * (2 * tig + c));
+      off[t][c] = __shfl_sync(0xffffffffu, rs, 4 * (2 * tig + c));
+      const int r = 8 * t + 2 * tig + c;
+      vis[t][c] = min(k1, un.ctx + (r < nrows ? r / G : qn - 1) + 1);
+    }
+  }
+  const int all_see = min(k1, un.ctx + 1);  // every row sees the keys before
+
+  // o[t][d]: output dimensions of the thread's two MMA rows (see below), columns 2 tig,
+  // + 1; sums of e and of e * zero over the thread's keys
+  float o[kT][8][4], l[kT][2], z[kT][2], ref[kT][2];
+#pragma unroll
+  for (int t = 0; t < kT; ++t) {
+#pragma unroll
+    for (int d = 0; d < 8; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[t][d][e] = 0.f;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      l[t][c] = z[t][c] = 0.f;
+      ref[t][c] = -INFINITY;
+    }
+  }
+  bool unset = true;  // some row has no reference yet (no key it sees)
+
+  // MMA row m < 8 of a page's first (second) eight is its key kappa(m) (+ 8)
+  const int key = ((gid >> 1) ^ (gid & 1)) + 4 * (gid & 1);
+
+  for (int p = 0; p < npages; ++p) {
+    const uint32_t x = ring.cnt + p, s = x % kStages;
+    if (!mbar_wait_warp(ring.bars + 8 * s, (x / kStages) & 1, abort, ws.err)) return false;
+    const uint32_t st = ring.base + s * kPage4;
+    const int pos0 = k0 + p * kBlockSize;
+    const uint4 ka = lds128(st + kRow4 * key + 16 * tig);
+    const uint4 kb = lds128(st + kRow4 * (key + 8) + 16 * tig);
+    uint32_t mk[2], mv[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      mk[i] = lds32(st + kMeta4 + 4 * (key + 8 * i));
+      mv[i] = lds32(st + kMeta4 + 64 + 4 * (key + 8 * i));
+    }
+    // values: keys kappa(2 tig), kappa(2 tig + 1) and those 8 on, dimensions 16 gid .. + 15
+    const uint32_t sv = st + kSide4 + 8 * gid;
+    const uint2 va = lds64(sv + kRow4 * tig), vb = lds64(sv + kRow4 * ((tig ^ 1) + 4));
+    const uint2 vc = lds64(sv + kRow4 * (tig + 8)), vd = lds64(sv + kRow4 * ((tig ^ 1) + 12));
+
+    // S^T = K Q^T
+    float acc[kT][4];
+#pragma unroll
+    for (int t = 0; t < kT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
+    const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t ca = wa[i >> 1] >> (8 * (i & 1)), cb = wb[i >> 1] >> (8 * (i & 1));
+#pragma unroll
+      for (int t = 0; t < kT; ++t)
+        mma_f16(acc[t], ca & kNib0, cb & kNib0, ca & kNib1, cb & kNib1, qb[t][i][0], qb[t][i][1]);
+    }
+    // the page is in registers: its stage can take another
+    __syncwarp();
+    if (p + kStages < npages) issue(p + kStages);
+
+    // logits: acc[t][0], [1] of the thread's first key, [2], [3] of its second
+    const bool edge = pos0 + kBlockSize > all_see;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int j = pos0 + key + 8 * i;
+      const float ks = lo16(mk[i]), kz = hi16(mk[i]);
+      if (edge && j >= k1) mv[i] = 0u;
+#pragma unroll
+      for (int t = 0; t < kT; ++t)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float v = fmaf(acc[t][2 * i + c] * ks, fac[t][c], kz * off[t][c]);
+          acc[t][2 * i + c] = edge && j >= vis[t][c] ? -INFINITY : v;
+        }
+    }
+    float e[kT][4], w[kT][4];
+    auto weights = [&]() {
+      float most = 0.f, tall = 0.f;
+#pragma unroll
+      for (int t = 0; t < kT; ++t) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float r = ref[t][i & 1];
+          e[t][i] = fast_exp2(acc[t][i] - (unset && r == -INFINITY ? 0.f : r));
+          w[t][i] = e[t][i] * lo16(mv[i >> 1]);
+        }
+        most = max3f(most, fmaxf(w[t][0], w[t][1]), fmaxf(w[t][2], w[t][3]));
+        tall = max3f(tall, fmaxf(e[t][0], e[t][1]), fmaxf(e[t][2], e[t][3]));
+      }
+      return most > kMaxWeight || tall > kMaxExp;
+    };
+    if (__any_sync(0xffffffffu, unset || weights())) {
+      // references moved up: to the largest logit + log2 of the value row's scale
+      // (weights up to 1), or so that e stays below 2^40
+      const float t0 = __log2f(lo16(mv[0])), t1 = __log2f(lo16(mv[1]));
+      bool none = false;
+#pragma unroll
+      for (int t = 0; t < kT; ++t)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float m = fmaxf(acc[t][c], acc[t][2 + c]) - 40.f;
+          m = max3f(m, acc[t][c] + t0, acc[t][2 + c] + t1);
+#pragma unroll
+          for (int b = 4; b < 32; b <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, b));
+          const float to = fmaxf(ref[t][c], m);
+          const float al = ref[t][c] == -INFINITY ? 0.f : fast_exp2(ref[t][c] - to);
+          ref[t][c] = to;
+          none |= to == -INFINITY;
+          l[t][c] *= al;
+          z[t][c] *= al;
+#pragma unroll
+          for (int d = 0; d < 8; ++d) {
+            o[t][d][c] *= al;
+            o[t][d][2 + c] *= al;
+          }
+        }
+      unset = true;  // (for the references still missing)
+      weights();
+      unset = __any_sync(0xffffffffu, none);
+    }
+    uint32_t pb[kT][2];
+#pragma unroll
+    for (int t = 0; t < kT; ++t) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        l[t][c] += e[t][c] + e[t][2 + c];
+        z[t][c] = fmaf(e[t][c], hi16(mv[0]), fmaf(e[t][2 + c], hi16(mv[1]), z[t][c]));
+        pb[t][c] = transpose8x8(pack_f16(w[t][2 * c], w[t][2 * c + 1]));
+      }
+    }
+
+    // O^T += V^T P^T: a word of codes of the two keys of an operand pair, their low
+    // halves together and their high ones, hold dimensions 0, 2, 4, 6 and 1, 3, 5, 7 of the
+    // eight; MMA rows gid and gid + 8 are the first and second nibble of each byte
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t a0 = h ? va.y : va.x, a1 = h ? vb.y : vb.x;
+      const uint32_t b0 = h ? vc.y : vc.x, b1 = h ? vd.y : vd.x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // even dimensions 0, 2 | 4, 6; odd 1, 3 | 5, 7
+        const uint32_t sel = i < 2 ? 0x5410 : 0x7632;
+        const uint32_t lo = __byte_perm(a0, a1, sel) >> (8 * (i & 1));
+        const uint32_t hi = __byte_perm(b0, b1, sel) >> (8 * (i & 1));
+#pragma unroll
+        for (int t = 0; t < kT; ++t)
+          mma_f16(o[t][4 * h + i], lo & kNib0, lo & kNib1, hi & kNib0, hi & kNib1, pb[t][0],
+                  pb[t][1]);
+      }
+    }
+  }
+  ring.cnt += npages;
+
+  // The thread's columns 2 tig, 2 tig + 1 are query rows, with dimensions 16 gid .. + 15:
+  // o[4 h + i][c] is dimension 8 h + 4 (i % 2) + i / 2, o[4 h + i][2 + c] the one 2 on.
+#pragma unroll
+  for (int t = 0; t < kT; ++t)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float ls = l[t][c], zs = z[t][c];
+#pragma unroll
+      for (int b = 4; b < 32; b <<= 1) {
+        ls += __shfl_xor_sync(0xffffffffu, ls, b);
+        zs += __shfl_xor_sync(0xffffffffu, zs, b);
+      }
+      const int row = 8 * t + 2 * tig + c;
+      if (row >= nrows) continue;
+      float v[16];
+#pragma unroll
+      for (int d = 0; d < 8; ++d) {
+        const int at = 8 * (d >> 2) + 4 * (d & 1) + ((d >> 1) & 1);
+        v[at] = fmaf(o[t][d][c], 0x1p24f, zs);
+        v[at + 2] = fmaf(o[t][d][2 + c], 0x1p20f, zs);
+      }
+      if (un.nsplit == 1) {
+        const float inv = 1.f / ls;
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = pack_bf16(v[2 * i] * inv, v[2 * i + 1] * inv);
+        uint4* dst = reinterpret_cast<uint4*>(
+            a.out + (int64_t)(un.q0 + row / G) * a.out_stride +
+            (int64_t)(ug * G + row % G) * kHeadSize + 16 * gid);
+        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      } else {
+        float4* dst = reinterpret_cast<float4*>(ws.part_o + ((int64_t)un.part + row) * kHeadSize +
+                                                16 * gid);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        if (gid == 0)
+          *reinterpret_cast<float2*>(ws.part_ml + ((int64_t)un.part + row) * 2) =
+              make_float2(ref[t][c], ls);
+      }
+    }
+  return true;
+}
+
+template <int kTiles>
+__global__ void __launch_bounds__(Cfg4<kTiles>::kThreads, 1)
+    decode_i4_kernel(AttnArgs a, Workspace ws) {
+  using C = Cfg4<kTiles>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) &
+                                             ~(uintptr_t)127);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t sbase = smem_u32(smem);
+  Ring ring{sbase + warp * C::kWarpBytes, sbase + C::kOffBar + warp * C::kStages * 8, 0};
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + C::kOffCtl);
+  if (lane == 0) {
+    for (int s = 0; s < C::kStages; ++s) mbar_init(ring.bars + 8u * s, 1);
+    if (warp == 0) *abort = 0;
+    fence_barrier_init();
+  }
+  // the set-up above overlaps the plan kernel; the work list is read after it
+  grid_dep_wait();
+  grid_dep_launch();
+  if (leaves_sm_to_prefill(a, ws, C::kWarps) || ws.hdr->n_dec_units == 0) return;
+  __syncthreads();
+  const int n_units = ws.hdr->n_dec_units;
+  const uint64_t pol = l2_evict_first();  // pages are read once
+  for (;;) {
+    int u = 0;
+    if (lane == 0) u = atomicAdd(&ws.hdr->dec_counter, 1);
+    u = __shfl_sync(0xffffffffu, u, 0);
+    if (u >= n_units || *abort) break;
+    const DecUnit un = load_unit(ws.units + u);
+    bool ok;
+    if (kTiles == 2 && (un.gq >> 16) * (a.hq / a.hkv) <= 8)
+      ok = run_unit<1, C::kStages>(a, ws, un, ring, pol, abort);
+    else
+      ok = run_unit<kTiles, C::kStages>(a, ws, un, ring, pol, abort);
+    if (!ok) break;
+  }
+}
+
+template <int kTiles>
+cudaError_t launch_i4(const AttnArgs& a, const Workspace& ws, int sms, cudaStream_t st) {
+  using C = Cfg4<kTiles>;
+  static std::atomic<bool> attr[kMaxAttrDevices];
+  if (cudaError_t e = smem_attr_once(decode_i4_kernel<kTiles>, C::kSmem, attr)) return e;
+  return launch_dependent(decode_i4_kernel<kTiles>, dim3(sms), dim3(C::kThreads), C::kSmem, st, a,
+                          ws);
+}
+
+}  // namespace
+
+int decode_i4_warps(int group) { return group <= 16 ? Cfg4<2>::kWarps : Cfg4<4>::kWarps; }
+
+cudaError_t launch_decode_i4(const AttnArgs& a, const Workspace& ws, int sms, cudaStream_t st) {
+  return a.hq / a.hkv <= 16 ? launch_i4<2>(a, ws, sms, st) : launch_i4<4>(a, ws, sms, st);
+}
+
+}  // namespace pkv

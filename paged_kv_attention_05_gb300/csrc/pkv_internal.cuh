@@ -128,6 +128,53 @@ cudaError_t launch_write_int8(const uint16_t* k, int64_t k_stride, const uint16_
                               int hkv, const int64_t* slots, int64_t n_tokens, float k_scale,
                               float v_scale, int* err, int sms, cudaStream_t st);
 
+// The cache of 4-bit codes: write, and read back into bf16 rows (pkv_write_i4.cu).
+cudaError_t launch_write_int4(const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                              int64_t v_stride, uint8_t* cache, int64_t num_blocks, int hkv,
+                              const int64_t* slots, int64_t n_tokens, int* err, int sms,
+                              cudaStream_t st);
+cudaError_t launch_read_int4(const uint8_t* cache, int64_t num_blocks, int hkv,
+                             const int64_t* slots, int64_t n_tokens, uint16_t* k_out,
+                             int64_t k_stride, uint16_t* v_out, int64_t v_stride, int* err, int sms,
+                             cudaStream_t st);
+
+// Page bounds and the selection of pages (pkv_pages.cu).
+cudaError_t launch_page_bounds(const uint16_t* kc, int64_t num_blocks, int hkv, uint16_t* bounds,
+                               const int64_t* slots, int64_t n_tokens, int* err, int sms,
+                               cudaStream_t st);
+struct SelectArgs {
+  const uint16_t* q;
+  int64_t q_stride, q_rows;
+  int hq, hkv;
+  const uint16_t* bounds;  // [num_blocks][hkv][2][128]
+  int64_t num_blocks;
+  const int32_t* qsl;
+  const int32_t* seq_lens;
+  const int32_t* bt;
+  int64_t bt_width;
+  int num_reqs;
+  int budget, first, last;
+  int32_t* sel_table;  // [q_rows][hkv][budget]
+  int32_t* sel_lens;   // [q_rows]
+  // workspace, by (row of a launch, KV head): the pages' fp32 scores, the largest
+  // bound each scoring warp met, scores in 64 bits and the pages they belong to
+  float* scores;
+  float* largest;
+  double* exact;
+  int32_t* index;
+  int64_t largest_stride;
+  int chunk_pages;  // pages of a scoring warp
+  int* err;
+};
+// Pages a scoring warp takes.
+int select_chunk_pages(int64_t rows, int hkv, int64_t bt_width, int sms);
+// Rows row0 .. row0 + rows - 1: the scores (of calls in which a row can need them),
+// and the selection.
+cudaError_t launch_page_scores(const SelectArgs& a, int64_t row0, int rows, int sms,
+                               cudaStream_t st);
+cudaError_t launch_select(const SelectArgs& a, int64_t row0, int rows, bool score,
+                          cudaStream_t st);
+
 // The cache write with the rotation (and the optional norms) of queries and
 // keys (pkv_rope.cu).
 struct RopeArgs {
@@ -205,12 +252,24 @@ struct AttnArgs {
   float scale;
   uint16_t* out;
   int64_t out_stride;
-  // int8 caches (kc / vc then point at int8 codes): K = code * k_scale,
-  // V = code * v_scale; decode-class requests only
-  int kv_int8;
+  // what the cache holds.  kInt8 (kc / vc point at codes): K = code * k_scale, V =
+  // code * v_scale; decode-class requests only.  kInt4: kc points at the pages of
+  // codes (pkv_int4.cuh), vc is not used
+  int kv;
   float k_scale;
   float v_scale;
+  // pkv_attention_selected: every query row is a request of one token, row r's keys
+  // (seq_lens[r] of them, 0: no row to write) lie in the pages of the rows
+  // r * (bt_more + 1) + KV head of bt, and seq_lens comes from the kernel before;
+  // else 0, and request r's row is r
+  int sel = 0;
+  int bt_more = 0;
 };
+enum KvType { kBf16 = 0, kInt8 = 1, kInt4 = 2 };
+// the block-table row of a decode unit's pages
+__host__ __device__ inline const int32_t* table_row(const AttnArgs& a, int r, int g) {
+  return a.bt + ((int64_t)r * (a.bt_more + 1) + (g < a.bt_more ? g : a.bt_more)) * a.bt_width;
+}
 
 // The launchers take the arguments with the scores'; the kernels of the plain
 // calls get them without (168 bytes less to pass at each launch).
@@ -257,11 +316,14 @@ cudaError_t launch_plan(const ScoredArgs& a, const Workspace& ws, int dec_grid, 
 cudaError_t launch_decode(const ScoredArgs& a, const Workspace& ws, int sms, cudaStream_t st);
 // the decode path over int8 caches (pkv_decode_i8.cu)
 cudaError_t launch_decode_i8(const AttnArgs& a, const Workspace& ws, int sms, cudaStream_t st);
+// the decode path over the cache of 4-bit codes (pkv_decode_i4.cu)
+cudaError_t launch_decode_i4(const AttnArgs& a, const Workspace& ws, int sms, cudaStream_t st);
 cudaError_t launch_combine(const AttnArgs& a, const Workspace& ws, int sms, cudaStream_t st);
 // Independent decode workers (warps) the decode grid runs for a head grouping
 // and cache type; the plan sizes its split chunks for this many.
-int decode_workers(int group, int kv_int8, int sms);
+int decode_workers(int group, int kv, int sms);
 int decode_i8_warps(int group);
+int decode_i4_warps(int group);
 cudaError_t launch_prefill(const ScoredArgs& a, const Workspace& ws, int sms, cudaStream_t st);
 
 // Programmatic dependent launch.  The cache write and the attention kernels

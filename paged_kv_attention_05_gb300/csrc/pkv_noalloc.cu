@@ -155,7 +155,7 @@ extern "C" int pkv_attention_noalloc(const void* q, int64_t q_row_stride, int64_
   a.scale = scale;
   a.out = static_cast<uint16_t*>(out);
   a.out_stride = out_row_stride;
-  a.kv_int8 = 0;
+  a.kv = kBf16;
   a.k_scale = a.v_scale = 1.f;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // the kernels of pkv_attention, one after the other on the caller's stream

@@ -109,7 +109,10 @@ struct ReqInfo {
 template <bool kScored>
 __device__ ReqInfo classify(const ArgsOf<kScored>& a, int r) {
   ReqInfo ri{0, 0, 0, 0, 0, 0};
-  const int q0 = __ldcg(a.qsl + r), q1 = __ldcg(a.qsl + r + 1), L = __ldcg(a.seq_lens + r);
+  const int L = __ldcg(a.seq_lens + r);
+  const bool sel = !kScored && a.sel;  // (pkv_attention_selected: row r is a request)
+  if (sel && L == 0) return ri;
+  const int q0 = sel ? r : __ldcg(a.qsl + r), q1 = sel ? r + 1 : __ldcg(a.qsl + r + 1);
   int bad = 0;
   if (q0 < 0 || q1 < q0 || (int64_t)q1 > a.q_rows)
     bad = PKV_DEV_ERR_QSL;
@@ -129,7 +132,7 @@ __device__ ReqInfo classify(const ArgsOf<kScored>& a, int r) {
   // (speculative / multi-token decode included); prefill: anything longer
   const int G = a.hq / a.hkv;
   ri.kind = ri.n == 0 ? 0 : (ri.n * G <= dec_rows_cap(G) ? 1 : 2);
-  if (ri.kind == 2 && a.kv_int8) {  // int8 caches are read by the decode path only
+  if (ri.kind == 2 && a.kv == kInt8) {  // int8 caches are read by the decode path only
     ri.kind = 0;
     ri.bad = PKV_DEV_ERR_INT8_PREFILL;
   }
@@ -172,6 +175,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ArgsOf<kScored> a, W
   // this grid does not finish before it: a kernel that waits for this one
   // also finds the cache write done.
   grid_dep_launch();
+  // (the lengths of selected pages come from the selection: waited for)
+  if (!kScored && a.sel) grid_dep_wait();
 
   // pass 1: total decode keys, decode requests and their longest length, to
   // size the split-KV chunk (a thread keeps its first request's

@@ -51,6 +51,7 @@
 
 #include "pkv_combine.cuh"
 #include "pkv_device.cuh"
+#include "pkv_int4.cuh"
 #include "pkv_score.cuh"
 
 namespace pkv {
@@ -106,6 +107,13 @@ constexpr int kOffXch = kOffItems + 2 * 48;        // [4 quarters][2 slots][2 ha
 constexpr int kOffCtl = kOffXch + 4 * 2 * 2 * 32 * 4;  // TMEM address, abort flag
 constexpr int kOffBarLF1 = kOffCtl + 16;           // [2] the same for odd items
 constexpr int kSmemBytes = kOffBarLF1 + 16 + 1024;  // + alignment slack
+// The instance for the cache of 4-bit codes: four more warps, and a tile's pages as
+// they are cached.
+constexpr int kDequantWarps = 2;
+constexpr int kOffBarRaw = kOffBarLF1 + 16;        // raw pages loaded, taken
+constexpr int kOffRaw = (kOffBarRaw + 16 + 127) / 128 * 128;
+constexpr int kSmemBytesI4 = kOffRaw + 8 * kPage4 + 1024;
+static_assert(kSmemBytesI4 <= 232448, "shared memory per CTA");
 
 struct Item {
   int r, qt, ha, hb;  // hb < 0: single-tile item
@@ -390,10 +398,22 @@ __device__ __forceinline__ void rescale16_bf16(uint32_t t, float alpha) {
   PKV_ST16U(t, u);
 }
 
+// Two codes (bits 0 .. 3 of each half of w) to the bf16 pair s * code + z, rounded
+// once: 128 + code has its code in the last bits of a bf16, less 128 is exact.
+__device__ __forceinline__ uint32_t dequant2(uint32_t w, __nv_bfloat162 s, __nv_bfloat162 z) {
+  const uint32_t u = (w & 0x000F000Fu) | 0x43004300u;
+  const __nv_bfloat162 c = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u),
+                                   __float2bfloat162_rn(128.f));
+  const __nv_bfloat162 v = __hfma2(c, s, z);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
 // kScored: a window, a prefix (runtime), and per instance a cap, a bias (kSym:
-// that may meet keys after a row's position, with a prefix).
-template <bool kScored, Cap kCap, bool kBias, bool kSym>
-__global__ void __launch_bounds__(threads_of(kCap == kFixedCap), 1)
+// that may meet keys after a row's position, with a prefix).  kI4: the cache of 4-bit
+// codes (pkv_attention_int4): the producer brings a tile's pages as they are cached,
+// and four more warps turn them into the bf16 K and V tiles that the others expect.
+template <bool kScored, Cap kCap, bool kBias, bool kSym, bool kI4 = false>
+__global__ void __launch_bounds__(threads_of(kCap == kFixedCap) + (kI4 ? 32 * kDequantWarps : 0), 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, ArgsOf<kScored> a,
                    Workspace ws) {
@@ -404,7 +424,8 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap), 1)
   // the kernels before it wrote is read through L2 (ld.global.cg).  The split
   // decode results are merged at the end, once the decode grid has finished
   // (so this grid finishing implies that every kernel before it has).
-  constexpr int kSoft = soft_warps(kCap == kFixedCap), kThreads = threads_of(kCap == kFixedCap);
+  constexpr int kSoft = soft_warps(kCap == kFixedCap), kDeq = kI4 ? kDequantWarps : 0;
+  constexpr int kThreads = threads_of(kCap == kFixedCap) + 32 * kDeq;
   constexpr int kHalves = kScored ? kSoft / 8 : 2;  // softmax warps that share a row
   // (a scored call lets the next kernel, usually another call's plan or cache
   // write, set up meanwhile: everything before this kernel has finished or, as
@@ -448,7 +469,12 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap), 1)
       mbar_init(bar(B_OE + x), 4);  // one arrival per epilogue warp
       mbar_init(bar(B_LF + x), 4 * kHalves);  // one arrival per softmax warp of the tile
       mbar_init(sbase + kOffBarLF1 + 8 * x, 4 * kHalves);
-      mbar_init(bar(B_IE + x), 1 + kSoft + 4);  // MMA warp, softmax warps, epilogue warps
+      mbar_init(bar(B_IE + x), 1 + kSoft + 4 + kDeq);  // MMA warp, softmax, epilogue (and these)
+      if (kI4) {  // one arrival per dequantising warp
+        mbar_init(bar(B_KF + x), kDeq);
+        mbar_init(bar(B_VF + x), kDeq);
+        mbar_init(sbase + kOffBarRaw + 8 * x, x == 0 ? 1 : kDeq);
+      }
     }
     for (int i = 0; i < 4; ++i) mbar_init(bar(B_XP + i), 2);
     ctl[1] = 0;
@@ -554,6 +580,28 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap), 1)
         const int s = c % kStages;
         const int key0 = tile_key(j);
         const int pages = tile_pages(key0);
+        if (kI4) {
+          int blk = blk_nxt;
+          if (j + 1 < it.nkv && lane < tile_pages(tile_key(j + 1)))
+            blk_nxt = __ldcg(btrow + (tile_key(j + 1) >> 4) + lane);
+          if (lane < pages && (blk < 0 || (int64_t)blk >= a.num_blocks)) {
+            atomicOr(ws.err, PKV_DEV_ERR_BLOCK_ID);
+            blk = 0;
+          }
+          const uint32_t full = sbase + kOffBarRaw, taken = full + 8;
+          if (c > 0 && !mbar_wait_warp(taken, (c - 1) & 1, abort, ws.err)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_expect_tx(full, pages * kPage4);
+          __syncwarp();
+          if (lane < pages)
+            bulk_load(sbase + kOffRaw + lane * kPage4,
+                      reinterpret_cast<const uint8_t*>(a.kc) +
+                          ((int64_t)blk * a.hkv + it.g) * kPage4,
+                      kPage4, full);
+          continue;
+        }
         const bool tail = key0 + kTileK > it.L || (kScored && key0 < vlow);
         int blk = blk_nxt;
         if (j + 1 < it.nkv && lane < tile_pages(tile_key(j + 1)))
@@ -1103,9 +1151,81 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap), 1)
       }
     }
     }
+  } else if (kI4 && warp >= 2 + kSoft + 4) {
+    // ----------------- 4-bit pages to bf16 tiles, a share of the rows a warp -----------------
+    // Four lanes a row, 32 dimensions each: a 16-byte read of codes, four 16-byte pieces
+    // written where TMA would put them (128-byte swizzle).  The lanes of the upper
+    // half row write their pieces in an order of their own, so that eight lanes
+    // meet eight different bank groups.  About 17 operations a word of eight codes: 550
+    // issue slots a warp and tile, beside the 4700 cycles that the tile's products and
+    // softmax take.
+    const int dw = warp - (2 + kSoft + 4), gid = lane >> 2, tig = lane & 3;
+    const uint32_t full = sbase + kOffBarRaw, taken = full + 8;
+    uint32_t tile_cnt = 0;
+    bool ok = true;
+    for (uint32_t it_cnt = 0; ok; ++it_cnt) {
+      const int slot = it_cnt & 1;
+      if (!mbar_wait_warp(bar(B_IF + slot), (it_cnt >> 1) & 1, abort, ws.err)) break;
+      const Item it = items[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_IE + slot));
+      if (it.r < 0) break;
+      for (int j = 0; j < it.nkv; ++j) {
+        const uint32_t c = tile_cnt++;
+        const int s = c % kStages;
+        const int keys = it.L - j * kTileK;  // rows past these are zeroed
+        if (!mbar_wait_warp(full, c & 1, abort, ws.err)) {
+          ok = false;
+          break;
+        }
+#pragma unroll 1
+        for (int side = 0; side < 2; ++side) {
+          if (c >= (uint32_t)kStages &&
+              !mbar_wait_warp(bar((side ? B_VE : B_KE) + s), ((c / kStages) - 1) & 1, abort,
+                              ws.err)) {
+            ok = false;
+            break;
+          }
+          const uint32_t dst = sbase + (side ? kOffV : kOffK) + s * kTileBytes;
+#pragma unroll
+          for (int k = 0; k < 16 / kDequantWarps; ++k) {
+            const int row = 128 / kDequantWarps * dw + 8 * k + gid;
+            const uint32_t page = sbase + kOffRaw + (row >> 4) * kPage4;
+            uint32_t w[4], pair;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(page + side * kSide4 + (row & 15) * kRow4 + 16 * tig));
+            asm volatile("ld.shared.b32 %0, [%1];\n"
+                         : "=r"(pair)
+                         : "r"(page + kMeta4 + 64 * side + 4 * (row & 15)));
+            const uint32_t ss = __byte_perm(pair, 0, 0x1010), zz = __byte_perm(pair, 0, 0x3232);
+            const __nv_bfloat162 s2 = *reinterpret_cast<const __nv_bfloat162*>(&ss);
+            const __nv_bfloat162 z2 = *reinterpret_cast<const __nv_bfloat162*>(&zz);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int m = i ^ (tig & 2);
+              const uint32_t x = m == 0 ? w[0] : m == 1 ? w[1] : m == 2 ? w[2] : w[3];
+              uint32_t v[4];
+#pragma unroll
+              for (int n = 0; n < 4; ++n)
+                v[n] = row < keys ? dequant2(x >> (4 * n), s2, z2) : 0u;
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(
+                               dst + (tig >> 1) * kHalfBytes + sw128(row, 4 * (tig & 1) + m)),
+                           "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                           : "memory");
+            }
+          }
+          fence_async_smem();  // (read by the MMAs)
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar((side ? B_VF : B_KF) + s));
+        }
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(taken);
+      }
+    }
   } else {
     // ------------------ epilogue: one warp per TMEM lane quarter ------------------
-    // Warp w (the last four) owns rows 32 * (w % 4) .. + 31 of both output tiles.  When
+    // Warp w (four after the softmax) owns rows 32 * (w % 4) .. + 31 of both output tiles.  When
     // O_x is final (its last P.V done) and both partial row sums are in, the
     // warp reads the 128-column row block out of TMEM in two halves,
     // normalises them and packs them to bf16 in registers, and releases O_x as
@@ -1208,24 +1328,30 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap), 1)
   combine_splits(a, ws, blockIdx.x * (kThreads / 32) + warp, gridDim.x * (kThreads / 32));
 }
 
-template <bool kScored, Cap kCap, bool kBias, bool kSym>
+// (K and V of 4-bit pages come by bulk copies: their maps are the query's, not used)
+template <bool kScored, Cap kCap, bool kBias, bool kSym, bool kI4 = false>
 cudaError_t launch_prefill_as(const ScoredArgs& a, const Workspace& ws, int sms, cudaStream_t st) {
   static std::atomic<bool> attr[kMaxAttrDevices];
-  auto* kernel = prefill_kernel<kScored, kCap, kBias, kSym>;
-  if (cudaError_t e = smem_attr_once(kernel, kSmemBytes, attr)) return e;
+  auto* kernel = prefill_kernel<kScored, kCap, kBias, kSym, kI4>;
+  constexpr int kSmem = kI4 ? kSmemBytesI4 : kSmemBytes;
+  constexpr int kThreads = threads_of(kCap == kFixedCap) + (kI4 ? 32 * kDequantWarps : 0);
+  if (cudaError_t e = smem_attr_once(kernel, kSmem, attr)) return e;
   CUtensorMap tq, tk, tv;
-  if (!make_rows_map(&tq, a.q, a.q_rows, a.hq, a.q_stride, 1, kPreTileQ) ||
-      !make_cache_map(&tk, a.kc, a.num_blocks, a.hkv) ||
-      !make_cache_map(&tv, a.vc, a.num_blocks, a.hkv))
+  if (!make_rows_map(&tq, a.q, a.q_rows, a.hq, a.q_stride, 1, kPreTileQ)) return cudaErrorInvalidValue;
+  if (kI4) {
+    tk = tv = tq;
+  } else if (!make_cache_map(&tk, a.kc, a.num_blocks, a.hkv) ||
+             !make_cache_map(&tv, a.vc, a.num_blocks, a.hkv)) {
     return cudaErrorInvalidValue;
-  return launch_dependent(kernel, dim3(sms), dim3(threads_of(kCap == kFixedCap)), kSmemBytes, st,
-                          tq, tk, tv, a, ws);
+  }
+  return launch_dependent(kernel, dim3(sms), dim3(kThreads), kSmem, st, tq, tk, tv, a, ws);
 }
 
 }  // namespace
 
 cudaError_t launch_prefill(const ScoredArgs& a, const Workspace& ws, int sms, cudaStream_t st) {
   const ScoreArgs& sc = a.score;
+  if (a.kv == kInt4) return launch_prefill_as<false, kNoCap, false, false, true>(a, ws, sms, st);
   if (!sc.on) return launch_prefill_as<false, kNoCap, false, false>(a, ws, sms, st);
   const bool bias = sc.slopes != nullptr, sym = bias && sc.prefix != nullptr;
   if (sc.softcap > 0.f) {
