@@ -494,9 +494,10 @@ int pkv_read_int4(const void* cache, int64_t num_blocks, int32_t block_size, int
  * for groups above 16) multiply the codes themselves, exact in fp16, with the
  * query rows scaled by a power of two to fp16's range, and apply each key's s and z
  * to the products in fp32; the weights, times the value rows' s, are rounded to
- * fp16.  Longer requests round each cached value to bf16 first.  A key that no
- * row of its request sees may hold any bits; the values of one that some row sees
- * must be finite (a row that does not see it weighs it with an exact zero).
+ * fp16.  Longer requests round each cached value to fp16 first, scaled by a power
+ * of two of its 128-key tile (cached values up to 2^105 in size; one far below its
+ * tile's largest is off by 2^-18 of that), and the weights to fp16.  A key that no
+ * row of its request sees may hold any bits.
  */
 int pkv_attention_int4(const void* q, int64_t q_row_stride, int64_t q_rows, int32_t num_heads,
                        const void* cache, int64_t num_blocks, int32_t block_size,

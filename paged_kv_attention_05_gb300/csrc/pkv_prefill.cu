@@ -47,6 +47,8 @@
 // the window's first page; the other roles are the same.
 // Every mbarrier wait is bounded; on expiry the kernel records
 // PKV_DEV_ERR_TIMEOUT, stops issuing work, frees its TMEM and returns.
+#include <cuda_fp16.h>
+
 #include <type_traits>
 
 #include "pkv_combine.cuh"
@@ -75,6 +77,7 @@ constexpr int kPageBoxBytes = 16 * 128;           // one 16-slot x 64-dim box
 constexpr int kTmemCols = 512;
 constexpr float kRescaleThreshold = 8.0f;         // log2 units
 constexpr float kMaxSum = 0x1p40f;                // scored calls: sum of a row over a pair of blocks
+constexpr float kMaxSum16 = 0x1p14f;              // 4-bit calls: sum of a row over 64 columns
 
 // shared-memory layout (offsets from a 1024-byte aligned base)
 constexpr int kOffQ = 0;                          // Q_a | Q_b
@@ -107,12 +110,46 @@ constexpr int kOffXch = kOffItems + 2 * 48;        // [4 quarters][2 slots][2 ha
 constexpr int kOffCtl = kOffXch + 4 * 2 * 2 * 32 * 4;  // TMEM address, abort flag
 constexpr int kOffBarLF1 = kOffCtl + 16;           // [2] the same for odd items
 constexpr int kSmemBytes = kOffBarLF1 + 16 + 1024;  // + alignment slack
-// The instance for the cache of 4-bit codes: four more warps, and a tile's pages as
-// they are cached.
-constexpr int kDequantWarps = 2;
-constexpr int kOffBarRaw = kOffBarLF1 + 16;        // raw pages loaded, taken
-constexpr int kOffRaw = (kOffBarRaw + 16 + 127) / 128 * 128;
-constexpr int kSmemBytesI4 = kOffRaw + 8 * kPage4 + 1024;
+// The instance for the cache of 4-bit codes: 20 warps (producer, MMA, two for the query
+// rows; 8 of softmax; 4 of epilogue; two for K tiles, two for V tiles), the scales and
+// zeros of the tiles, and the powers of two that its fp16 tiles are scaled by.  The
+// softmax takes registers from the other warps: with the 96 that 640 threads have each
+// it spills (999 against 870 us for 4 chunks of 2047 tokens, the tiles left zero).
+constexpr int kThreadsI4 = 640;
+constexpr int kRegsLaunch = 96, kRegsSoft = 120, kRegsEpi = 96, kRegsFew = 72;
+static_assert(256 * kRegsSoft + 128 * kRegsEpi + 256 * kRegsFew <= kThreadsI4 * kRegsLaunch,
+              "the shares must fit what the block is launched with");
+constexpr int kDequantWarps = 2;  // of K; of V; of Q
+constexpr int kOffBarI4 = kOffBarLF1 + 16;
+enum {
+  I_KR = 0,   // [2] key codes of a tile loaded
+  I_KT = 2,   // [2] and turned into its K tile
+  I_QD = 4,   // [2] Q tile converted
+  I_MR = 6,   // [4] scales and zeros of a tile loaded
+  I_XR = 10,  // [4] and its exponents found
+  kNumBarsI4 = 14
+};
+constexpr int kOffTileExp = kOffBarI4 + 8 * kNumBarsI4;  // [4 tiles] exponents of K and V (int2)
+constexpr int kMetaBytes = kPage4 - kMeta4;
+constexpr int kOffMeta = (kOffTileExp + 4 * 8 + 127) / 128 * 128;  // scales: see meta_offset
+constexpr int kOffKRaw = kOffMeta + 2 * 8 * kMetaBytes;            // [2] key codes of a tile
+constexpr int kSmemBytesI4 = kOffKRaw + 2 * 8 * kSide4 + 1024;
+// The scales and zeros of tile c: of four tiles at a time, two where the plain softmax
+// exchanges values.  The query rows' factors lie beside their row sums, in the places of
+// the second warp of a row, which this softmax does not have.
+static_assert(kOffXch % 16 == 0 && kOffCtl - kOffXch >= 2 * 8 * kMetaBytes, "room for two tiles");
+__host__ __device__ constexpr int meta_offset(uint32_t c) {
+  return (c & 2 ? kOffMeta : kOffXch) + (int)(c & 1) * 8 * kMetaBytes;
+}
+__host__ __device__ constexpr int qfac_offset(uint32_t it_cnt, int x) {
+  return kOffLsum + (((int)(it_cnt & 1) * 2 + x) * 2 + 1) * 128 * 4;
+}
+// Where page p's value codes of a tile land in its stage: in the first half of the rows of
+// the warp that turns them into the tile (half 0 of a row, 128 bytes each).
+constexpr int kPagesPerWarp = 8 / kDequantWarps;
+__host__ __device__ constexpr int raw_offset(int p) {
+  return p / kPagesPerWarp * (128 / kDequantWarps * 128) + p % kPagesPerWarp * kSide4;
+}
 static_assert(kSmemBytesI4 <= 232448, "shared memory per CTA");
 
 struct Item {
@@ -166,11 +203,11 @@ __device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo) {
   return d;
 }
 
-// Instruction descriptor, kind::f16: bf16 A and B, fp32 D, M = N = 128.
-__host__ __device__ constexpr uint32_t idesc_bf16(bool b_mn_major) {
+// Instruction descriptor, kind::f16: bf16 (or fp16) A and B, fp32 D, M = N = 128.
+__host__ __device__ constexpr uint32_t idesc_16(bool b_mn_major, bool bf16) {
   return (1u << 4)                         // D format f32
-         | (1u << 7)                       // A format bf16
-         | (1u << 10)                      // B format bf16
+         | ((bf16 ? 1u : 0u) << 7)         // A format
+         | ((bf16 ? 1u : 0u) << 10)        // B format
          | ((b_mn_major ? 1u : 0u) << 16)  // B major-ness
          | ((128u >> 3) << 17)             // N
          | ((128u >> 4) << 24);            // M
@@ -385,6 +422,20 @@ __device__ __forceinline__ void rescale16(uint32_t t, float alpha) {
   for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(v[i] * alpha);
   PKV_ST16U(t, u);
 }
+__device__ __forceinline__ void rescale16_f16(uint32_t t, float alpha) {
+  float v[16];
+  uint32_t u[16];
+  PKV_LD16(t, v);
+  tmem_wait_ld();
+  const __half2 a2 = __float2half2_rn(alpha);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t w = __float_as_uint(v[i]);
+    const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&w), a2);
+    u[i] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+  PKV_ST16U(t, u);
+}
 __device__ __forceinline__ void rescale16_bf16(uint32_t t, float alpha) {
   float v[16];
   uint32_t u[16];
@@ -398,22 +449,93 @@ __device__ __forceinline__ void rescale16_bf16(uint32_t t, float alpha) {
   PKV_ST16U(t, u);
 }
 
-// Two codes (bits 0 .. 3 of each half of w) to the bf16 pair s * code + z, rounded
-// once: 128 + code has its code in the last bits of a bf16, less 128 is exact.
-__device__ __forceinline__ uint32_t dequant2(uint32_t w, __nv_bfloat162 s, __nv_bfloat162 z) {
-  const uint32_t u = (w & 0x000F000Fu) | 0x43004300u;
-  const __nv_bfloat162 c = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u),
-                                   __float2bfloat162_rn(128.f));
-  const __nv_bfloat162 v = __hfma2(c, s, z);
+// The instance for 4-bit caches runs on fp16 tiles: a cached value has up to 12
+// significant bits (s with 8 times a code with 4, plus z), of which bf16 keeps 8 and
+// fp16 11, and the same goes for the weights (outputs off by 3.0e-3 of their size with
+// bf16 tiles, 1.7e-3 with these, of which the bf16 output is 1.6e-3).  What fp16 lacks
+// in range, powers of two make up: each query row, each K tile and an item's V tiles so
+// far have one, by which their largest value lies in [2^13, 2^14) (query rows) or
+// [2^-7, 2^-6) (tiles, see dequant8): values down to 2^-7 of the largest keep all
+// their bits, and what is below is off by 2^-18 of it at most.
+__device__ __forceinline__ int q_exponent(uint32_t x) {
+  return max((int)(x >> 23) - 127 - 13, -100);
+}
+__device__ __forceinline__ int tile_exponent(uint32_t x) {  // (of values up to 2^105)
+  return min(max((int)(x >> 23) - 127 + 7, -100), 112);
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+// The share of the block's registers that this warpgroup goes on with.
+template <int kRegs, bool kMore>
+__device__ __forceinline__ void take_regs() {
+  if (kMore)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegs));
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegs));
+}
+// A word's eight codes to the fp16 values s * code + z, each rounded once.  A code in the
+// last bits of a half is the subnormal code * 2^-24, four bits up code * 2^-20: nothing
+// but a mask makes it the operand of the multiply-add (s: the row's scale times 2^24,
+// below 2^16 as the tile's values are below 2^-6; t: times 2^20).
+__device__ __forceinline__ uint4 dequant8(uint32_t w, uint32_t s, uint32_t t, uint32_t z) {
+  uint32_t v[4];
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    const uint32_t c = (n < 2 ? w : w >> 8) & (n & 1 ? 0x00F000F0u : 0x000F000Fu);
+    const __half2 y = __hfma2(*reinterpret_cast<const __half2*>(&c),
+                              *reinterpret_cast<const __half2*>(n & 1 ? &t : &s),
+                              *reinterpret_cast<const __half2*>(&z));
+    v[n] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// Rows 8 set .. + 7 of a Q tile to fp16 in place, their powers of two to fac.  Four lanes a
+// row; a lane takes every fourth of its 16-byte pieces (in odd rows the two halves of a
+// 128-byte line swapped: eight lanes meet eight bank groups).  `scale` gives the sign:
+// the softmax takes its size.
+__device__ __forceinline__ void convert_q(uint8_t* q, float* fac, int set, float scale) {
+  const int lane = threadIdx.x & 31, row = 8 * set + (lane >> 2), tig = lane & 3;
+  auto piece = [&](int i) {
+    return reinterpret_cast<uint4*>(q + (i >> 1) * kHalfBytes + sw128(row, tig + 4 * ((i + row) & 1)));
+  };
+  __nv_bfloat162 m = __float2bfloat162_rn(0.f);
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    const uint4 v = *piece(i);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[k])));
+  }
+  float big = fmaxf(__low2float(m), __high2float(m));
+  big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+  big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+  const int e = q_exponent(__float_as_uint(big));
+  const float down = copysignf(pow2(-e), scale);
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    const uint4 v = *piece(i);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      o[k] = pack_f16(__uint_as_float(w[k] << 16) * down,
+                      __uint_as_float(w[k] & 0xFFFF0000u) * down);
+    *piece(i) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+  if (tig == 0) fac[row] = pow2(e);
 }
 
 // kScored: a window, a prefix (runtime), and per instance a cap, a bias (kSym:
 // that may meet keys after a row's position, with a prefix).  kI4: the cache of 4-bit
 // codes (pkv_attention_int4): the producer brings a tile's pages as they are cached,
-// and four more warps turn them into the bf16 K and V tiles that the others expect.
+// and two more warps turn them, and the query rows, into fp16 tiles.
 template <bool kScored, Cap kCap, bool kBias, bool kSym, bool kI4 = false>
-__global__ void __launch_bounds__(threads_of(kCap == kFixedCap) + (kI4 ? 32 * kDequantWarps : 0), 1)
+__global__ void __launch_bounds__(kI4 ? kThreadsI4 : threads_of(kCap == kFixedCap), 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, ArgsOf<kScored> a,
                    Workspace ws) {
@@ -424,9 +546,10 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap) + (kI4 ? 32 * kD
   // the kernels before it wrote is read through L2 (ld.global.cg).  The split
   // decode results are merged at the end, once the decode grid has finished
   // (so this grid finishing implies that every kernel before it has).
-  constexpr int kSoft = soft_warps(kCap == kFixedCap), kDeq = kI4 ? kDequantWarps : 0;
-  constexpr int kThreads = threads_of(kCap == kFixedCap) + 32 * kDeq;
-  constexpr int kHalves = kScored ? kSoft / 8 : 2;  // softmax warps that share a row
+  constexpr int kSoft = soft_warps(kCap == kFixedCap), kDeq = kI4 ? 3 * kDequantWarps : 0;
+  constexpr int kThreads = kI4 ? kThreadsI4 : threads_of(kCap == kFixedCap);
+  constexpr int kSoft0 = kI4 ? 4 : 2;  // the first softmax warp
+  constexpr int kHalves = kScored ? kSoft / 8 : kI4 ? 1 : 2;  // softmax warps that share a row
   // (a scored call lets the next kernel, usually another call's plan or cache
   // write, set up meanwhile: everything before this kernel has finished or, as
   // the decode grid, writes only what those wait for)
@@ -452,8 +575,12 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap) + (kI4 ? 32 * kD
   auto lf_bar = [&](uint32_t it_cnt, int x) {
     return (it_cnt & 1) ? sbase + kOffBarLF1 + 8u * (uint32_t)x : bar(B_LF + x);
   };
+  auto i4_bar = [&](int i) { return sbase + kOffBarI4 + 8u * (uint32_t)i; };
   volatile int* ctl = reinterpret_cast<volatile int*>(smem + kOffCtl);
   volatile int* abort = ctl + 1;  // ctl[0] = TMEM base address
+  auto wait = [&](uint32_t b, uint32_t parity) {
+    return mbar_wait_warp(b, parity, abort, ws.err);
+  };
   Item* items = reinterpret_cast<Item*>(smem + kOffItems);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -471,9 +598,15 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap) + (kI4 ? 32 * kD
       mbar_init(sbase + kOffBarLF1 + 8 * x, 4 * kHalves);
       mbar_init(bar(B_IE + x), 1 + kSoft + 4 + kDeq);  // MMA warp, softmax, epilogue (and these)
       if (kI4) {  // one arrival per dequantising warp
-        mbar_init(bar(B_KF + x), kDeq);
-        mbar_init(bar(B_VF + x), kDeq);
-        mbar_init(sbase + kOffBarRaw + 8 * x, x == 0 ? 1 : kDeq);
+        mbar_init(bar(B_KF + x), kDequantWarps);
+        mbar_init(bar(B_VF + x), kDequantWarps);
+        mbar_init(i4_bar(I_KR + x), 1);
+        mbar_init(i4_bar(I_KT + x), kDequantWarps);
+        mbar_init(i4_bar(I_QD + x), kDeq);
+        for (int i = x; i < 4; i += 2) {
+          mbar_init(i4_bar(I_MR + i), 1);
+          mbar_init(i4_bar(I_XR + i), 1);
+        }
       }
     }
     for (int i = 0; i < 4; ++i) mbar_init(bar(B_XP + i), 2);
@@ -491,8 +624,25 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap) + (kI4 ? 32 * kD
   tc_fence_after();
   const uint32_t tmem = (uint32_t)ctl[0];
   const int n_items = n_pre * per_entry;
+  // The Q tiles of item it_cnt to fp16, by the six warps that form tiles (w: 0 .. 5): the
+  // query rows come when the item before has issued its last S, and the next S waits for
+  // them; each warp has formed its share of the first K or V tile by then (the V tile after
+  // the rows: 804 us for 4 chunks of 2047 tokens of 64 heads, so 762).
+  auto query_rows = [&](const Item& it, uint32_t it_cnt, uint32_t (&q_cnt)[2], int w) {
+    for (int x = 0; x < (it.hb >= 0 ? 2 : 1); ++x) {
+      if (!wait(bar(B_QF + x), q_cnt[x]++ & 1)) return false;
+      for (int set = w; set < 16; set += 6)
+        convert_q(smem + kOffQ + x * kTileBytes,
+                  reinterpret_cast<float*>(smem + qfac_offset(it_cnt, x)), set, a.scale);
+      fence_async_smem();  // (read by the MMAs)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(i4_bar(I_QD + x));
+    }
+    return true;
+  };
 
   if (warp == 0) {
+    if (kI4) take_regs<kRegsFew, false>();
     // ------------------------------ producer ------------------------------
     // Global loads are issued one step before their values are needed: the
     // next item's cursor and entry (which carries its request's lengths)
@@ -516,7 +666,7 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap) + (kI4 ? 32 * kD
       const PreEntry e = e_nxt;
       const int q0 = e.q0, q1 = e.q0 + e.n, Lr = e.L;
       if (it_cnt >= 2 &&
-          !mbar_wait_warp(bar(B_IE + slot), ((it_cnt >> 1) - 1) & 1, abort, ws.err))
+          !wait(bar(B_IE + slot), ((it_cnt >> 1) - 1) & 1))
         break;
       if (w >= n_items || *abort) {
         if (lane == 0) {
@@ -553,34 +703,40 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap) + (kI4 ? 32 * kD
       const int row0 = it.q0 + it.qt * kPreTileQ;
       // Q tiles, once the previous item's last S has read them
       bool ok = true;
-      for (int x = 0; x < 2 && ok; ++x) {
-        const int h = x == 0 ? it.ha : it.hb;
-        if (h < 0) continue;
-        if (qx_cnt[x] > 0 &&
-            !mbar_wait_warp(bar(B_QE + x), (qx_cnt[x] - 1) & 1, abort, ws.err)) {
-          ok = false;
-          break;
+      auto load_q = [&]() {
+        for (int x = 0; x < 2 && ok; ++x) {
+          const int h = x == 0 ? it.ha : it.hb;
+          if (h < 0) continue;
+          if (qx_cnt[x] > 0 &&
+              !wait(bar(B_QE + x), (qx_cnt[x] - 1) & 1)) {
+            ok = false;
+            break;
+          }
+          qx_cnt[x]++;
+          if (lane == 0) {
+            const uint32_t qd = sbase + kOffQ + x * kTileBytes;
+            mbar_expect_tx(bar(B_QF + x), kTileBytes);
+            tma_load_3d(qd, &tm_q, bar(B_QF + x), 0, h, row0);
+            tma_load_3d(qd + kHalfBytes, &tm_q, bar(B_QF + x), 64, h, row0);
+          }
         }
-        qx_cnt[x]++;
-        if (lane == 0) {
-          const uint32_t qd = sbase + kOffQ + x * kTileBytes;
-          mbar_expect_tx(bar(B_QF + x), kTileBytes);
-          tma_load_3d(qd, &tm_q, bar(B_QF + x), 0, h, row0);
-          tma_load_3d(qd + kHalfBytes, &tm_q, bar(B_QF + x), 64, h, row0);
-        }
-      }
+      };
+      if (!kI4) load_q();
       // lane p < pages(j) holds the block id of page p of tile j
       auto tile_key = [&](int j) { return tile_key0<kScored, kBias>(it, j); };
       auto tile_pages = [&](int key) { return min(8, (it.L - key + 15) / 16); };
       // first key any row of the item sees (its tiles start at this key's page)
       const int vlow = kScored ? first_key(it.ctx + it.qt * kPreTileQ, score_of(a).window) : 0;
       int blk_nxt = lane < tile_pages(tile_key(0)) ? __ldcg(btrow + (tile_key(0) >> 4) + lane) : 0;
-      for (int j = 0; ok && j < it.nkv; ++j) {
-        const uint32_t c = tile_cnt++;
-        const int s = c % kStages;
-        const int key0 = tile_key(j);
-        const int pages = tile_pages(key0);
-        if (kI4) {
+      if constexpr (kI4) {
+        // A tile's key codes into one of two buffers of their own, with its scales and
+        // zeros, two tiles ahead of its value codes, which go into the V stage: the K
+        // tile, formed when its stage is free, waits for no load.
+        auto page_of = [&](int blk) {
+          return reinterpret_cast<const uint8_t*>(a.kc) + ((int64_t)blk * a.hkv + it.g) * kPage4;
+        };
+        auto load_keys = [&](int j, uint32_t c) {  // the blocks of tile j, checked
+          const int pages = tile_pages(tile_key(j));
           int blk = blk_nxt;
           if (j + 1 < it.nkv && lane < tile_pages(tile_key(j + 1)))
             blk_nxt = __ldcg(btrow + (tile_key(j + 1) >> 4) + lane);
@@ -588,26 +744,55 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap) + (kI4 ? 32 * kD
             atomicOr(ws.err, PKV_DEV_ERR_BLOCK_ID);
             blk = 0;
           }
-          const uint32_t full = sbase + kOffBarRaw, taken = full + 8;
-          if (c > 0 && !mbar_wait_warp(taken, (c - 1) & 1, abort, ws.err)) {
+          if (c >= 2 && !wait(i4_bar(I_KT + (c & 1)), ((c >> 1) - 1) & 1)) {
+            ok = false;
+            return blk;
+          }
+          const uint32_t mbar = i4_bar(I_MR + (c & 3)), kbar = i4_bar(I_KR + (c & 1));
+          if (lane == 0) {
+            mbar_expect_tx(mbar, pages * kMetaBytes);
+            mbar_expect_tx(kbar, pages * kSide4);
+          }
+          __syncwarp();
+          if (lane < pages) {
+            bulk_load(sbase + meta_offset(c) + lane * kMetaBytes, page_of(blk) + kMeta4, kMetaBytes,
+                      mbar);
+            bulk_load(sbase + kOffKRaw + ((c & 1) * 8 + lane) * kSide4, page_of(blk), kSide4, kbar);
+          }
+          return blk;
+        };
+        int blk = load_keys(0, tile_cnt), blk1 = 0;
+        if (ok && it.nkv > 1) blk1 = load_keys(1, tile_cnt + 1);
+        if (ok) load_q();
+        for (int j = 0; ok && j < it.nkv; ++j) {
+          const uint32_t c = tile_cnt++;
+          const int s = c % kStages, pages = tile_pages(tile_key(j));
+          if (c >= (uint32_t)kStages &&
+              !wait(bar(B_VE + s), ((c / kStages) - 1) & 1)) {
             ok = false;
             break;
           }
-          if (lane == 0) mbar_expect_tx(full, pages * kPage4);
+          if (lane == 0) mbar_expect_tx(bar(B_VT + s), pages * kSide4);
           __syncwarp();
           if (lane < pages)
-            bulk_load(sbase + kOffRaw + lane * kPage4,
-                      reinterpret_cast<const uint8_t*>(a.kc) +
-                          ((int64_t)blk * a.hkv + it.g) * kPage4,
-                      kPage4, full);
-          continue;
+            bulk_load(sbase + kOffV + s * kTileBytes + raw_offset(lane), page_of(blk) + kSide4,
+                      kSide4, bar(B_VT + s));
+          // (V of tile c - 2 is done with: the scales of four tiles are enough)
+          blk = blk1;
+          if (j + 2 < it.nkv) blk1 = load_keys(j + 2, c + 2);
         }
+      }
+      for (int j = 0; !kI4 && ok && j < it.nkv; ++j) {
+        const uint32_t c = tile_cnt++;
+        const int s = c % kStages;
+        const int key0 = tile_key(j);
+        const int pages = tile_pages(key0);
         const bool tail = key0 + kTileK > it.L || (kScored && key0 < vlow);
         int blk = blk_nxt;
         if (j + 1 < it.nkv && lane < tile_pages(tile_key(j + 1)))
           blk_nxt = __ldcg(btrow + (tile_key(j + 1) >> 4) + lane);
         if (c >= (uint32_t)kStages &&
-            !mbar_wait_warp(bar(B_KE + s), ((c / kStages) - 1) & 1, abort, ws.err)) {
+            !wait(bar(B_KE + s), ((c / kStages) - 1) & 1)) {
           ok = false;
           break;
         }
@@ -624,7 +809,7 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap) + (kI4 ? 32 * kD
                       0, blk);
         }
         if (c >= (uint32_t)kStages &&
-            !mbar_wait_warp(bar(B_VE + s), ((c / kStages) - 1) & 1, abort, ws.err)) {
+            !wait(bar(B_VE + s), ((c / kStages) - 1) & 1)) {
           ok = false;
           break;
         }
@@ -639,7 +824,7 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap) + (kI4 ? 32 * kD
         if (tail) {
           // wait for the V boxes, zero the rows of keys >= seq_len (and, at a
           // window's start, of the keys no row sees), publish
-          ok = mbar_wait_warp(bar(B_VT + s), vt_uses[s] & 1, abort, ws.err);
+          ok = wait(bar(B_VT + s), vt_uses[s] & 1);
           vt_uses[s]++;
           if (!ok) break;
           uint8_t* v = smem + kOffV + s * kTileBytes;
@@ -660,10 +845,11 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap) + (kI4 ? 32 * kD
       if (!ok) break;
     }
   } else if (warp == 1) {
+    if (kI4) take_regs<kRegsFew, false>();
     // ------------------------------ MMA issuer ------------------------------
     // (the whole warp runs this, in step; see mma_ss)
     {
-      const uint32_t id_s = idesc_bf16(false), id_o = idesc_bf16(true);
+      const uint32_t id_s = idesc_16(false, !kI4), id_o = idesc_16(true, !kI4);
       uint32_t tile_cnt = 0, s_cnt[2] = {0, 0}, o_cnt[2] = {0, 0}, q_cnt[2] = {0, 0};
       // Operand descriptors of every buffer, built once: a descriptor's low
       // field is the address / 16, so a k-step's offset is added to it.
@@ -699,16 +885,16 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap) + (kI4 ? 32 * kD
       bool ok = true;
       for (uint32_t it_cnt = 0; ok; ++it_cnt) {
         const int slot = it_cnt & 1;
-        if (!mbar_wait_warp(bar(B_IF + slot), (it_cnt >> 1) & 1, abort, ws.err)) break;
+        if (!wait(bar(B_IF + slot), (it_cnt >> 1) & 1)) break;
         const Item it = items[slot];
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_IE + slot));
         if (it.r < 0) break;
         const int nx = it.hb >= 0 ? 2 : 1;
         for (int x = 0; x < nx && ok; ++x)
-          ok = mbar_wait_warp(bar(B_QF + x), q_cnt[x]++ & 1, abort, ws.err);
+          ok = wait(kI4 ? i4_bar(I_QD + x) : bar(B_QF + x), q_cnt[x]++ & 1);
         const uint32_t c0 = tile_cnt;
-        if (!ok || !mbar_wait_warp(bar(B_KF + c0 % kStages), (c0 / kStages) & 1, abort, ws.err)) break;
+        if (!ok || !wait(bar(B_KF + c0 % kStages), (c0 / kStages) & 1)) break;
         tc_fence_after();
         for (int x = 0; x < nx; ++x) issue_s(x, c0);
         mma_commit(bar(B_KE + c0 % kStages));
@@ -717,14 +903,14 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap) + (kI4 ? 32 * kD
         for (int j = 0; j < it.nkv && ok; ++j) {
           const uint32_t c = c0 + j;
           const bool more = j + 1 < it.nkv;
-          if (!mbar_wait_warp(bar(B_VF + c % kStages), (c / kStages) & 1, abort, ws.err)) {
+          if (!wait(bar(B_VF + c % kStages), (c / kStages) & 1)) {
             ok = false;
             break;
           }
           for (int x = 0; x < nx; ++x) {
-            if (!mbar_wait_warp(bar(B_PF + x), (s_cnt[x] - 1) & 1, abort, ws.err) ||
+            if (!wait(bar(B_PF + x), (s_cnt[x] - 1) & 1) ||
                 (j == 0 && o_cnt[x] > 0 &&
-                 !mbar_wait_warp(bar(B_OE + x), (o_cnt[x] - 1) & 1, abort, ws.err))) {
+                 !wait(bar(B_OE + x), (o_cnt[x] - 1) & 1))) {
               ok = false;
               break;
             }
@@ -733,8 +919,7 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap) + (kI4 ? 32 * kD
             if (x == nx - 1) mma_commit(bar(B_VE + c % kStages));  // every PV of V_c issued
             if (more) {
               // the next K tile is waited for only now, with PV_x already queued
-              if (x == 0 && !mbar_wait_warp(bar(B_KF + (c + 1) % kStages), ((c + 1) / kStages) & 1,
-                                           abort, ws.err)) {
+              if (x == 0 && !wait(bar(B_KF + (c + 1) % kStages), ((c + 1) / kStages) & 1)) {
                 ok = false;
                 break;
               }
@@ -807,7 +992,7 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap) + (kI4 ? 32 * kD
     bool ok = true;
     for (uint32_t it_cnt = 0; ok; ++it_cnt) {
       const int slot = it_cnt & 1;
-      if (!mbar_wait_warp(bar(B_IF + slot), (it_cnt >> 1) & 1, abort, ws.err)) break;
+      if (!wait(bar(B_IF + slot), (it_cnt >> 1) & 1)) break;
       const Item it = items[slot];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_IE + slot));
@@ -834,7 +1019,7 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap) + (kI4 ? 32 * kD
       for (int j = 0; j < it.nkv; ++j) {
         const int key0 = tile_key0<kScored, kBias>(it, j) + 32 * b0;  // key of my first column
         const int lim = last - key0, low = first - key0;  // low <= column <= lim is visible
-        if (!mbar_wait_warp(bar(B_SF + x), s_cnt++ & 1, abort, ws.err)) {
+        if (!wait(bar(B_SF + x), s_cnt++ & 1)) {
           ok = false;
           break;
         }
@@ -996,8 +1181,178 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap) + (kI4 ? 32 * kD
       if (lane == 0) mbar_arrive(lf_bar(it_cnt, x));
     }
     }
-  } else if (warp < 10) {
-    if constexpr (!kScored) {
+  } else if (kI4 && warp < kSoft0) {
+    if constexpr (kI4) {
+      take_regs<kRegsFew, false>();
+      // ------------- the tiles' exponents; query rows with the warps below -------------
+      uint32_t q_cnt[2] = {0, 0}, tile_cnt = 0;
+      bool ok = true;
+      for (uint32_t it_cnt = 0; ok; ++it_cnt) {
+        const int slot = it_cnt & 1;
+        if (!wait(bar(B_IF + slot), (it_cnt >> 1) & 1)) break;
+        const Item it = items[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_IE + slot));
+        if (it.r < 0) break;
+        // tile j's exponents (the first of the two warps): the largest of |z| and
+        // |z + 15 s| of its keys, and of its values and those before them
+        int vexp = -100;
+        auto exponents = [&](int j) {
+          const uint32_t c = tile_cnt + j;
+          if (warp != 2) return;
+          if (!wait(i4_bar(I_MR + (c & 3)), (c >> 2) & 1)) {
+            ok = false;
+            return;
+          }
+          uint32_t big[2] = {0, 0};
+#pragma unroll
+          for (int row = lane; row < 128; row += 32) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t pair = *reinterpret_cast<const uint32_t*>(
+                  smem + meta_offset(c) + (row >> 4) * kMetaBytes + 64 * i + 4 * (row & 15));
+              const float sc = __uint_as_float(pair << 16);
+              const float z = __uint_as_float(pair & 0xFFFF0000u);
+              const float m = fmaxf(fabsf(z), fabsf(fmaf(15.f, sc, z)));
+              if (row < it.L - j * kTileK) big[i] = max(big[i], __float_as_uint(m));
+            }
+          }
+          const int kexp = tile_exponent(__reduce_max_sync(0xffffffffu, big[0]));
+          vexp = max(vexp, tile_exponent(__reduce_max_sync(0xffffffffu, big[1])));
+          if (lane == 0) {
+            *reinterpret_cast<int2*>(smem + kOffTileExp + 8 * (c & 3)) = make_int2(kexp, vexp);
+            mbar_arrive(i4_bar(I_XR + (c & 3)));
+          }
+        };
+#pragma unroll 1
+        for (int j = 0; ok && j < it.nkv; ++j) {
+          exponents(j);
+          if (ok && j == min(1, it.nkv - 1)) ok = query_rows(it, it_cnt, q_cnt, warp - 2);
+        }
+        tile_cnt += it.nkv;
+      }
+    }
+  } else if (warp < kSoft0 + 8) {
+    if constexpr (kI4) {
+      take_regs<kRegsSoft, true>();
+      // ------------- softmax of a 4-bit call: four warps for each query tile -------------
+      // A row per thread, its 128 scores in two rounds of 64: nothing passes between
+      // warps.  The scores are scaled by the powers of two of the row and of the K tile;
+      // the V tiles', when it grows, is a change to O.  The reference (whole log2 units)
+      // moves when the sum of a round passes 2^14, which keeps each weight in fp16's
+      // range.  One loop for everything, on purpose: with the exponentials in two places
+      // and both query tiles in one warp the kernel's roles did not fit the instruction
+      // caches together, and all of them, the MMA's too, took two to three times as long
+      // (4 chunks of 2047 tokens, 64 heads: 1368 us, 940 with the tiles' loop rolled).
+      const int x = (warp - kSoft0) >> 2;
+      const int qd = warp & 3;
+      const int row = qd * 32 + lane;  // == TMEM lane
+      const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
+      const uint32_t t_s0 = tmem + x * 128 + lane_off, t_o = tmem + 256 + x * 128 + lane_off;
+      float* lsum = reinterpret_cast<float*>(smem + kOffLsum);
+      const float sl2 = fabsf(a.scale) * kLog2e;
+      uint32_t s_cnt = 0, tile_cnt = 0;
+      bool ok = true;
+      for (uint32_t it_cnt = 0; ok; ++it_cnt) {
+        const int slot = it_cnt & 1;
+        if (!mbar_wait_warp(bar(B_IF + slot), (it_cnt >> 1) & 1, abort, ws.err)) break;
+        const Item it = items[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_IE + slot));
+        if (it.r < 0) break;
+        if (x == 1 && it.hb < 0) {  // an item of one tile
+          tile_cnt += it.nkv;
+          continue;
+        }
+        const int qrow = it.qt * kPreTileQ + row;           // row inside the request
+        const int qpos = qrow < it.n ? it.ctx + qrow : 0;   // last visible key
+        float ref = -INFINITY, l = 0.f;
+        int vexp = 0;
+        for (int j = 0; j < it.nkv; ++j, ++tile_cnt) {
+          if (!mbar_wait_warp(bar(B_SF + x), s_cnt++ & 1, abort, ws.err)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const int2 te = *reinterpret_cast<const int2*>(smem + kOffTileExp + 8 * (tile_cnt & 3));
+          const float f =
+              sl2 * pow2(te.x) * reinterpret_cast<const float*>(smem + qfac_offset(it_cnt, x))[row];
+          float o_alpha = j > 0 ? pow2(max(vexp - te.y, -126)) : 1.f;
+          vexp = te.y;
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            const int lim = qpos - j * kTileK - 64 * h;  // columns <= lim are visible
+            const uint32_t t_s = t_s0 + 64 * h;
+            float sv[64], sum;
+            bool move = ref == -INFINITY;  // look for the maximum
+#pragma unroll 1
+            for (;;) {
+              PKV_LD32(t_s + 0, (sv + 0));
+              PKV_LD32(t_s + 32, (sv + 32));
+              tmem_wait_ld();
+              if (!__all_sync(0xffffffffu, lim >= 63)) {
+#pragma unroll
+                for (int i = 0; i < 64; ++i) sv[i] = (i <= lim) ? sv[i] : -INFINITY;
+              }
+              const bool any_move = __any_sync(0xffffffffu, move);
+              if (any_move) {
+                float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 64; i += 4) {
+                  m0 = max3f(m0, sv[i], sv[i + 1]);
+                  m1 = max3f(m1, sv[i + 2], sv[i + 3]);
+                }
+                const float m = ceilf(fmaxf(m0, m1) * f);
+                const float to = move ? fmaxf(ref, m) : ref;
+                const float alpha = ref == -INFINITY ? 0.f : fast_exp2(ref - to);
+                ref = to;
+                l *= alpha;
+                o_alpha *= alpha;
+                if (h == 1) {  // the weights of the first round
+                  tmem_wait_st();
+#pragma unroll 1
+                  for (int ch = 0; ch < 2; ++ch) rescale16_f16(t_s0 + 16 * ch, alpha);
+                }
+              }
+              // p = exp2(s * f - ref), packed over sv[0 .. 31] (sv[2i], sv[2i + 1] are read
+              // before sv[i] is written)
+              float rs[4] = {0.f, 0.f, 0.f, 0.f};
+              const float nm = -ref;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                float x0, x1;
+                fma2(x0, x1, sv[2 * i], sv[2 * i + 1], f, f, nm, nm);
+                const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+                add2(rs[2 * (i & 1)], rs[2 * (i & 1) + 1], p0, p1);
+                sv[i] = __uint_as_float(pack_f16(p0, p1));
+              }
+              sum = (rs[0] + rs[1]) + (rs[2] + rs[3]);
+              if (any_move) break;
+              move = !(sum <= kMaxSum16);
+              if (!__any_sync(0xffffffffu, move)) break;
+            }
+            PKV_ST32(t_s, (sv + 0));  // 32 packed columns where my scores began
+            l += sum;
+          }
+          if (j > 0 && __any_sync(0xffffffffu, o_alpha != 1.f)) {
+            // (PV of the tile before is complete: S of this one is)
+#pragma unroll 1
+            for (int ch = 0; ch < 8; ++ch) rescale16(t_o + ch * 16, o_alpha);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_PF + x));
+        }
+        if (!ok) break;
+        // the row sum of the item, for the epilogue; the output is to be multiplied by
+        // 2^vexp
+        lsum[((it_cnt & 1) * 2 + x) * 2 * 128 + row] = l * pow2(-vexp);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(lf_bar(it_cnt, x));
+      }
+    }
+    if constexpr (!kScored && !kI4) {
     // ------------------- softmax: two warps per row, a column half each -------------------
     // Warp w reads TMEM lanes 32 * (w % 4) .. + 31 (its 32 rows, one per
     // thread) and key columns 64 * hf .. 64 * hf + 63, hf = (w - 2) / 4, of
@@ -1007,7 +1362,7 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap) + (kI4 ? 32 * kD
     // quarter exchange per-row values (the need for a max pass, the partial
     // maxima, the partial sums) through shared memory and a two-arrival
     // mbarrier, whose waits are bounded like every other.
-    const int hf = (warp - 2) >> 2;
+    const int hf = (warp - kSoft0) >> 2;
     const int qd = warp & 3;
     const int row = qd * 32 + lane;  // == TMEM lane
     const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
@@ -1021,14 +1376,14 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap) + (kI4 ? 32 * kD
       xch[((qd * 2 + sl) * 2 + hf) * 32 + lane] = v;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_XP + qd));
-      if (!mbar_wait_warp(bar(B_XP + qd), x_cnt & 1, abort, ws.err)) ok = false;
+      if (!wait(bar(B_XP + qd), x_cnt & 1)) ok = false;
       x_cnt++;
       return xch[((qd * 2 + sl) * 2 + (1 - hf)) * 32 + lane];
     };
     float* lsum = reinterpret_cast<float*>(smem + kOffLsum);
     for (uint32_t it_cnt = 0; ok; ++it_cnt) {
       const int slot = it_cnt & 1;
-      if (!mbar_wait_warp(bar(B_IF + slot), (it_cnt >> 1) & 1, abort, ws.err)) break;
+      if (!wait(bar(B_IF + slot), (it_cnt >> 1) & 1)) break;
       const Item it = items[slot];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_IE + slot));
@@ -1042,7 +1397,7 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap) + (kI4 ? 32 * kD
         const int lim = qpos - j * kTileK - 64 * hf;  // my columns <= lim are visible
         const bool masked = !__all_sync(0xffffffffu, lim >= 63);
         for (int x = 0; x < nx && ok; ++x) {
-          if (!mbar_wait_warp(bar(B_SF + x), s_cnt[x]++ & 1, abort, ws.err)) {
+          if (!wait(bar(B_SF + x), s_cnt[x]++ & 1)) {
             ok = false;
             break;
           }
@@ -1151,79 +1506,86 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap) + (kI4 ? 32 * kD
       }
     }
     }
-  } else if (kI4 && warp >= 2 + kSoft + 4) {
-    // ----------------- 4-bit pages to bf16 tiles, a share of the rows a warp -----------------
-    // Four lanes a row, 32 dimensions each: a 16-byte read of codes, four 16-byte pieces
-    // written where TMA would put them (128-byte swizzle).  The lanes of the upper
-    // half row write their pieces in an order of their own, so that eight lanes
-    // meet eight different bank groups.  About 17 operations a word of eight codes: 550
-    // issue slots a warp and tile, beside the 4700 cycles that the tile's products and
-    // softmax take.
-    const int dw = warp - (2 + kSoft + 4), gid = lane >> 2, tig = lane & 3;
-    const uint32_t full = sbase + kOffBarRaw, taken = full + 8;
-    uint32_t tile_cnt = 0;
-    bool ok = true;
-    for (uint32_t it_cnt = 0; ok; ++it_cnt) {
-      const int slot = it_cnt & 1;
-      if (!mbar_wait_warp(bar(B_IF + slot), (it_cnt >> 1) & 1, abort, ws.err)) break;
-      const Item it = items[slot];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_IE + slot));
-      if (it.r < 0) break;
-      for (int j = 0; j < it.nkv; ++j) {
-        const uint32_t c = tile_cnt++;
-        const int s = c % kStages;
-        const int keys = it.L - j * kTileK;  // rows past these are zeroed
-        if (!mbar_wait_warp(full, c & 1, abort, ws.err)) {
-          ok = false;
-          break;
-        }
-#pragma unroll 1
-        for (int side = 0; side < 2; ++side) {
-          if (c >= (uint32_t)kStages &&
-              !mbar_wait_warp(bar((side ? B_VE : B_KE) + s), ((c / kStages) - 1) & 1, abort,
-                              ws.err)) {
+  } else if (kI4 && warp >= kSoft0 + kSoft + 4) {
+    if constexpr (kI4) {
+      take_regs<kRegsFew, false>();
+      // -------- 4-bit codes to fp16 tiles: two warps the K tiles, two the V tiles --------
+      // Four lanes a row, 32 dimensions each: a 16-byte read, four 16-byte pieces written
+      // where TMA would put them (128-byte swizzle).  The lanes of the upper half row take
+      // another row of the eight, so that eight lanes meet eight different bank groups.  10
+      // instructions a word of eight codes, 1600 a tile of keys and values; a loop of eight
+      // rows a step (its eight steps in a row were 8 KB of code, see the softmax).
+      const int side = (warp - kSoft0 - kSoft - 4) >> 1, dw = warp & 1;  // 1: V
+      const int gid = lane >> 2, tig = lane & 3;
+      constexpr int kWarpRows = 128 / kDequantWarps;
+      const int lane_row = gid ^ (tig & 2);  // of eight
+      const uint32_t src0 = (side ? raw_offset(kPagesPerWarp * dw) : kPagesPerWarp * dw * kSide4) +
+                            lane_row * kRow4 + 16 * tig;
+      uint32_t dst0[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        dst0[i] = (tig >> 1) * kHalfBytes + kWarpRows * dw * 128 +
+                  sw128(lane_row, 4 * (tig & 1) + i);
+      uint32_t tile_cnt = 0, q_cnt[2] = {0, 0};
+      bool ok = true;
+      for (uint32_t it_cnt = 0; ok; ++it_cnt) {
+        const int slot = it_cnt & 1;
+        if (!wait(bar(B_IF + slot), (it_cnt >> 1) & 1)) break;
+        const Item it = items[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_IE + slot));
+        if (it.r < 0) break;
+        for (int j = 0; ok && j < it.nkv; ++j) {
+          const uint32_t c = tile_cnt++;
+          const int s = c % kStages;
+          const int keys = it.L - j * kTileK;  // rows past these are zeroed
+          const uint8_t* meta = smem + meta_offset(c);
+          // scales, exponents, codes (the values' are in their stage), and a K stage's room
+          if (!wait(i4_bar(I_MR + (c & 3)), (c >> 2) & 1) ||
+              !wait(i4_bar(I_XR + (c & 3)), (c >> 2) & 1) ||
+              !wait(side ? bar(B_VT + s) : i4_bar(I_KR + s), (c / kStages) & 1) ||
+              (!side && c >= (uint32_t)kStages &&
+               !wait(bar(B_KE + s), ((c / kStages) - 1) & 1))) {
             ok = false;
             break;
           }
-          const uint32_t dst = sbase + (side ? kOffV : kOffK) + s * kTileBytes;
-#pragma unroll
-          for (int k = 0; k < 16 / kDequantWarps; ++k) {
-            const int row = 128 / kDequantWarps * dw + 8 * k + gid;
-            const uint32_t page = sbase + kOffRaw + (row >> 4) * kPage4;
-            uint32_t w[4], pair;
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
-                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                         : "r"(page + side * kSide4 + (row & 15) * kRow4 + 16 * tig));
-            asm volatile("ld.shared.b32 %0, [%1];\n"
-                         : "=r"(pair)
-                         : "r"(page + kMeta4 + 64 * side + 4 * (row & 15)));
-            const uint32_t ss = __byte_perm(pair, 0, 0x1010), zz = __byte_perm(pair, 0, 0x3232);
-            const __nv_bfloat162 s2 = *reinterpret_cast<const __nv_bfloat162*>(&ss);
-            const __nv_bfloat162 z2 = *reinterpret_cast<const __nv_bfloat162*>(&zz);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int m = i ^ (tig & 2);
-              const uint32_t x = m == 0 ? w[0] : m == 1 ? w[1] : m == 2 ? w[2] : w[3];
-              uint32_t v[4];
-#pragma unroll
-              for (int n = 0; n < 4; ++n)
-                v[n] = row < keys ? dequant2(x >> (4 * n), s2, z2) : 0u;
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(
-                               dst + (tig >> 1) * kHalfBytes + sw128(row, 4 * (tig & 1) + m)),
-                           "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
-                           : "memory");
-            }
+          const int2 te = *reinterpret_cast<const int2*>(smem + kOffTileExp + 8 * (c & 3));
+          uint8_t* stage = smem + (side ? kOffV : kOffK) + s * kTileBytes;
+          const uint8_t* raw = side ? stage : smem + kOffKRaw + s * 8 * kSide4;
+          const uint32_t* pairs =
+              reinterpret_cast<const uint32_t*>(meta + kPagesPerWarp * dw * kMetaBytes) + 16 * side;
+          const float down = pow2(-(side ? te.y : te.x));
+          // eight rows a step, from the last: in the V stage a step overwrites codes of rows
+          // behind its own only
+          uint4 w = *reinterpret_cast<const uint4*>(raw + src0 + (kWarpRows / 8 - 1) * 8 * kRow4);
+#pragma unroll 1
+          for (int k = kWarpRows / 8 - 1; k >= 0; --k) {
+            uint32_t pair = pairs[(k >> 1) * (kMetaBytes / 4) + 8 * (k & 1) + lane_row];
+            if (kWarpRows * dw + 8 * k + lane_row >= keys) pair = 0;
+            const float sc = __uint_as_float(pair << 16) * down;
+            const float z = __uint_as_float(pair & 0xFFFF0000u) * down;
+            const float sh = sc * 0x1p24f, sl = sc * 0x1p20f;
+            const uint32_t s2 = pack_f16(sh, sh), t2 = pack_f16(sl, sl), z2 = pack_f16(z, z);
+            const uint4 now = w;
+            if (k > 0) w = *reinterpret_cast<const uint4*>(raw + src0 + (k - 1) * 8 * kRow4);
+            __syncwarp();
+            *reinterpret_cast<uint4*>(stage + dst0[0] + k * 1024) = dequant8(now.x, s2, t2, z2);
+            *reinterpret_cast<uint4*>(stage + dst0[1] + k * 1024) = dequant8(now.y, s2, t2, z2);
+            *reinterpret_cast<uint4*>(stage + dst0[2] + k * 1024) = dequant8(now.z, s2, t2, z2);
+            *reinterpret_cast<uint4*>(stage + dst0[3] + k * 1024) = dequant8(now.w, s2, t2, z2);
           }
           fence_async_smem();  // (read by the MMAs)
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar((side ? B_VF : B_KF) + s));
+          if (lane == 0) {
+            mbar_arrive(bar((side ? B_VF : B_KF) + s));
+            if (!side) mbar_arrive(i4_bar(I_KT + s));
+          }
+          if (j == 0) ok = query_rows(it, it_cnt, q_cnt, 2 + 2 * side + dw);
         }
-        if (!ok) break;
-        if (lane == 0) mbar_arrive(taken);
       }
     }
   } else {
+    if (kI4) take_regs<kRegsEpi, false>();
     // ------------------ epilogue: one warp per TMEM lane quarter ------------------
     // Warp w (four after the softmax) owns rows 32 * (w % 4) .. + 31 of both output tiles.  When
     // O_x is final (its last P.V done) and both partial row sums are in, the
@@ -1238,11 +1600,11 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap) + (kI4 ? 32 * kD
     const int row = qd * 32 + lane;  // == TMEM lane
     const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
     const float* lsum = reinterpret_cast<const float*>(smem + kOffLsum);
-    const uint32_t stg = sbase + kOffStage + (warp - 2 - kSoft) * kStageWarp;
+    const uint32_t stg = sbase + kOffStage + (warp - kSoft0 - kSoft) * kStageWarp;
     uint32_t o_cnt[2] = {0, 0};
     for (uint32_t it_cnt = 0;; ++it_cnt) {
       const int slot = it_cnt & 1;
-      if (!mbar_wait_warp(bar(B_IF + slot), (it_cnt >> 1) & 1, abort, ws.err)) break;
+      if (!wait(bar(B_IF + slot), (it_cnt >> 1) & 1)) break;
       const Item it = items[slot];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_IE + slot));
@@ -1251,8 +1613,8 @@ __global__ void __launch_bounds__(threads_of(kCap == kFixedCap) + (kI4 ? 32 * kD
       bool ok = true;
       for (int x = 0; x < nx && ok; ++x) {
         const uint32_t par = o_cnt[x]++ & 1;
-        if (!mbar_wait_warp(bar(B_OF + x), par, abort, ws.err) ||
-            !mbar_wait_warp(lf_bar(it_cnt, x), (it_cnt >> 1) & 1, abort, ws.err)) {
+        if (!wait(bar(B_OF + x), par) ||
+            !wait(lf_bar(it_cnt, x), (it_cnt >> 1) & 1)) {
           ok = false;
           break;
         }
@@ -1334,7 +1696,16 @@ cudaError_t launch_prefill_as(const ScoredArgs& a, const Workspace& ws, int sms,
   static std::atomic<bool> attr[kMaxAttrDevices];
   auto* kernel = prefill_kernel<kScored, kCap, kBias, kSym, kI4>;
   constexpr int kSmem = kI4 ? kSmemBytesI4 : kSmemBytes;
-  constexpr int kThreads = threads_of(kCap == kFixedCap) + (kI4 ? 32 * kDequantWarps : 0);
+  constexpr int kThreads = kI4 ? kThreadsI4 : threads_of(kCap == kFixedCap);
+  if (kI4) {  // (shares that the launch does not have would be waited for without end)
+    static std::atomic<int> regs{0};
+    if (regs.load(std::memory_order_acquire) == 0) {
+      cudaFuncAttributes fa;
+      if (cudaError_t e = cudaFuncGetAttributes(&fa, kernel)) return e;
+      regs.store(fa.numRegs, std::memory_order_release);
+    }
+    if (regs.load(std::memory_order_acquire) < kRegsLaunch) return cudaErrorInvalidConfiguration;
+  }
   if (cudaError_t e = smem_attr_once(kernel, kSmem, attr)) return e;
   CUtensorMap tq, tk, tv;
   if (!make_rows_map(&tq, a.q, a.q_rows, a.hq, a.q_stride, 1, kPreTileQ)) return cudaErrorInvalidValue;

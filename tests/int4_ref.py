@@ -65,9 +65,10 @@ def attention(q, cache, qsl, seq_lens, block_table, scale):
       (17 additions and 4 other operations of 2^-24, the MMA's own sums of 2^-22),
       where they turn a weight by that much;
     for prefill requests:
-      the same rounding of the output, one of the weights to bf16 (2^-8 each), one of
-      the values to bf16 (2^-8 each), and of the keys to bf16: 2^-8 of the sizes of the
-      products in a logit."""
+      the same rounding of the output; of the weights to fp16 (2^-11, and below fp16's
+      normal range 2^-24 of the largest weight a key); of keys and values to fp16 (2^-11,
+      and for those far below the largest of their tile 2^-18 of that), the keys' in the
+      products of a logit."""
     rows, hq, _ = q.shape
     hkv = cache.shape[1]
     G = hq // hkv
@@ -94,8 +95,10 @@ def attention(q, cache, qsl, seq_lens, block_table, scale):
                 o = p @ v
                 av = p @ v.abs()
                 if prefill:
-                    dx = 2.0 ** -8 * scale * (qd.abs() @ k.abs().T)
-                    t = 2 * 2.0 ** -8 * av
+                    dx = scale * (2.0 ** -11 * (qd.abs() @ k.abs().T) + 2.0 ** -18 * k.abs().max() *
+                                  qd.abs().sum(-1, keepdim=True))
+                    t = 2 * 2.0 ** -11 * av + 2.0 ** -18 * v.abs().max() + \
+                        2.0 ** -24 * L * p.amax(-1, keepdim=True) * v.abs().amax(0)
                 else:
                     dx = 2.0 ** -17 * scale * (qd.abs() @ (kc * ks[:, None]).T +
                                                qd.abs().sum(-1, keepdim=True) * kz.abs())
