@@ -47,18 +47,17 @@ namespace {
 
 using namespace dev;
 
-constexpr int kIdRegs4 = kMaxChunk / kBlockSize / 32;
 constexpr uint32_t kNib0 = 0x000F000Fu, kNib1 = 0x00F000F0u;
 constexpr float kMaxWeight = 16384.f;  // e_j t_j that the reference is kept for
 constexpr float kMaxExp = 0x1p54f;     // e_j (of value rows with tiny or no scale)
 
-// kTiles: the most tiles of 8 query rows a unit has
+// kTiles: the most tiles of 8 query rows a unit has.  A stage holds two pages.
 template <int kTiles>
 struct Cfg4 {
   static constexpr int kWarps = kTiles <= 2 ? 12 : 8;
   static constexpr int kThreads = kWarps * 32;
-  static constexpr int kStages = kTiles <= 2 ? 8 : 12;
-  static constexpr int kWarpBytes = kStages * kPage4;
+  static constexpr int kStages = kTiles <= 2 ? 4 : 6;
+  static constexpr int kWarpBytes = kStages * 2 * kPage4;
   static constexpr int kOffBar = kWarps * kWarpBytes;
   static constexpr int kOffCtl = kOffBar + kWarps * kStages * 8;
   static constexpr int kSmem = kOffCtl + 16 + 128;
@@ -103,14 +102,14 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 }
 __device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-// One warp's view of its ring.
+// One warp's ring: the stage its next step takes, and the parity of that step's wait.
 struct Ring {
-  uint32_t base, bars;
-  uint32_t cnt;  // pages taken so far
+  uint32_t base, bars, stage, parity;
 };
 
-// A unit of at most 8 * kT query rows.  Returns false when a wait gave up.
-template <int kT, int kStages>
+// A unit of at most 8 * kT query rows, two pages (32 keys) a step, kPg of them at a time.
+// Returns false when a wait gave up.
+template <int kT, int kPg, int kStages>
 __device__ __forceinline__ bool run_unit(const AttnArgs& a, const Workspace& ws, const DecUnit& un,
                                          Ring& ring, uint64_t pol, volatile int* abort) {
   const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
@@ -119,43 +118,50 @@ __device__ __forceinline__ bool run_unit(const AttnArgs& a, const Workspace& ws,
   const int qn = un.gq >> 16;     // query tokens of the request
   const int k0 = un.k0, k1 = un.k1;
   const int p0 = k0 / kBlockSize;
-  const int npages = (k1 + kBlockSize - 1) / kBlockSize - p0;
+  const int npages = (k1 + kBlockSize - 1) / kBlockSize - p0, nsteps = (npages + 1) / 2;
   const int nrows = qn * G;
 
-  // block ids of the unit, one per lane per 32 pages
-  int ids[kIdRegs4];
+  // The pages of 16 steps at a time, one per lane, and those of the next 16.
   const int* btrow = table_row(a, un.r, ug) + p0;
-#pragma unroll
-  for (int j = 0; j < kIdRegs4; ++j) {
-    const int p = lane + 32 * j;
-    int blk = 0;
-    if (p < npages) {
-      blk = __ldg(btrow + p);
+  auto load_ids = [&](int p) {
+    const uint8_t* page = nullptr;
+    if (p + lane < npages) {
+      int blk = __ldg(btrow + p + lane);
       if (blk < 0 || (int64_t)blk >= a.num_blocks) {
         atomicOr(ws.err, PKV_DEV_ERR_BLOCK_ID);
         blk = 0;
       }
+      page = reinterpret_cast<const uint8_t*>(a.kc) + ((int64_t)blk * a.hkv + ug) * kPage4;
     }
-    ids[j] = blk;
-  }
-  // page p into its stage, by the lane that holds its id; the stage's last page was
-  // taken by this warp already (program order)
-  auto issue = [&](int p) {
-    const uint32_t s = (ring.cnt + p) % kStages;
-    int id = ids[0];
-#pragma unroll
-    for (int j = 1; j < kIdRegs4; ++j)
-      if ((p >> 5) == j) id = ids[j];
-    if (lane == (p & 31)) {
+    return page;
+  };
+  const uint8_t *ids = load_ids(0), *ids_next = load_ids(32);
+  // step j into stage st, each page by the lane that holds it; the stage's last pages
+  // were taken by this warp already (program order)
+  auto issue = [&](int j, uint32_t st) {
+    if ((j & 15) == 0 && j > 0) {
+      ids = ids_next;
+      ids_next = load_ids(2 * j + 32);
+    }
+    const int first = 2 * (j & 15);
+    const uint32_t bar = ring.bars + 8 * st;
+    if (lane == first) {
       fence_async_smem();
-      const uint32_t bar = ring.bars + 8 * s;
-      mbar_expect_tx(bar, kPage4);
-      bulk_load_hint(ring.base + s * kPage4,
-                     reinterpret_cast<const uint8_t*>(a.kc) + ((int64_t)id * a.hkv + ug) * kPage4,
-                     kPage4, bar, pol);
+      mbar_expect_tx(bar, 2 * j + 1 < npages ? 2 * kPage4 : kPage4);
+    }
+    __syncwarp();
+    if ((lane & ~1) == first && ids != nullptr) {
+      fence_async_smem();
+      bulk_load_hint(ring.base + (2 * st + (lane & 1)) * kPage4, ids, kPage4, bar, pol);
     }
   };
-  for (int p = 0; p < kStages && p < npages; ++p) issue(p);
+  {
+    uint32_t st = ring.stage;
+    for (int j = 0; j < kStages && j < nsteps; ++j) {
+      issue(j, st);
+      st = st + 1 == kStages ? 0 : st + 1;
+    }
+  }
 
   // Query rows: tile t has rows 8 t .. 8 t + 7 (token * G + head in group), a thread
   // dimensions 32 tig .. + 31 of row gid.  Operand pair 2 i + h of k-step order: word
@@ -215,8 +221,9 @@ __device__ __forceinline__ bool run_unit(const AttnArgs& a, const Workspace& ws,
   const int all_see = min(k1, un.ctx + 1);  // every row sees the keys before
 
   // o[t][d]: output dimensions of the thread's two MMA rows (see below), columns 2 tig,
-  // + 1; sums of e and of e * zero over the thread's keys
-  float o[kT][8][4], l[kT][2], z[kT][2], ref[kT][2];
+  // + 1; sums of e and of e * zero over the thread's keys; the negative reference of
+  // each column (0 and `unset` while a row has seen no key)
+  float o[kT][8][4], l[kT][2], z[kT][2], nref[kT][2];
 #pragma unroll
   for (int t = 0; t < kT; ++t) {
 #pragma unroll
@@ -224,143 +231,182 @@ __device__ __forceinline__ bool run_unit(const AttnArgs& a, const Workspace& ws,
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[t][d][e] = 0.f;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      l[t][c] = z[t][c] = 0.f;
-      ref[t][c] = -INFINITY;
-    }
+    for (int c = 0; c < 2; ++c) l[t][c] = z[t][c] = nref[t][c] = 0.f;
   }
-  bool unset = true;  // some row has no reference yet (no key it sees)
+  uint32_t unset = (1u << 2 * kT) - 1;  // columns without a reference (the same in each gid)
 
   // MMA row m < 8 of a page's first (second) eight is its key kappa(m) (+ 8)
   const int key = ((gid >> 1) ^ (gid & 1)) + 4 * (gid & 1);
+  const uint32_t at_k = ring.base + kRow4 * key + 16 * tig;
+  const uint32_t at_m = ring.base + kMeta4 + 4 * key;
+  const uint32_t at_v = ring.base + kSide4 + 8 * gid + kRow4 * tig;
+  const uint32_t at_w = ring.base + kSide4 + 8 * gid + kRow4 * ((tig ^ 1) + 4);
 
-  for (int p = 0; p < npages; ++p) {
-    const uint32_t x = ring.cnt + p, s = x % kStages;
-    if (!mbar_wait_warp(ring.bars + 8 * s, (x / kStages) & 1, abort, ws.err)) return false;
-    const uint32_t st = ring.base + s * kPage4;
-    const int pos0 = k0 + p * kBlockSize;
-    const uint4 ka = lds128(st + kRow4 * key + 16 * tig);
-    const uint4 kb = lds128(st + kRow4 * (key + 8) + 16 * tig);
-    uint32_t mk[2], mv[2];
+  for (int j = 0; j < nsteps; ++j) {
+    if (!mbar_wait_warp(ring.bars + 8 * ring.stage, ring.parity, abort, ws.err)) return false;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      mk[i] = lds32(st + kMeta4 + 4 * (key + 8 * i));
-      mv[i] = lds32(st + kMeta4 + 64 + 4 * (key + 8 * i));
-    }
-    // values: keys kappa(2 tig), kappa(2 tig + 1) and those 8 on, dimensions 16 gid .. + 15
-    const uint32_t sv = st + kSide4 + 8 * gid;
-    const uint2 va = lds64(sv + kRow4 * tig), vb = lds64(sv + kRow4 * ((tig ^ 1) + 4));
-    const uint2 vc = lds64(sv + kRow4 * (tig + 8)), vd = lds64(sv + kRow4 * ((tig ^ 1) + 12));
-
-    // S^T = K Q^T
-    float acc[kT][4];
+    for (int half = 0; half < 2; half += kPg) {
+      const uint32_t st = (2 * ring.stage + half) * kPage4;
+      // S^T = K Q^T
+      float acc[kPg][kT][4];
+      uint32_t mk[kPg][2], mv[kPg][2];
 #pragma unroll
-    for (int t = 0; t < kT; ++t)
+      for (int g = 0; g < kPg; ++g) {
+        const uint4 ka = lds128(at_k + st + g * kPage4);
+        const uint4 kb = lds128(at_k + st + g * kPage4 + 8 * kRow4);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
-    const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t ca = wa[i >> 1] >> (8 * (i & 1)), cb = wb[i >> 1] >> (8 * (i & 1));
-#pragma unroll
-      for (int t = 0; t < kT; ++t)
-        mma_f16(acc[t], ca & kNib0, cb & kNib0, ca & kNib1, cb & kNib1, qb[t][i][0], qb[t][i][1]);
-    }
-    // the page is in registers: its stage can take another
-    __syncwarp();
-    if (p + kStages < npages) issue(p + kStages);
-
-    // logits: acc[t][0], [1] of the thread's first key, [2], [3] of its second
-    const bool edge = pos0 + kBlockSize > all_see;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int j = pos0 + key + 8 * i;
-      const float ks = lo16(mk[i]), kz = hi16(mk[i]);
-      if (edge && j >= k1) mv[i] = 0u;
-#pragma unroll
-      for (int t = 0; t < kT; ++t)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float v = fmaf(acc[t][2 * i + c] * ks, fac[t][c], kz * off[t][c]);
-          acc[t][2 * i + c] = edge && j >= vis[t][c] ? -INFINITY : v;
+        for (int i = 0; i < 2; ++i) {
+          mk[g][i] = lds32(at_m + st + g * kPage4 + 32 * i);
+          mv[g][i] = lds32(at_m + st + g * kPage4 + 64 + 32 * i);
         }
-    }
-    float e[kT][4], w[kT][4];
-    auto weights = [&]() {
-      float most = 0.f, tall = 0.f;
-#pragma unroll
-      for (int t = 0; t < kT; ++t) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float r = ref[t][i & 1];
-          e[t][i] = fast_exp2(acc[t][i] - (unset && r == -INFINITY ? 0.f : r));
-          w[t][i] = e[t][i] * lo16(mv[i >> 1]);
-        }
-        most = max3f(most, fmaxf(w[t][0], w[t][1]), fmaxf(w[t][2], w[t][3]));
-        tall = max3f(tall, fmaxf(e[t][0], e[t][1]), fmaxf(e[t][2], e[t][3]));
-      }
-      return most > kMaxWeight || tall > kMaxExp;
-    };
-    if (__any_sync(0xffffffffu, unset || weights())) {
-      // references moved up: to the largest logit + log2 of the value row's scale
-      // (weights up to 1), or so that e stays below 2^40
-      const float t0 = __log2f(lo16(mv[0])), t1 = __log2f(lo16(mv[1]));
-      bool none = false;
-#pragma unroll
-      for (int t = 0; t < kT; ++t)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float m = fmaxf(acc[t][c], acc[t][2 + c]) - 40.f;
-          m = max3f(m, acc[t][c] + t0, acc[t][2 + c] + t1);
-#pragma unroll
-          for (int b = 4; b < 32; b <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, b));
-          const float to = fmaxf(ref[t][c], m);
-          const float al = ref[t][c] == -INFINITY ? 0.f : fast_exp2(ref[t][c] - to);
-          ref[t][c] = to;
-          none |= to == -INFINITY;
-          l[t][c] *= al;
-          z[t][c] *= al;
-#pragma unroll
-          for (int d = 0; d < 8; ++d) {
-            o[t][d][c] *= al;
-            o[t][d][2 + c] *= al;
-          }
-        }
-      unset = true;  // (for the references still missing)
-      weights();
-      unset = __any_sync(0xffffffffu, none);
-    }
-    uint32_t pb[kT][2];
-#pragma unroll
-    for (int t = 0; t < kT; ++t) {
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        l[t][c] += e[t][c] + e[t][2 + c];
-        z[t][c] = fmaf(e[t][c], hi16(mv[0]), fmaf(e[t][2 + c], hi16(mv[1]), z[t][c]));
-        pb[t][c] = transpose8x8(pack_f16(w[t][2 * c], w[t][2 * c + 1]));
-      }
-    }
-
-    // O^T += V^T P^T: a word of codes of the two keys of an operand pair, their low
-    // halves together and their high ones, hold dimensions 0, 2, 4, 6 and 1, 3, 5, 7 of the
-    // eight; MMA rows gid and gid + 8 are the first and second nibble of each byte
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t a0 = h ? va.y : va.x, a1 = h ? vb.y : vb.x;
-      const uint32_t b0 = h ? vc.y : vc.x, b1 = h ? vd.y : vd.x;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {  // even dimensions 0, 2 | 4, 6; odd 1, 3 | 5, 7
-        const uint32_t sel = i < 2 ? 0x5410 : 0x7632;
-        const uint32_t lo = __byte_perm(a0, a1, sel) >> (8 * (i & 1));
-        const uint32_t hi = __byte_perm(b0, b1, sel) >> (8 * (i & 1));
 #pragma unroll
         for (int t = 0; t < kT; ++t)
-          mma_f16(o[t][4 * h + i], lo & kNib0, lo & kNib1, hi & kNib0, hi & kNib1, pb[t][0],
-                  pb[t][1]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[g][t][e] = 0.f;
+        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t ca = wa[i >> 1] >> (8 * (i & 1)), cb = wb[i >> 1] >> (8 * (i & 1));
+#pragma unroll
+          for (int t = 0; t < kT; ++t)
+            mma_f16(acc[g][t], ca & kNib0, cb & kNib0, ca & kNib1, cb & kNib1, qb[t][i][0],
+                    qb[t][i][1]);
+        }
+      }
+
+      // logits less the reference: acc[g][t][0], [1] of the thread's first key of page g,
+      // [2], [3] of its second
+#pragma unroll
+      for (int g = 0; g < kPg; ++g)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float ks = lo16(mk[g][i]), kz = hi16(mk[g][i]);
+#pragma unroll
+          for (int t = 0; t < kT; ++t)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              acc[g][t][2 * i + c] =
+                  fmaf(acc[g][t][2 * i + c] * ks, fac[t][c], fmaf(kz, off[t][c], nref[t][c]));
+        }
+      const int pos = k0 + (2 * j + half) * kBlockSize;
+      if (pos + kPg * kBlockSize > all_see) {
+#pragma unroll
+        for (int g = 0; g < kPg; ++g)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int at = pos + kBlockSize * g + key + 8 * i;
+            if (at >= k1) mv[g][i] = 0u;
+#pragma unroll
+            for (int t = 0; t < kT; ++t)
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                if (at >= vis[t][c]) acc[g][t][2 * i + c] = -INFINITY;
+          }
+      }
+      float e[kPg][kT][4], w[kPg][kT][4];
+      auto weights = [&]() {
+        float most = 0.f, tall = 0.f;
+#pragma unroll
+        for (int g = 0; g < kPg; ++g)
+#pragma unroll
+          for (int t = 0; t < kT; ++t) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              e[g][t][i] = fast_exp2(acc[g][t][i]);
+              w[g][t][i] = e[g][t][i] * lo16(mv[g][i >> 1]);
+            }
+            most = max3f(most, max3f(w[g][t][0], w[g][t][1], w[g][t][2]), w[g][t][3]);
+            tall = max3f(tall, max3f(e[g][t][0], e[g][t][1], e[g][t][2]), e[g][t][3]);
+          }
+        return most > kMaxWeight || tall > kMaxExp;
+      };
+      const bool over = weights();
+      if (__any_sync(0xffffffffu, over || unset != 0)) {
+        // references moved up: to the largest logit + log2 of the value row's scale
+        // (weights up to 1), or so that e stays below 2^40
+#pragma unroll
+        for (int t = 0; t < kT; ++t)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float m = -INFINITY;
+#pragma unroll
+            for (int g = 0; g < kPg; ++g)
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                m = fmaxf(m, acc[g][t][2 * i + c] + fmaxf(__log2f(lo16(mv[g][i])), -40.f));
+#pragma unroll
+            for (int b = 4; b < 32; b <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, b));
+            const uint32_t bit = 1u << (2 * t + c);
+            const bool none = (unset & bit) != 0;
+            // (m is relative to the reference, 0 if there is none; a row without one takes
+            // whatever it sees first, another moves up only)
+            const float up = none ? (m == -INFINITY ? 0.f : m) : fmaxf(m, 0.f);
+            const float al = fast_exp2(-up);
+            if (m != -INFINITY) unset &= ~bit;
+            nref[t][c] -= up;
+            if (!none) {  // (nothing is summed yet of a row without a reference)
+              l[t][c] *= al;
+              z[t][c] *= al;
+#pragma unroll
+              for (int d = 0; d < 8; ++d) {
+                o[t][d][c] *= al;
+                o[t][d][2 + c] *= al;
+              }
+            }
+#pragma unroll
+            for (int g = 0; g < kPg; ++g)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) acc[g][t][2 * i + c] -= up;
+          }
+        weights();
+      }
+      uint32_t pb[kPg][kT][2];
+#pragma unroll
+      for (int g = 0; g < kPg; ++g)
+#pragma unroll
+        for (int t = 0; t < kT; ++t)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            l[t][c] += e[g][t][c] + e[g][t][2 + c];
+            z[t][c] = fmaf(e[g][t][c], hi16(mv[g][0]), fmaf(e[g][t][2 + c], hi16(mv[g][1]), z[t][c]));
+            pb[g][t][c] = transpose8x8(pack_f16(w[g][t][2 * c], w[g][t][2 * c + 1]));
+          }
+
+      // O^T += V^T P^T: a word of codes of the two keys of an operand pair, their low
+      // halves together and their high ones, hold dimensions 0, 2, 4, 6 and 1, 3, 5, 7 of
+      // the eight; MMA rows gid and gid + 8 are the first and second nibble of each byte.
+      // Values: keys kappa(2 tig), kappa(2 tig + 1) and those 8 on, dimensions 16 gid .. + 15.
+#pragma unroll
+      for (int g = 0; g < kPg; ++g) {
+        const uint2 va = lds64(at_v + st + g * kPage4), vb = lds64(at_w + st + g * kPage4);
+        const uint2 vc = lds64(at_v + st + g * kPage4 + 8 * kRow4);
+        const uint2 vd = lds64(at_w + st + g * kPage4 + 8 * kRow4);
+        if (half + g == 1) {  // the stage is in registers: it can take another step
+          __syncwarp();
+          if (j + kStages < nsteps) issue(j + kStages, ring.stage);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t a0 = h ? va.y : va.x, a1 = h ? vb.y : vb.x;
+          const uint32_t b0 = h ? vc.y : vc.x, b1 = h ? vd.y : vd.x;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {  // even dimensions 0, 2 | 4, 6; odd 1, 3 | 5, 7
+            const uint32_t sel = i < 2 ? 0x5410 : 0x7632;
+            const uint32_t lo = __byte_perm(a0, a1, sel) >> (8 * (i & 1));
+            const uint32_t hi = __byte_perm(b0, b1, sel) >> (8 * (i & 1));
+#pragma unroll
+            for (int t = 0; t < kT; ++t)
+              mma_f16(o[t][4 * h + i], lo & kNib0, lo & kNib1, hi & kNib0, hi & kNib1, pb[g][t][0],
+                      pb[g][t][1]);
+          }
+        }
       }
     }
+    if (++ring.stage == kStages) {
+      ring.stage = 0;
+      ring.parity ^= 1;
+    }
   }
-  ring.cnt += npages;
 
   // The thread's columns 2 tig, 2 tig + 1 are query rows, with dimensions 16 gid .. + 15:
   // o[4 h + i][c] is dimension 8 h + 4 (i % 2) + i / 2, o[4 h + i][2 + c] the one 2 on.
@@ -399,9 +445,9 @@ __device__ __forceinline__ bool run_unit(const AttnArgs& a, const Workspace& ws,
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        if (gid == 0)
+        if (gid == 0)  // (no key seen: the merge skips a split with reference -inf)
           *reinterpret_cast<float2*>(ws.part_ml + ((int64_t)un.part + row) * 2) =
-              make_float2(ref[t][c], ls);
+              make_float2((unset >> (2 * t + c)) & 1 ? -INFINITY : -nref[t][c], ls);
       }
     }
   return true;
@@ -416,7 +462,7 @@ __global__ void __launch_bounds__(Cfg4<kTiles>::kThreads, 1)
                                              ~(uintptr_t)127);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t sbase = smem_u32(smem);
-  Ring ring{sbase + warp * C::kWarpBytes, sbase + C::kOffBar + warp * C::kStages * 8, 0};
+  Ring ring{sbase + warp * C::kWarpBytes, sbase + C::kOffBar + warp * C::kStages * 8, 0, 0};
   volatile int* abort = reinterpret_cast<volatile int*>(smem + C::kOffCtl);
   if (lane == 0) {
     for (int s = 0; s < C::kStages; ++s) mbar_init(ring.bars + 8u * s, 1);
@@ -438,9 +484,9 @@ __global__ void __launch_bounds__(Cfg4<kTiles>::kThreads, 1)
     const DecUnit un = load_unit(ws.units + u);
     bool ok;
     if (kTiles == 2 && (un.gq >> 16) * (a.hq / a.hkv) <= 8)
-      ok = run_unit<1, C::kStages>(a, ws, un, ring, pol, abort);
+      ok = run_unit<1, 2, C::kStages>(a, ws, un, ring, pol, abort);
     else
-      ok = run_unit<kTiles, C::kStages>(a, ws, un, ring, pol, abort);
+      ok = run_unit<kTiles, 1, C::kStages>(a, ws, un, ring, pol, abort);
     if (!ok) break;
   }
 }
