@@ -49,14 +49,17 @@ using namespace dev;
 
 constexpr uint32_t kNib0 = 0x000F000Fu, kNib1 = 0x00F000F0u;
 constexpr float kMaxWeight = 16384.f;  // e_j t_j that the reference is kept for
-constexpr float kMaxExp = 0x1p54f;     // e_j (of value rows with tiny or no scale)
+// The scale of a value row without spread counts as this (its codes are zero), so that
+// its e_j is held below 2^54 by the same bound; scales of others are above it.
+constexpr float kMinScale = 0x1p-40f;
 
-// kTiles: the most tiles of 8 query rows a unit has.  A stage holds two pages.
+// Instances: items of at most 8 * kTiles query rows, kPg pages of a step at a time.
 template <int kTiles>
 struct Cfg4 {
-  static constexpr int kWarps = kTiles <= 2 ? 12 : 8;
+  static constexpr int kPg = 2;
+  static constexpr int kWarps = kTiles == 1 ? 16 : 8;
   static constexpr int kThreads = kWarps * 32;
-  static constexpr int kStages = kTiles <= 2 ? 4 : 6;
+  static constexpr int kStages = 48 / kWarps;  // of two pages
   static constexpr int kWarpBytes = kStages * 2 * kPage4;
   static constexpr int kOffBar = kWarps * kWarpBytes;
   static constexpr int kOffCtl = kOffBar + kWarps * kStages * 8;
@@ -107,11 +110,13 @@ struct Ring {
   uint32_t base, bars, stage, parity;
 };
 
-// A unit of at most 8 * kT query rows, two pages (32 keys) a step, kPg of them at a time.
-// Returns false when a wait gave up.
-template <int kT, int kPg, int kStages>
+// Query rows row0 .. of a unit (nrows of them in all), at most 8 * kT, two pages (32
+// keys) a step, kPg of them at a time.  Returns false when a wait gave up.
+template <int kT, int kPg = Cfg4<kT>::kPg>
 __device__ __forceinline__ bool run_unit(const AttnArgs& a, const Workspace& ws, const DecUnit& un,
-                                         Ring& ring, uint64_t pol, volatile int* abort) {
+                                         int row0, Ring& ring, uint64_t pol,
+                                         volatile int* abort) {
+  constexpr int kStages = Cfg4<kT>::kStages;
   const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
   const int G = a.hq / a.hkv;
   const int ug = un.gq & 0xFFFF;  // KV head
@@ -163,7 +168,7 @@ __device__ __forceinline__ bool run_unit(const AttnArgs& a, const Workspace& ws,
     }
   }
 
-  // Query rows: tile t has rows 8 t .. 8 t + 7 (token * G + head in group), a thread
+  // Query rows: tile t has rows row0 + 8 t .. + 7 (token * G + head in group), a thread
   // dimensions 32 tig .. + 31 of row gid.  Operand pair 2 i + h of k-step order: word
   // i of the keys' codes, shifted by 8 h.
   uint32_t qb[kT][8][2];
@@ -172,7 +177,7 @@ __device__ __forceinline__ bool run_unit(const AttnArgs& a, const Workspace& ws,
   const float f = a.scale * kLog2e;
 #pragma unroll
   for (int t = 0; t < kT; ++t) {
-    const int row = 8 * t + gid;
+    const int row = row0 + 8 * t + gid;
     uint4 raw[4] = {};
     if (row < nrows) {
       const uint4* src = reinterpret_cast<const uint4*>(
@@ -214,7 +219,7 @@ __device__ __forceinline__ bool run_unit(const AttnArgs& a, const Workspace& ws,
     for (int c = 0; c < 2; ++c) {
       fac[t][c] = __shfl_sync(0xffffffffu, rf, 4 * (2 * tig + c));
       off[t][c] = __shfl_sync(0xffffffffu, rs, 4 * (2 * tig + c));
-      const int r = 8 * t + 2 * tig + c;
+      const int r = row0 + 8 * t + 2 * tig + c;
       vis[t][c] = min(k1, un.ctx + (r < nrows ? r / G : qn - 1) + 1);
     }
   }
@@ -244,7 +249,7 @@ __device__ __forceinline__ bool run_unit(const AttnArgs& a, const Workspace& ws,
 
   for (int j = 0; j < nsteps; ++j) {
     if (!mbar_wait_warp(ring.bars + 8 * ring.stage, ring.parity, abort, ws.err)) return false;
-#pragma unroll
+#pragma unroll 1
     for (int half = 0; half < 2; half += kPg) {
       const uint32_t st = (2 * ring.stage + half) * kPage4;
       // S^T = K Q^T
@@ -303,9 +308,13 @@ __device__ __forceinline__ bool run_unit(const AttnArgs& a, const Workspace& ws,
                 if (at >= vis[t][c]) acc[g][t][2 * i + c] = -INFINITY;
           }
       }
-      float e[kPg][kT][4], w[kPg][kT][4];
+      float vs[kPg][2], e[kPg][kT][4], w[kPg][kT][4];
+#pragma unroll
+      for (int g = 0; g < kPg; ++g)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) vs[g][i] = fmaxf(lo16(mv[g][i]), kMinScale);
       auto weights = [&]() {
-        float most = 0.f, tall = 0.f;
+        float most = 0.f;
 #pragma unroll
         for (int g = 0; g < kPg; ++g)
 #pragma unroll
@@ -313,17 +322,16 @@ __device__ __forceinline__ bool run_unit(const AttnArgs& a, const Workspace& ws,
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               e[g][t][i] = fast_exp2(acc[g][t][i]);
-              w[g][t][i] = e[g][t][i] * lo16(mv[g][i >> 1]);
+              w[g][t][i] = e[g][t][i] * vs[g][i >> 1];
             }
             most = max3f(most, max3f(w[g][t][0], w[g][t][1], w[g][t][2]), w[g][t][3]);
-            tall = max3f(tall, max3f(e[g][t][0], e[g][t][1], e[g][t][2]), e[g][t][3]);
           }
-        return most > kMaxWeight || tall > kMaxExp;
+        return most > kMaxWeight;
       };
       const bool over = weights();
       if (__any_sync(0xffffffffu, over || unset != 0)) {
         // references moved up: to the largest logit + log2 of the value row's scale
-        // (weights up to 1), or so that e stays below 2^40
+        // (weights up to 1)
 #pragma unroll
         for (int t = 0; t < kT; ++t)
 #pragma unroll
@@ -333,7 +341,7 @@ __device__ __forceinline__ bool run_unit(const AttnArgs& a, const Workspace& ws,
             for (int g = 0; g < kPg; ++g)
 #pragma unroll
               for (int i = 0; i < 2; ++i)
-                m = fmaxf(m, acc[g][t][2 * i + c] + fmaxf(__log2f(lo16(mv[g][i])), -40.f));
+                m = fmaxf(m, acc[g][t][2 * i + c] + __log2f(vs[g][i]));
 #pragma unroll
             for (int b = 4; b < 32; b <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, b));
             const uint32_t bit = 1u << (2 * t + c);
@@ -420,7 +428,7 @@ __device__ __forceinline__ bool run_unit(const AttnArgs& a, const Workspace& ws,
         ls += __shfl_xor_sync(0xffffffffu, ls, b);
         zs += __shfl_xor_sync(0xffffffffu, zs, b);
       }
-      const int row = 8 * t + 2 * tig + c;
+      const int row = row0 + 8 * t + 2 * tig + c;
       if (row >= nrows) continue;
       float v[16];
 #pragma unroll
@@ -453,6 +461,9 @@ __device__ __forceinline__ bool run_unit(const AttnArgs& a, const Workspace& ws,
   return true;
 }
 
+// Groups of up to 8 heads: a unit's rows 8 at a time (single tokens: one time).  Larger
+// groups: two tiles, and above 16 heads a unit is two items, of its first 16 query rows
+// and of the rest, for two warps that each read its pages (the second out of the L2).
 template <int kTiles>
 __global__ void __launch_bounds__(Cfg4<kTiles>::kThreads, 1)
     decode_i4_kernel(AttnArgs a, Workspace ws) {
@@ -469,24 +480,28 @@ __global__ void __launch_bounds__(Cfg4<kTiles>::kThreads, 1)
     if (warp == 0) *abort = 0;
     fence_barrier_init();
   }
+  const int G = a.hq / a.hkv, shift = kTiles == 2 && G > 16 ? 1 : 0;
   // the set-up above overlaps the plan kernel; the work list is read after it
   grid_dep_wait();
   grid_dep_launch();
-  if (leaves_sm_to_prefill(a, ws, C::kWarps) || ws.hdr->n_dec_units == 0) return;
+  if (leaves_sm_to_prefill(a, ws, C::kWarps >> shift) || ws.hdr->n_dec_units == 0) return;
   __syncthreads();
-  const int n_units = ws.hdr->n_dec_units;
-  const uint64_t pol = l2_evict_first();  // pages are read once
+  const int n_items = ws.hdr->n_dec_units << shift;
+  const uint64_t pol = l2_evict_first();  // pages are read once (or twice at a time)
   for (;;) {
     int u = 0;
     if (lane == 0) u = atomicAdd(&ws.hdr->dec_counter, 1);
     u = __shfl_sync(0xffffffffu, u, 0);
-    if (u >= n_units || *abort) break;
-    const DecUnit un = load_unit(ws.units + u);
-    bool ok;
-    if (kTiles == 2 && (un.gq >> 16) * (a.hq / a.hkv) <= 8)
-      ok = run_unit<1, 2, C::kStages>(a, ws, un, ring, pol, abort);
-    else
-      ok = run_unit<kTiles, 1, C::kStages>(a, ws, un, ring, pol, abort);
+    if (u >= n_items || *abort) break;
+    const DecUnit un = load_unit(ws.units + (u >> shift));
+    bool ok = true;
+    if (kTiles == 1) {
+      const int rows = (un.gq >> 16) * G;
+      for (int row0 = 0; ok && row0 < rows; row0 += 8)
+        ok = run_unit<kTiles>(a, ws, un, row0, ring, pol, abort);
+    } else {
+      ok = run_unit<kTiles>(a, ws, un, 16 * (u & shift), ring, pol, abort);
+    }
     if (!ok) break;
   }
 }
@@ -502,10 +517,13 @@ cudaError_t launch_i4(const AttnArgs& a, const Workspace& ws, int sms, cudaStrea
 
 }  // namespace
 
-int decode_i4_warps(int group) { return group <= 16 ? Cfg4<2>::kWarps : Cfg4<4>::kWarps; }
+// units at a time of a CTA
+int decode_i4_warps(int group) {
+  return group <= 8 ? Cfg4<1>::kWarps : group <= 16 ? Cfg4<2>::kWarps : Cfg4<2>::kWarps / 2;
+}
 
 cudaError_t launch_decode_i4(const AttnArgs& a, const Workspace& ws, int sms, cudaStream_t st) {
-  return a.hq / a.hkv <= 16 ? launch_i4<2>(a, ws, sms, st) : launch_i4<4>(a, ws, sms, st);
+  return a.hq / a.hkv <= 8 ? launch_i4<1>(a, ws, sms, st) : launch_i4<2>(a, ws, sms, st);
 }
 
 }  // namespace pkv
