@@ -474,7 +474,7 @@ int pkv_write_int4(const void* k, int64_t k_row_stride, const void* v, int64_t v
 
 /*
  * pkv_read_int4 — cached tokens back as bf16 rows, for instance for a prefix that
- * moves to a bf16 cache: the cached values (s * code + z in fp32, rounded once) of
+ * moves to a bf16 cache: the cached values (s * code + z, rounded once) of
  * slot slots[t] go to k_out[t] and v_out[t], bf16 [n_tokens, num_kv_heads,
  * head_size] with row strides as in pkv_write.  A negative slot leaves its rows as
  * they were, one past the pool too (PKV_DEV_ERR_SLOT_RANGE); a slot may come
