@@ -547,7 +547,7 @@ int pkv_attention_int4(const void* q, int64_t q_row_stride, int64_t q_rows, int3
  * query_start_loc, seq_lens, block_table, num_reqs and their errors are
  * pkv_attention's; a block id outside the pool is reported and its page's score
  * unspecified.  The call keeps scores in a workspace of its own (20 bytes a
- * block-table entry, row and KV head, at most 336 MB or one row's), grown as the
+ * block-table entry, row and KV head, at most 340 MB or one row's), grown as the
  * other one is: call pkv_reserve_select before a capture.  As with the other
  * workspace, calls on one device must not overlap on the GPU.
  *

@@ -791,17 +791,21 @@ int check_rows4(const void* k, int64_t k_row_stride, const void* v, int64_t v_ro
   return PKV_OK;
 }
 
-// The workspace of pkv_select_pages: 20 bytes a page of `rows` rows and KV heads.  A
-// launch takes at most as many rows as 2^24 pages have, so that many rows over
-// wide tables need no more than 336 MB.  (A room that never shrinks with the
-// arguments: what is reserved for large ones serves smaller ones.)
+// The workspace of pkv_select_pages: a counter for each row of a launch and KV head (in
+// front), and 20 bytes a page of theirs.  A launch takes at most as
+// many rows as 2^24 pages, or 65535 (row, KV head)s, have, so that many rows over wide
+// tables need no more than 340 MB.  (Room that never shrinks with the arguments: what is
+// reserved for large ones serves smaller ones.)
+constexpr int64_t kSelectPairs = 65535;  // also the grid's limit
 struct SelectSizes {
   int64_t rows;  // of a launch
   size_t bytes;
 };
 SelectSizes select_sizes(int64_t q_rows, int64_t width, int hkv) {
   const int64_t per_row = width * hkv, most = std::max<int64_t>(per_row, int64_t(1) << 24);
-  return {std::min(q_rows, most / per_row), (size_t)std::min(q_rows * per_row, most) * 20};
+  const int64_t rows = std::min(most / per_row, kSelectPairs / hkv);
+  return {std::min(q_rows, rows), (size_t)std::min(q_rows * per_row, most) * 20 +
+                                      (size_t)(kSelectPairs + 1) * sizeof(int)};
 }
 
 }  // namespace
@@ -959,7 +963,8 @@ extern "C" int pkv_select_pages(const void* q, int64_t q_row_stride, int64_t q_r
                        st, &grown);
     if (rc) return rc;
     note_capture(&s->sel_in_graph, st);
-    uint8_t* p = static_cast<uint8_t*>(s->sel_ws);
+    a.done = static_cast<int*>(s->sel_ws);
+    uint8_t* p = static_cast<uint8_t*>(s->sel_ws) + (kSelectPairs + 1) * sizeof(int);
     const int64_t n = z.rows * num_kv_heads * block_table_width;
     a.exact = reinterpret_cast<double*>(p);
     a.scores = reinterpret_cast<float*>(p + n * 8);
@@ -970,10 +975,7 @@ extern "C" int pkv_select_pages(const void* q, int64_t q_row_stride, int64_t q_r
   }
   for (int64_t row0 = 0; row0 < q_rows; row0 += z.rows) {
     const int rows = (int)std::min(z.rows, q_rows - row0);
-    cudaError_t e = cudaSuccess;
-    if (score) e = traced(5, st, [&] { return launch_page_scores(a, row0, rows, s->sms, st); });
-    if (e == cudaSuccess)
-      e = traced(5, st, [&] { return launch_select(a, row0, rows, score, st); });
+    cudaError_t e = traced(5, st, [&] { return launch_select(a, row0, rows, score, st); });
     if (e != cudaSuccess) return cuda_fail(e, "pkv_select_pages launch");
   }
   return PKV_OK;

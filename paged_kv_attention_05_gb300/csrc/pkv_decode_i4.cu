@@ -53,10 +53,9 @@ constexpr float kMaxWeight = 16384.f;  // e_j t_j that the reference is kept for
 // its e_j is held below 2^54 by the same bound; scales of others are above it.
 constexpr float kMinScale = 0x1p-40f;
 
-// Instances: items of at most 8 * kTiles query rows, kPg pages of a step at a time.
+// Instances: items of at most 8 * kTiles query rows.
 template <int kTiles>
 struct Cfg4 {
-  static constexpr int kPg = 2;
   static constexpr int kWarps = kTiles == 1 ? 16 : 8;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kStages = 48 / kWarps;  // of two pages
@@ -112,7 +111,7 @@ struct Ring {
 
 // Query rows row0 .. of a unit (nrows of them in all), at most 8 * kT, two pages (32
 // keys) a step, kPg of them at a time.  Returns false when a wait gave up.
-template <int kT, int kPg = Cfg4<kT>::kPg>
+template <int kT, int kPg = 2>
 __device__ __forceinline__ bool run_unit(const AttnArgs& a, const Workspace& ws, const DecUnit& un,
                                          int row0, Ring& ring, uint64_t pol,
                                          volatile int* abort) {

@@ -156,22 +156,20 @@ struct SelectArgs {
   int budget, first, last;
   int32_t* sel_table;  // [q_rows][hkv][budget]
   int32_t* sel_lens;   // [q_rows]
-  // workspace, by (row of a launch, KV head): the pages' fp32 scores, the largest
-  // bound each scoring warp met, scores in 64 bits and the pages they belong to
-  float* scores;
-  float* largest;
+  // workspace, by (row of a launch, KV head): scores in 64 bits, the pages' fp32
+  // scores, the pages that the former belong to, the largest bound each CTA met, and
+  // the CTAs that are done (zero between calls)
   double* exact;
+  float* scores;
   int32_t* index;
+  float* largest;
+  int* done;
   int64_t largest_stride;
-  int chunk_pages;  // pages of a scoring warp
+  int chunk_pages;  // pages a CTA scores
   int* err;
 };
-// Pages a scoring warp takes.
 int select_chunk_pages(int64_t rows, int hkv, int64_t bt_width, int sms);
-// Rows row0 .. row0 + rows - 1: the scores (of calls in which a row can need them),
-// and the selection.
-cudaError_t launch_page_scores(const SelectArgs& a, int64_t row0, int rows, int sms,
-                               cudaStream_t st);
+// The lists of rows row0 .. row0 + rows - 1; score: some row can need its pages' scores.
 cudaError_t launch_select(const SelectArgs& a, int64_t row0, int rows, bool score,
                           cudaStream_t st);
 

@@ -92,14 +92,15 @@ __global__ void __launch_bounds__(256)
 
 // ------------------------------------------------------------------ selection
 
+constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32;
+constexpr int kSelKeys = 8192;  // scores of a (row, KV head) kept in shared memory
+
 struct Row {
   int r, pos;  // request (-1: the row belongs to no valid one), position
   int n;       // pages
 };
 
-// The PKV_DEV_ERR_* bits of request r.
-__device__ __forceinline__ int request_errors(const SelectArgs& a, int r) {
-  const int q0 = __ldcg(a.qsl + r), q1 = __ldcg(a.qsl + r + 1), L = __ldcg(a.seq_lens + r);
+__device__ __forceinline__ int meta_errors(const SelectArgs& a, int q0, int q1, int L) {
   if (q0 < 0 || q1 < q0 || (int64_t)q1 > a.q_rows) return PKV_DEV_ERR_QSL;
   if (L < 0 || L < q1 - q0) return PKV_DEV_ERR_SEQ_LEN;
   if (((int64_t)L + kBlockSize - 1) / kBlockSize > a.bt_width) return PKV_DEV_ERR_BT_WIDTH;
@@ -110,17 +111,17 @@ __device__ __forceinline__ int request_errors(const SelectArgs& a, int r) {
 // request: the guess r = row saves the search's chain of reads.)
 __device__ __forceinline__ Row find_row(const SelectArgs& a, int64_t row) {
   Row x{-1, 0, 0};
-  int lo = 0, hi = a.num_reqs - 1;
-  if (row < a.num_reqs) {
-    const int q0 = __ldcg(a.qsl + row), q1 = __ldcg(a.qsl + row + 1);
-    if (q0 <= row && row < q1) lo = hi = (int)row;
+  int lo = (int)min(row, (int64_t)a.num_reqs - 1);
+  int q0 = __ldcg(a.qsl + lo), q1 = __ldcg(a.qsl + lo + 1), L = __ldcg(a.seq_lens + lo);
+  if (!(q0 <= row && row < q1)) {
+    lo = 0;
+    for (int hi = a.num_reqs - 1; lo < hi;) {  // the last request that starts at or before it
+      const int mid = (lo + hi + 1) >> 1;
+      if (__ldcg(a.qsl + mid) <= row) lo = mid; else hi = mid - 1;
+    }
+    q0 = __ldcg(a.qsl + lo), q1 = __ldcg(a.qsl + lo + 1), L = __ldcg(a.seq_lens + lo);
   }
-  while (lo < hi) {  // the last request that starts at or before the row
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldcg(a.qsl + mid) <= row) lo = mid; else hi = mid - 1;
-  }
-  const int q0 = __ldcg(a.qsl + lo), q1 = __ldcg(a.qsl + lo + 1), L = __ldcg(a.seq_lens + lo);
-  if (row < q0 || row >= q1 || request_errors(a, lo)) return x;  // (or past the last request)
+  if (row < q0 || row >= q1 || meta_errors(a, q0, q1, L)) return x;  // (or past the last)
   x.r = lo;
   x.pos = L - (q1 - q0) + (int)(row - q0);
   x.n = x.pos / kBlockSize + 1;
@@ -129,105 +130,7 @@ __device__ __forceinline__ Row find_row(const SelectArgs& a, int64_t row) {
 
 __device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-
-// The fp32 scores of a row's pages for one KV head.  A warp takes kPages pages of a
-// (row, head); a half-warp reads one page's bounds (512 consecutive bytes), eight
-// dimensions a lane.  Bound by HBM: 512 bytes a page, a sixteenth of the page's
-// own keys and values.  Beside the scores each warp leaves the largest bound it
-// met, for eps.
-template <int kPages>
-__global__ void __launch_bounds__(256) page_scores_kernel(SelectArgs a, int64_t row0, int rows) {
-  grid_dep_wait();
-  grid_dep_launch();
-  const int lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
-  const int G = a.hq / a.hkv;
-  const int64_t chunks = (a.bt_width + kPages - 1) / kPages;
-  const int64_t units = (int64_t)rows * a.hkv * chunks;
-  const int64_t nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
-  for (int64_t u = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5; u < units; u += nwarps) {
-    // (chunk by chunk of all rows: the chunks that hold pages come first)
-    const int chunk = (int)(u / (rows * a.hkv));
-    const int rh = (int)(u - (int64_t)chunk * rows * a.hkv);
-    const int64_t row = row0 + rh / a.hkv;
-    const int g = rh % a.hkv;
-    const Row x = find_row(a, row);
-    const int from = chunk * kPages;
-    const int end = x.n - a.last;  // (the last pages are taken unseen)
-    if (x.r < 0 || x.n <= a.budget || from >= end) continue;
-    const int count = min(kPages, end - from);
-    float up[8], dn[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) up[i] = dn[i] = 0.f;
-    const uint16_t* q = a.q + row * a.q_stride + (int64_t)g * G * kHeadSize + l * 8;
-#pragma unroll 4
-    for (int h = 0; h < G; ++h) {
-      const uint4 w4 = __ldg(reinterpret_cast<const uint4*>(q + h * kHeadSize));
-      const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float v = i & 1 ? hi16(w[i >> 1]) : lo16(w[i >> 1]);
-        up[i] += fmaxf(v, 0.f);
-        dn[i] += fminf(v, 0.f);
-      }
-    }
-    const int32_t* bt = a.bt + (int64_t)x.r * a.bt_width + from;
-    float* out = a.scores + ((int64_t)rh * a.bt_width + from);
-    __nv_bfloat162 m2 = __float2bfloat162_rn(0.f);
-    for (int b = 0; b < count; b += 32) {
-      const int page = b + lane;
-      int id = page < count ? __ldg(bt + page) : 0;
-      if (id < 0 || (int64_t)id >= a.num_blocks) {
-        atomicOr(a.err, PKV_DEV_ERR_BLOCK_ID);
-        id = 0;
-      }
-      float mine = 0.f;  // the score of page b + lane
-      const int steps = min(16, (count - b + 1) / 2);
-#pragma unroll 4
-      for (int i = 0; i < steps; ++i) {
-        const int blk = __shfl_sync(0xffffffffu, id, 2 * i + half);
-        const uint16_t* p = a.bounds + ((int64_t)blk * a.hkv + g) * 2 * kHeadSize + l * 8;
-        const uint4 lo4 = __ldg(reinterpret_cast<const uint4*>(p));
-        const uint4 hi4 = __ldg(reinterpret_cast<const uint4*>(p + kHeadSize));
-        const uint32_t lo[4] = {lo4.x, lo4.y, lo4.z, lo4.w}, hi[4] = {hi4.x, hi4.y, hi4.z, hi4.w};
-        float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          s0 = fmaf(up[2 * k], lo16(hi[k]), s0);
-          s1 = fmaf(dn[2 * k], lo16(lo[k]), s1);
-          s0 = fmaf(up[2 * k + 1], hi16(hi[k]), s0);
-          s1 = fmaf(dn[2 * k + 1], hi16(lo[k]), s1);
-          m2 = __hmax2(m2, __hmax2(__habs2(*reinterpret_cast<const __nv_bfloat162*>(&lo[k])),
-                                   __habs2(*reinterpret_cast<const __nv_bfloat162*>(&hi[k]))));
-        }
-        float s = s0 + s1;
-#pragma unroll
-        for (int o = 1; o < 16; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        const float other = __shfl_xor_sync(0xffffffffu, s, 16);
-        // lanes 2 i and 2 i + 1 keep the two halves' scores
-        if (lane >> 1 == i) mine = ((lane & 1) == half) ? s : other;
-      }
-      if (page < count) out[page] = mine;
-    }
-    float m = fmaxf(__low2float(m2), __high2float(m2));
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) a.largest[(int64_t)rh * a.largest_stride + chunk] = m;
-  }
-}
-
-constexpr int kSelThreads = 256;
-
-// total over the block of one int per thread
-__device__ __forceinline__ int block_sum(int v, int* part) {
-  v = __reduce_add_sync(0xffffffffu, v);
-  __syncthreads();  // (part may still be read)
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-  __syncthreads();
-  int s = 0;
-#pragma unroll
-  for (int w = 0; w < kSelThreads / 32; ++w) s += part[w];
-  return s;
-}
+// fp32 and fp64 values as whole numbers of the same order
 __device__ __forceinline__ uint32_t ordered(float f) {
   const uint32_t u = __float_as_uint(f);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
@@ -239,182 +142,385 @@ __device__ __forceinline__ unsigned long long ordered64(double f) {
   const unsigned long long u = (unsigned long long)__double_as_longlong(f);
   return u >> 63 ? ~u : u | 1ull << 63;
 }
-// The k-th largest of n keys (1 <= k <= n), by its bits from the highest.
-template <typename Key, typename Get>
-__device__ Key kth_largest(int n, int k, int* part, Get get) {
-  Key t = 0;
-#pragma unroll 1
-  for (int bit = 8 * (int)sizeof(Key) - 1; bit >= 0; --bit) {
-    const Key c = t | (Key)1 << bit;
-    int more = 0;
-    for (int i = threadIdx.x; i < n; i += kSelThreads) more += get(i) >= c;
-    if (block_sum(more, part) >= k) t = c;
-  }
-  return t;
+
+// total over the block of one int per thread
+__device__ __forceinline__ int block_sum(int v, int* part) {
+  v = __reduce_add_sync(0xffffffffu, v);
+  __syncthreads();  // (part may still be read)
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  int s = 0;
+#pragma unroll
+  for (int w = 0; w < kSelWarps; ++w) s += part[w];
+  return s;
 }
 
-// A page's state in the selection (in place of its key).
-enum : uint32_t { kOut = 0, kTie = 1, kIn = 2 };
+// The fp32 scores of pages from .. from + count - 1 of a row for one KV head, by the
+// calling warp: put(page, score) for each; returns the largest bound met (in every
+// lane).  A half-warp reads one page's bounds (512 consecutive bytes), eight dimensions
+// a lane.
+template <typename Put>
+__device__ __forceinline__ float score_pages(const SelectArgs& a, const int32_t* bt, int g,
+                                             int from, int count, const float (&up)[8],
+                                             const float (&dn)[8], Put put) {
+  const int lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
+  __nv_bfloat162 m2 = __float2bfloat162_rn(0.f);
+  for (int b = 0; b < count; b += 32) {
+    const int page = b + lane;
+    int id = page < count ? __ldg(bt + from + page) : 0;
+    if (id < 0 || (int64_t)id >= a.num_blocks) {
+      atomicOr(a.err, PKV_DEV_ERR_BLOCK_ID);
+      id = 0;
+    }
+    float mine = 0.f;  // the score of page b + lane
+    const int steps = min(16, (count - b + 1) / 2);
+#pragma unroll 8
+    for (int i = 0; i < steps; ++i) {
+      const int blk = __shfl_sync(0xffffffffu, id, 2 * i + half);
+      const uint16_t* p = a.bounds + ((int64_t)blk * a.hkv + g) * 2 * kHeadSize + l * 8;
+      const uint4 lo4 = __ldg(reinterpret_cast<const uint4*>(p));
+      const uint4 hi4 = __ldg(reinterpret_cast<const uint4*>(p + kHeadSize));
+      const uint32_t lo[4] = {lo4.x, lo4.y, lo4.z, lo4.w}, hi[4] = {hi4.x, hi4.y, hi4.z, hi4.w};
+      float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        s0 = fmaf(up[2 * k], lo16(hi[k]), s0);
+        s1 = fmaf(dn[2 * k], lo16(lo[k]), s1);
+        s0 = fmaf(up[2 * k + 1], hi16(hi[k]), s0);
+        s1 = fmaf(dn[2 * k + 1], hi16(lo[k]), s1);
+        m2 = __hmax2(m2, __hmax2(__habs2(*reinterpret_cast<const __nv_bfloat162*>(&lo[k])),
+                                 __habs2(*reinterpret_cast<const __nv_bfloat162*>(&hi[k]))));
+      }
+      float s = s0 + s1;
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      const float other = __shfl_xor_sync(0xffffffffu, s, 16);
+      // lanes 2 i and 2 i + 1 keep the two halves' scores
+      if (lane >> 1 == i) mine = ((lane & 1) == half) ? s : other;
+    }
+    if (page < count) put(from + page, mine);
+  }
+  float m = fmaxf(__low2float(m2), __high2float(m2));
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
 
-// The pages of one (row, KV head): a CTA each.  The keys sit in shared memory; the
-// k-th largest is found bit by bit (a count of the block for each).
-__global__ void __launch_bounds__(kSelThreads) select_pages_kernel(SelectArgs a, int64_t row0) {
-  extern __shared__ uint32_t keys[];  // [bt_width] in calls that score
-  __shared__ int part[kSelThreads / 32];
-  __shared__ float s_max[kSelThreads / 32];
-  grid_dep_wait();
+// Scores and selection.  A CTA scores kPages pages of a (row, KV head), its warps an
+// eighth each; the last CTA of the (row, KV head) to finish selects.  Where one CTA has
+// all of its pages the scores never leave it.
+// Bound by HBM while it scores (512 bytes a page, a sixteenth of the page's own keys
+// and values), by a chain of block-wide counts while it selects.
+template <int kPages>
+__global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a, int64_t row0) {
+  extern __shared__ uint32_t keys[];  // [min(bt_width, kSelKeys)] in calls that score
+  __shared__ int part[kSelWarps], part2[kSelWarps];
+  __shared__ int hist[kSelThreads];
+  __shared__ float s_max[kSelWarps], s_sum[kSelWarps];
+  __shared__ int s_last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rh = blockIdx.x;
+  const int rh = blockIdx.y, chunk = blockIdx.x;
   const int64_t row = row0 + rh / a.hkv;
   const int g = rh % a.hkv, G = a.hq / a.hkv;
-  if (blockIdx.x == 0 && row0 == 0)
-    for (int r = tid; r < a.num_reqs; r += kSelThreads)
-      if (const int bad = request_errors(a, r)) atomicOr(a.err, bad);
+  grid_dep_wait();
+  // U and D, eight dimensions a lane (asked for beside the metadata)
+  const uint16_t* q = a.q + row * a.q_stride + (int64_t)g * G * kHeadSize;
+  float up[8], dn[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) up[i] = dn[i] = 0.f;
+#pragma unroll 4
+  for (int h = 0; h < G; ++h) {
+    const uint4 w4 = __ldg(reinterpret_cast<const uint4*>(q + h * kHeadSize + (lane & 15) * 8));
+    const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float v = i & 1 ? hi16(w[i >> 1]) : lo16(w[i >> 1]);
+      up[i] += fmaxf(v, 0.f);
+      dn[i] += fminf(v, 0.f);
+    }
+  }
+  if (chunk == 0 && rh == 0 && row0 == 0)
+    for (int r = tid; r < a.num_reqs; r += kSelThreads) {
+      const int bad = meta_errors(a, __ldcg(a.qsl + r), __ldcg(a.qsl + r + 1), __ldcg(a.seq_lens + r));
+      if (bad) atomicOr(a.err, bad);
+    }
   const Row x = find_row(a, row);
-  if (x.r < 0) {
-    if (tid == 0 && g == 0) a.sel_lens[row] = 0;
+  const int n = x.n;
+  if (x.r < 0 || n <= a.budget || a.budget == a.first + a.last) {
+    // nothing to score: no list, or all pages, or the first and last ones
+    if (chunk > 0) return;
+    const int taken = min(n, a.budget);
+    if (tid == 0 && g == 0)
+      a.sel_lens[row] = x.r < 0 ? 0 : (taken - 1) * kBlockSize + x.pos % kBlockSize + 1;
+    if (x.r < 0) return;
+    int32_t* out = a.sel_table + (row * a.hkv + g) * (int64_t)a.budget;
+    const int32_t* bt = a.bt + (int64_t)x.r * a.bt_width;
+    for (int i = tid; i < a.budget; i += kSelThreads)
+      out[i] = i >= taken ? -1 : __ldg(bt + (n <= a.budget || i < a.first ? i : n - taken + i));
     return;
   }
-  const int n = x.n, taken = min(n, a.budget);
-  int32_t* out = a.sel_table + (row * a.hkv + g) * (int64_t)a.budget;
+  const int end = n - a.last;  // (the last pages are taken unseen)
+  const int needed = (end + kPages - 1) / kPages;
+  if (chunk >= needed) return;
   const int32_t* bt = a.bt + (int64_t)x.r * a.bt_width;
-  if (tid == 0 && g == 0) a.sel_lens[row] = (taken - 1) * kBlockSize + x.pos % kBlockSize + 1;
-  for (int i = taken + tid; i < a.budget; i += kSelThreads) out[i] = -1;
-  if (n <= a.budget) {
-    for (int i = tid; i < n; i += kSelThreads) out[i] = __ldg(bt + i);
+  float* scores = a.scores + (int64_t)rh * a.bt_width;
+  const int first = a.first, mid = end - first, k = a.budget - first - a.last;
+  const bool in_smem = mid <= kSelKeys;
+
+  float m = 0.f, size = 0.f;  // largest bound of the row's pages; sum of |q|
+  {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) size += up[i] - dn[i];
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) size += __shfl_xor_sync(0xffffffffu, size, o);
+    const int from = chunk * kPages + warp * (kPages / kSelWarps);
+    const int count = min(kPages / kSelWarps, end - from);
+    if (count > 0)
+      m = score_pages(a, bt, g, from, count, up, dn, [&](int page, float s) {
+        if (needed > 1)
+          scores[page] = s;
+        else if (page >= first)
+          keys[page - first] = ordered(s);
+      });
+    if (lane == 0) s_max[warp] = m;
+  }
+  __syncthreads();
+  m = 0.f;
+#pragma unroll
+  for (int w = 0; w < kSelWarps; ++w) m = fmaxf(m, s_max[w]);
+  if (needed > 1) {
+    // (counted by atomics in no order that matters: whoever comes last selects)
+    if (tid == 0) {
+      a.largest[(int64_t)rh * a.largest_stride + chunk] = m;
+      __threadfence();
+      s_last = atomicAdd(a.done + rh, 1) == needed - 1;
+      if (s_last) a.done[rh] = 0;  // for the next call
+      __threadfence();
+    }
+    __syncthreads();
+    if (!s_last) return;
+    m = 0.f;
+    for (int i = tid; i < needed; i += kSelThreads)
+      m = fmaxf(m, __ldcg(a.largest + (int64_t)rh * a.largest_stride + i));
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) s_sum[warp] = m;
+    if (in_smem)
+      for (int i = tid; i < mid; i += kSelThreads) keys[i] = ordered(__ldcg(scores + first + i));
+    __syncthreads();
+    m = 0.f;
+#pragma unroll
+    for (int w = 0; w < kSelWarps; ++w) m = fmaxf(m, s_sum[w]);
+  }
+  // Each thread has `own` consecutive pages (an odd number: neighbouring threads meet
+  // different banks).
+  const int own = ((mid + kSelThreads - 1) / kSelThreads) | 1;
+  const int i0 = min(tid * own, mid), i1 = min(i0 + own, mid);
+  auto key_of = [&](int i) { return in_smem ? keys[i] : ordered(__ldcg(scores + first + i)); };
+  // (a little more than (G + 16) 2^-24, for the roundings of S itself, and what
+  // products below fp32's range lose)
+  const float eps = (float)(G + 18) * 0x1p-24f * size * m + 0x1p-140f;
+
+  // The k-th largest key, eight bits a step from the highest that differs, until what is
+  // left of it is below eps: it lies in t .. t + 2^bits - 1.
+  uint32_t t;
+  int bits, left = k;  // keys still to be counted from above within the prefix
+  {
+    uint32_t lo = 0xFFFFFFFFu, hi = 0;
+#pragma unroll 4
+    for (int i = i0; i < i1; ++i) {
+      const uint32_t v = key_of(i);
+      lo = min(lo, v);
+      hi = max(hi, v);
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) {
+      part[warp] = (int)lo;
+      part2[warp] = (int)hi;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kSelWarps; ++w) {
+      lo = min(lo, (uint32_t)part[w]);
+      hi = max(hi, (uint32_t)part2[w]);
+    }
+    bits = 32 - __clz(lo ^ hi);
+    t = bits >= 32 ? 0 : hi & ~((1u << bits) - 1);
+  }
+  while (bits > 0 && !(unordered(t + (uint32_t)((1ull << bits) - 1)) - unordered(t) <= eps)) {
+    const int shift = max(bits - 8, 0);
+    hist[tid] = 0;
+    __syncthreads();
+#pragma unroll 4
+    for (int i = i0; i < i1; ++i) {
+      const uint32_t d = key_of(i) - t;  // (keys below t wrap far up)
+      if (bits >= 32 || d >> bits == 0) atomicAdd(hist + (d >> shift), 1);
+    }
+    __syncthreads();
+    // thread i: bin 255 - i and the bins above it
+    const int mine = hist[kSelThreads - 1 - tid];
+    int sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    if (lane == 31) part[warp] = sum;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kSelWarps; ++w) sum += w < warp ? part[w] : 0;
+    if (sum >= left && sum - mine < left) {
+      part2[0] = kSelThreads - 1 - tid;
+      part2[1] = left - (sum - mine);
+    }
+    __syncthreads();
+    t += (uint32_t)part2[0] << shift;
+    left = part2[1];
+    bits = shift;
+  }
+  const float above = unordered(t + (uint32_t)((1ull << bits) - 1)) + 2.f * eps;
+  const float below = unordered(t) - 2.f * eps;
+  // kIn and kOut for certain, kTie: between
+  enum { kOut, kTie, kIn };
+  auto state_of = [&](int i) {
+    const float e = unordered(key_of(i));
+    return e > above ? kIn : e < below ? kOut : kTie;
+  };
+  // exclusive sums over the block of a thread's count, two in a word; *total for all
+  auto scan = [&](unsigned v, unsigned* total) {
+    unsigned s = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned u = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += u;
+    }
+    __syncthreads();  // (part may still be read)
+    if (lane == 31) part[warp] = (int)s;
+    __syncthreads();
+    unsigned before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kSelWarps; ++w) {
+      if (w < warp) before += (unsigned)part[w];
+      all += (unsigned)part[w];
+    }
+    *total = all;
+    return before + s - v;
+  };
+  unsigned total;
+  unsigned mine = 0;  // of this thread's pages: certain ones << 16 | those between
+#pragma unroll 4
+  for (int i = i0; i < i1; ++i) {
+    const int st = state_of(i);
+    mine += st == kIn ? 0x10000u : st == kTie ? 1u : 0u;
+  }
+  const unsigned before = scan(mine, &total);
+  int ties = k - (int)(total >> 16);  // of the pages between, how many are taken
+  const int cand = (int)(total & 0xFFFF);
+  if (tid == 0 && g == 0) a.sel_lens[row] = (a.budget - 1) * kBlockSize + x.pos % kBlockSize + 1;
+  int32_t* out = a.sel_table + (row * a.hkv + g) * (int64_t)a.budget;
+  for (int i = tid; i < first; i += kSelThreads) out[i] = __ldg(bt + i);
+  for (int i = tid; i < a.last; i += kSelThreads) out[a.budget - a.last + i] = __ldg(bt + end + i);
+  out += first;
+  if (cand <= ties || size == 0.f || m == 0.f) {
+    // all of those between, or (every score zero, exactly) the first of them
+    int in = (int)(before >> 16), tie = (int)(before & 0xFFFF);
+    for (int i = i0; i < i1; ++i) {
+      const int st = state_of(i);
+      if (st == kIn || (st == kTie && tie < ties)) out[in + min(tie, ties)] = __ldg(bt + first + i);
+      in += st == kIn;
+      tie += st == kTie;
+    }
     return;
   }
-  const int first = a.first, mid = n - a.first - a.last, k = a.budget - a.first - a.last;
-  int ties = 0;  // of the pages in state kTie, the first `ties` are taken
-  if (k > 0) {
-    const float* sc = a.scores + (int64_t)rh * a.bt_width + first;
-    for (int i = tid; i < mid; i += kSelThreads) keys[i] = ordered(__ldcg(sc + i));
-    // eps
-    const uint16_t* q = a.q + row * a.q_stride + (int64_t)g * G * kHeadSize;
-    float m = 0.f, s = 0.f;
-    const int chunks = (n - a.last + a.chunk_pages - 1) / a.chunk_pages;
-    for (int i = tid; i < chunks; i += kSelThreads)
-      m = fmaxf(m, __ldcg(a.largest + (int64_t)rh * a.largest_stride + i));
-    for (int i = tid; i < G * kHeadSize / 2; i += kSelThreads) {
-      const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(q) + i);
-      s += fabsf(lo16(w)) + fabsf(hi16(w));
-    }
-    for (int o = 16; o > 0; o >>= 1) {
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      s += __shfl_xor_sync(0xffffffffu, s, o);
-    }
-    __shared__ float s_sum[kSelThreads / 32];
-    if (lane == 0) {
-      s_max[warp] = m;
-      s_sum[warp] = s;
-    }
+
+  // More pages between than places: their scores in 64 bits, in the order of the pages.
+  double* s64 = a.exact + (int64_t)rh * a.bt_width;
+  {
+    int32_t* idx = a.index + (int64_t)rh * a.bt_width;
+    int at = (int)(before & 0xFFFF);
+    for (int i = i0; i < i1; ++i)
+      if (state_of(i) == kTie) idx[at++] = i;
     __syncthreads();
-    m = s = 0.f;
-    for (int w = 0; w < kSelThreads / 32; ++w) {
-      m = fmaxf(m, s_max[w]);
-      s += s_sum[w];
-    }
-    // (a little more than (G + 16) 2^-24, for the roundings of S itself, and what
-    // products below fp32's range lose)
-    const float eps = (float)(G + 18) * 0x1p-24f * s * m + 0x1p-140f;
-    const uint32_t t = kth_largest<uint32_t>(mid, k, part, [&](int i) { return keys[i]; });
-    const float tf = unordered(t);
-    const float above = tf + 2.f * eps, below = tf - 2.f * eps;
-    int in = 0, cand = 0;
-    __syncthreads();
-    for (int i = tid; i < mid; i += kSelThreads) {
-      const float e = unordered(keys[i]);
-      const uint32_t st = e > above ? kIn : e < below ? kOut : kTie;
-      in += st == kIn;
-      cand += st == kTie;
-      keys[i] = st;
-    }
-    in = block_sum(in, part);
-    cand = block_sum(cand, part);
-    ties = k - in;
-    if (cand > ties && s != 0.f && m != 0.f) {  // (else every score is zero, exactly)
-      // more pages about the border than places: their scores in 64 bits
-      double* s64 = a.exact + (int64_t)rh * a.bt_width;
-      int32_t* idx = a.index + (int64_t)rh * a.bt_width;
-      int at = 0;
-      for (int b = 0; b < mid; b += kSelThreads) {  // their indices, in order
-        const int i = b + tid;
-        const bool c = i < mid && keys[i] == kTie;
-        const uint32_t bal = __ballot_sync(0xffffffffu, c);
-        __syncthreads();
-        if (lane == 0) part[warp] = __popc(bal);
-        __syncthreads();
-        int before = at, all = at;
-        for (int w = 0; w < kSelThreads / 32; ++w) {
-          if (w < warp) before += part[w];
-          all += part[w];
-        }
-        if (c) idx[before + __popc(bal & ((1u << lane) - 1))] = i;
-        at = all;
-      }
-      __syncthreads();
-      double up[4] = {}, dn[4] = {};
+    if (warp < cand) {
+      double du[4] = {}, dd[4] = {};
       for (int h = 0; h < G; ++h) {
         const uint2 w = __ldg(reinterpret_cast<const uint2*>(q + h * kHeadSize + lane * 4));
         const float v[4] = {lo16(w.x), hi16(w.x), lo16(w.y), hi16(w.y)};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          up[i] += fmaxf(v[i], 0.f);
-          dn[i] += fminf(v[i], 0.f);
-        }
+        for (int i = 0; i < 4; ++i) (v[i] > 0.f ? du[i] : dd[i]) += v[i];
       }
-      for (int c = warp; c < cand; c += kSelThreads / 32) {
+      for (int c = warp; c < cand; c += kSelWarps) {
         const int id = __ldg(bt + first + idx[c]);
         const int64_t blk = id < 0 || (int64_t)id >= a.num_blocks ? 0 : id;
         const uint16_t* p = a.bounds + (blk * a.hkv + g) * 2 * kHeadSize + lane * 4;
         const uint2 lo = __ldg(reinterpret_cast<const uint2*>(p));
         const uint2 hi = __ldg(reinterpret_cast<const uint2*>(p + kHeadSize));
-        double s = up[0] * lo16(hi.x) + up[1] * hi16(hi.x) + up[2] * lo16(hi.y) + up[3] * hi16(hi.y);
-        s += dn[0] * lo16(lo.x) + dn[1] * hi16(lo.x) + dn[2] * lo16(lo.y) + dn[3] * hi16(lo.y);
+        double s = du[0] * lo16(hi.x) + du[1] * hi16(hi.x) + du[2] * lo16(hi.y) + du[3] * hi16(hi.y);
+        s += dd[0] * lo16(lo.x) + dd[1] * hi16(lo.x) + dd[2] * lo16(lo.y) + dd[3] * hi16(lo.y);
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         if (lane == 0) s64[c] = s + 0.0;  // (-0 as 0)
       }
-      __syncthreads();
-      const unsigned long long t64 = kth_largest<unsigned long long>(
-          cand, ties, part, [&](int i) { return ordered64(s64[i]); });
-      int more = 0;
-      __syncthreads();
-      for (int c = tid; c < cand; c += kSelThreads) {
-        const unsigned long long v = ordered64(s64[c]);
-        keys[idx[c]] = v > t64 ? kIn : v == t64 ? kTie : kOut;
-        more += v > t64;
-      }
-      ties -= block_sum(more, part);
     }
     __syncthreads();
   }
-  // the taken pages in their order
-  int at = 0, tied = 0;
-  for (int b = 0; b < n; b += kSelThreads) {
-    const int i = b + tid, j = i - first;
-    uint32_t st = kOut;
-    if (i < n) st = j < 0 || j >= mid ? kIn : k > 0 ? keys[j] : kOut;
-    const uint32_t bt_ = __ballot_sync(0xffffffffu, st == kTie);
-    const uint32_t bi = __ballot_sync(0xffffffffu, st == kIn);
-    __syncthreads();
-    if (lane == 0) part[warp] = __popc(bt_) << 16 | __popc(bi);
-    __syncthreads();
-    int tb = tied, ib = 0, ta = tied, ia = 0;
-    for (int w = 0; w < kSelThreads / 32; ++w) {
-      if (w < warp) {
-        tb += part[w] >> 16;
-        ib += part[w] & 0xFFFF;
-      }
-      ta += part[w] >> 16;
-      ia += part[w] & 0xFFFF;
+  // A candidate's rank: those with a larger score, or an equal one and before it.  Up to
+  // 256 of them by comparing each with all; more by the ties-th largest, bit by bit.
+  unsigned long long t64 = 0;
+  if (cand > kSelThreads) {
+#pragma unroll 1
+    for (int bit = 63; bit >= 0; --bit) {
+      const unsigned long long c = t64 | 1ull << bit;
+      int more = 0;
+      for (int i = tid; i < cand; i += kSelThreads) more += ordered64(s64[i]) >= c;
+      if (block_sum(more, part) >= ties) t64 = c;
     }
-    // ties before this page, and so how many of them are taken
-    const uint32_t below = (1u << lane) - 1;
-    const int t = tb + __popc(bt_ & below);
-    const int place = at + ib + __popc(bi & below) + min(t, ties) - min(tied, ties);
-    if (st == kIn || (st == kTie && t < ties)) out[place] = __ldg(bt + i);
-    at += ia + min(ta, ties) - min(tied, ties);
-    tied = ta;
+    int more = 0;
+    for (int i = tid; i < cand; i += kSelThreads) more += ordered64(s64[i]) > t64;
+    ties -= block_sum(more, part);  // of the equal ones, the first
+  }
+  auto taken = [&](int c, int equal) {  // candidate c; equal: candidates at t64 before it
+    const unsigned long long v = ordered64(s64[c]);
+    if (cand > kSelThreads) return v > t64 || (v == t64 && equal < ties);
+    int rank = 0;
+    for (int i = 0; i < cand; ++i) {
+      const unsigned long long u = ordered64(s64[i]);
+      rank += u > v || (u == v && i < c);
+    }
+    return rank < ties;
+  };
+  // equal ones before this thread's pages, then taken ones
+  unsigned equal = 0;
+  int c = (int)(before & 0xFFFF);
+  if (cand > kSelThreads) {
+    for (int i = i0; i < i1; ++i)
+      if (state_of(i) == kTie) equal += ordered64(s64[c++]) == t64;
+    equal = scan(equal, &total);
+  }
+  unsigned count = 0, e = equal;
+  c = (int)(before & 0xFFFF);
+  for (int i = i0; i < i1; ++i) {
+    const int st = state_of(i);
+    if (st == kTie) {
+      count += taken(c, (int)e);
+      e += cand > kSelThreads && ordered64(s64[c]) == t64;
+      ++c;
+    } else {
+      count += st == kIn;
+    }
+  }
+  int at = (int)scan(count, &total);
+  c = (int)(before & 0xFFFF);
+  e = equal;
+  for (int i = i0; i < i1; ++i) {
+    const int st = state_of(i);
+    bool in = st == kIn;
+    if (st == kTie) {
+      in = taken(c, (int)e);
+      e += cand > kSelThreads && ordered64(s64[c]) == t64;
+      ++c;
+    }
+    if (in) out[at++] = __ldg(bt + first + i);
   }
 }
 
@@ -431,25 +537,18 @@ cudaError_t launch_page_bounds(const uint16_t* kc, int64_t num_blocks, int hkv, 
                           n_tokens, err);
 }
 
+// Pages a CTA scores: 128 where that gives every SM a CTA, else 32.
 int select_chunk_pages(int64_t rows, int hkv, int64_t bt_width, int sms) {
-  return rows * hkv * bt_width >= (int64_t)sms * 32 * 128 ? 128 : 32;
-}
-
-cudaError_t launch_page_scores(const SelectArgs& a, int64_t row0, int rows, int sms,
-                               cudaStream_t st) {
-  const int64_t chunks = (a.bt_width + a.chunk_pages - 1) / a.chunk_pages;
-  const int64_t warps = (int64_t)rows * a.hkv * chunks;
-  const unsigned blocks = (unsigned)std::min<int64_t>((warps + 7) / 8, (int64_t)sms * 8);
-  return launch_dependent(a.chunk_pages == 128 ? page_scores_kernel<128> : page_scores_kernel<32>,
-                          dim3(blocks), dim3(256), 0, st, a, row0, rows);
+  return rows * hkv * bt_width >= (int64_t)sms * 128 ? 128 : 32;
 }
 
 cudaError_t launch_select(const SelectArgs& a, int64_t row0, int rows, bool score,
                           cudaStream_t st) {
-  static std::atomic<bool> attr[kMaxAttrDevices];
-  if (cudaError_t e = smem_attr_once(select_pages_kernel, kMaxBtWidth * 4, attr)) return e;
-  return launch_dependent(select_pages_kernel, dim3((unsigned)(rows * a.hkv)), dim3(kSelThreads),
-                          score ? (size_t)a.bt_width * 4 : 0, st, a, row0);
+  const int64_t chunks = score ? (a.bt_width + a.chunk_pages - 1) / a.chunk_pages : 1;
+  const size_t smem = score ? (size_t)std::min<int64_t>(a.bt_width, kSelKeys) * 4 : 0;
+  return launch_dependent(a.chunk_pages == 128 ? select_kernel<128> : select_kernel<32>,
+                          dim3((unsigned)chunks, (unsigned)(rows * a.hkv)), dim3(kSelThreads), smem,
+                          st, a, row0);
 }
 
 }  // namespace pkv
