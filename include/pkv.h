@@ -23,14 +23,14 @@
  *     refinement: the step plan of the attention calls and of pkv_plan reads
  *     query_start_loc and seq_lens (and prefix_lens) as soon as its kernel
  *     starts, which is after the kernel before it on the stream has finished,
- *     or, when that kernel is a cache write's (pkv_write*), another plan's or
- *     the last of a pkv_attention_scored call's, after everything enqueued
- *     before the run of such calls that it ends (they write none of the
- *     three): so enqueue the metadata before the write (as a step does), or
- *     from a kernel launched without programmatic serialisation.  Within a
- *     bf16 attention call that has prefill work, the decode kernel leaves
- *     some SMs to the prefill kernel, whose items run there beside the decode
- *     units.
+ *     or, when that kernel is a cache write's (pkv_write*), pkv_read_int4's,
+ *     pkv_page_bounds', another plan's or the last of a pkv_attention_scored
+ *     call's, after everything enqueued before the run of such calls that it
+ *     ends (they write none of the three): so enqueue the metadata before the
+ *     write (as a step does), or from a kernel launched without programmatic
+ *     serialisation.  Within a bf16 or int4 attention call that has prefill
+ *     work, the decode kernel leaves some SMs to the prefill kernel, whose
+ *     items run there beside the decode units.
  *   - The caller owns every buffer it passes; the library keeps no pointer to
  *     any of them after the call returns.  The library owns one grow-only
  *     device workspace per device (step plan, split-KV partial results and

@@ -1027,7 +1027,9 @@ extern "C" int pkv_reserve_workspace(int32_t max_reqs, int64_t max_q_rows,
   if (rc) return rc;
   Workspace ws;
   const int group = num_heads / num_kv_heads;
-  const int workers = std::max(decode_workers(group, 0, s->sms), decode_workers(group, 1, s->sms));
+  const int workers = std::max({decode_workers(group, kBf16, s->sms),
+                                decode_workers(group, kInt8, s->sms),
+                                decode_workers(group, kInt4, s->sms)});
   return ensure_workspace(s, with_wave_room(sizes_for(max_reqs, max_q_rows, block_table_width,
                                                       num_heads, num_kv_heads),
                                             max_q_rows, group, workers),
@@ -1044,11 +1046,11 @@ extern "C" int pkv_workspace_size(int32_t max_reqs, int64_t max_q_rows,
       num_heads <= 0 || num_heads % num_kv_heads || num_sms <= 0)
     return fail(PKV_ERR_ARG, "bad sizes");
   const int group = num_heads / num_kv_heads;
-  const int w16 = decode_workers(group, 0, num_sms), w8 = decode_workers(group, 1, num_sms);
-  // what pkv_reserve_workspace holds: room for both cache types' plans
+  const int w16 = decode_workers(group, kBf16, num_sms), w8 = decode_workers(group, kInt8, num_sms);
+  // what pkv_reserve_workspace holds: room for the plans of every cache type
   const Sizes z = with_wave_room(
       sizes_for(max_reqs, max_q_rows, block_table_width, num_heads, num_kv_heads), max_q_rows,
-      group, std::max(w16, w8));
+      group, std::max({w16, w8, decode_workers(group, kInt4, num_sms)}));
   info->bytes = (int64_t)workspace_bytes(z);
   info->decode_units = z.units;
   info->prefill_tiles = z.pre;

@@ -483,7 +483,9 @@ __global__ void __launch_bounds__(Cfg4<kTiles>::kThreads, 1)
   // the set-up above overlaps the plan kernel; the work list is read after it
   grid_dep_wait();
   grid_dep_launch();
-  if (leaves_sm_to_prefill(a, ws, C::kWarps >> shift) || ws.hdr->n_dec_units == 0) return;
+  if ((int)blockIdx.x < sms_to_prefill<false, true>(a, ws, C::kWarps >> shift) ||
+      ws.hdr->n_dec_units == 0)
+    return;
   __syncthreads();
   const int n_items = ws.hdr->n_dec_units << shift;
   const uint64_t pol = l2_evict_first();  // pages are read once (or twice at a time)

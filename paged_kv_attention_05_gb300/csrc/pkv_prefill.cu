@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(kI4 ? kThreadsI4 : threads_of(kCap == kFixedCa
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.hq / a.hkv;
   // two heads of one KV head per item
-  const bool pairs = (G % 2) == 0 && !(kScored && single_head_items(a, n_pre, gridDim.x));
+  const bool pairs = (G % 2) == 0 && !((kScored || kI4) && single_head_items(a, n_pre, gridDim.x));
   const int per_entry = pairs ? a.hq / 2 : a.hq;
 
   if (tid == 0) {
@@ -1275,8 +1275,10 @@ __global__ void __launch_bounds__(kI4 ? kThreadsI4 : threads_of(kCap == kFixedCa
           }
           tc_fence_after();
           const int2 te = *reinterpret_cast<const int2*>(smem + kOffTileExp + 8 * (tile_cnt & 3));
-          const float f =
-              sl2 * pow2(te.x) * reinterpret_cast<const float*>(smem + qfac_offset(it_cnt, x))[row];
+          // (never 0, so that a masked -inf stays one: zero rows have the smallest factors)
+          const float f = fmaxf(
+              sl2 * pow2(te.x) * reinterpret_cast<const float*>(smem + qfac_offset(it_cnt, x))[row],
+              0x1p-126f);
           float o_alpha = j > 0 ? pow2(max(vexp - te.y, -126)) : 1.f;
           vexp = te.y;
 #pragma unroll 1

@@ -33,11 +33,11 @@ namespace dev {
 // Every CTA computes the same from the plan header (read after the plan
 // wait): P, 0 without prefill items.
 constexpr int kTilesPerStep = 320;
-template <bool kScored>
+template <bool kScored, bool kSingle = kScored>  // kSingle: items may be single heads
 __device__ __forceinline__ int sms_to_prefill(const AttnArgs& a, const Workspace& ws,
                                               int units_per_cta) {
   const int G = a.hq / a.hkv;
-  const bool single = kScored && single_head_items(a, ws.hdr->n_pre_entries, gridDim.x);
+  const bool single = kSingle && single_head_items(a, ws.hdr->n_pre_entries, gridDim.x);
   const int per_entry = G % 2 == 0 && !single ? a.hq / 2 : a.hq;  // items per entry
   const int items = ws.hdr->n_pre_entries * per_entry;
   if (items == 0) return 0;

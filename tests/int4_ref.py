@@ -91,16 +91,17 @@ def attention(q, cache, qsl, seq_lens, block_table, scale):
             for h in range(g * G, (g + 1) * G):
                 qd = q[a:b, h].double()
                 x = (qd @ k.T * scale).masked_fill(hidden, -torch.inf)
+                size = abs(scale)
                 p = torch.softmax(x, -1)
                 o = p @ v
                 av = p @ v.abs()
                 if prefill:
-                    dx = scale * (2.0 ** -11 * (qd.abs() @ k.abs().T) + 2.0 ** -18 * k.abs().max() *
+                    dx = size * (2.0 ** -11 * (qd.abs() @ k.abs().T) + 2.0 ** -18 * k.abs().max() *
                                   qd.abs().sum(-1, keepdim=True))
                     t = 2 * 2.0 ** -11 * av + 2.0 ** -18 * v.abs().max() + \
                         2.0 ** -24 * L * p.amax(-1, keepdim=True) * v.abs().amax(0)
                 else:
-                    dx = 2.0 ** -17 * scale * (qd.abs() @ (kc * ks[:, None]).T +
+                    dx = 2.0 ** -17 * size * (qd.abs() @ (kc * ks[:, None]).T +
                                                qd.abs().sum(-1, keepdim=True) * kz.abs())
                     w = p * vs
                     t = 2.0 ** -11 * (w @ vc) + \

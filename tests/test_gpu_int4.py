@@ -226,7 +226,7 @@ def test_many_short_requests():
 @pytest.mark.parametrize("hq,hkv", [(16, 4), (32, 1)])
 @pytest.mark.parametrize("kind", ["value rows of all sizes", "one huge value row", "sharp scores",
                                   "constant rows", "large queries", "tiny queries", "zero queries",
-                                  "offset rows"])
+                                  "offset rows", "all zero", "tiny everything"])
 def test_ranges(hq, hkv, kind):
     s = Step([(1500, 1), (70, 1), (0, 1), (700, 150 if hkv == 4 else 1), (33, 2 if hkv == 4 else 1)],
              hq, hkv, 4242)
@@ -249,6 +249,12 @@ def test_ranges(hq, hkv, kind):
         s.q *= 2.0 ** -40
     elif kind == "zero queries":
         s.q.zero_()
+    elif kind == "all zero":
+        s.q.zero_(), s.k.zero_(), s.v.zero_()
+    elif kind == "tiny everything":
+        s.q *= 2.0 ** -60
+        s.k *= 2.0 ** -30
+        s.v *= 2.0 ** -30
     elif kind == "offset rows":
         s.k += 4
         s.v -= 3
@@ -331,6 +337,49 @@ def test_strides_streams_and_graphs():
         torch.cuda.synchronize()
         assert torch.equal(s.out[:s.rows], want[:s.rows])
     assert pkv.pkv_get_error() == 0
+
+
+@pytest.mark.parametrize("scale", [-0.11, 0.0, 1.0])
+def test_scales(scale):
+    s = Step([(700, 1), (1500, 2), (0, 200), (300, 140)], 8, 2, 77)
+    s.scale = scale
+    s.write()
+    s.attention()
+    assert pkv.pkv_get_error() == 0
+    s.check("scale %g" % scale)
+
+
+SCRIPT = r"""
+import sys
+sys.path[:0] = [%r, %r]
+import torch, test_gpu_int4 as T, paged_kv_attention_05_gb300 as pkv
+# one decode: its plan's one-wave split has more units than the bound for its lengths
+s = T.Step([(5000, 1)], %d, %d, 3, pad=0)
+pkv.pkv_reserve_workspace(1, 1, s.bt.shape[1], s.hq, s.hkv)
+s.write()
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    s.attention()
+for _ in range(3):
+    s.out.fill_(float("nan"))
+    g.replay()
+torch.cuda.synchronize()
+assert pkv.pkv_get_error() == 0
+s.check("captured first")
+print("as it should be")
+"""
+
+
+@pytest.mark.parametrize("hq,hkv", [(8, 1), (16, 1), (32, 1), (8, 8)])
+def test_a_reservation_of_exact_sizes_serves_a_capture(hq, hkv):
+    import os
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, "-c", SCRIPT % (os.path.dirname(here), here, hq, hkv)],
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "as it should be" in r.stdout, r.stdout + r.stderr
 
 
 def test_offsets_past_32_bits():
