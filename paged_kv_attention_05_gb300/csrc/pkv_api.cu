@@ -792,10 +792,10 @@ int check_rows4(const void* k, int64_t k_row_stride, const void* v, int64_t v_ro
 }
 
 // The workspace of pkv_select_pages: a counter for each row of a launch and KV head (in
-// front), and 20 bytes a page of theirs.  A launch takes at most as
-// many rows as 2^24 pages, or 65535 (row, KV head)s, have, so that many rows over wide
-// tables need no more than 340 MB.  (Room that never shrinks with the arguments: what is
-// reserved for large ones serves smaller ones.)
+// front, at the same place in every call: they are zero between calls), and 20 bytes a
+// page of theirs.  A launch takes at most as many rows as 2^24 pages, or 65535 (row, KV
+// head)s, have, so that many rows over wide tables need no more than 340 MB.  (Room that
+// never shrinks with the arguments: what is reserved for large ones serves smaller ones.)
 constexpr int64_t kSelectPairs = 65535;  // also the grid's limit
 struct SelectSizes {
   int64_t rows;  // of a launch

@@ -34,9 +34,24 @@
 //   * weights: e_j t_j is rounded to fp16 (2^-12 of itself at most).  The
 //     reference follows the largest e_j t_j of a row, not the largest e_j: fp16's range
 //     then holds every weight that counts, however large or small the value rows'
-//     scales.  It is moved only when a weight passes 2^14 (checked by one vote a
-//     page, no exchange between the lanes otherwise).
+//     scales.  It is moved only when a weight passes 2^14 (checked by one vote for
+//     two pages, no exchange between the lanes otherwise).
 // Keys past the unit's end get weight 0 and scale and zero 0.
+//
+// Two pages are taken a step: their chains of dependent operations (S's products,
+// the weights, P's transposition) run beside one another.  128 decodes of 8192 keys,
+// 32 query heads on 8 | 32 decodes of 32,768 keys, 32 on one, us:
+//   one page a step, 8 | 8 warps                  252 | 160
+//   two pages a step, 12 | 8 warps                202 |  99
+//   and one MMA tile with 16 warps | two with 8   190 |  82
+//   the last with 20 | 10 warps, fewer registers  199 |  96
+//   one page a step with 16 | 12 warps            194 |  88
+//   four tiles with 8 warps, one page a step            87
+//   the next step's S before this one's weights (spills)  90
+// The first is bound by HBM (6.1 TB/s of codes and scales, 0.90 of the copy rate) with
+// the alu pipe, which takes the masks and shifts, at 64%; the second by the latency of
+// a step's chain (two warps a scheduler, whose registers the tiles take: issue slots
+// 44%, tensor pipe 41%, HBM 25%).
 #include <cuda_fp16.h>
 
 #include "pkv_int4.cuh"
@@ -53,7 +68,8 @@ constexpr float kMaxWeight = 16384.f;  // e_j t_j that the reference is kept for
 // its e_j is held below 2^54 by the same bound; scales of others are above it.
 constexpr float kMinScale = 0x1p-40f;
 
-// Instances: items of at most 8 * kTiles query rows.
+// Instances: items of at most 8 * kTiles query rows.  The ring takes what shared memory
+// there is: 96 pages of the CTA's warps.
 template <int kTiles>
 struct Cfg4 {
   static constexpr int kWarps = kTiles == 1 ? 16 : 8;

@@ -78,6 +78,7 @@ constexpr int kTmemCols = 512;
 constexpr float kRescaleThreshold = 8.0f;         // log2 units
 constexpr float kMaxSum = 0x1p40f;                // scored calls: sum of a row over a pair of blocks
 constexpr float kMaxSum16 = 0x1p14f;              // 4-bit calls: sum of a row over 64 columns
+constexpr float kLift16 = 8.f;                    // and log2 of the largest weight at first
 
 // shared-memory layout (offsets from a 1024-byte aligned base)
 constexpr int kOffQ = 0;                          // Q_a | Q_b
@@ -1239,8 +1240,9 @@ __global__ void __launch_bounds__(kI4 ? kThreadsI4 : threads_of(kCap == kFixedCa
       // A row per thread, its 128 scores in two rounds of 64: nothing passes between
       // warps.  The scores are scaled by the powers of two of the row and of the K tile;
       // the V tiles', when it grows, is a change to O.  The reference (whole log2 units)
-      // moves when the sum of a round passes 2^14, which keeps each weight in fp16's
-      // range.  One loop for everything, on purpose: with the exponentials in two places
+      // moves when the sum of a round passes 2^14, to where the largest weight is 2^8: below
+      // fp16's largest number, and far enough above its smallest that 2^19 keys' roundings
+      // to halves of 2^-24 are 2^-13 of the largest weight together.  One loop for everything, on purpose: with the exponentials in two places
       // and both query tiles in one warp the kernel's roles did not fit the instruction
       // caches together, and all of them, the MMA's too, took two to three times as long
       // (4 chunks of 2047 tokens, 64 heads: 1368 us, 940 with the tiles' loop rolled).
@@ -1304,7 +1306,7 @@ __global__ void __launch_bounds__(kI4 ? kThreadsI4 : threads_of(kCap == kFixedCa
                   m0 = max3f(m0, sv[i], sv[i + 1]);
                   m1 = max3f(m1, sv[i + 2], sv[i + 3]);
                 }
-                const float m = ceilf(fmaxf(m0, m1) * f);
+                const float m = ceilf(fmaxf(m0, m1) * f) - kLift16;
                 const float to = move ? fmaxf(ref, m) : ref;
                 const float alpha = ref == -INFINITY ? 0.f : fast_exp2(ref - to);
                 ref = to;

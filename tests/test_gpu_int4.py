@@ -1,6 +1,8 @@
 """The cache of 4-bit codes on the GPU: the write byte for byte against a 64-bit
 quantiser, the read back, and attention over it (decodes and prompts) within a
 bound that counts the kernels' roundings (int4_ref.attention)."""
+import math
+
 import pytest
 import torch
 
@@ -419,3 +421,32 @@ def test_the_other_caches_after_an_int4_call():
     kc = torch.zeros((4, 16, 2, R.D), dtype=torch.bfloat16, device="cuda")
     with pytest.raises(pkv.PkvError):
         pkv.pkv_attention_planned(s.q, kc, kc, s.bt, s.scale, s.out)
+
+
+def test_many_keys_of_little_weight():
+    """A first key that takes nearly all of the weight, and 2^17 others of 2^-23 each:
+    their share of the output stays, although a weight of theirs alone would be below
+    fp16's normal numbers.  Keys are constant rows (cached exactly), values 0 and 150 by
+    turns."""
+    n_keys, n, hq = 1 << 17, 300, 2
+    k = torch.full((n_keys, 1, R.D), 0.03125, dtype=torch.bfloat16, device="cuda")
+    k[0] = 1.4375
+    v = torch.zeros(n_keys, 1, R.D, dtype=torch.bfloat16, device="cuda")
+    v[1:, :, 1::2] = 150.0
+    cache = torch.empty(n_keys // R.BS, 1, R.PAGE, dtype=torch.uint8, device="cuda")
+    pkv.pkv_write_int4(k, v, cache, torch.arange(n_keys, device="cuda"))
+    q = torch.ones(n, hq, R.D, dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(q, float("nan"))
+    scale = R.D ** -0.5
+    i32 = dict(dtype=torch.int32, device="cuda")
+    pkv.pkv_attention_int4(q, cache, torch.tensor([0, n], **i32), torch.tensor([n_keys], **i32),
+                           torch.arange(n_keys // R.BS, **i32).view(1, -1), 1, scale, out)
+    assert pkv.pkv_get_error() == 0
+    w = math.exp(-128 * (1.4375 - 0.03125) * scale)
+    others = torch.arange(n_keys - n, n_keys, device="cuda").double()
+    want = 150.0 * others * w / (1 + others * w)
+    # bf16's rounding of the output; of each weight fp16's, half of 2^-24 where the largest
+    # is at least 2^7; logits of up to 2^5 in fp32 (2^-19 of a weight), exp2 and the sums
+    tol = want * (2.0 ** -8 + 2.0 ** -17) + 150.0 * others * 2.0 ** -32
+    assert bool(((out[:, :, 1::2].double() - want[:, None, None]).abs() <= tol[:, None, None]).all())
+    assert not out[:, :, 0::2].any()
