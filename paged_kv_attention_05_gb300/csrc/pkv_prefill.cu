@@ -45,6 +45,16 @@
 // pkv_attention_scored runs instances with softmax warps of their own kind (8
 // or 16, a set for each query tile; described there), whose key tiles start at
 // the window's first page; the other roles are the same.
+// pkv_attention_int4 runs an instance of 20 warps: the producer brings pages of
+// codes and scales by bulk copies, four warps turn them into the fp16 K and V tiles,
+// one finds the tiles' exponents (and these five with one more convert the query rows);
+// the softmax is described there.  4 chunks of 2047 tokens of 64 heads on 8, after 4099
+// (us; floor 423, pkv_attention on the same batch 630): 1267 with two warps that form
+// bf16 tiles, 1083 with four and fp16 tiles, 940 with registers moved to the softmax and
+// the tiles' loop rolled, 857 with a row per softmax thread, 843 with key codes in
+// buffers of their own, 788 with codes taken as fp16 subnormals, 755 with the query rows
+// converted by all six.  What it has over pkv_attention's 630 is the forming of the
+// tiles: beside it tensor pipe 49%, issue slots 53%, alu 43%.
 // Every mbarrier wait is bounded; on expiry the kernel records
 // PKV_DEV_ERR_TIMEOUT, stops issuing work, frees its TMEM and returns.
 #include <cuda_fp16.h>
@@ -534,7 +544,7 @@ __device__ __forceinline__ void convert_q(uint8_t* q, float* fac, int set, float
 // kScored: a window, a prefix (runtime), and per instance a cap, a bias (kSym:
 // that may meet keys after a row's position, with a prefix).  kI4: the cache of 4-bit
 // codes (pkv_attention_int4): the producer brings a tile's pages as they are cached,
-// and two more warps turn them, and the query rows, into fp16 tiles.
+// and warps of their own turn them, and the query rows, into fp16 tiles.
 template <bool kScored, Cap kCap, bool kBias, bool kSym, bool kI4 = false>
 __global__ void __launch_bounds__(kI4 ? kThreadsI4 : threads_of(kCap == kFixedCap), 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -1242,10 +1252,11 @@ __global__ void __launch_bounds__(kI4 ? kThreadsI4 : threads_of(kCap == kFixedCa
       // the V tiles', when it grows, is a change to O.  The reference (whole log2 units)
       // moves when the sum of a round passes 2^14, to where the largest weight is 2^8: below
       // fp16's largest number, and far enough above its smallest that 2^19 keys' roundings
-      // to halves of 2^-24 are 2^-13 of the largest weight together.  One loop for everything, on purpose: with the exponentials in two places
-      // and both query tiles in one warp the kernel's roles did not fit the instruction
-      // caches together, and all of them, the MMA's too, took two to three times as long
-      // (4 chunks of 2047 tokens, 64 heads: 1368 us, 940 with the tiles' loop rolled).
+      // to halves of 2^-24 are 2^-13 of the largest weight together.  One loop for
+      // everything, on purpose: with the exponentials in two places and both query tiles in
+      // one warp the kernel's roles did not fit the instruction caches together, and all of
+      // them, the MMA's too, took two to three times as long (4 chunks of 2047 tokens, 64
+      // heads: 1368 us, 940 with the tiles' loop rolled).
       const int x = (warp - kSoft0) >> 2;
       const int qd = warp & 3;
       const int row = qd * 32 + lane;  // == TMEM lane
