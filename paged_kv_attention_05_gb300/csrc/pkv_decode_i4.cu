@@ -89,9 +89,15 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
                : "r"(addr));
   return v;
 }
-__device__ __forceinline__ uint2 lds64(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+// Two matrices of 16 rows of 16 bytes, transposed: lane l gives row l % 16 of matrix l / 16
+// and receives, of the first (second) matrix in x, y (z, w), bytes 4 (l % 4) .. + 3 of
+// columns l / 4 and l / 4 + 8.
+__device__ __forceinline__ uint4 load_transposed(uint32_t addr) {
+  uint4 v;
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
@@ -126,12 +132,12 @@ struct Ring {
 };
 
 // Query rows row0 .. of a unit (nrows of them in all), at most 8 * kT, two pages (32
-// keys) a step, kPg of them at a time.  Returns false when a wait gave up.
-template <int kT, int kPg = 2>
+// keys) a step.  Returns false when a wait gave up.
+template <int kT>
 __device__ __forceinline__ bool run_unit(const AttnArgs& a, const Workspace& ws, const DecUnit& un,
                                          int row0, Ring& ring, uint64_t pol,
                                          volatile int* abort) {
-  constexpr int kStages = Cfg4<kT>::kStages;
+  constexpr int kStages = Cfg4<kT>::kStages, kPg = 2;
   const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
   const int G = a.hq / a.hkv;
   const int ug = un.gq & 0xFFFF;  // KV head
@@ -157,7 +163,8 @@ __device__ __forceinline__ bool run_unit(const AttnArgs& a, const Workspace& ws,
   };
   const uint8_t *ids = load_ids(0), *ids_next = load_ids(32);
   // step j into stage st, each page by the lane that holds it; the stage's last pages
-  // were taken by this warp already (program order)
+  // were taken by this warp already (program order; one lane's fence is for all: with one
+  // by each lane that loads, 32 decodes of 32,768 keys took 82.5 us for 79.6)
   auto issue = [&](int j, uint32_t st) {
     if ((j & 15) == 0 && j > 0) {
       ids = ids_next;
@@ -170,10 +177,8 @@ __device__ __forceinline__ bool run_unit(const AttnArgs& a, const Workspace& ws,
       mbar_expect_tx(bar, 2 * j + 1 < npages ? 2 * kPage4 : kPage4);
     }
     __syncwarp();
-    if ((lane & ~1) == first && ids != nullptr) {
-      fence_async_smem();
+    if ((lane & ~1) == first && ids != nullptr)
       bulk_load_hint(ring.base + (2 * st + (lane & 1)) * kPage4, ids, kPage4, bar, pol);
-    }
   };
   {
     uint32_t st = ring.stage;
@@ -259,170 +264,161 @@ __device__ __forceinline__ bool run_unit(const AttnArgs& a, const Workspace& ws,
   const int key = ((gid >> 1) ^ (gid & 1)) + 4 * (gid & 1);
   const uint32_t at_k = ring.base + kRow4 * key + 16 * tig;
   const uint32_t at_m = ring.base + kMeta4 + 4 * key;
-  const uint32_t at_v = ring.base + kSide4 + 8 * gid + kRow4 * tig;
-  const uint32_t at_w = ring.base + kSide4 + 8 * gid + kRow4 * ((tig ^ 1) + 4);
+  // values, transposed: row 4 t + u of a matrix is the key that MMA column 2 t (u = 0), 2 t + 1
+  // (u = 2), 2 t + 8 (u = 1), 2 t + 9 (u = 3) has
+  const int vt = (lane >> 2) & 3, vkey = ((lane & 2) ? (vt ^ 1) + 4 : vt) + 8 * (lane & 1);
+  const uint32_t at_v = ring.base + kSide4 + kRow4 * vkey + 16 * (lane >> 4);
 
   for (int j = 0; j < nsteps; ++j) {
     if (!mbar_wait_warp(ring.bars + 8 * ring.stage, ring.parity, abort, ws.err)) return false;
-#pragma unroll 1
-    for (int half = 0; half < 2; half += kPg) {
-      const uint32_t st = (2 * ring.stage + half) * kPage4;
-      // S^T = K Q^T
-      float acc[kPg][kT][4];
-      uint32_t mk[kPg][2], mv[kPg][2];
+    const uint32_t st = 2 * ring.stage * kPage4;
+    // S^T = K Q^T
+    float acc[kPg][kT][4];
+    uint32_t mk[kPg][2], mv[kPg][2];
 #pragma unroll
-      for (int g = 0; g < kPg; ++g) {
-        const uint4 ka = lds128(at_k + st + g * kPage4);
-        const uint4 kb = lds128(at_k + st + g * kPage4 + 8 * kRow4);
+    for (int g = 0; g < kPg; ++g) {
+      const uint4 ka = lds128(at_k + st + g * kPage4);
+      const uint4 kb = lds128(at_k + st + g * kPage4 + 8 * kRow4);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          mk[g][i] = lds32(at_m + st + g * kPage4 + 32 * i);
-          mv[g][i] = lds32(at_m + st + g * kPage4 + 64 + 32 * i);
-        }
+      for (int i = 0; i < 2; ++i) {
+        mk[g][i] = lds32(at_m + st + g * kPage4 + 32 * i);
+        mv[g][i] = lds32(at_m + st + g * kPage4 + 64 + 32 * i);
+      }
+#pragma unroll
+      for (int t = 0; t < kT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[g][t][e] = 0.f;
+      const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t ca = wa[i >> 1] >> (8 * (i & 1)), cb = wb[i >> 1] >> (8 * (i & 1));
+#pragma unroll
+        for (int t = 0; t < kT; ++t)
+          mma_f16(acc[g][t], ca & kNib0, cb & kNib0, ca & kNib1, cb & kNib1, qb[t][i][0],
+                  qb[t][i][1]);
+      }
+    }
+
+    // logits less the reference: acc[g][t][0], [1] of the thread's first key of page g,
+    // [2], [3] of its second
+#pragma unroll
+    for (int g = 0; g < kPg; ++g)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float ks = lo16(mk[g][i]), kz = hi16(mk[g][i]);
 #pragma unroll
         for (int t = 0; t < kT; ++t)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[g][t][e] = 0.f;
-        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t ca = wa[i >> 1] >> (8 * (i & 1)), cb = wb[i >> 1] >> (8 * (i & 1));
-#pragma unroll
-          for (int t = 0; t < kT; ++t)
-            mma_f16(acc[g][t], ca & kNib0, cb & kNib0, ca & kNib1, cb & kNib1, qb[t][i][0],
-                    qb[t][i][1]);
-        }
+          for (int c = 0; c < 2; ++c)
+            acc[g][t][2 * i + c] =
+                fmaf(acc[g][t][2 * i + c] * ks, fac[t][c], fmaf(kz, off[t][c], nref[t][c]));
       }
-
-      // logits less the reference: acc[g][t][0], [1] of the thread's first key of page g,
-      // [2], [3] of its second
+    const int pos = k0 + 2 * j * kBlockSize;
+    if (pos + kPg * kBlockSize > all_see) {
 #pragma unroll
       for (int g = 0; g < kPg; ++g)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float ks = lo16(mk[g][i]), kz = hi16(mk[g][i]);
+          const int at = pos + kBlockSize * g + key + 8 * i;
+          if (at >= k1) mv[g][i] = 0u;
 #pragma unroll
           for (int t = 0; t < kT; ++t)
 #pragma unroll
             for (int c = 0; c < 2; ++c)
-              acc[g][t][2 * i + c] =
-                  fmaf(acc[g][t][2 * i + c] * ks, fac[t][c], fmaf(kz, off[t][c], nref[t][c]));
+              if (at >= vis[t][c]) acc[g][t][2 * i + c] = -INFINITY;
         }
-      const int pos = k0 + (2 * j + half) * kBlockSize;
-      if (pos + kPg * kBlockSize > all_see) {
+    }
+    float vs[kPg][2], e[kPg][kT][4], w[kPg][kT][4];
 #pragma unroll
-        for (int g = 0; g < kPg; ++g)
+    for (int g = 0; g < kPg; ++g)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int at = pos + kBlockSize * g + key + 8 * i;
-            if (at >= k1) mv[g][i] = 0u;
-#pragma unroll
-            for (int t = 0; t < kT; ++t)
-#pragma unroll
-              for (int c = 0; c < 2; ++c)
-                if (at >= vis[t][c]) acc[g][t][2 * i + c] = -INFINITY;
-          }
-      }
-      float vs[kPg][2], e[kPg][kT][4], w[kPg][kT][4];
+      for (int i = 0; i < 2; ++i) vs[g][i] = fmaxf(lo16(mv[g][i]), kMinScale);
+    auto weights = [&]() {
+      float most = 0.f;
 #pragma unroll
       for (int g = 0; g < kPg; ++g)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) vs[g][i] = fmaxf(lo16(mv[g][i]), kMinScale);
-      auto weights = [&]() {
-        float most = 0.f;
+        for (int t = 0; t < kT; ++t) {
 #pragma unroll
-        for (int g = 0; g < kPg; ++g)
+          for (int i = 0; i < 4; ++i) {
+            e[g][t][i] = fast_exp2(acc[g][t][i]);
+            w[g][t][i] = e[g][t][i] * vs[g][i >> 1];
+          }
+          most = max3f(most, max3f(w[g][t][0], w[g][t][1], w[g][t][2]), w[g][t][3]);
+        }
+      return most > kMaxWeight;
+    };
+    const bool over = weights();
+    if (__any_sync(0xffffffffu, over || unset != 0)) {
+      // references moved up: to the largest logit + log2 of the value row's scale
+      // (weights up to 1)
 #pragma unroll
-          for (int t = 0; t < kT; ++t) {
+      for (int t = 0; t < kT; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              e[g][t][i] = fast_exp2(acc[g][t][i]);
-              w[g][t][i] = e[g][t][i] * vs[g][i >> 1];
+        for (int c = 0; c < 2; ++c) {
+          float m = -INFINITY;
+#pragma unroll
+          for (int g = 0; g < kPg; ++g)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              m = fmaxf(m, acc[g][t][2 * i + c] + __log2f(vs[g][i]));
+#pragma unroll
+          for (int b = 4; b < 32; b <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, b));
+          const uint32_t bit = 1u << (2 * t + c);
+          const bool none = (unset & bit) != 0;
+          // (m is relative to the reference, 0 if there is none; a row without one takes
+          // whatever it sees first, another moves up only)
+          const float up = none ? (m == -INFINITY ? 0.f : m) : fmaxf(m, 0.f);
+          const float al = fast_exp2(-up);
+          if (m != -INFINITY) unset &= ~bit;
+          nref[t][c] -= up;
+          if (!none) {  // (nothing is summed yet of a row without a reference)
+            l[t][c] *= al;
+            z[t][c] *= al;
+#pragma unroll
+            for (int d = 0; d < 8; ++d) {
+              o[t][d][c] *= al;
+              o[t][d][2 + c] *= al;
             }
-            most = max3f(most, max3f(w[g][t][0], w[g][t][1], w[g][t][2]), w[g][t][3]);
           }
-        return most > kMaxWeight;
-      };
-      const bool over = weights();
-      if (__any_sync(0xffffffffu, over || unset != 0)) {
-        // references moved up: to the largest logit + log2 of the value row's scale
-        // (weights up to 1)
 #pragma unroll
-        for (int t = 0; t < kT; ++t)
+          for (int g = 0; g < kPg; ++g)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float m = -INFINITY;
+            for (int i = 0; i < 2; ++i) acc[g][t][2 * i + c] -= up;
+        }
+      weights();
+    }
+    uint32_t pb[kPg][kT][2];
 #pragma unroll
-            for (int g = 0; g < kPg; ++g)
+    for (int g = 0; g < kPg; ++g)
 #pragma unroll
-              for (int i = 0; i < 2; ++i)
-                m = fmaxf(m, acc[g][t][2 * i + c] + __log2f(vs[g][i]));
+      for (int t = 0; t < kT; ++t)
 #pragma unroll
-            for (int b = 4; b < 32; b <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, b));
-            const uint32_t bit = 1u << (2 * t + c);
-            const bool none = (unset & bit) != 0;
-            // (m is relative to the reference, 0 if there is none; a row without one takes
-            // whatever it sees first, another moves up only)
-            const float up = none ? (m == -INFINITY ? 0.f : m) : fmaxf(m, 0.f);
-            const float al = fast_exp2(-up);
-            if (m != -INFINITY) unset &= ~bit;
-            nref[t][c] -= up;
-            if (!none) {  // (nothing is summed yet of a row without a reference)
-              l[t][c] *= al;
-              z[t][c] *= al;
-#pragma unroll
-              for (int d = 0; d < 8; ++d) {
-                o[t][d][c] *= al;
-                o[t][d][2 + c] *= al;
-              }
-            }
-#pragma unroll
-            for (int g = 0; g < kPg; ++g)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) acc[g][t][2 * i + c] -= up;
-          }
-        weights();
-      }
-      uint32_t pb[kPg][kT][2];
-#pragma unroll
-      for (int g = 0; g < kPg; ++g)
-#pragma unroll
-        for (int t = 0; t < kT; ++t)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            l[t][c] += e[g][t][c] + e[g][t][2 + c];
-            z[t][c] = fmaf(e[g][t][c], hi16(mv[g][0]), fmaf(e[g][t][2 + c], hi16(mv[g][1]), z[t][c]));
-            pb[g][t][c] = transpose8x8(pack_f16(w[g][t][2 * c], w[g][t][2 * c + 1]));
-          }
+        for (int c = 0; c < 2; ++c) {
+          l[t][c] += e[g][t][c] + e[g][t][2 + c];
+          z[t][c] = fmaf(e[g][t][c], hi16(mv[g][0]), fmaf(e[g][t][2 + c], hi16(mv[g][1]), z[t][c]));
+          pb[g][t][c] = transpose8x8(pack_f16(w[g][t][2 * c], w[g][t][2 * c + 1]));
+        }
 
-      // O^T += V^T P^T: a word of codes of the two keys of an operand pair, their low
-      // halves together and their high ones, hold dimensions 0, 2, 4, 6 and 1, 3, 5, 7 of
-      // the eight; MMA rows gid and gid + 8 are the first and second nibble of each byte.
-      // Values: keys kappa(2 tig), kappa(2 tig + 1) and those 8 on, dimensions 16 gid .. + 15.
+    // O^T += V^T P^T: a register of a transposed load has a byte, two dimensions, of four
+    // keys; the first and third are one operand register, the others the next, MMA rows
+    // gid and gid + 8 the two nibbles.
 #pragma unroll
-      for (int g = 0; g < kPg; ++g) {
-        const uint2 va = lds64(at_v + st + g * kPage4), vb = lds64(at_w + st + g * kPage4);
-        const uint2 vc = lds64(at_v + st + g * kPage4 + 8 * kRow4);
-        const uint2 vd = lds64(at_w + st + g * kPage4 + 8 * kRow4);
-        if (half + g == 1) {  // the stage is in registers: it can take another step
-          __syncwarp();
-          if (j + kStages < nsteps) issue(j + kStages, ring.stage);
-        }
+    for (int g = 0; g < kPg; ++g) {
+      const uint4 va = load_transposed(at_v + st + g * kPage4);
+      const uint4 vb = load_transposed(at_v + st + g * kPage4 + 32);
+      if (g == kPg - 1) {  // the stage is in registers: it can take another step
+        __syncwarp();
+        if (j + kStages < nsteps) issue(j + kStages, ring.stage);
+      }
+      const uint32_t v[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t a0 = h ? va.y : va.x, a1 = h ? vb.y : vb.x;
-          const uint32_t b0 = h ? vc.y : vc.x, b1 = h ? vd.y : vd.x;
+      for (int d = 0; d < 8; ++d) {
+        const uint32_t lo = v[d], hi = v[d] >> 8;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {  // even dimensions 0, 2 | 4, 6; odd 1, 3 | 5, 7
-            const uint32_t sel = i < 2 ? 0x5410 : 0x7632;
-            const uint32_t lo = __byte_perm(a0, a1, sel) >> (8 * (i & 1));
-            const uint32_t hi = __byte_perm(b0, b1, sel) >> (8 * (i & 1));
-#pragma unroll
-            for (int t = 0; t < kT; ++t)
-              mma_f16(o[t][4 * h + i], lo & kNib0, lo & kNib1, hi & kNib0, hi & kNib1, pb[g][t][0],
-                      pb[g][t][1]);
-          }
-        }
+        for (int t = 0; t < kT; ++t)
+          mma_f16(o[t][d], lo & kNib0, lo & kNib1, hi & kNib0, hi & kNib1, pb[g][t][0],
+                  pb[g][t][1]);
       }
     }
     if (++ring.stage == kStages) {
@@ -431,8 +427,11 @@ __device__ __forceinline__ bool run_unit(const AttnArgs& a, const Workspace& ws,
     }
   }
 
-  // The thread's columns 2 tig, 2 tig + 1 are query rows, with dimensions 16 gid .. + 15:
-  // o[4 h + i][c] is dimension 8 h + 4 (i % 2) + i / 2, o[4 h + i][2 + c] the one 2 on.
+  // The thread's columns 2 tig, 2 tig + 1 are query rows, o[d] the two dimensions of byte 8 d +
+  // gid of a row's codes: 16 d + at and two on, at = 8 (gid / 4) + 4 (gid % 2) + (gid / 2) % 2.
+  // Lanes gid and gid ^ 2 exchange one, so that each has two neighbours.
+  const bool odd = gid & 2;
+  const int at = 8 * (gid >> 2) + 4 * (gid & 1) + (gid & 2);
 #pragma unroll
   for (int t = 0; t < kT; ++t)
 #pragma unroll
@@ -443,31 +442,26 @@ __device__ __forceinline__ bool run_unit(const AttnArgs& a, const Workspace& ws,
         ls += __shfl_xor_sync(0xffffffffu, ls, b);
         zs += __shfl_xor_sync(0xffffffffu, zs, b);
       }
-      const int row = row0 + 8 * t + 2 * tig + c;
-      if (row >= nrows) continue;
-      float v[16];
+      float2 v[8];
 #pragma unroll
       for (int d = 0; d < 8; ++d) {
-        const int at = 8 * (d >> 2) + 4 * (d & 1) + ((d >> 1) & 1);
-        v[at] = fmaf(o[t][d][c], 0x1p24f, zs);
-        v[at + 2] = fmaf(o[t][d][2 + c], 0x1p20f, zs);
+        const float x = fmaf(o[t][d][c], 0x1p24f, zs), y = fmaf(o[t][d][2 + c], 0x1p20f, zs);
+        const float other = __shfl_xor_sync(0xffffffffu, odd ? x : y, 8);
+        v[d] = odd ? make_float2(other, y) : make_float2(x, other);
       }
+      const int row = row0 + 8 * t + 2 * tig + c;
+      if (row >= nrows) continue;
       if (un.nsplit == 1) {
         const float inv = 1.f / ls;
-        uint32_t w[8];
+        uint16_t* dst = a.out + (int64_t)(un.q0 + row / G) * a.out_stride +
+                        (int64_t)(ug * G + row % G) * kHeadSize + at;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = pack_bf16(v[2 * i] * inv, v[2 * i + 1] * inv);
-        uint4* dst = reinterpret_cast<uint4*>(
-            a.out + (int64_t)(un.q0 + row / G) * a.out_stride +
-            (int64_t)(ug * G + row % G) * kHeadSize + 16 * gid);
-        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        for (int d = 0; d < 8; ++d)
+          *reinterpret_cast<uint32_t*>(dst + 16 * d) = pack_bf16(v[d].x * inv, v[d].y * inv);
       } else {
-        float4* dst = reinterpret_cast<float4*>(ws.part_o + ((int64_t)un.part + row) * kHeadSize +
-                                                16 * gid);
+        float* dst = ws.part_o + ((int64_t)un.part + row) * kHeadSize + at;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        for (int d = 0; d < 8; ++d) *reinterpret_cast<float2*>(dst + 16 * d) = v[d];
         if (gid == 0)  // (no key seen: the merge skips a split with reference -inf)
           *reinterpret_cast<float2*>(ws.part_ml + ((int64_t)un.part + row) * 2) =
               make_float2((unset >> (2 * t + c)) & 1 ? -INFINITY : -nref[t][c], ls);
