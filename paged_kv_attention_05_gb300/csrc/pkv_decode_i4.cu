@@ -27,8 +27,8 @@
 //     operand.  P^T's operand is S^T's accumulator transposed, 8x8 by 8x8
 //     (movmatrix).
 //   * k order of S: a thread holds 32 consecutive dimensions of its two keys; the
-//     16 keys of a page are the MMA rows in the order kappa(m), so that the value
-//     rows that the threads of a quad read lie in different banks.
+//     16 keys of a page are the MMA rows in the order kappa(m), so that the key rows
+//     that eight lanes read lie in different banks.
 //   * query rows are scaled by a power of two, so that their largest value is
 //     between 2^10 and 2^11 in fp16: bf16's 8 bits stay exact, whatever the range.
 //   * weights: e_j t_j is rounded to fp16 (2^-12 of itself at most).  The
@@ -36,22 +36,31 @@
 //     then holds every weight that counts, however large or small the value rows'
 //     scales.  It is moved only when a weight passes 2^14 (checked by one vote for
 //     two pages, no exchange between the lanes otherwise).
+//   * values come by ldmatrix, transposed: a register has a byte, two dimensions, of
+//     four keys, so that a mask and a shift by 8 make MMA operands of it too.
 // Keys past the unit's end get weight 0 and scale and zero 0.
 //
-// Two pages are taken a step: their chains of dependent operations (S's products,
+// Two pages are taken at a time: their chains of dependent operations (S's products,
 // the weights, P's transposition) run beside one another.  128 decodes of 8192 keys,
 // 32 query heads on 8 | 32 decodes of 32,768 keys, 32 on one, us:
-//   one page a step, 8 | 8 warps                  252 | 160
-//   two pages a step, 12 | 8 warps                202 |  99
+//   one page at a time, 8 | 8 warps               252 | 160
+//   two pages, 12 | 8 warps                       202 |  99
 //   and one MMA tile with 16 warps | two with 8   190 |  82
-//   the last with 20 | 10 warps, fewer registers  199 |  96
-//   one page a step with 16 | 12 warps            194 |  88
-//   four tiles with 8 warps, one page a step            87
-//   the next step's S before this one's weights (spills)  90
-// The first is bound by HBM (6.1 TB/s of codes and scales, 0.90 of the copy rate) with
-// the alu pipe, which takes the masks and shifts, at 64%; the second by the latency of
-// a step's chain (two warps a scheduler, whose registers the tiles take: issue slots
-// 44%, tensor pipe 41%, HBM 25%).
+//   (with 20 | 10 warps, fewer registers          199 |  96
+//   one page at a time with 16 | 12 warps         194 |  88
+//   four tiles with 8 warps, one page                    87
+//   the next pages' S before these ones' weights         90, spills
+//   shifts by a high product, off the alu pipe    211 |  89)
+//   values by transposed loads, one fence a stage 187 |  80
+//   four pages a stage with two tiles             187 |  77
+//   three units a worker for four (the plan)      183 |  77
+// The first is bound by HBM (6.2 TB/s of codes and scales, 0.92 of the copy rate) with
+// the alu pipe, which takes the masks and shifts; the second by the latency of a
+// step's chain, with two warps a scheduler, whose registers the tiles take (of about 2000
+// cycles for two pages the tensor pipe is busy 1000, the alu pipe 900; asking for a
+// stage's copies takes 300 to 400, waiting for them 120).  Asking for the next unit's
+// pages while this one's last steps run, in the loop, cost more registers and code than
+// it saved (189 | 86).
 #include <cuda_fp16.h>
 
 #include "pkv_int4.cuh"
@@ -68,14 +77,15 @@ constexpr float kMaxWeight = 16384.f;  // e_j t_j that the reference is kept for
 // its e_j is held below 2^54 by the same bound; scales of others are above it.
 constexpr float kMinScale = 0x1p-40f;
 
-// Instances: items of at most 8 * kTiles query rows.  The ring takes what shared memory
-// there is: 96 pages of the CTA's warps.
+// Instances: items of at most 8 * kTiles query rows.  The rings take what shared memory
+// there is: 96 pages for the CTA's warps, in stages of kStagePages.
 template <int kTiles>
 struct Cfg4 {
   static constexpr int kWarps = kTiles == 1 ? 16 : 8;
   static constexpr int kThreads = kWarps * 32;
-  static constexpr int kStages = 48 / kWarps;  // of two pages
-  static constexpr int kWarpBytes = kStages * 2 * kPage4;
+  static constexpr int kStagePages = kTiles == 1 ? 2 : 4;
+  static constexpr int kStages = 96 / kWarps / kStagePages;
+  static constexpr int kWarpBytes = kStages * kStagePages * kPage4;
   static constexpr int kOffBar = kWarps * kWarpBytes;
   static constexpr int kOffCtl = kOffBar + kWarps * kStages * 8;
   static constexpr int kSmem = kOffCtl + (2 + kWarps) * 4 + 128;  // (abort, items given out, first items)
@@ -131,23 +141,23 @@ struct Ring {
   uint32_t base, bars, stage, parity;
 };
 
-// Query rows row0 .. of a unit (nrows of them in all), at most 8 * kT, two pages (32
-// keys) a step.  Returns false when a wait gave up.
+// Query rows row0 .. of a unit (nrows of them in all), at most 8 * kT, kSp pages a
+// stage, two (32 keys) at a time.  Returns false when a wait gave up.
 template <int kT>
 __device__ __forceinline__ bool run_unit(const AttnArgs& a, const Workspace& ws, const DecUnit& un,
                                          int row0, Ring& ring, uint64_t pol,
                                          volatile int* abort) {
-  constexpr int kStages = Cfg4<kT>::kStages, kPg = 2;
+  constexpr int kStages = Cfg4<kT>::kStages, kSp = Cfg4<kT>::kStagePages, kPg = 2;
   const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
   const int G = a.hq / a.hkv;
   const int ug = un.gq & 0xFFFF;  // KV head
   const int qn = un.gq >> 16;     // query tokens of the request
   const int k0 = un.k0, k1 = un.k1;
   const int p0 = k0 / kBlockSize;
-  const int npages = (k1 + kBlockSize - 1) / kBlockSize - p0, nsteps = (npages + 1) / 2;
+  const int npages = (k1 + kBlockSize - 1) / kBlockSize - p0, nstages = (npages + kSp - 1) / kSp;
   const int nrows = qn * G;
 
-  // The pages of 16 steps at a time, one per lane, and those of the next 16.
+  // The ids of 32 pages, one per lane, and of the next 32.
   const int* btrow = table_row(a, un.r, ug) + p0;
   auto load_ids = [&](int p) {
     const uint8_t* page = nullptr;
@@ -162,27 +172,27 @@ __device__ __forceinline__ bool run_unit(const AttnArgs& a, const Workspace& ws,
     return page;
   };
   const uint8_t *ids = load_ids(0), *ids_next = load_ids(32);
-  // step j into stage st, each page by the lane that holds it; the stage's last pages
-  // were taken by this warp already (program order; one lane's fence is for all: with one
-  // by each lane that loads, 32 decodes of 32,768 keys took 82.5 us for 79.6)
+  // pages kSp * j .. + kSp - 1 into stage st, each by the lane that holds its id; the stage's
+  // last pages were taken by this warp already (program order; one lane's fence is for all:
+  // with one by each lane that loads, 32 decodes of 32,768 keys took 82.5 us for 79.6)
   auto issue = [&](int j, uint32_t st) {
-    if ((j & 15) == 0 && j > 0) {
+    const int first = kSp * j & 31;
+    if (first == 0 && j > 0) {
       ids = ids_next;
-      ids_next = load_ids(2 * j + 32);
+      ids_next = load_ids(kSp * j + 32);
     }
-    const int first = 2 * (j & 15);
     const uint32_t bar = ring.bars + 8 * st;
     if (lane == first) {
       fence_async_smem();
-      mbar_expect_tx(bar, 2 * j + 1 < npages ? 2 * kPage4 : kPage4);
+      mbar_expect_tx(bar, min(kSp, npages - kSp * j) * kPage4);
     }
     __syncwarp();
-    if ((lane & ~1) == first && ids != nullptr)
-      bulk_load_hint(ring.base + (2 * st + (lane & 1)) * kPage4, ids, kPage4, bar, pol);
+    if ((lane & ~(kSp - 1)) == first && ids != nullptr)
+      bulk_load_hint(ring.base + (kSp * st + (lane & (kSp - 1))) * kPage4, ids, kPage4, bar, pol);
   };
   {
     uint32_t st = ring.stage;
-    for (int j = 0; j < kStages && j < nsteps; ++j) {
+    for (int j = 0; j < kStages && j < nstages; ++j) {
       issue(j, st);
       st = st + 1 == kStages ? 0 : st + 1;
     }
@@ -269,156 +279,160 @@ __device__ __forceinline__ bool run_unit(const AttnArgs& a, const Workspace& ws,
   const int vt = (lane >> 2) & 3, vkey = ((lane & 2) ? (vt ^ 1) + 4 : vt) + 8 * (lane & 1);
   const uint32_t at_v = ring.base + kSide4 + kRow4 * vkey + 16 * (lane >> 4);
 
-  for (int j = 0; j < nsteps; ++j) {
+  for (int j = 0; j < nstages; ++j) {
     if (!mbar_wait_warp(ring.bars + 8 * ring.stage, ring.parity, abort, ws.err)) return false;
-    const uint32_t st = 2 * ring.stage * kPage4;
-    // S^T = K Q^T
-    float acc[kPg][kT][4];
-    uint32_t mk[kPg][2], mv[kPg][2];
+#pragma unroll 1
+    for (int half = 0; half < kSp; half += kPg) {
+      if (kSp > kPg && half > 0 && kSp * j + half >= npages) break;
+      const uint32_t st = (kSp * ring.stage + half) * kPage4;
+      // S^T = K Q^T
+      float acc[kPg][kT][4];
+      uint32_t mk[kPg][2], mv[kPg][2];
 #pragma unroll
-    for (int g = 0; g < kPg; ++g) {
-      const uint4 ka = lds128(at_k + st + g * kPage4);
-      const uint4 kb = lds128(at_k + st + g * kPage4 + 8 * kRow4);
+      for (int g = 0; g < kPg; ++g) {
+        const uint4 ka = lds128(at_k + st + g * kPage4);
+        const uint4 kb = lds128(at_k + st + g * kPage4 + 8 * kRow4);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        mk[g][i] = lds32(at_m + st + g * kPage4 + 32 * i);
-        mv[g][i] = lds32(at_m + st + g * kPage4 + 64 + 32 * i);
-      }
-#pragma unroll
-      for (int t = 0; t < kT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[g][t][e] = 0.f;
-      const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t ca = wa[i >> 1] >> (8 * (i & 1)), cb = wb[i >> 1] >> (8 * (i & 1));
+        for (int i = 0; i < 2; ++i) {
+          mk[g][i] = lds32(at_m + st + g * kPage4 + 32 * i);
+          mv[g][i] = lds32(at_m + st + g * kPage4 + 64 + 32 * i);
+        }
 #pragma unroll
         for (int t = 0; t < kT; ++t)
-          mma_f16(acc[g][t], ca & kNib0, cb & kNib0, ca & kNib1, cb & kNib1, qb[t][i][0],
-                  qb[t][i][1]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[g][t][e] = 0.f;
+        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t ca = wa[i >> 1] >> (8 * (i & 1)), cb = wb[i >> 1] >> (8 * (i & 1));
+#pragma unroll
+          for (int t = 0; t < kT; ++t)
+            mma_f16(acc[g][t], ca & kNib0, cb & kNib0, ca & kNib1, cb & kNib1, qb[t][i][0],
+                    qb[t][i][1]);
+        }
       }
-    }
 
-    // logits less the reference: acc[g][t][0], [1] of the thread's first key of page g,
-    // [2], [3] of its second
-#pragma unroll
-    for (int g = 0; g < kPg; ++g)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float ks = lo16(mk[g][i]), kz = hi16(mk[g][i]);
-#pragma unroll
-        for (int t = 0; t < kT; ++t)
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-            acc[g][t][2 * i + c] =
-                fmaf(acc[g][t][2 * i + c] * ks, fac[t][c], fmaf(kz, off[t][c], nref[t][c]));
-      }
-    const int pos = k0 + 2 * j * kBlockSize;
-    if (pos + kPg * kBlockSize > all_see) {
+      // logits less the reference: acc[g][t][0], [1] of the thread's first key of page g,
+      // [2], [3] of its second
 #pragma unroll
       for (int g = 0; g < kPg; ++g)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int at = pos + kBlockSize * g + key + 8 * i;
-          if (at >= k1) mv[g][i] = 0u;
+          const float ks = lo16(mk[g][i]), kz = hi16(mk[g][i]);
 #pragma unroll
           for (int t = 0; t < kT; ++t)
 #pragma unroll
             for (int c = 0; c < 2; ++c)
-              if (at >= vis[t][c]) acc[g][t][2 * i + c] = -INFINITY;
+              acc[g][t][2 * i + c] =
+                  fmaf(acc[g][t][2 * i + c] * ks, fac[t][c], fmaf(kz, off[t][c], nref[t][c]));
         }
-    }
-    float vs[kPg][2], e[kPg][kT][4], w[kPg][kT][4];
+      const int pos = k0 + (kSp * j + half) * kBlockSize;
+      if (pos + kPg * kBlockSize > all_see) {
 #pragma unroll
-    for (int g = 0; g < kPg; ++g)
+        for (int g = 0; g < kPg; ++g)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) vs[g][i] = fmaxf(lo16(mv[g][i]), kMinScale);
-    auto weights = [&]() {
-      float most = 0.f;
+          for (int i = 0; i < 2; ++i) {
+            const int at = pos + kBlockSize * g + key + 8 * i;
+            if (at >= k1) mv[g][i] = 0u;
+#pragma unroll
+            for (int t = 0; t < kT; ++t)
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                if (at >= vis[t][c]) acc[g][t][2 * i + c] = -INFINITY;
+          }
+      }
+      float vs[kPg][2], e[kPg][kT][4], w[kPg][kT][4];
 #pragma unroll
       for (int g = 0; g < kPg; ++g)
 #pragma unroll
-        for (int t = 0; t < kT; ++t) {
+        for (int i = 0; i < 2; ++i) vs[g][i] = fmaxf(lo16(mv[g][i]), kMinScale);
+      auto weights = [&]() {
+        float most = 0.f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            e[g][t][i] = fast_exp2(acc[g][t][i]);
-            w[g][t][i] = e[g][t][i] * vs[g][i >> 1];
-          }
-          most = max3f(most, max3f(w[g][t][0], w[g][t][1], w[g][t][2]), w[g][t][3]);
-        }
-      return most > kMaxWeight;
-    };
-    const bool over = weights();
-    if (__any_sync(0xffffffffu, over || unset != 0)) {
-      // references moved up: to the largest logit + log2 of the value row's scale
-      // (weights up to 1)
+        for (int g = 0; g < kPg; ++g)
 #pragma unroll
-      for (int t = 0; t < kT; ++t)
+          for (int t = 0; t < kT; ++t) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float m = -INFINITY;
-#pragma unroll
-          for (int g = 0; g < kPg; ++g)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              m = fmaxf(m, acc[g][t][2 * i + c] + __log2f(vs[g][i]));
-#pragma unroll
-          for (int b = 4; b < 32; b <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, b));
-          const uint32_t bit = 1u << (2 * t + c);
-          const bool none = (unset & bit) != 0;
-          // (m is relative to the reference, 0 if there is none; a row without one takes
-          // whatever it sees first, another moves up only)
-          const float up = none ? (m == -INFINITY ? 0.f : m) : fmaxf(m, 0.f);
-          const float al = fast_exp2(-up);
-          if (m != -INFINITY) unset &= ~bit;
-          nref[t][c] -= up;
-          if (!none) {  // (nothing is summed yet of a row without a reference)
-            l[t][c] *= al;
-            z[t][c] *= al;
-#pragma unroll
-            for (int d = 0; d < 8; ++d) {
-              o[t][d][c] *= al;
-              o[t][d][2 + c] *= al;
+            for (int i = 0; i < 4; ++i) {
+              e[g][t][i] = fast_exp2(acc[g][t][i]);
+              w[g][t][i] = e[g][t][i] * vs[g][i >> 1];
             }
+            most = max3f(most, max3f(w[g][t][0], w[g][t][1], w[g][t][2]), w[g][t][3]);
           }
-#pragma unroll
-          for (int g = 0; g < kPg; ++g)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) acc[g][t][2 * i + c] -= up;
-        }
-      weights();
-    }
-    uint32_t pb[kPg][kT][2];
-#pragma unroll
-    for (int g = 0; g < kPg; ++g)
-#pragma unroll
-      for (int t = 0; t < kT; ++t)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          l[t][c] += e[g][t][c] + e[g][t][2 + c];
-          z[t][c] = fmaf(e[g][t][c], hi16(mv[g][0]), fmaf(e[g][t][2 + c], hi16(mv[g][1]), z[t][c]));
-          pb[g][t][c] = transpose8x8(pack_f16(w[g][t][2 * c], w[g][t][2 * c + 1]));
-        }
-
-    // O^T += V^T P^T: a register of a transposed load has a byte, two dimensions, of four
-    // keys; the first and third are one operand register, the others the next, MMA rows
-    // gid and gid + 8 the two nibbles.
-#pragma unroll
-    for (int g = 0; g < kPg; ++g) {
-      const uint4 va = load_transposed(at_v + st + g * kPage4);
-      const uint4 vb = load_transposed(at_v + st + g * kPage4 + 32);
-      if (g == kPg - 1) {  // the stage is in registers: it can take another step
-        __syncwarp();
-        if (j + kStages < nsteps) issue(j + kStages, ring.stage);
-      }
-      const uint32_t v[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
-#pragma unroll
-      for (int d = 0; d < 8; ++d) {
-        const uint32_t lo = v[d], hi = v[d] >> 8;
+        return most > kMaxWeight;
+      };
+      const bool over = weights();
+      if (__any_sync(0xffffffffu, over || unset != 0)) {
+        // references moved up: to the largest logit + log2 of the value row's scale
+        // (weights up to 1)
 #pragma unroll
         for (int t = 0; t < kT; ++t)
-          mma_f16(o[t][d], lo & kNib0, lo & kNib1, hi & kNib0, hi & kNib1, pb[g][t][0],
-                  pb[g][t][1]);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float m = -INFINITY;
+#pragma unroll
+            for (int g = 0; g < kPg; ++g)
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                m = fmaxf(m, acc[g][t][2 * i + c] + __log2f(vs[g][i]));
+#pragma unroll
+            for (int b = 4; b < 32; b <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, b));
+            const uint32_t bit = 1u << (2 * t + c);
+            const bool none = (unset & bit) != 0;
+            // (m is relative to the reference, 0 if there is none; a row without one takes
+            // whatever it sees first, another moves up only)
+            const float up = none ? (m == -INFINITY ? 0.f : m) : fmaxf(m, 0.f);
+            const float al = fast_exp2(-up);
+            if (m != -INFINITY) unset &= ~bit;
+            nref[t][c] -= up;
+            if (!none) {  // (nothing is summed yet of a row without a reference)
+              l[t][c] *= al;
+              z[t][c] *= al;
+#pragma unroll
+              for (int d = 0; d < 8; ++d) {
+                o[t][d][c] *= al;
+                o[t][d][2 + c] *= al;
+              }
+            }
+#pragma unroll
+            for (int g = 0; g < kPg; ++g)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) acc[g][t][2 * i + c] -= up;
+          }
+        weights();
+      }
+      uint32_t pb[kPg][kT][2];
+#pragma unroll
+      for (int g = 0; g < kPg; ++g)
+#pragma unroll
+        for (int t = 0; t < kT; ++t)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            l[t][c] += e[g][t][c] + e[g][t][2 + c];
+            z[t][c] = fmaf(e[g][t][c], hi16(mv[g][0]), fmaf(e[g][t][2 + c], hi16(mv[g][1]), z[t][c]));
+            pb[g][t][c] = transpose8x8(pack_f16(w[g][t][2 * c], w[g][t][2 * c + 1]));
+          }
+
+      // O^T += V^T P^T: a register of a transposed load has a byte, two dimensions, of four
+      // keys; the first and third are one operand register, the others the next, MMA rows
+      // gid and gid + 8 the two nibbles.
+#pragma unroll
+      for (int g = 0; g < kPg; ++g) {
+        const uint4 va = load_transposed(at_v + st + g * kPage4);
+        const uint4 vb = load_transposed(at_v + st + g * kPage4 + 32);
+        if (half + g == kSp - 1) {  // the stage is in registers: it can take another step
+          __syncwarp();
+          if (j + kStages < nstages) issue(j + kStages, ring.stage);
+        }
+        const uint32_t v[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
+#pragma unroll
+        for (int d = 0; d < 8; ++d) {
+          const uint32_t lo = v[d], hi = v[d] >> 8;
+#pragma unroll
+          for (int t = 0; t < kT; ++t)
+            mma_f16(o[t][d], lo & kNib0, lo & kNib1, hi & kNib0, hi & kNib1, pb[g][t][0],
+                    pb[g][t][1]);
+        }
       }
     }
     if (++ring.stage == kStages) {

@@ -262,7 +262,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(ArgsOf<kScored> a, W
   // largest chunk times the divisor and the capacities at INT_MAX, which
   // changes no result: past those bounds the clamp to kMaxChunk, or the
   // smaller per-pair count, decides.)
-  const unsigned den = 4u * (unsigned)dec_grid;  // dec_grid: a few thousand workers at most
+  // Three units a worker over 4-bit caches, whose units are twice to four times as many
+  // (us with three | four: 128 decodes of 8192 keys, 32/8 heads 183 | 187; 16 of about 63,000
+  // 186 | 193; 64 of 2000 to 16,000, 64/4 heads 109 | 116; two were better but for the first,
+  // 213).
+  const unsigned den = (a.kv == kInt4 ? 3u : 4u) * (unsigned)dec_grid;  // (a few thousand workers)
   const long long tk = total_keys * a.hkv;
   unsigned want = tk > (long long)kMaxChunk * den ? (unsigned)kMaxChunk + 1u
                                                   : ((unsigned)tk + den - 1u) / den;
