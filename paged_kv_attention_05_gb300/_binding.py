@@ -541,20 +541,16 @@ def pkv_attention_scored(q, key_cache, value_cache, query_start_loc, seq_lens, b
         _check(rc)
 
 
-def _on_device(*named):
-    """True when every (tensor, name, dtype) is a tensor of its dtype on the
-    current CUDA device, or raises for the first that is not."""
-    dev = _get_device()
-    try:
-        for t, _, dtype in named:
-            if t.dtype is not dtype or t.get_device() != dev:
-                break
-        else:
-            return
-    except AttributeError:
-        for t, name, _ in named:
-            if t is None:
-                raise TypeError("%s must be a torch.Tensor" % name) from None
+# The checks of the calls below are one pass of plain attribute reads each, as a small
+# call's time is theirs (a list of triples and a helper for each tensor: a call over
+# selected pages 13.2 us of host time for 11.9); a failing one is named afterwards.
+
+def _refuse(*named):
+    """Raises for the first of these (tensor, name, dtype) that is no tensor of its
+    dtype on the current CUDA device."""
+    for t, name, _ in named:
+        if t is None:
+            raise TypeError("%s must be a torch.Tensor" % name)
     _name_culprit(*named)
     raise ValueError("arguments must be tensors on the current CUDA device")
 
@@ -569,26 +565,38 @@ def _cache4(cache):
 
 def _head_rows(t, name, heads, d=128):
     """Rows and row stride of a [rows, heads, d] tensor with contiguous rows."""
-    sh, st = t.shape, t.stride()
-    if len(sh) != 3 or sh[1] != heads or sh[2] != d:
+    try:
+        rows, h, w = t.shape
+    except ValueError:
+        h = w = -1
+    if w != d or h != heads:
         raise ValueError("%s must be [rows, %d, %d]" % (name, heads, d))
-    if st[2] != 1 or (st[1] != d and heads != 1):
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != d and heads != 1):
         raise ValueError("%s must have contiguous rows" % name)
-    return sh[0], heads * d if sh[0] == 1 else st[0]
+    return rows, heads * d if rows == 1 else s0
 
 
 def _rows4(k, v, cache, slots, n_tokens, names):
     torch = _torch or _T()
     bf16 = torch.bfloat16
-    _on_device((k, names[0], bf16), (v, names[1], bf16), (cache, "cache", torch.uint8),
-               (slots, names[2], torch.int64))
+    try:
+        good = (k.dtype is bf16 and v.dtype is bf16 and cache.dtype is torch.uint8 and
+                slots.dtype is torch.int64 and _get_device() == k.get_device() == v.get_device() ==
+                cache.get_device() == slots.get_device())
+    except AttributeError:
+        good = False
+    if not good:
+        _refuse((k, names[0], bf16), (v, names[1], bf16), (cache, "cache", torch.uint8),
+                (slots, names[2], torch.int64))
     nb, hkv = _cache4(cache)
     krows, ks = _head_rows(k, names[0], hkv)
     vrows, vs = _head_rows(v, names[1], hkv)
-    if slots.dim() != 1 or not slots.is_contiguous():
+    if not slots.is_contiguous() or slots.dim() != 1:
         raise ValueError("%s must be contiguous, one-dimensional" % names[2])
-    n = slots.shape[0] if n_tokens is None else int(n_tokens)
-    if n > slots.shape[0] or n > krows or n > vrows:
+    most = slots.shape[0]
+    n = most if n_tokens is None else int(n_tokens)
+    if n > most or n > krows or n > vrows:
         raise ValueError("n_tokens exceeds the rows of %s/%s/%s" % names)
     return nb, hkv, ks, vs, n
 
@@ -630,9 +638,10 @@ def _step_metadata(query_start_loc, seq_lens, block_table, num_reqs):
 
 
 def _query_and_out(q, out):
-    if len(q.shape) != 3:
+    sh = q.shape
+    if len(sh) != 3:
         raise ValueError("q must be [rows, num_heads, head_size]")
-    hq = q.shape[1]
+    hq = sh[1]
     rows, qs = _head_rows(q, "q", hq)
     orows, os_ = _head_rows(out, "out", hq)
     if orows < rows:
@@ -648,9 +657,18 @@ def pkv_attention_int4(q, cache, query_start_loc, seq_lens, block_table, num_req
     prompts; see include/pkv.h."""
     torch = _torch or _T()
     bf16, i32 = torch.bfloat16, torch.int32
-    _on_device((q, "q", bf16), (cache, "cache", torch.uint8), (out, "out", bf16),
-               (query_start_loc, "query_start_loc", i32), (seq_lens, "seq_lens", i32),
-               (block_table, "block_table", i32))
+    try:
+        good = (q.dtype is bf16 and cache.dtype is torch.uint8 and out.dtype is bf16 and
+                query_start_loc.dtype is i32 and seq_lens.dtype is i32 and
+                block_table.dtype is i32 and _get_device() == q.get_device() ==
+                cache.get_device() == out.get_device() == query_start_loc.get_device() ==
+                seq_lens.get_device() == block_table.get_device())
+    except AttributeError:
+        good = False
+    if not good:
+        _refuse((q, "q", bf16), (cache, "cache", torch.uint8), (out, "out", bf16),
+                (query_start_loc, "query_start_loc", i32), (seq_lens, "seq_lens", i32),
+                (block_table, "block_table", i32))
     nb, hkv = _cache4(cache)
     rows, hq, qs, os_ = _query_and_out(q, out)
     num_reqs = int(num_reqs)
@@ -672,8 +690,16 @@ def pkv_page_bounds(key_cache, bounds, slot_mapping, n_tokens=None, stream=None)
     """The smallest and largest keys (bounds: [num_blocks, Hkv, 2, 128] bf16) of
     the pages that the step's tokens (slot_mapping, as in pkv_write) lie in."""
     torch = _torch or _T()
-    _on_device((key_cache, "key_cache", torch.bfloat16), (bounds, "bounds", torch.bfloat16),
-               (slot_mapping, "slot_mapping", torch.int64))
+    bf16 = torch.bfloat16
+    try:
+        good = (key_cache.dtype is bf16 and bounds.dtype is bf16 and
+                slot_mapping.dtype is torch.int64 and _get_device() == key_cache.get_device() ==
+                bounds.get_device() == slot_mapping.get_device())
+    except AttributeError:
+        good = False
+    if not good:
+        _refuse((key_cache, "key_cache", bf16), (bounds, "bounds", bf16),
+                (slot_mapping, "slot_mapping", torch.int64))
     cs = key_cache.shape
     if len(cs) != 4 or not key_cache.is_contiguous():
         raise ValueError("key_cache must be a contiguous [num_blocks, block_size, Hkv, head_size]")
@@ -706,21 +732,33 @@ def pkv_select_pages(q, bounds, query_start_loc, seq_lens, block_table, num_reqs
     the keys in them into sel_lens ([rows] int32); see include/pkv.h."""
     torch = _torch or _T()
     bf16, i32 = torch.bfloat16, torch.int32
-    _on_device((q, "q", bf16), (bounds, "bounds", bf16), (query_start_loc, "query_start_loc", i32),
-               (seq_lens, "seq_lens", i32), (block_table, "block_table", i32),
-               (sel_table, "sel_table", i32), (sel_lens, "sel_lens", i32))
-    if len(bounds.shape) != 4:
+    try:
+        good = (q.dtype is bf16 and bounds.dtype is bf16 and query_start_loc.dtype is i32 and
+                seq_lens.dtype is i32 and block_table.dtype is i32 and sel_table.dtype is i32 and
+                sel_lens.dtype is i32 and _get_device() == q.get_device() ==
+                bounds.get_device() == query_start_loc.get_device() == seq_lens.get_device() ==
+                block_table.get_device() == sel_table.get_device() == sel_lens.get_device())
+    except AttributeError:
+        good = False
+    if not good:
+        _refuse((q, "q", bf16), (bounds, "bounds", bf16),
+                (query_start_loc, "query_start_loc", i32), (seq_lens, "seq_lens", i32),
+                (block_table, "block_table", i32), (sel_table, "sel_table", i32),
+                (sel_lens, "sel_lens", i32))
+    sh = bounds.shape
+    if len(sh) != 4 or sh[2] != 2 or not bounds.is_contiguous():
         raise ValueError("bounds must be a contiguous [num_blocks, num_kv_heads, 2, head_size]")
-    nb, hkv, _, d = bounds.shape
-    _bounds(bounds, nb, hkv, d)
-    if len(q.shape) != 3:
+    nb, hkv, _, d = sh
+    sh = q.shape
+    if len(sh) != 3:
         raise ValueError("q must be [rows, num_heads, head_size]")
-    rows, qs = _head_rows(q, "q", q.shape[1])
+    hq = sh[1]
+    rows, qs = _head_rows(q, "q", hq)
     budget = _lists(sel_table, sel_lens, rows, hkv)
     num_reqs = int(num_reqs)
     width = _step_metadata(query_start_loc, seq_lens, block_table, num_reqs)
     rc = (_lib or load()).pkv_select_pages(
-        q.data_ptr(), qs, rows, q.shape[1], bounds.data_ptr(), nb, 16, hkv, d,
+        q.data_ptr(), qs, rows, hq, bounds.data_ptr(), nb, 16, hkv, d,
         query_start_loc.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), width, num_reqs,
         budget, int(first_pages), int(last_pages), sel_table.data_ptr(), sel_lens.data_ptr(),
         _stream(stream))
@@ -740,9 +778,24 @@ def pkv_attention_selected(q, key_cache, value_cache, sel_table, sel_lens, scale
     (pkv_select_pages); see include/pkv.h."""
     torch = _torch or _T()
     bf16, i32 = torch.bfloat16, torch.int32
-    _on_device((q, "q", bf16), (key_cache, "key_cache", bf16), (value_cache, "value_cache", bf16),
-               (sel_table, "sel_table", i32), (sel_lens, "sel_lens", i32), (out, "out", bf16))
-    nb, bs, hkv, d = _caches(key_cache, value_cache, bf16)
+    try:
+        good = (q.dtype is bf16 and key_cache.dtype is bf16 and value_cache.dtype is bf16 and
+                sel_table.dtype is i32 and sel_lens.dtype is i32 and out.dtype is bf16 and
+                _get_device() == q.get_device() == key_cache.get_device() ==
+                value_cache.get_device() == sel_table.get_device() == sel_lens.get_device() ==
+                out.get_device())
+    except AttributeError:
+        good = False
+    if not good:
+        _refuse((q, "q", bf16), (key_cache, "key_cache", bf16),
+                (value_cache, "value_cache", bf16), (sel_table, "sel_table", i32),
+                (sel_lens, "sel_lens", i32), (out, "out", bf16))
+    sh = key_cache.shape
+    if len(sh) != 4 or not (key_cache.is_contiguous() and value_cache.is_contiguous()):
+        raise ValueError("caches must be contiguous [num_blocks, block_size, Hkv, head_size]")
+    if sh != value_cache.shape:
+        raise ValueError("key_cache and value_cache shapes differ")
+    nb, bs, hkv, d = sh
     rows, hq, qs, os_ = _query_and_out(q, out)
     width = _lists(sel_table, sel_lens, rows, hkv)
     rc = (_lib or load()).pkv_attention_selected(
