@@ -93,7 +93,6 @@ __global__ void __launch_bounds__(256)
 
 // ------------------------------------------------------------------ selection
 
-constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32;
 constexpr int kSelKeys = 8192;  // scores of a (row, KV head) kept in shared memory
 
 struct Row {
@@ -145,6 +144,7 @@ __device__ __forceinline__ unsigned long long ordered64(double f) {
 }
 
 // total over the block of one int per thread
+template <int kSelWarps>
 __device__ __forceinline__ int block_sum(int v, int* part) {
   v = __reduce_add_sync(0xffffffffu, v);
   __syncthreads();  // (part may still be read)
@@ -214,13 +214,16 @@ __device__ __forceinline__ float score_pages(const SelectArgs& a, const int32_t*
 // and values), by a chain of block-wide counts while it selects.  64 of 2050 pages for one
 // row | 64 of 513 for 128 rows, 8 KV heads, us (floors 1.2 and 39.7): scores and selection
 // in two launches, the border found bit by bit 32 | 112; in one 43 | 100; the border by
-// histograms of eight bits 15 | 80; 256 pages a CTA where there are many 15 | 71 (issue
-// slots 50%, HBM 47%).
-template <int kPages>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a, int64_t row0) {
+// histograms of eight bits 15 | 80; 256 pages a CTA 16 | 72; and all of a row's by four
+// warps 14 | 65.  Of these the scores alone take 56; the border by one warp, without
+// barriers, and block ids kept in shared memory were slower (80, 73).
+template <int kPages, int kSelThreads>
+__global__ void __launch_bounds__(kSelThreads, kPages > 32 ? 1024 / kSelThreads : 1)
+    select_kernel(SelectArgs a, int64_t row0) {
+  constexpr int kSelWarps = kSelThreads / 32, kBins = kSelThreads < 256 ? 256 / kSelThreads : 1;
   extern __shared__ uint32_t keys[];  // [min(bt_width, kSelKeys)] in calls that score
   __shared__ int part[kSelWarps], part2[kSelWarps];
-  __shared__ int hist[kSelThreads];
+  __shared__ int hist[256];
   __shared__ float s_max[kSelWarps], s_sum[kSelWarps];
   __shared__ int s_last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -278,8 +281,10 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a, int64
     for (int i = 0; i < 8; ++i) size += up[i] - dn[i];
 #pragma unroll
     for (int o = 1; o < 16; o <<= 1) size += __shfl_xor_sync(0xffffffffu, size, o);
-    const int from = chunk * kPages + warp * (kPages / kSelWarps);
-    const int count = min(kPages / kSelWarps, end - from);
+    const int n_here = min(kPages, end - chunk * kPages);  // a warp's share: a multiple of 4
+    const int share = (n_here + 4 * kSelWarps - 1) / (4 * kSelWarps) * 4;
+    const int from = chunk * kPages + warp * share;
+    const int count = min(share, n_here - warp * share);
     if (count > 0)
       m = score_pages(a, bt, g, from, count, up, dn, [&](int page, float s) {
         if (needed > 1)
@@ -355,7 +360,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a, int64
   }
   while (bits > 0 && !(unordered(t + (uint32_t)((1ull << bits) - 1)) - unordered(t) <= eps)) {
     const int shift = max(bits - 8, 0);
-    hist[tid] = 0;
+    for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
     __syncthreads();
 #pragma unroll 4
     for (int i = i0; i < i1; ++i) {
@@ -363,8 +368,13 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a, int64
       if (bits >= 32 || d >> bits == 0) atomicAdd(hist + (d >> shift), 1);
     }
     __syncthreads();
-    // thread i: bin 255 - i and the bins above it
-    const int mine = hist[kSelThreads - 1 - tid];
+    // a thread's kBins bins, the highest first, and those above them
+    int c[kBins], mine = 0;
+#pragma unroll
+    for (int i = 0; i < kBins; ++i) {
+      c[i] = tid * kBins < 256 ? hist[255 - tid * kBins - i] : 0;
+      mine += c[i];
+    }
     int sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -376,8 +386,15 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a, int64
 #pragma unroll
     for (int w = 0; w < kSelWarps; ++w) sum += w < warp ? part[w] : 0;
     if (sum >= left && sum - mine < left) {
-      part2[0] = kSelThreads - 1 - tid;
-      part2[1] = left - (sum - mine);
+      int bin = 255 - tid * kBins, rest = left - (sum - mine);
+#pragma unroll
+      for (int i = 0; i + 1 < kBins; ++i)
+        if (rest > c[i] && bin == 255 - tid * kBins - i) {
+          rest -= c[i];
+          --bin;
+        }
+      part2[0] = bin;
+      part2[1] = rest;
     }
     __syncthreads();
     t += (uint32_t)part2[0] << shift;
@@ -471,22 +488,23 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a, int64
   }
   // A candidate's rank: those with a larger score, or an equal one and before it.  Up to
   // 256 of them by comparing each with all; more by the ties-th largest, bit by bit.
+  constexpr int kRanked = 256;
   unsigned long long t64 = 0;
-  if (cand > kSelThreads) {
+  if (cand > kRanked) {
 #pragma unroll 1
     for (int bit = 63; bit >= 0; --bit) {
       const unsigned long long c = t64 | 1ull << bit;
       int more = 0;
       for (int i = tid; i < cand; i += kSelThreads) more += ordered64(s64[i]) >= c;
-      if (block_sum(more, part) >= ties) t64 = c;
+      if (block_sum<kSelWarps>(more, part) >= ties) t64 = c;
     }
     int more = 0;
     for (int i = tid; i < cand; i += kSelThreads) more += ordered64(s64[i]) > t64;
-    ties -= block_sum(more, part);  // of the equal ones, the first
+    ties -= block_sum<kSelWarps>(more, part);  // of the equal ones, the first
   }
   auto taken = [&](int c, int equal) {  // candidate c; equal: candidates at t64 before it
     const unsigned long long v = ordered64(s64[c]);
-    if (cand > kSelThreads) return v > t64 || (v == t64 && equal < ties);
+    if (cand > kRanked) return v > t64 || (v == t64 && equal < ties);
     int rank = 0;
     for (int i = 0; i < cand; ++i) {
       const unsigned long long u = ordered64(s64[i]);
@@ -497,7 +515,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a, int64
   // equal ones before this thread's pages, then taken ones
   unsigned equal = 0;
   int c = (int)(before & 0xFFFF);
-  if (cand > kSelThreads) {
+  if (cand > kRanked) {
     for (int i = i0; i < i1; ++i)
       if (state_of(i) == kTie) equal += ordered64(s64[c++]) == t64;
     equal = scan(equal, &total);
@@ -508,7 +526,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a, int64
     const int st = state_of(i);
     if (st == kTie) {
       count += taken(c, (int)e);
-      e += cand > kSelThreads && ordered64(s64[c]) == t64;
+      e += cand > kRanked && ordered64(s64[c]) == t64;
       ++c;
     } else {
       count += st == kIn;
@@ -522,7 +540,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(SelectArgs a, int64
     bool in = st == kIn;
     if (st == kTie) {
       in = taken(c, (int)e);
-      e += cand > kSelThreads && ordered64(s64[c]) == t64;
+      e += cand > kRanked && ordered64(s64[c]) == t64;
       ++c;
     }
     if (in) out[at++] = __ldg(bt + first + i);
@@ -542,20 +560,31 @@ cudaError_t launch_page_bounds(const uint16_t* kc, int64_t num_blocks, int hkv, 
                           n_tokens, err);
 }
 
-// Pages a CTA scores: 256 where that gives every SM a CTA, else 32.  (64 of 513 pages for 128
-// rows of 8 KV heads: 80 us with 128 pages, 73 with 256, 75 with 512; one row with 2050
-// pages 15 us with 32.)
+// Pages a CTA scores.  512, by four warps, where one CTA then has all of a row's pages (the
+// last is not scored) and the CTAs fill five of the eight places of each SM: no scores pass
+// through memory, and eight CTAs an SM select and score at different times.  Else 256 by
+// eight warps, or 128 where that leaves SMs without one.  us with 128 | 256 | 512, 8 KV heads:
+//   4 rows of 513 pages    14 | 14 | 21      100 of 513    72 |  66 |  61
+//   1 of 2050              15 | 16 | 29      128 of 513    87 |  78 |  65
+//   1 of 8000              28 | 28 | 48      256 of 260   109 |  99 |  72
+//   64 of 513              47 | 44 | 55      512 of 70     76 |  76 |  54
+//   32 of 2050             79 | 71 | 77      256 of 513   154 | 135 | 119
+// (512 by eight warps, four CTAs an SM: 128 of 513 in 75; by sixteen 82; 32 a CTA: 1 of
+// 8000 in 55.)
 int select_chunk_pages(int64_t rows, int hkv, int64_t bt_width, int sms) {
-  return rows * hkv * bt_width >= (int64_t)sms * 256 ? 256 : 32;
+  if (bt_width - 1 <= 512 && rows * hkv >= 5 * (int64_t)sms) return 512;
+  return rows * hkv * bt_width >= (int64_t)sms * 256 ? 256 : 128;
 }
 
 cudaError_t launch_select(const SelectArgs& a, int64_t row0, int rows, bool score,
                           cudaStream_t st) {
   const int64_t chunks = score ? (a.bt_width + a.chunk_pages - 1) / a.chunk_pages : 1;
   const size_t smem = score ? (size_t)std::min<int64_t>(a.bt_width, kSelKeys) * 4 : 0;
-  return launch_dependent(a.chunk_pages == 256 ? select_kernel<256> : select_kernel<32>,
-                          dim3((unsigned)chunks, (unsigned)(rows * a.hkv)), dim3(kSelThreads), smem,
-                          st, a, row0);
+  return launch_dependent(a.chunk_pages == 512   ? select_kernel<512, 128>
+                          : a.chunk_pages == 256 ? select_kernel<256, 256>
+                                                 : select_kernel<128, 256>,
+                          dim3((unsigned)chunks, (unsigned)(rows * a.hkv)),
+                          dim3(a.chunk_pages == 512 ? 128 : 256), smem, st, a, row0);
 }
 
 }  // namespace pkv
