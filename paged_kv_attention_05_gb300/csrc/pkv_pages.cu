@@ -207,8 +207,8 @@ __device__ __forceinline__ float score_pages(const SelectArgs& a, const int32_t*
   return m;
 }
 
-// Scores and selection.  A CTA scores kPages pages of a (row, KV head), its warps an
-// eighth each; the last CTA of the (row, KV head) to finish selects.  Where one CTA has
+// Scores and selection.  A CTA scores kPages pages of a (row, KV head), its warps equal
+// shares; the last CTA of the (row, KV head) to finish selects.  Where one CTA has
 // all of its pages the scores never leave it.
 // Bound by HBM while it scores (512 bytes a page, a sixteenth of the page's own keys
 // and values), by a chain of block-wide counts while it selects.  64 of 2050 pages for one
@@ -218,7 +218,7 @@ __device__ __forceinline__ float score_pages(const SelectArgs& a, const int32_t*
 // warps 14 | 65.  Of these the scores alone take 56; the border by one warp, without
 // barriers, and block ids kept in shared memory were slower (80, 73).
 template <int kPages, int kSelThreads>
-__global__ void __launch_bounds__(kSelThreads, kPages > 32 ? 1024 / kSelThreads : 1)
+__global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads)
     select_kernel(SelectArgs a, int64_t row0) {
   constexpr int kSelWarps = kSelThreads / 32, kBins = kSelThreads < 256 ? 256 / kSelThreads : 1;
   extern __shared__ uint32_t keys[];  // [min(bt_width, kSelKeys)] in calls that score

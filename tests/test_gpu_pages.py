@@ -186,6 +186,29 @@ def test_select_ties_and_ranges(kind):
     assert pkv.pkv_get_error() == 0
 
 
+@pytest.mark.parametrize("width", [513, 200, 40])
+@pytest.mark.parametrize("kind", ["random", "few values", "twins", "near ties"])
+def test_select_of_many_rows_with_narrow_tables(kind, width):
+    """Enough rows and KV heads that one CTA of four warps takes all of a row's pages."""
+    top = 16 * width - 1
+    reqs = [(min(c, top), 1) for c in (top, top - 15, top - 16, 0, 15, 16, 255, 256, 400, 1000,
+                                       2047, 2048, 3333, 4096, 5000, 6100, 7001, 8000)] * 2
+    q, bounds, reqs, bt, qsl, seq = a_case(48, 24, reqs, width)
+    g, nb = gen(5), bounds.shape[0]
+    if kind == "few values":
+        q[:] = torch.randint(-1, 2, q.shape, generator=g, device="cuda").to(torch.bfloat16)
+        bounds[:] = 0
+        bounds[..., :3] = torch.randint(0, 2, (nb, 24, 2, 3), generator=g, device="cuda").float()
+    elif kind == "twins":
+        bounds[:] = bounds[torch.arange(nb, device="cuda") // 7 * 7]
+    elif kind == "near ties":
+        bounds[:] = bounds[:1]
+        bounds[:, :, 1, 5] = 1 + torch.randint(0, 8, (nb, 24), generator=g, device="cuda") * 2.0 ** -7
+        q[..., 5] = q[..., 5] * 2.0 ** -12
+    check_select(q, bounds, reqs, bt[:, :width].contiguous(), qsl, seq, 16, 1, 2)
+    assert pkv.pkv_get_error() == 0
+
+
 def test_select_launches_of_many_rows():
     """More rows times table entries than one launch takes, and a table of the
     largest width."""
