@@ -37,12 +37,21 @@ using namespace dev;
 // Smallest and largest keys of the pages that the step's tokens wrote.  A token
 // whose successor in the call lies in another page has the last slot of its page:
 // it forms the bounds of slots 0 .. its own.  A warp takes kTok tokens and one KV
-// head, four dimensions a lane, the page's 16 rows all in flight; the packed bf16
-// minimum and maximum are exact.  HBM-bound: 256 bytes a key.
-// One token a warp while there are few (their pages are read side by side), eight
-// when warps abound: a prompt's warps then look at eight slots at once instead of
-// one, and half of them have a page (8 chunks of 2047 tokens, 8 KV heads: 12.8 us with the
-// caches flushed, 7.4 in a row, floor 5.5; a step of 128 decodes 6.0, a launch's time).
+// head, a half-warp eight of a page's rows, eight dimensions a lane, all 16 rows in
+// flight; the packed bf16 minimum and maximum are exact.  HBM-bound: 256 bytes a key.
+// One token a warp while there are few (their pages are read side by side), sixteen
+// when warps abound: nearly every warp of a prompt has a page then.  8 chunks of 2047
+// tokens, 8 KV heads, floor 5.5 us: 8.6 (eight tokens a warp 9.0; and 8 bytes a lane, which
+// the compiler did not keep in flight, 12.6); a step of 128 decodes 5.0, a launch's time.
+// (asked for in program order: the compiler would rather wait than hold 16 rows)
+__device__ __forceinline__ uint4 load16(const uint16_t* p) {
+  uint4 v;
+  asm volatile("ld.global.cg.v4.b32 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
 template <int kTok>
 __global__ void __launch_bounds__(256)
     page_bounds_kernel(const uint16_t* __restrict__ kc, int64_t num_slots, int hkv,
@@ -69,24 +78,34 @@ __global__ void __launch_bounds__(256)
       todo &= todo - 1;
       const int64_t block = slot / kBlockSize;
       const int last = (int)(slot % kBlockSize);
-      const uint16_t* src = kc + (block * kBlockSize * hkv + h) * kHeadSize + lane * 4;
-      uint2 r[kBlockSize];
+      // (rows past the last are it again)
+      const uint16_t* src = kc + (block * kBlockSize * hkv + h) * kHeadSize + (lane & 15) * 8;
+      uint4 r[kBlockSize / 2];
 #pragma unroll
-      for (int i = 0; i < kBlockSize; ++i)  // (rows past the last are it again)
-        r[i] = __ldcg(reinterpret_cast<const uint2*>(src + (int64_t)min(i, last) * hkv * kHeadSize));
+      for (int i = 0; i < kBlockSize / 2; ++i)
+        r[i] = load16(src + (int64_t)min(2 * i + (lane >> 4), last) * hkv * kHeadSize);
       auto as2 = [](uint32_t w) { return *reinterpret_cast<__nv_bfloat162*>(&w); };
       auto bits = [](__nv_bfloat162 v) { return *reinterpret_cast<uint32_t*>(&v); };
-      __nv_bfloat162 lo0 = as2(r[0].x), lo1 = as2(r[0].y), hi0 = lo0, hi1 = lo1;
+      uint32_t lo[4] = {r[0].x, r[0].y, r[0].z, r[0].w}, hi[4] = {r[0].x, r[0].y, r[0].z, r[0].w};
 #pragma unroll
-      for (int i = 1; i < kBlockSize; ++i) {
-        lo0 = __hmin2(lo0, as2(r[i].x));
-        lo1 = __hmin2(lo1, as2(r[i].y));
-        hi0 = __hmax2(hi0, as2(r[i].x));
-        hi1 = __hmax2(hi1, as2(r[i].y));
+      for (int i = 1; i < kBlockSize / 2; ++i) {
+        const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          lo[k] = bits(__hmin2(as2(lo[k]), as2(w[k])));
+          hi[k] = bits(__hmax2(as2(hi[k]), as2(w[k])));
+        }
       }
-      uint16_t* dst = bounds + (block * hkv + h) * 2 * kHeadSize + lane * 4;
-      *reinterpret_cast<uint2*>(dst) = make_uint2(bits(lo0), bits(lo1));
-      *reinterpret_cast<uint2*>(dst + kHeadSize) = make_uint2(bits(hi0), bits(hi1));
+      // the other half-warp has the other eight rows: it keeps the maxima, this one the minima
+      uint32_t o[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const bool upper = lane >= 16;
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, upper ? lo[k] : hi[k], 16);
+        o[k] = bits(upper ? __hmax2(as2(hi[k]), as2(other)) : __hmin2(as2(lo[k]), as2(other)));
+      }
+      *reinterpret_cast<uint4*>(bounds + (block * hkv + h) * 2 * kHeadSize + lane * 8) =
+          make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
 }
@@ -553,9 +572,9 @@ cudaError_t launch_page_bounds(const uint16_t* kc, int64_t num_blocks, int hkv, 
                                const int64_t* slots, int64_t n_tokens, int* err, int sms,
                                cudaStream_t st) {
   const bool many = n_tokens * hkv > (int64_t)sms * 64;  // more than the warps an SM holds
-  const int64_t warps = (many ? (n_tokens + 7) / 8 : n_tokens) * hkv;
+  const int64_t warps = (many ? (n_tokens + 15) / 16 : n_tokens) * hkv;
   const unsigned blocks = (unsigned)std::min<int64_t>((warps + 7) / 8, (int64_t)sms * 8);
-  return launch_dependent(many ? page_bounds_kernel<8> : page_bounds_kernel<1>, dim3(blocks),
+  return launch_dependent(many ? page_bounds_kernel<16> : page_bounds_kernel<1>, dim3(blocks),
                           dim3(256), 0, st, kc, num_blocks * kBlockSize, hkv, bounds, slots,
                           n_tokens, err);
 }
