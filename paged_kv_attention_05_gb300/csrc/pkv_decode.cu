@@ -45,6 +45,8 @@
 // shares the plan, the work units and the merge.  pkv_attention_scored runs
 // instances of the two kernels here with its scores in step_logits (see Mode);
 // its units begin at the page of the first key that a row's window lets it see.
+#include <algorithm>
+
 #include "pkv_combine.cuh"
 #include "pkv_device.cuh"
 #include "pkv_sched.cuh"
@@ -1007,7 +1009,11 @@ cudaError_t launch_decode(const ScoredArgs& a, const Workspace& ws, int sms, cud
 }
 
 cudaError_t launch_combine(const AttnArgs& a, const Workspace& ws, int sms, cudaStream_t st) {
-  return launch_dependent(combine_kernel, dim3(sms * 8), dim3(kCombineThreads), 0, st, a, ws);
+  // (rows of selected pages: a warp for each row and head at most; one row of 32 heads, 64
+  // pages: 13.7 us for 15.1 with eight CTAs an SM)
+  const int64_t warps = a.sel ? a.q_rows * a.hq : INT32_MAX, per_block = kCombineThreads / 32;
+  const int blocks = (int)std::min<int64_t>(sms * 8, (warps + per_block - 1) / per_block);
+  return launch_dependent(combine_kernel, dim3(blocks), dim3(kCombineThreads), 0, st, a, ws);
 }
 
 }  // namespace pkv
