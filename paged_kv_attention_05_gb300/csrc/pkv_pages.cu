@@ -178,8 +178,9 @@ __device__ __forceinline__ int block_sum(int v, int* part) {
 // The fp32 scores of pages from .. from + count - 1 of a row for one KV head, by the
 // calling warp: put(page, score) for each; returns the largest bound met (in every
 // lane).  A half-warp reads one page's bounds (512 consecutive bytes), eight dimensions
-// a lane.
-template <typename Put>
+// a lane.  kStream: more bounds than the L2 holds pass by, none twice (64 of 513 pages for
+// 128 rows 63 -> 61 us, 68 for 78 after other work).
+template <bool kStream, typename Put>
 __device__ __forceinline__ float score_pages(const SelectArgs& a, const int32_t* bt, int g,
                                              int from, int count, const float (&up)[8],
                                              const float (&dn)[8], Put put) {
@@ -194,12 +195,13 @@ __device__ __forceinline__ float score_pages(const SelectArgs& a, const int32_t*
     }
     float mine = 0.f;  // the score of page b + lane
     const int steps = min(16, (count - b + 1) / 2);
-#pragma unroll 8
+#pragma unroll kStream ? 4 : 8
     for (int i = 0; i < steps; ++i) {
       const int blk = __shfl_sync(0xffffffffu, id, 2 * i + half);
       const uint16_t* p = a.bounds + ((int64_t)blk * a.hkv + g) * 2 * kHeadSize + l * 8;
-      const uint4 lo4 = __ldg(reinterpret_cast<const uint4*>(p));
-      const uint4 hi4 = __ldg(reinterpret_cast<const uint4*>(p + kHeadSize));
+      const uint4* at = reinterpret_cast<const uint4*>(p);
+      const uint4 lo4 = kStream ? __ldcs(at) : __ldg(at);
+      const uint4 hi4 = kStream ? __ldcs(at + kHeadSize / 8) : __ldg(at + kHeadSize / 8);
       const uint32_t lo[4] = {lo4.x, lo4.y, lo4.z, lo4.w}, hi[4] = {hi4.x, hi4.y, hi4.z, hi4.w};
       float s0 = 0.f, s1 = 0.f;
 #pragma unroll
@@ -234,7 +236,7 @@ __device__ __forceinline__ float score_pages(const SelectArgs& a, const int32_t*
 // row | 64 of 513 for 128 rows, 8 KV heads, us (floors 1.2 and 39.7): scores and selection
 // in two launches, the border found bit by bit 32 | 112; in one 43 | 100; the border by
 // histograms of eight bits 15 | 80; 256 pages a CTA 16 | 72; and all of a row's by four
-// warps 14 | 65.  Of these the scores alone take 56; the border by one warp, without
+// warps 14 | 61.  Of these the scores alone take 47; the border by one warp, without
 // barriers, and block ids kept in shared memory were slower (80, 73).
 template <int kPages, int kSelThreads>
 __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads)
@@ -244,7 +246,9 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads)
   __shared__ int part[kSelWarps], part2[kSelWarps];
   __shared__ int hist[256];
   __shared__ float s_max[kSelWarps], s_sum[kSelWarps];
-  __shared__ int s_last;
+  constexpr int kFew = 64;
+  __shared__ int s_last, s_idx[kFew];
+  __shared__ double s_exact[kFew];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rh = blockIdx.y, chunk = blockIdx.x;
   const int64_t row = row0 + rh / a.hkv;
@@ -305,7 +309,7 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads)
     const int from = chunk * kPages + warp * share;
     const int count = min(share, n_here - warp * share);
     if (count > 0)
-      m = score_pages(a, bt, g, from, count, up, dn, [&](int page, float s) {
+      m = score_pages<(kPages == 512)>(a, bt, g, from, count, up, dn, [&](int page, float s) {
         if (needed > 1)
           scores[page] = s;
         else if (page >= first)
@@ -476,9 +480,12 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads)
   }
 
   // More pages between than places: their scores in 64 bits, in the order of the pages.
-  double* s64 = a.exact + (int64_t)rh * a.bt_width;
+  // (a few, usually: kept in shared memory then.  Of 1024 selections in one wave one is
+  // among the last, and this is its path: 64 of 513 pages for 128 rows 65 -> 63 us)
+  const bool few = cand <= kFew;
+  double* s64 = few ? s_exact : a.exact + (int64_t)rh * a.bt_width;
   {
-    int32_t* idx = a.index + (int64_t)rh * a.bt_width;
+    int32_t* idx = few ? s_idx : a.index + (int64_t)rh * a.bt_width;
     int at = (int)(before & 0xFFFF);
     for (int i = i0; i < i1; ++i)
       if (state_of(i) == kTie) idx[at++] = i;
@@ -583,11 +590,11 @@ cudaError_t launch_page_bounds(const uint16_t* kc, int64_t num_blocks, int hkv, 
 // last is not scored) and the CTAs fill five of the eight places of each SM: no scores pass
 // through memory, and eight CTAs an SM select and score at different times.  Else 256 by
 // eight warps, or 128 where that leaves SMs without one.  us with 128 | 256 | 512, 8 KV heads:
-//   4 rows of 513 pages    14 | 14 | 21      100 of 513    72 |  66 |  61
-//   1 of 2050              15 | 16 | 29      128 of 513    87 |  78 |  65
-//   1 of 8000              28 | 28 | 48      256 of 260   109 |  99 |  72
-//   64 of 513              47 | 44 | 55      512 of 70     76 |  76 |  54
-//   32 of 2050             79 | 71 | 77      256 of 513   154 | 135 | 119
+//   4 rows of 513 pages    14 | 14 | 21      100 of 513    72 |  66 |  56
+//   1 of 2050              15 | 16 | 29      128 of 513    87 |  78 |  60
+//   1 of 8000              28 | 28 | 48      256 of 260   109 |  99 |  67
+//   64 of 513              47 | 44 | 55      512 of 70     76 |  76 |  51
+//   32 of 2050             79 | 71 | 77      256 of 513   154 | 135 | 111
 // (512 by eight warps, four CTAs an SM: 128 of 513 in 75; by sixteen 82; 32 a CTA: 1 of
 // 8000 in 55.)
 int select_chunk_pages(int64_t rows, int hkv, int64_t bt_width, int sms) {
