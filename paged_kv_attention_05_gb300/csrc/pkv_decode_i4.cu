@@ -53,6 +53,7 @@
 //   shifts by a high product, off the alu pipe    211 |  89)
 //   values by transposed loads, one fence a stage 187 |  80
 //   four pages a stage with two tiles             187 |  77
+//   (with 12 warps and one | two pages at a time         81 | 84, spills)
 //   three units a worker for four (the plan)      183 |  77
 // The first is bound by HBM (6.2 TB/s of codes and scales, 0.92 of the copy rate) with
 // the alu pipe, which takes the masks and shifts; the second by the latency of a

@@ -178,8 +178,7 @@ __device__ __forceinline__ int block_sum(int v, int* part) {
 // The fp32 scores of pages from .. from + count - 1 of a row for one KV head, by the
 // calling warp: put(page, score) for each; returns the largest bound met (in every
 // lane).  A half-warp reads one page's bounds (512 consecutive bytes), eight dimensions
-// a lane.  kStream: more bounds than the L2 holds pass by, none twice (64 of 513 pages for
-// 128 rows 63 -> 61 us, 68 for 78 after other work).
+// a lane.  kStream: the bounds, none read twice, are not to push others out of the L2.
 template <bool kStream, typename Put>
 __device__ __forceinline__ float score_pages(const SelectArgs& a, const int32_t* bt, int g,
                                              int from, int count, const float (&up)[8],
@@ -238,7 +237,7 @@ __device__ __forceinline__ float score_pages(const SelectArgs& a, const int32_t*
 // histograms of eight bits 15 | 80; 256 pages a CTA 16 | 72; and all of a row's by four
 // warps 14 | 61.  Of these the scores alone take 47; the border by one warp, without
 // barriers, and block ids kept in shared memory were slower (80, 73).
-template <int kPages, int kSelThreads>
+template <int kPages, int kSelThreads, bool kStream>
 __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads)
     select_kernel(SelectArgs a, int64_t row0) {
   constexpr int kSelWarps = kSelThreads / 32, kBins = kSelThreads < 256 ? 256 / kSelThreads : 1;
@@ -309,7 +308,7 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads)
     const int from = chunk * kPages + warp * share;
     const int count = min(share, n_here - warp * share);
     if (count > 0)
-      m = score_pages<(kPages == 512)>(a, bt, g, from, count, up, dn, [&](int page, float s) {
+      m = score_pages<kStream>(a, bt, g, from, count, up, dn, [&](int page, float s) {
         if (needed > 1)
           scores[page] = s;
         else if (page >= first)
@@ -596,7 +595,8 @@ cudaError_t launch_page_bounds(const uint16_t* kc, int64_t num_blocks, int hkv, 
 //   64 of 513              47 | 44 | 55      512 of 70     76 |  76 |  51
 //   32 of 2050             79 | 71 | 77      256 of 513   154 | 135 | 111
 // (512 by eight warps, four CTAs an SM: 128 of 513 in 75; by sixteen 82; 32 a CTA: 1 of
-// 8000 in 55.)
+// 8000 in 55.)  Half of the L2 or more of bounds are streamed: 128 of 513 pages 63 -> 61, 32
+// of 2050 77 -> 72, 30 of 1000 43 -> 40, 8 of 8000 94 -> 89.
 int select_chunk_pages(int64_t rows, int hkv, int64_t bt_width, int sms) {
   if (bt_width - 1 <= 512 && rows * hkv >= 5 * (int64_t)sms) return 512;
   return rows * hkv * bt_width >= (int64_t)sms * 256 ? 256 : 128;
@@ -606,9 +606,11 @@ cudaError_t launch_select(const SelectArgs& a, int64_t row0, int rows, bool scor
                           cudaStream_t st) {
   const int64_t chunks = score ? (a.bt_width + a.chunk_pages - 1) / a.chunk_pages : 1;
   const size_t smem = score ? (size_t)std::min<int64_t>(a.bt_width, kSelKeys) * 4 : 0;
-  return launch_dependent(a.chunk_pages == 512   ? select_kernel<512, 128>
-                          : a.chunk_pages == 256 ? select_kernel<256, 256>
-                                                 : select_kernel<128, 256>,
+  const bool stream = rows * a.hkv * a.bt_width >= 131072;  // (pages' bounds of 512 bytes)
+  return launch_dependent(a.chunk_pages == 512 ? select_kernel<512, 128, true>
+                          : a.chunk_pages == 128 ? select_kernel<128, 256, false>
+                          : stream               ? select_kernel<256, 256, true>
+                                                 : select_kernel<256, 256, false>,
                           dim3((unsigned)chunks, (unsigned)(rows * a.hkv)),
                           dim3(a.chunk_pages == 512 ? 128 : 256), smem, st, a, row0);
 }
