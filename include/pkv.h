@@ -342,9 +342,9 @@ int pkv_attention_scored_packed(const pkv_attention_scored_args* args);
  *   hold every request's query rows and lengths, and no later call reads
  *   query_start_loc or seq_lens again.  The plan lives in this device's
  *   workspace (grown here if needed, so reserve it before a graph capture)
- *   and replaces the previous one; pkv_attention, pkv_attention_int8 and a
- *   workspace reallocation (a call needing more room, pkv_reserve_workspace)
- *   replace or drop it too.  Requests whose metadata fail a check are
+ *   and replaces the previous one; pkv_attention, its int8, int4, scored and
+ *   selected forms and a workspace reallocation (a call needing more room,
+ *   pkv_reserve_workspace) replace or drop it too.  Requests whose metadata fail a check are
  *   reported in the error word when the plan kernel runs.
  *
  * pkv_attention_planned(q, q_row_stride, num_heads, key_cache, value_cache,

@@ -459,3 +459,47 @@ def test_other_stream_and_lists_from_it():
     torch.cuda.current_stream().wait_stream(side)
     d.check()
     assert pkv.pkv_get_error() == 0
+
+
+def test_a_step_plan_and_the_page_calls():
+    """The write, the bounds and the selection leave a step plan as it is (their workspace
+    is another); the attention over selected pages replaces it with its own, which serves
+    no planned call."""
+    d = Decode([900, 5, 333, 2000], 1, 16, 4, 12, 6)
+    d.next()
+    want = torch.full_like(d.out, float("nan"))
+    plain = (d.qsl, d.seq, d.bt, d.R, D ** -0.5)
+    pkv.pkv_write(d.k, d.v, d.kc, d.vc, d.slots)
+    pkv.pkv_attention(d.q, d.kc, d.vc, *plain, want)
+    pkv.pkv_plan(d.q.shape[0], 16, 4, d.qsl, d.seq, d.bt.shape[1], d.R)
+    pkv.pkv_write(d.k, d.v, d.kc, d.vc, d.slots)
+    pkv.pkv_page_bounds(d.kc, d.bounds, d.slots)
+    pkv.pkv_select_pages(d.q, d.bounds, d.qsl, d.seq, d.bt, d.R, d.table, d.lens, 1, 2)
+    got = torch.full_like(d.out, float("nan"))
+    pkv.pkv_attention_planned(d.q, d.kc, d.vc, d.bt, D ** -0.5, got)
+    assert torch.equal(got[:d.rows], want[:d.rows])
+    pkv.pkv_attention_selected(d.q, d.kc, d.vc, d.table, d.lens, D ** -0.5, d.out)
+    d.check()
+    with pytest.raises(pkv.PkvError):
+        pkv.pkv_attention_planned(d.q, d.kc, d.vc, d.bt, D ** -0.5, got)
+    assert pkv.pkv_get_error() == 0
+
+
+def test_selected_lists_as_a_block_table():
+    """With one KV head the lists are a block table and the keys in them sequence lengths:
+    attention over the lists is pkv_attention over those, whose plan must see the selection
+    finished."""
+    d = Decode([900, 5, 333, 2000], 1, 8, 1, 12, 9)
+    other = torch.full_like(d.out, float("nan"))
+    for _ in range(8):
+        d.next()
+        pkv.pkv_write(d.k, d.v, d.kc, d.vc, d.slots)
+        pkv.pkv_page_bounds(d.kc, d.bounds, d.slots)
+        pkv.pkv_select_pages(d.q, d.bounds, d.qsl, d.seq, d.bt, d.R, d.table, d.lens, 1, 2)
+        pkv.pkv_attention(d.q, d.kc, d.vc, d.qsl, d.lens, d.table.view(-1, 12), d.R, D ** -0.5,
+                          other)
+        pkv.pkv_attention_selected(d.q, d.kc, d.vc, d.table, d.lens, D ** -0.5, d.out)
+        d.check()
+        d.out.copy_(other)
+        d.check()
+    assert pkv.pkv_get_error() == 0
