@@ -86,6 +86,13 @@ int cuda_fail(cudaError_t e, const char* what) {
   return fail(PKV_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
+// Zeroes device memory, before it returns: a clear on the legacy stream goes on after the
+// call, and a stream made non-blocking (every stream of torch's pool) does not wait for it.
+cudaError_t clear_now(void* p, size_t bytes) {
+  const cudaError_t e = cudaMemset(p, 0, bytes);
+  return e == cudaSuccess ? cudaStreamSynchronize(nullptr) : e;
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // Device state of the current device, initialised on first use.
@@ -105,8 +112,8 @@ int current_state(DeviceState** out) {
     s.sms = prop.multiProcessorCount;
     e = cudaMalloc(&s.err, sizeof(int));
     if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(error word)");
-    e = cudaMemset(s.err, 0, sizeof(int));
-    if (e != cudaSuccess) return cuda_fail(e, "cudaMemset(error word)");
+    e = clear_now(s.err, sizeof(int));
+    if (e != cudaSuccess) return cuda_fail(e, "clear a new error word");
     s.ready = true;
   }
   *out = &s;
@@ -138,8 +145,8 @@ int ensure_buffer(void** buf, size_t* bytes, bool* in_graph, size_t need, const 
   const size_t grow = need + need / 4;
   e = cudaMalloc(buf, grow);
   if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(workspace)");
-  e = cudaMemset(*buf, 0, grow);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaMemset(workspace)");
+  e = clear_now(*buf, grow);
+  if (e != cudaSuccess) return cuda_fail(e, "clear a new workspace");
   *bytes = grow;
   return PKV_OK;
 }
@@ -1080,7 +1087,7 @@ extern "C" int pkv_get_error(void* stream, int32_t* bits) {
   if (s.ready) {
     e = cudaMemcpy(&v, s.err, sizeof(int), cudaMemcpyDeviceToHost);
     if (e != cudaSuccess) return cuda_fail(e, "read error word");
-    e = cudaMemset(s.err, 0, sizeof(int));
+    e = clear_now(s.err, sizeof(int));
     if (e != cudaSuccess) return cuda_fail(e, "clear error word");
   }
   int w = 0;

@@ -175,6 +175,8 @@ int noalloc_take_error(int dev, int* bits) {
   int v = 0;
   cudaError_t e = cudaMemcpy(&v, g_err_ptr[dev], sizeof(int), cudaMemcpyDeviceToHost);
   if (e == cudaSuccess) e = cudaMemset(g_err_ptr[dev], 0, sizeof(int));
+  // (a call on a non-blocking stream does not wait for the clear by itself)
+  if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
   if (e != cudaSuccess) return (int)e;
   *bits = v;
   return 0;
