@@ -21,7 +21,8 @@
 // chain, a join, 4 exchanges, G - 1 additions in U and D, and one in reserve for
 // each product's second order.  With T the k-th largest fp32 score, a page above
 // T + 2 eps is among the k largest and one below T - 2 eps is not; where those between
-// are more than the places left, they are scored again in 64 bits.
+// are more than the places left, they are scored again in 64 bits.  (Where S M is 2^126
+// or more, fp32 sums may overflow: all are.)
 #include <algorithm>
 
 #include "pkv_internal.cuh"
@@ -350,8 +351,10 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads)
   const int i0 = min(tid * own, mid), i1 = min(i0 + own, mid);
   auto key_of = [&](int i) { return in_smem ? keys[i] : ordered(__ldcg(scores + first + i)); };
   // (a little more than (G + 16) 2^-24, for the roundings of S itself, and what
-  // products below fp32's range lose)
-  const float eps = (float)(G + 18) * 0x1p-24f * size * m + 0x1p-140f;
+  // products below fp32's range lose; sums that may have passed its largest number, 2^128,
+  // say nothing: every page is scored again then)
+  const float eps =
+      size * m < 0x1p126f ? (float)(G + 18) * 0x1p-24f * (size * m) + 0x1p-140f : INFINITY;
 
   // The k-th largest key, eight bits a step from the highest that differs, until what is
   // left of it is below eps: it lies in t .. t + 2^bits - 1.

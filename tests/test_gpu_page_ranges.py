@@ -1,0 +1,49 @@
+"""pkv_select_pages where its 32-bit scores cannot be trusted, beside bad requests and
+next to other requests' bounds, against the 64-bit definition."""
+import pytest
+import torch
+
+import paged_kv_attention_05_gb300 as pkv
+
+pytestmark = pytest.mark.gpu
+
+import test_gpu_pages as P  # noqa: E402
+
+BITS = pkv.DEV_ERR_BITS
+
+
+@pytest.mark.parametrize("e", [50, 58, 60, 61, 62, 64, 66, 68, 71, 75])
+@pytest.mark.parametrize("hq,hkv,width", [(16, 4, None), (2, 2, None), (48, 24, 513)])
+def test_scores_past_32_bits(e, hq, hkv, width):
+    """Sums of products past fp32's largest number (2^128) that cancel, or do not, over pages
+    whose bounds differ in size: q and bounds of about 2^e, queries of both signs."""
+    if width:
+        top = 16 * width - 1
+        reqs = [(min(c, top), 1) for c in (top, 0, 400, 1000, 2048, 3333, 5000, 7001, 8000)] * 4
+    else:
+        reqs = P.REQS
+    q, bounds, reqs, bt, qsl, seq = P.a_case(hq, hkv, reqs, 100 + e)
+    g = P.gen(e)
+    size = torch.randint(-12, 1, (bounds.shape[0], hkv, 1, 1), generator=g, device="cuda")
+    bounds *= 2.0 ** (e + size).double()
+    q *= 2.0 ** e
+    if width:
+        bt = bt[:, :width].contiguous()
+    P.check_select(q, bounds, reqs, bt, qsl, seq, 16, 1, 2)
+    assert pkv.pkv_get_error() == 0
+
+
+def test_a_page_whose_sums_overflow_to_both_sides():
+    """Its score is 0, its fp32 sums are inf - inf; eleven small pages are larger."""
+    q = torch.full((1, 1, P.D), 2.0 ** 62, dtype=torch.bfloat16, device="cuda")
+    q[..., 64:] *= -1
+    bounds = torch.zeros(13, 1, 2, P.D, dtype=torch.bfloat16, device="cuda")
+    bounds[0] = 2.0 ** 62
+    for j in range(1, 12):
+        bounds[j, :, :, :64] = 2.0 ** 50 * (1 + j / 16)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table, lens = P.run_select(q, bounds, [(12 * 16 + 3, 1)], torch.arange(13, **i32).view(1, -1),
+                               torch.tensor([0, 1], **i32), torch.tensor([12 * 16 + 4], **i32),
+                               4, 0, 1)
+    assert pkv.pkv_get_error() == 0
+    assert table.flatten().tolist() == [9, 10, 11, 12] and lens.tolist() == [3 * 16 + 4]
