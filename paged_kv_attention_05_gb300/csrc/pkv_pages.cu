@@ -188,7 +188,8 @@ __device__ __forceinline__ float score_pages(const SelectArgs& a, const int32_t*
   __nv_bfloat162 m2 = __float2bfloat162_rn(0.f);
   for (int b = 0; b < count; b += 32) {
     const int page = b + lane;
-    int id = page < count ? __ldg(bt + from + page) : 0;
+    // (past the last page it is the last one again: no other page's bounds count)
+    int id = __ldg(bt + from + min(page, count - 1));
     if (id < 0 || (int64_t)id >= a.num_blocks) {
       atomicOr(a.err, PKV_DEV_ERR_BLOCK_ID);
       id = 0;

@@ -47,3 +47,30 @@ def test_a_page_whose_sums_overflow_to_both_sides():
                                4, 0, 1)
     assert pkv.pkv_get_error() == 0
     assert table.flatten().tolist() == [9, 10, 11, 12] and lens.tolist() == [3 * 16 + 4]
+
+
+def test_bounds_of_a_page_of_nobody_cost_nothing():
+    """Block 0 belongs to no row here, and its bounds are infinite: the lists are those of
+    the definition, and no row's pages are scored again in 64 bits for its sake (all were)."""
+    reqs = [(16 * 2047 - 5 - 16 * r, 1) for r in range(8)]
+    q, bounds, reqs, bt, qsl, seq = P.a_case(16, 4, reqs, 7)
+    bounds = torch.cat([bounds[:1], bounds]).contiguous()
+    bt = torch.where(bt >= 0, bt + 1, bt)
+
+    def once():
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        for _ in range(10):
+            got = P.run_select(q, bounds, reqs, bt, qsl, seq, 64, 0, 1)
+        b.record()
+        b.synchronize()
+        return a.elapsed_time(b), got
+
+    times = {}
+    for value in (0.5, float("inf")):
+        bounds[0] = value
+        once()
+        times[value] = sorted(once()[0] for _ in range(9))[4]
+        P.check_select(q, bounds, reqs, bt, qsl, seq, 64, 0, 1)
+    assert pkv.pkv_get_error() == 0
+    assert times[float("inf")] < 1.5 * times[0.5], times
