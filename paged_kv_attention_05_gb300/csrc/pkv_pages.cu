@@ -115,8 +115,9 @@ __global__ void __launch_bounds__(256)
 
 constexpr int kSelKeys = 8192;  // scores of a (row, KV head) kept in shared memory
 
+constexpr int kNone = -1, kUnknown = -2;
 struct Row {
-  int r, pos;  // request (-1: the row belongs to no valid one), position
+  int r, pos;  // request (kNone: the row belongs to no valid one), position
   int n;       // pages
 };
 
@@ -127,10 +128,14 @@ __device__ __forceinline__ int meta_errors(const SelectArgs& a, int q0, int q1, 
   return 0;
 }
 
+__device__ __forceinline__ Row row_of(int64_t row, int r, int q0, int q1, int L) {
+  const int pos = L - (q1 - q0) + (int)(row - q0);
+  return Row{r, pos, pos / kBlockSize + 1};
+}
 // The request and position of a query row.  (Decode batches have a row per
-// request: the guess r = row saves the search's chain of reads.)
+// request: the guess r = row saves the search's chain of reads.)  kUnknown: an entry out
+// of order misled the search, or the request that owns the row is bad (see scan_row).
 __device__ __forceinline__ Row find_row(const SelectArgs& a, int64_t row) {
-  Row x{-1, 0, 0};
   int lo = (int)min(row, (int64_t)a.num_reqs - 1);
   int q0 = __ldcg(a.qsl + lo), q1 = __ldcg(a.qsl + lo + 1), L = __ldcg(a.seq_lens + lo);
   if (!(q0 <= row && row < q1)) {
@@ -141,11 +146,21 @@ __device__ __forceinline__ Row find_row(const SelectArgs& a, int64_t row) {
     }
     q0 = __ldcg(a.qsl + lo), q1 = __ldcg(a.qsl + lo + 1), L = __ldcg(a.seq_lens + lo);
   }
-  if (row < q0 || row >= q1 || meta_errors(a, q0, q1, L)) return x;  // (or past the last)
-  x.r = lo;
-  x.pos = L - (q1 - q0) + (int)(row - q0);
-  x.n = x.pos / kBlockSize + 1;
-  return x;
+  const bool past = lo == a.num_reqs - 1 && q0 <= q1 && q1 <= row;  // of the last request
+  if (q0 <= row && row < q1 && !meta_errors(a, q0, q1, L)) return row_of(row, lo, q0, q1, L);
+  return Row{past ? kNone : kUnknown, 0, 0};
+}
+// The first request that has the row and passes the checks, if there is one (by the whole
+// warp, 32 at a time).
+__device__ __forceinline__ Row scan_row(const SelectArgs& a, int64_t row) {
+  int found = a.num_reqs;
+  for (int r = threadIdx.x & 31; r < a.num_reqs && found == a.num_reqs; r += 32) {
+    const int q0 = __ldcg(a.qsl + r), q1 = __ldcg(a.qsl + r + 1);
+    if (q0 <= row && row < q1 && !meta_errors(a, q0, q1, __ldcg(a.seq_lens + r))) found = r;
+  }
+  const int r = (int)__reduce_min_sync(0xffffffffu, (unsigned)found);
+  if (r == a.num_reqs) return Row{kNone, 0, 0};
+  return row_of(row, r, __ldcg(a.qsl + r), __ldcg(a.qsl + r + 1), __ldcg(a.seq_lens + r));
 }
 
 __device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
@@ -255,28 +270,35 @@ __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads)
   const int64_t row = row0 + rh / a.hkv;
   const int g = rh % a.hkv, G = a.hq / a.hkv;
   grid_dep_wait();
-  // U and D, eight dimensions a lane (asked for beside the metadata)
+  // U and D, eight dimensions a lane (asked for beside the metadata; once more where the
+  // request has to be looked for, as they would cost registers meanwhile)
   const uint16_t* q = a.q + row * a.q_stride + (int64_t)g * G * kHeadSize;
   float up[8], dn[8];
+  Row x{kUnknown, 0, 0};
+  for (;;) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) up[i] = dn[i] = 0.f;
+    for (int i = 0; i < 8; ++i) up[i] = dn[i] = 0.f;
 #pragma unroll 4
-  for (int h = 0; h < G; ++h) {
-    const uint4 w4 = __ldg(reinterpret_cast<const uint4*>(q + h * kHeadSize + (lane & 15) * 8));
-    const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+    for (int h = 0; h < G; ++h) {
+      const uint4 w4 = __ldg(reinterpret_cast<const uint4*>(q + h * kHeadSize + (lane & 15) * 8));
+      const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float v = i & 1 ? hi16(w[i >> 1]) : lo16(w[i >> 1]);
-      up[i] += fmaxf(v, 0.f);
-      dn[i] += fminf(v, 0.f);
+      for (int i = 0; i < 8; ++i) {
+        const float v = i & 1 ? hi16(w[i >> 1]) : lo16(w[i >> 1]);
+        up[i] += fmaxf(v, 0.f);
+        dn[i] += fminf(v, 0.f);
+      }
     }
+    if (x.r != kUnknown) break;
+    x = find_row(a, row);
+    if (x.r != kUnknown) break;
+    x = scan_row(a, row);
   }
   if (chunk == 0 && rh == 0 && row0 == 0)
     for (int r = tid; r < a.num_reqs; r += kSelThreads) {
       const int bad = meta_errors(a, __ldcg(a.qsl + r), __ldcg(a.qsl + r + 1), __ldcg(a.seq_lens + r));
       if (bad) atomicOr(a.err, bad);
     }
-  const Row x = find_row(a, row);
   const int n = x.n;
   if (x.r < 0 || n <= a.budget || a.budget == a.first + a.last) {
     // nothing to score: no list, or all pages, or the first and last ones

@@ -74,3 +74,25 @@ def test_bounds_of_a_page_of_nobody_cost_nothing():
         P.check_select(q, bounds, reqs, bt, qsl, seq, 64, 0, 1)
     assert pkv.pkv_get_error() == 0
     assert times[float("inf")] < 1.5 * times[0.5], times
+
+
+def test_rows_of_valid_requests_beside_bad_ones():
+    """A request of decreasing or negative query_start_loc is skipped; the others keep
+    their rows, as in pkv_attention."""
+    reqs = [(100 + 90 * r, 2) for r in range(12)]
+    q, bounds, reqs, bt, qsl, seq = P.a_case(8, 2, reqs, 21)
+    good, lens = P.run_select(q, bounds, reqs, bt, qsl, seq, 8, 0, 1)
+    assert pkv.pkv_get_error() == 0
+    for at, value in ((3, -5), (6, -1), (5, 999), (6, 999), (9, 1000), (1, 30)):
+        bad = qsl.clone()
+        bad[at] = value
+        t, n = P.run_select(q, bounds, reqs, bt, bad, seq, 8, 0, 1)
+        assert pkv.pkv_get_error() & BITS["QSL"]
+        for r in range(12):
+            rows = slice(2 * r, 2 * r + 2)
+            if r in (at - 1, at):       # the two requests that the entry belongs to
+                assert not n[rows].any() and bool((t[rows] == -5).all()), (at, value, r)
+            else:
+                assert torch.equal(n[rows], lens[rows]) and torch.equal(t[rows], good[rows]), \
+                    (at, value, r)
+        assert not n[24:].any()
