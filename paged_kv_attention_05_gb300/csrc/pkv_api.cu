@@ -120,10 +120,10 @@ int current_state(DeviceState** out) {
   return PKV_OK;
 }
 
-// Grows *buf to `need` bytes and a quarter more, zeroed; allocation only outside
-// capture.  *grown tells whether it did.
-int ensure_buffer(void** buf, size_t* bytes, bool* in_graph, size_t need, const char* reserve,
-                  cudaStream_t st, bool* grown) {
+// Grows *buf to `need` bytes and a quarter more (but to no more than `most` where that
+// is enough), zeroed; allocation only outside capture.  *grown tells whether it did.
+int ensure_buffer(void** buf, size_t* bytes, bool* in_graph, size_t need, size_t most,
+                  const char* reserve, cudaStream_t st, bool* grown) {
   *grown = false;
   if (need <= *bytes) return PKV_OK;
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
@@ -142,7 +142,7 @@ int ensure_buffer(void** buf, size_t* bytes, bool* in_graph, size_t need, const 
   *buf = nullptr;
   *bytes = 0;
   *grown = true;
-  const size_t grow = need + need / 4;
+  const size_t grow = std::max(need, std::min(need + need / 4, most));
   e = cudaMalloc(buf, grow);
   if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(workspace)");
   e = clear_now(*buf, grow);
@@ -155,7 +155,7 @@ int ensure_buffer(void** buf, size_t* bytes, bool* in_graph, size_t need, const 
 int ensure_workspace(DeviceState* s, const Sizes& z, cudaStream_t st, Workspace* ws) {
   bool grown = false;
   const int rc = ensure_buffer(&s->ws, &s->ws_bytes, &s->ws_in_graph, workspace_bytes(z),
-                               "pkv_reserve_workspace", st, &grown);
+                               SIZE_MAX, "pkv_reserve_workspace", st, &grown);
   if (grown) s->plan_valid = false;  // the plan lived in the old workspace
   if (rc) return rc;
   // carve for the capacity actually held, scaled from the request
@@ -801,18 +801,21 @@ int check_rows4(const void* k, int64_t k_row_stride, const void* v, int64_t v_ro
 // The workspace of pkv_select_pages: a counter for each row of a launch and KV head (in
 // front, at the same place in every call: they are zero between calls), and 20 bytes a
 // page of theirs.  A launch takes at most as many rows as 2^24 pages, or 65535 (row, KV
-// head)s, have, so that many rows over wide tables need no more than 340 MB.  (Room that
+// head)s, have, so that many rows over wide tables take no more than 340 MB.  (Room that
 // never shrinks with the arguments: what is reserved for large ones serves smaller ones.)
 constexpr int64_t kSelectPairs = 65535;  // also the grid's limit
+constexpr int64_t kSelectPages = int64_t(1) << 24;
+constexpr size_t kSelectCounters = (size_t)(kSelectPairs + 1) * sizeof(int);
+constexpr size_t kSelectBytes = (size_t)kSelectPages * 20 + kSelectCounters;  // of most calls
 struct SelectSizes {
   int64_t rows;  // of a launch
   size_t bytes;
 };
 SelectSizes select_sizes(int64_t q_rows, int64_t width, int hkv) {
-  const int64_t per_row = width * hkv, most = std::max<int64_t>(per_row, int64_t(1) << 24);
+  const int64_t per_row = width * hkv, most = std::max<int64_t>(per_row, kSelectPages);
   const int64_t rows = std::min(most / per_row, kSelectPairs / hkv);
-  return {std::min(q_rows, rows), (size_t)std::min(q_rows * per_row, most) * 20 +
-                                      (size_t)(kSelectPairs + 1) * sizeof(int)};
+  return {std::min(q_rows, rows),
+          (size_t)std::min(q_rows * per_row, most) * 20 + kSelectCounters};
 }
 
 }  // namespace
@@ -966,12 +969,12 @@ extern "C" int pkv_select_pages(const void* q, int64_t q_row_stride, int64_t q_r
   const bool score = block_table_width > budget && budget > first_pages + last_pages;
   if (score) {
     bool grown = false;
-    rc = ensure_buffer(&s->sel_ws, &s->sel_bytes, &s->sel_in_graph, z.bytes, "pkv_reserve_select",
-                       st, &grown);
+    rc = ensure_buffer(&s->sel_ws, &s->sel_bytes, &s->sel_in_graph, z.bytes, kSelectBytes,
+                       "pkv_reserve_select", st, &grown);
     if (rc) return rc;
     note_capture(&s->sel_in_graph, st);
     a.done = static_cast<int*>(s->sel_ws);
-    uint8_t* p = static_cast<uint8_t*>(s->sel_ws) + (kSelectPairs + 1) * sizeof(int);
+    uint8_t* p = static_cast<uint8_t*>(s->sel_ws) + kSelectCounters;
     const int64_t n = z.rows * num_kv_heads * block_table_width;
     a.exact = reinterpret_cast<double*>(p);
     a.scores = reinterpret_cast<float*>(p + n * 8);
@@ -1002,7 +1005,7 @@ extern "C" int pkv_reserve_select(int64_t max_q_rows, int64_t block_table_width,
   bool grown = false;
   return ensure_buffer(&s->sel_ws, &s->sel_bytes, &s->sel_in_graph,
                        select_sizes(max_q_rows, block_table_width, num_kv_heads).bytes,
-                       "pkv_reserve_select", nullptr, &grown);
+                       kSelectBytes, "pkv_reserve_select", nullptr, &grown);
 }
 
 extern "C" int pkv_attention_selected(const void* q, int64_t q_row_stride, int64_t q_rows,
