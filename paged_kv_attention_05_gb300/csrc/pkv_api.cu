@@ -997,6 +997,7 @@ extern "C" int pkv_reserve_select(int64_t max_q_rows, int64_t block_table_width,
   if (max_q_rows < 0 || block_table_width < 0 || block_table_width > kMaxBtWidth ||
       num_kv_heads <= 0 || num_kv_heads > 32767)
     return fail(PKV_ERR_ARG, "bad sizes");
+  if (max_q_rows > INT32_MAX) return fail(PKV_ERR_UNSUPPORTED, "max_q_rows above 2^31");
   std::lock_guard<std::mutex> lock(g_mu);
   DeviceState* s = nullptr;
   int rc = current_state(&s);
