@@ -30,7 +30,10 @@
 //     16 keys of a page are the MMA rows in the order kappa(m), so that the key rows
 //     that eight lanes read lie in different banks.
 //   * query rows are scaled by a power of two, so that their largest value is
-//     between 2^10 and 2^11 in fp16: bf16's 8 bits stay exact, whatever the range.
+//     between 2^10 and 2^11 in fp16: bf16's 8 bits stay exact, whatever the range.  Rows of up
+//     to 2^110: the factor that undoes it, and the codes' 2^24, stays finite (applied to the
+//     scales and zeros apart, for rows up to 2^127, it took 128 decodes of 8192 keys from
+//     182.4 to 183.9 us, and lost keys above 2^104).
 //   * weights: e_j t_j is rounded to fp16 (2^-12 of itself at most).  The
 //     reference follows the largest e_j t_j of a row, not the largest e_j: fp16's range
 //     then holds every weight that counts, however large or small the value rows'
@@ -75,7 +78,8 @@ using namespace dev;
 constexpr uint32_t kNib0 = 0x000F000Fu, kNib1 = 0x00F000F0u;
 constexpr float kMaxWeight = 16384.f;  // e_j t_j that the reference is kept for
 // The scale of a value row without spread counts as this (its codes are zero), so that
-// its e_j is held below 2^54 by the same bound; scales of others are above it.
+// its e_j is held below 2^54 by the same bound; scales of others are above it.  (Zeros of up
+// to 2^60: a unit's sum of e_j y_j stays finite.)
 constexpr float kMinScale = 0x1p-40f;
 
 // Instances: items of at most 8 * kTiles query rows.  The rings take what shared memory
