@@ -492,8 +492,9 @@ int pkv_read_int4(const void* cache, int64_t num_blocks, int32_t block_size, int
  *
  * Decode-path requests (query_len * (num_heads / num_kv_heads) at most 16, or 32
  * for groups above 16) multiply the codes themselves, exact in fp16, with the
- * query rows scaled by a power of two to fp16's range, and apply each key's s and z
- * to the products in fp32; the weights, times the value rows' s, are rounded to
+ * query rows scaled by a power of two to fp16's range (exact but for values below 2^-23
+ * of the row's largest, which are off by 2^-31 of it at most), and apply each key's s
+ * and z to the products in fp32; the weights, times the value rows' s, are rounded to
  * fp16.  Longer requests round each cached value to fp16 first, scaled by a power
  * of two of its 128-key tile (one far below its
  * tile's largest is off by 2^-18 of that), and the weights to fp16.  A key that no

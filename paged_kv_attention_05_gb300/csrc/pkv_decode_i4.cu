@@ -30,11 +30,12 @@
 //     16 keys of a page are the MMA rows in the order kappa(m), so that the key rows
 //     that eight lanes read lie in different banks.
 //   * query rows are scaled by a power of two, so that their largest value is
-//     between 2^10 and 2^11 in fp16: bf16's 8 bits stay exact, whatever the range.  Rows of up
+//     between 2^10 and 2^11 in fp16: values down to 2^-23 of it stay exact, smaller ones
+//     are off by 2^-31 of it at most (half of the row is divided by 16 more).  Rows of up
 //     to 2^110: the factor that undoes it, and the codes' 2^24, stays finite (applied to the
 //     scales and zeros apart, for rows up to 2^127, it took 128 decodes of 8192 keys from
 //     182.4 to 183.9 us, and lost keys above 2^104).
-//   * weights: e_j t_j is rounded to fp16 (2^-12 of itself at most).  The
+//   * weights: e_j t_j is rounded to fp16 (2^-11 of itself at most).  The
 //     reference follows the largest e_j t_j of a row, not the largest e_j: fp16's range
 //     then holds every weight that counts, however large or small the value rows'
 //     scales.  It is moved only when a weight passes 2^14 (checked by one vote for

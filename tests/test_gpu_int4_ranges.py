@@ -62,6 +62,20 @@ def test_decodes_with_very_large_queries(e, hq, hkv, scale):
 
 
 @pytest.mark.parametrize("hq,hkv", [(8, 2), (12, 1), (32, 1)])
+def test_queries_whose_dimensions_differ_widely(hq, hkv):
+    """Dimensions of a query row that differ by 2^30: the small ones meet keys that are as
+    much larger."""
+    s = I.Step([(300, 1), (33, 2 if hq == 8 else 1), (2000, 1)], hq, hkv, 5)
+    e = torch.linspace(0, 30, R.D, device="cuda").round().double()
+    e = e[torch.randperm(R.D, generator=I.gen(4), device="cuda")]
+    s.q[:] = (s.q.double() * 2.0 ** -e).to(torch.bfloat16)
+    s.write()
+    s.attention()
+    assert pkv.pkv_get_error() == 0
+    s.check("wide queries")
+
+
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (12, 1), (32, 1)])
 @pytest.mark.parametrize("grow", [0.0, 0.4])
 def test_large_constant_value_rows(grow, hq, hkv):
     """Value rows without spread have the scale 0: their size, up to 2^60, is in the zeros
