@@ -497,7 +497,8 @@ int pkv_read_int4(const void* cache, int64_t num_blocks, int32_t block_size, int
  * and z to the products in fp32; the weights, times the value rows' s, are rounded to
  * fp16.  Longer requests round each cached value to fp16 first, scaled by a power
  * of two of its 128-key tile (one far below its
- * tile's largest is off by 2^-18 of that), and the weights to fp16.  A key that no
+ * tile's largest is off by 2^-18 of that; for values this largest counts as at least
+ * 2^-36, and 2^-60 of those of the tiles before), and the weights to fp16.  A key that no
  * row of its request sees may hold any bits.  Query values of up to 2^110 in size (with
  * a scale of at most 1), cached keys of up to 2^105 and cached values of up to 2^60 are
  * taken; beyond, outputs can be NaN.

@@ -53,7 +53,8 @@
 // bf16 tiles, 1083 with four and fp16 tiles, 940 with registers moved to the softmax and
 // the tiles' loop rolled, 857 with a row per softmax thread, 843 with key codes in
 // buffers of their own, 788 with codes taken as fp16 subnormals, 755 with the query rows
-// converted by all six.  What it has over pkv_attention's 630 is the forming of the
+// converted by all six, 760 with V tiles scaled each by its own largest value (by that of
+// all tiles so far, values far below it were lost).  What it has over pkv_attention's 630 is the forming of the
 // tiles: beside it tensor pipe 49%, issue slots 53%, alu 43%.
 // Every mbarrier wait is bounded; on expiry the kernel records
 // PKV_DEV_ERR_TIMEOUT, stops issuing work, frees its TMEM and returns.
@@ -87,7 +88,7 @@ constexpr int kPageBoxBytes = 16 * 128;           // one 16-slot x 64-dim box
 constexpr int kTmemCols = 512;
 constexpr float kRescaleThreshold = 8.0f;         // log2 units
 constexpr float kMaxSum = 0x1p40f;                // scored calls: sum of a row over a pair of blocks
-constexpr float kMaxSum16 = 0x1p14f;              // 4-bit calls: sum of a row over 64 columns
+constexpr float kMaxSum16 = 0x1.fp15f;            // 4-bit calls: sum of a row over 64 columns
 constexpr float kLift16 = 8.f;                    // and log2 of the largest weight at first
 
 // shared-memory layout (offsets from a 1024-byte aligned base)
@@ -464,8 +465,8 @@ __device__ __forceinline__ void rescale16_bf16(uint32_t t, float alpha) {
 // significant bits (s with 8 times a code with 4, plus z), of which bf16 keeps 8 and
 // fp16 11, and the same goes for the weights (outputs off by 3.0e-3 of their size with
 // bf16 tiles, 1.7e-3 with these, of which the bf16 output is 1.6e-3).  What fp16 lacks
-// in range, powers of two make up: each query row, each K tile and an item's V tiles so
-// far have one, by which their largest value lies in [2^13, 2^14) (query rows) or
+// in range, powers of two make up: each query row and each K and V tile have one, by which
+// their largest value lies in [2^13, 2^14) (query rows) or
 // [2^-7, 2^-6) (tiles, see dequant8): values down to 2^-7 of the largest keep all
 // their bits, and what is below is off by 2^-18 of it at most.
 __device__ __forceinline__ int q_exponent(uint32_t x) {
@@ -1206,8 +1207,11 @@ __global__ void __launch_bounds__(kI4 ? kThreadsI4 : threads_of(kCap == kFixedCa
         if (lane == 0) mbar_arrive(bar(B_IE + slot));
         if (it.r < 0) break;
         // tile j's exponents (the first of the two warps): the largest of |z| and
-        // |z + 15 s| of its keys, and of its values and those before them
-        int vexp = -100;
+        // |z + 15 s| of its keys, and of its values.  The weights and their sum follow the
+        // values': it counts as 2^-36 at least, and 2^-60 of those before it, which keeps
+        // them in fp32's range for values of up to 2^60.
+        constexpr int kLeast = 7 - 36;
+        int vmax = kLeast;
         auto exponents = [&](int j) {
           const uint32_t c = tile_cnt + j;
           if (warp != 2) return;
@@ -1229,7 +1233,9 @@ __global__ void __launch_bounds__(kI4 ? kThreadsI4 : threads_of(kCap == kFixedCa
             }
           }
           const int kexp = tile_exponent(__reduce_max_sync(0xffffffffu, big[0]));
-          vexp = max(vexp, tile_exponent(__reduce_max_sync(0xffffffffu, big[1])));
+          const int e = tile_exponent(__reduce_max_sync(0xffffffffu, big[1]));
+          const int vexp = max(max(e, kLeast), vmax - 60);
+          vmax = max(vmax, e);
           if (lane == 0) {
             *reinterpret_cast<int2*>(smem + kOffTileExp + 8 * (c & 3)) = make_int2(kexp, vexp);
             mbar_arrive(i4_bar(I_XR + (c & 3)));
@@ -1248,12 +1254,14 @@ __global__ void __launch_bounds__(kI4 ? kThreadsI4 : threads_of(kCap == kFixedCa
       take_regs<kRegsSoft, true>();
       // ------------- softmax of a 4-bit call: four warps for each query tile -------------
       // A row per thread, its 128 scores in two rounds of 64: nothing passes between
-      // warps.  The scores are scaled by the powers of two of the row and of the K tile;
-      // the V tiles', when it grows, is a change to O.  The reference (whole log2 units)
-      // moves when the sum of a round passes 2^14, to where the largest weight is 2^8: below
-      // fp16's largest number, and far enough above its smallest that 2^19 keys' roundings
-      // to halves of 2^-24 are 2^-13 of the largest weight together.  One loop for
-      // everything, on purpose: with the exponentials in two places and both query tiles in
+      // warps.  The scores are scaled by the powers of two of the row and of the K tile; a V
+      // tile's, 2^ev, goes into its weights, w = 2^(x + ev - ref), so that a tile keeps its
+      // values' bits whatever the size of the others'.  The reference (whole log2 units)
+      // moves when the sum of a round passes 63488, close below fp16's largest number (with
+      // 2^14, more often: 788 us for 760, see above), to where the largest weight is 2^8: far
+      // enough above fp16's smallest that 2^19 keys' roundings to halves of 2^-24 are 2^-13
+      // of the largest weight together.  The row's sum of 2^x is kept in units of the present
+      // tile's, l 2^(ref - ev).  One loop for everything, on purpose: with the exponentials in two places and both query tiles in
       // one warp the kernel's roles did not fit the instruction caches together, and all of
       // them, the MMA's too, took two to three times as long (4 chunks of 2047 tokens, 64
       // heads: 1368 us, 940 with the tiles' loop rolled).
@@ -1292,8 +1300,10 @@ __global__ void __launch_bounds__(kI4 ? kThreadsI4 : threads_of(kCap == kFixedCa
           const float f = fmaxf(
               sl2 * pow2(te.x) * reinterpret_cast<const float*>(smem + qfac_offset(it_cnt, x))[row],
               0x1p-126f);
-          float o_alpha = j > 0 ? pow2(max(vexp - te.y, -126)) : 1.f;
+          l *= pow2(min(te.y - vexp, 127));
           vexp = te.y;
+          const float ev = (float)vexp;
+          float o_alpha = 1.f;
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             const int lim = qpos - j * kTileK - 64 * h;  // columns <= lim are visible
@@ -1317,7 +1327,7 @@ __global__ void __launch_bounds__(kI4 ? kThreadsI4 : threads_of(kCap == kFixedCa
                   m0 = max3f(m0, sv[i], sv[i + 1]);
                   m1 = max3f(m1, sv[i + 2], sv[i + 3]);
                 }
-                const float m = ceilf(fmaxf(m0, m1) * f) - kLift16;
+                const float m = ceilf(fmaxf(m0, m1) * f) + ev - kLift16;
                 const float to = move ? fmaxf(ref, m) : ref;
                 const float alpha = ref == -INFINITY ? 0.f : fast_exp2(ref - to);
                 ref = to;
@@ -1329,10 +1339,10 @@ __global__ void __launch_bounds__(kI4 ? kThreadsI4 : threads_of(kCap == kFixedCa
                   for (int ch = 0; ch < 2; ++ch) rescale16_f16(t_s0 + 16 * ch, alpha);
                 }
               }
-              // p = exp2(s * f - ref), packed over sv[0 .. 31] (sv[2i], sv[2i + 1] are read
+              // w = exp2(s * f + ev - ref), packed over sv[0 .. 31] (sv[2i], sv[2i + 1] are read
               // before sv[i] is written)
               float rs[4] = {0.f, 0.f, 0.f, 0.f};
-              const float nm = -ref;
+              const float nm = ev - ref;
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
                 float x0, x1;
@@ -1360,8 +1370,7 @@ __global__ void __launch_bounds__(kI4 ? kThreadsI4 : threads_of(kCap == kFixedCa
           if (lane == 0) mbar_arrive(bar(B_PF + x));
         }
         if (!ok) break;
-        // the row sum of the item, for the epilogue; the output is to be multiplied by
-        // 2^vexp
+        // the row's sum in units of the weights, for the epilogue
         lsum[((it_cnt & 1) * 2 + x) * 2 * 128 + row] = l * pow2(-vexp);
         __syncwarp();
         if (lane == 0) mbar_arrive(lf_bar(it_cnt, x));

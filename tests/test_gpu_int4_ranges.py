@@ -91,3 +91,85 @@ def test_large_constant_value_rows(grow, hq, hkv):
     s.attention()
     assert pkv.pkv_get_error() == 0
     s.check("constant rows")
+
+
+def prompt_bound(s, r):
+    """Attention of request r of a step in 64 bits and what a prompt's kernel may be off by:
+    the output's rounding (2^-8); weights rounded to fp16, twice where the reference moved
+    within a tile (2^-11 each); keys and values rounded to fp16 (2^-11), and what lies far
+    below the largest of its own tile of 128 keys by 2^-18 of that (tiles 2^60 below the
+    largest before them count as 2^-60 of it); and weights below fp16's normal range, of
+    which the reference keeps the largest weight times its tile's size above 2^7: half of
+    2^-24 a rounding, 2^-31 of the largest of weight times the tile's largest value, per key."""
+    a, b, L = int(s.qsl[r]), int(s.qsl[r + 1]), int(s.seq[r])
+    pages = s.cache[s.bt[r, :-(-L // R.BS)].long()]
+    pos = torch.arange(L - (b - a), L, device="cuda")
+    hidden = torch.arange(L, device="cuda")[None] > pos[:, None]
+    G = s.hq // s.hkv
+    pad = -L % TILE
+
+    def largest(x):    # of each key's tile
+        t = torch.nn.functional.pad(x.abs().amax(-1), (0, pad)).view(-1, TILE).amax(-1)
+        return t
+
+    outs, bounds = [], []
+    for h in range(s.hq):
+        g = h // G
+        (kc, ks, kz), (vc, vs, vz) = (tuple(t.reshape(-1, *t.shape[2:])[:L]
+                                            for t in R.unpack(pages[:, g], side))
+                                      for side in (0, 1))
+        k, v = kc * ks[:, None] + kz[:, None], vc * vs[:, None] + vz[:, None]
+        kt = largest(k).repeat_interleave(TILE)[:L]
+        vt = largest(v)
+        vt = torch.maximum(vt, 2.0 ** -60 * vt.cummax(0).values).repeat_interleave(TILE)[:L]
+        q = s.q[a:b, h].double()
+        p = torch.softmax((q @ k.T * s.scale).masked_fill(hidden, -torch.inf), -1)
+        o, av = p @ v, p @ v.abs()
+        dx = abs(s.scale) * (2.0 ** -11 * (q.abs() @ k.abs().T) +
+                             2.0 ** -18 * q.abs().sum(-1, keepdim=True) * kt)
+        dx = dx.masked_fill(hidden, 0.)
+        t = 2 * 2.0 ** -11 * av + 2.0 ** -18 * (p @ vt)[:, None] + \
+            2 * 2.0 ** -31 * L * (p * vt).amax(-1, keepdim=True)
+        turn = (p * dx) @ v.abs() + (p * dx).sum(-1, keepdim=True) * av
+        outs.append(o)
+        bounds.append(2.0 ** -8 * o.abs() + 1.01 * (t + 1.1 * turn) + 2.0 ** -20 * av)
+    return torch.stack(outs, 1), torch.stack(bounds, 1)
+
+
+def check_prompts(s, what):
+    for r in range(len(s.reqs)):
+        ref, bound = prompt_bound(s, r)
+        got = s.out[int(s.qsl[r]):int(s.qsl[r + 1])].double()
+        err = (got - ref).abs()
+        assert bool((err <= bound).all()), "%s, request %d: error up to %g of the bound" % (
+            what, r, float((err / bound).nan_to_num(9e9).max()))
+
+
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (3, 1)])
+@pytest.mark.parametrize("kind", ["one large row", "larger by and by", "smaller by and by",
+                                  "by turns", "zero first", "zero tiles", "far apart"])
+def test_values_whose_size_changes_from_tile_to_tile(kind, hq, hkv):
+    s = I.Step([(700, 150), (0, 777), (1300, 33)], hq, hkv, 17)
+    g = I.gen(3)
+    s.q[:] = (1 + 0.3 * s.q.float()).to(torch.bfloat16)
+    at = torch.cat([torch.arange(c + n, device="cuda") for c, n in s.reqs])
+    tile = (at // TILE).double()
+    if kind == "one large row":        # of which no weight is left
+        s.k[at == 0] = -4
+        s.v[at == 0] *= 2.0 ** 20
+    else:
+        e = {"larger by and by": 5 * tile, "smaller by and by": 20 - 7 * tile,
+             "by turns": 30 * (tile % 2), "zero first": 5 - 4 * tile, "zero tiles": 3 * tile,
+             "far apart": torch.where(tile % 3 == 1, 60., -20. * (tile % 3))}[kind]
+        s.v[:] = (s.v.double() * (2.0 ** e)[:, None, None]).to(torch.bfloat16)
+        if kind == "zero first":
+            s.v[tile == 0] = 0
+        if kind == "zero tiles":
+            s.v[tile % 2 == 1] = 0
+        if kind in ("smaller by and by", "by turns", "far apart"):
+            # the small ones' keys have nearly all of the weight
+            s.k[:] = (s.k.double() - (e - e.min())[:, None, None] / 16).to(torch.bfloat16)
+    s.write()
+    s.attention()
+    assert pkv.pkv_get_error() == 0
+    check_prompts(s, kind)
