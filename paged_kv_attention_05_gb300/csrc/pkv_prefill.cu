@@ -1261,10 +1261,10 @@ __global__ void __launch_bounds__(kI4 ? kThreadsI4 : threads_of(kCap == kFixedCa
       // 2^14, more often: 788 us for 760, see above), to where the largest weight is 2^8: far
       // enough above fp16's smallest that 2^19 keys' roundings to halves of 2^-24 are 2^-13
       // of the largest weight together.  The row's sum of 2^x is kept in units of the present
-      // tile's, l 2^(ref - ev).  One loop for everything, on purpose: with the exponentials in two places and both query tiles in
-      // one warp the kernel's roles did not fit the instruction caches together, and all of
-      // them, the MMA's too, took two to three times as long (4 chunks of 2047 tokens, 64
-      // heads: 1368 us, 940 with the tiles' loop rolled).
+      // tile's, l 2^(ref - ev).  One loop for everything, on purpose: with the exponentials in
+      // two places and both query tiles in one warp the kernel's roles did not fit the
+      // instruction caches together, and all of them, the MMA's too, took two to three times
+      // as long (4 chunks of 2047 tokens, 64 heads: 1368 us, 940 with the tiles' loop rolled).
       const int x = (warp - kSoft0) >> 2;
       const int qd = warp & 3;
       const int row = qd * 32 + lane;  // == TMEM lane
