@@ -490,8 +490,10 @@ __device__ __forceinline__ bool run_unit(const AttnArgs& a, const Workspace& ws,
   return true;
 }
 
-// Groups of up to 8 heads: a unit's rows 8 at a time (single tokens: one time).  Larger
-// groups: two tiles, and above 16 heads a unit is two items, of its first 16 query rows
+// Groups of up to 8 heads: a unit's rows 8 at a time, its pages read again each time
+// (single tokens: one time.  64 decodes of 8192 keys, 32 heads on 8, of 1 | 2 | 4 tokens:
+// 120 | 124 | 220 us, pkv_attention 190 | 194 | 203; 64 of 2048 keys, 32 on 32, of 1 | 8 |
+// 16: 120 | 128 | 231).  Larger groups: two tiles, and above 16 heads a unit is two items, of its first 16 query rows
 // and of the rest, for two warps that each read its pages (the second out of the L2).
 template <int kTiles>
 __global__ void __launch_bounds__(Cfg4<kTiles>::kThreads, 1)

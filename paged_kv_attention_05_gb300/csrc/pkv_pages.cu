@@ -252,8 +252,13 @@ __device__ __forceinline__ float score_pages(const SelectArgs& a, const int32_t*
 // row | 64 of 513 for 128 rows, 8 KV heads, us (floors 1.2 and 39.7): scores and selection
 // in two launches, the border found bit by bit 32 | 112; in one 43 | 100; the border by
 // histograms of eight bits 15 | 80; 256 pages a CTA 16 | 72; and all of a row's by four
-// warps 14 | 61.  Of these the scores alone take 47; the border by one warp, without
-// barriers, and block ids kept in shared memory were slower (80, 73).
+// warps 14 | 60; with U and D formed again where a row's request has to be looked for, and
+// so in other registers, 14 | 57.  Of these the scores alone take 47; the border by one
+// warp, without barriers, and block ids kept in shared memory were slower (80, 73).  64
+// registers a thread, of which 8 to 24 bytes are spilled; more would cost CTAs.
+// The grid follows the block table's width, not the rows' pages: a CTA past its row's pages
+// reads the queries and the metadata before it returns (the 128 rows in tables of 513 |
+// 1024 | 8192 | 32,768 pages, one call at a time: 67 | 79 | 159 | 487).
 template <int kPages, int kSelThreads, bool kStream>
 __global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads)
     select_kernel(SelectArgs a, int64_t row0) {
@@ -615,13 +620,13 @@ cudaError_t launch_page_bounds(const uint16_t* kc, int64_t num_blocks, int hkv, 
 // last is not scored) and the CTAs fill five of the eight places of each SM: no scores pass
 // through memory, and eight CTAs an SM select and score at different times.  Else 256 by
 // eight warps, or 128 where that leaves SMs without one.  us with 128 | 256 | 512, 8 KV heads:
-//   4 rows of 513 pages    14 | 14 | 21      100 of 513    72 |  66 |  56
-//   1 of 2050              15 | 16 | 29      128 of 513    87 |  78 |  60
-//   1 of 8000              28 | 28 | 48      256 of 260   109 |  99 |  67
-//   64 of 513              47 | 44 | 55      512 of 70     76 |  76 |  51
-//   32 of 2050             79 | 71 | 77      256 of 513   154 | 135 | 111
-// (512 by eight warps, four CTAs an SM: 128 of 513 in 75; by sixteen 82; 32 a CTA: 1 of
-// 8000 in 55.)  Half of the L2 or more of bounds are streamed: 128 of 513 pages 63 -> 61, 32
+//   4 rows of 513 pages    12 | 12 | 18      100 of 513    68 |  58 |  51
+//   1 of 2050              16 | 16 | 26      128 of 513    82 |  67 |  56
+//   1 of 8000              42 | 42 | 80      256 of 260   100 |  85 |  62
+//   64 of 513              44 | 39 | 45      512 of 70     79 |  68 |  48
+//   32 of 2050             80 | 68 | 69      256 of 513   148 | 119 | 103
+// (512 by eight warps, four CTAs an SM: 128 of 513 in 75, by sixteen 82, before the last step
+// at the kernel; 32 a CTA: 1 of 8000 in 55.)  Half of the L2 or more of bounds are streamed: 128 of 513 pages 63 -> 61, 32
 // of 2050 77 -> 72, 30 of 1000 43 -> 40, 8 of 8000 94 -> 89.
 int select_chunk_pages(int64_t rows, int hkv, int64_t bt_width, int sms) {
   if (bt_width - 1 <= 512 && rows * hkv >= 5 * (int64_t)sms) return 512;
