@@ -126,7 +126,8 @@ constexpr int kSmemBytes = kOffBarLF1 + 16 + 1024;  // + alignment slack
 // rows; 8 of softmax; 4 of epilogue; two for K tiles, two for V tiles), the scales and
 // zeros of the tiles, and the powers of two that its fp16 tiles are scaled by.  The
 // softmax takes registers from the other warps: with the 96 that 640 threads have each
-// it spills (999 against 870 us for 4 chunks of 2047 tokens, the tiles left zero).
+// it spills (999 against 870 us for 4 chunks of 2047 tokens, the tiles left zero); with the
+// shares below 28 bytes still are.
 constexpr int kThreadsI4 = 640;
 constexpr int kRegsLaunch = 96, kRegsSoft = 120, kRegsEpi = 96, kRegsFew = 72;
 static_assert(256 * kRegsSoft + 128 * kRegsEpi + 256 * kRegsFew <= kThreadsI4 * kRegsLaunch,
